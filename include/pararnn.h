@@ -336,6 +336,116 @@ int pararnn_gru_forward_noalloc(int64_t B, int64_t L, int64_t H,
                                 const float *h0, float *h, float tol, int32_t max_iter,
                                 int32_t *info, float *trace, void *stream);
 
+/*
+ * Operators around the recurrences
+ * --------------------------------
+ * What a sequence model built on the recurrences needs next to them: linear
+ * attention with a decay per head (a linear recurrence with a matrix state),
+ * layer norm and the embedding lookup, each with its gradient.  Tensors are
+ * fp32 or bf16 (`dtype`, all sequence tensors of a call alike); states,
+ * decays, norm weights and statistics are always fp32, and so is every sum.
+ * bf16 results are rounded once, to nearest even.  Outputs are dense and must
+ * not alias inputs unless stated.  Workspaces follow the rules above and may
+ * be shared with every other entry point.  Results do not depend on timing:
+ * the same inputs give the same bits.
+ */
+enum { PARARNN_F32 = 0, PARARNN_BF16 = 1 };
+
+/*
+ * Linear attention with decay: for each batch row and head, with g the head's
+ * log decay (g <= 0; -infinity forgets everything at once),
+ *     S_t = e^g S_{t-1} + k_t^T v_t,   o_t = scale q_t S_t,   S_{-1} = state.
+ * q, k: [B, L, H, dk]; v, o: [B, L, H, dv]; state, out_state: [B, H, dk, dv]
+ * fp32 (state NULL: zeros; out_state NULL: not wanted; out_state may be
+ * state itself).  log_decay: [H] fp32.  1 <= dk, dv <= 256 (above:
+ * PARARNN_ERR_UNSUPPORTED).
+ * strides: HOST array of {batch row, position, head} strides in elements for
+ * q, k and v in turn (9 values), not negative; the last dimension is dense.
+ * NULL: dense tensors.  Operands whose rows are 16-byte aligned move faster.
+ * A value that is not finite at position t of q, k or v affects no output
+ * before t; from t on the affected outputs are not finite (an infinity may
+ * come out as NaN).
+ */
+size_t pararnn_linattn_workspace_bytes(int32_t backward, int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk,
+                                       int64_t dv);
+int pararnn_linattn_forward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk, int64_t dv,
+                            const void *q, const void *k, const void *v, const int64_t *strides,
+                            const float *log_decay, const float *state, float scale, void *o,
+                            float *out_state, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Its gradients for a loss with dLoss/do = grad_o ([B, L, H, dv]) and
+ * dLoss/d(final state) = grad_out_state ([B, H, dk, dv] or NULL for zeros):
+ *     D_t = e^g D_{t+1} + scale q_t^T do_t   (plus grad_out_state at L-1),
+ *     dq_t = scale do_t S_t^T,  dk_t = v_t D_t^T,  dv_t = k_t D_t,
+ *     dstate = e^g D_0.
+ * The log decay is a constant of the model and gets no gradient.
+ * strides: as above for q, k, v and grad_o (12 values).  grad_state: NULL if
+ * not wanted.
+ */
+int pararnn_linattn_backward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk, int64_t dv,
+                             const void *q, const void *k, const void *v, const void *grad_o,
+                             const int64_t *strides, const float *log_decay, const float *state,
+                             const float *grad_out_state, float scale, void *grad_q, void *grad_k,
+                             void *grad_v, float *grad_state, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * One token of the recurrence above (its form for decoding): q, k [B, H, dk],
+ * v, o [B, H, dv], state and out_state [B, H, dk, dv], both required;
+ * out_state may be state itself.  strides: as above with the position's
+ * stride ignored, or NULL.  No workspace.
+ */
+int pararnn_linattn_step(int32_t dtype, int64_t B, int64_t H, int64_t dk, int64_t dv, const void *q,
+                         const void *k, const void *v, const int64_t *strides, const float *log_decay,
+                         const float *state, float scale, void *o, float *out_state, void *stream);
+
+/*
+ * Layer norm over the last dimension of [rows, D], after an optional residual
+ * sum: s = x + residual (rounded to dtype; s = x without one),
+ *     y = (s - mean) rstd weight + bias,  rstd = 1 / sqrt(var + eps)
+ * with the biased variance.  weight, bias: [D] fp32 or NULL (one, zero).
+ * sum: [rows, D] output, given exactly when residual is.  mean, rstd: [rows]
+ * fp32 outputs or NULL.  eps >= 0; D < 2^24.
+ */
+int pararnn_layernorm_forward(int32_t dtype, int64_t rows, int64_t D, const void *x, const void *residual,
+                              const float *weight, const float *bias, float eps, void *sum, void *y,
+                              float *mean, float *rstd, void *stream);
+
+/*
+ * Its gradients: s is the forward's sum (x without a residual), mean and rstd
+ * its statistics; grad_sum: [rows, D], what reaches s past the norm, or NULL.
+ *     xh = (s - mean) rstd, g = grad_y weight,
+ *     grad_x = rstd (g - mean(g) - xh mean(g xh)) + grad_sum
+ * (the gradient of x and of the residual alike), grad_weight = sum over rows
+ * of grad_y xh, grad_bias = sum over rows of grad_y, [D] fp32 each or NULL.
+ * ws: pararnn_layernorm_workspace_bytes (unused, may be NULL, when neither
+ * weight nor bias gradient is wanted).
+ */
+size_t pararnn_layernorm_workspace_bytes(int64_t rows, int64_t D);
+int pararnn_layernorm_backward(int32_t dtype, int64_t rows, int64_t D, const void *s, const float *weight,
+                               const float *mean, const float *rstd, const void *grad_y,
+                               const void *grad_sum, void *grad_x, float *grad_weight, float *grad_bias,
+                               void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Embedding lookup: out[n] = scale table[ids[n]], table [V, D], out [N, D];
+ * ids: int32 or int64 (id_bytes 4 or 8).  An id outside [0, V) reads nothing
+ * and gives a row of NaN.  N, V < 2^30, D < 2^24.
+ */
+int pararnn_embedding_forward(int32_t dtype, int64_t N, int64_t V, int64_t D, const void *ids,
+                              int32_t id_bytes, const void *table, float scale, void *out, void *stream);
+
+/*
+ * Its gradient: grad_table[r] = scale * sum of grad[n] over the n with
+ * ids[n] = r in ascending n, for every row r of [V, D] (zeros where no id
+ * names the row).  The ids are sorted, so the order of the sums is fixed.
+ * padding_idx: a row that gets zeros, or -1.  Ids outside [0, V) are left out.
+ */
+size_t pararnn_embedding_workspace_bytes(int64_t N, int64_t V, int64_t D);
+int pararnn_embedding_backward(int32_t dtype, int64_t N, int64_t V, int64_t D, const void *ids,
+                               int32_t id_bytes, const void *grad, float scale, int64_t padding_idx,
+                               void *grad_table, void *ws, size_t ws_bytes, void *stream);
+
 /* Short text for a status code (static storage). */
 const char *pararnn_status_string(int status);
 

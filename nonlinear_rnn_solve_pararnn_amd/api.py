@@ -26,7 +26,11 @@ CELL_GRU, CELL_LSTM = 0, 1
 EXPORTS = ("pararnn_workspace_bytes", "rnn_linscan_diag", "rnn_linscan_blk2", "rnn_linscan_blk",
            "pararnn_gru_forward", "pararnn_lstm_forward", "pararnn_adjoint_backward",
            "pararnn_gru_sequential", "pararnn_lstm_sequential", "pararnn_status_string",
-           "pararnn_gru_forward_noalloc", "pararnn_hgru_forward", "pararnn_hgru_backward")
+           "pararnn_gru_forward_noalloc", "pararnn_hgru_forward", "pararnn_hgru_backward",
+           "pararnn_linattn_workspace_bytes", "pararnn_linattn_forward", "pararnn_linattn_backward",
+           "pararnn_linattn_step", "pararnn_layernorm_workspace_bytes", "pararnn_layernorm_forward",
+           "pararnn_layernorm_backward", "pararnn_embedding_forward",
+           "pararnn_embedding_workspace_bytes", "pararnn_embedding_backward")
 NOALLOC_SCRATCH_BYTES = 64 << 20   # PARARNN_NOALLOC_SCRATCH_BYTES
 
 _lib = None
@@ -77,6 +81,29 @@ def load_library():
     lib.pararnn_gru_forward_noalloc.argtypes = [i64, i64, i64] + [vp] * 8 + [
         ctypes.c_float, i32, vp, vp, vp]
     lib.pararnn_gru_forward_noalloc.restype = ctypes.c_int
+    lib.pararnn_linattn_workspace_bytes.argtypes = [i32, i32] + [i64] * 5
+    lib.pararnn_linattn_workspace_bytes.restype = sz
+    lib.pararnn_linattn_forward.argtypes = [i32] + [i64] * 5 + [vp] * 6 + [
+        ctypes.c_float, vp, vp, vp, sz, vp]
+    lib.pararnn_linattn_forward.restype = ctypes.c_int
+    lib.pararnn_linattn_backward.argtypes = [i32] + [i64] * 5 + [vp] * 8 + [
+        ctypes.c_float, vp, vp, vp, vp, vp, sz, vp]
+    lib.pararnn_linattn_backward.restype = ctypes.c_int
+    lib.pararnn_linattn_step.argtypes = [i32] + [i64] * 4 + [vp] * 6 + [ctypes.c_float, vp, vp, vp]
+    lib.pararnn_linattn_step.restype = ctypes.c_int
+    lib.pararnn_layernorm_workspace_bytes.argtypes = [i64, i64]
+    lib.pararnn_layernorm_workspace_bytes.restype = sz
+    lib.pararnn_layernorm_forward.argtypes = [i32, i64, i64] + [vp] * 4 + [ctypes.c_float] + [vp] * 5
+    lib.pararnn_layernorm_forward.restype = ctypes.c_int
+    lib.pararnn_layernorm_backward.argtypes = [i32, i64, i64] + [vp] * 10 + [sz, vp]
+    lib.pararnn_layernorm_backward.restype = ctypes.c_int
+    lib.pararnn_embedding_forward.argtypes = [i32, i64, i64, i64, vp, i32, vp, ctypes.c_float, vp, vp]
+    lib.pararnn_embedding_forward.restype = ctypes.c_int
+    lib.pararnn_embedding_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.pararnn_embedding_workspace_bytes.restype = sz
+    lib.pararnn_embedding_backward.argtypes = [i32, i64, i64, i64, vp, i32, vp, ctypes.c_float, i64,
+                                               vp, vp, sz, vp]
+    lib.pararnn_embedding_backward.restype = ctypes.c_int
     lib.pararnn_status_string.argtypes = [ctypes.c_int]
     lib.pararnn_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -137,6 +164,11 @@ def _workspace(op, B, L, H, device, max_iter=1, ws=None):
     n = workspace_bytes(op, B, L, H, max_iter)
     if n == 0:
         raise PararnnError("invalid sizes B=%d L=%d H=%d" % (B, L, H))
+    return _workspace_of(n, device, ws)
+
+
+def _workspace_of(n: int, device, ws=None):
+    """The caller's workspace if one is given, else the stream's, of at least n bytes."""
     if ws is not None:
         if ws.device != device or ws.numel() * ws.element_size() < n or ws.data_ptr() % 256:
             raise ValueError("workspace too small, misaligned or on the wrong device")
@@ -467,3 +499,288 @@ def adjoint_backward(cell: int, p: Sequence[torch.Tensor], u: Sequence[torch.Ten
                                         _ptr(grad_h), _ptr(grad_c), GP, GU, _ptr(gh0), _ptr(gc0),
                                         _ptr(ws), n, _stream(dev)), "pararnn_adjoint_backward")
     return {"p": gp, "u": gu, "h0": gh0, "c0": gc0}
+
+
+# ---------------------------------------------------------------- operators around the recurrences
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}   # PARARNN_F32, PARARNN_BF16
+MAX_HEAD_DIM = 256
+
+
+def _type_code(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    if t.device.type != "cuda":
+        raise ValueError("%s must be on a HIP device" % name)
+    return code
+
+
+def _need_typed(t, shape, dtype, name, device):
+    """A dense tensor of the given shape, type and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _linattn_views(tensors, shapes, names, dtype, device):
+    """Checks the operands; the strides array the library takes, or None if all are dense."""
+    dense = True
+    for t, shape, name in zip(tensors, shapes, names):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if t.dtype != dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if t.device != device:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+        if t.shape != shape:
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+        if not t.is_contiguous():
+            dense = False
+            if t.shape[-1] > 1 and t.stride(-1) != 1:
+                raise ValueError("the last dimension of %s must be dense" % name)
+    if dense:
+        return None
+    st = []
+    for t in tensors:
+        s = t.stride()
+        st += (s[0], s[1], s[2]) if t.dim() == 4 else (s[0], 0, s[1])
+    return (ctypes.c_int64 * len(st))(*st)
+
+
+def _linattn_check(q, v, seq: bool):
+    code = _type_code(q, "q")
+    if q.dim() != 3 + seq or not isinstance(v, torch.Tensor) or v.dim() != 3 + seq:
+        raise ValueError("q, k and v must be %s" % ("[B, L, H, d]" if seq else "[B, H, d]"))
+    dk, dv = q.shape[-1], v.shape[-1]
+    if q.numel() == 0 or dv == 0:
+        raise PararnnError("invalid sizes q %s, v %s" % (tuple(q.shape), tuple(v.shape)))
+    if dk > MAX_HEAD_DIM or dv > MAX_HEAD_DIM:
+        raise PararnnError("linear attention supports head sizes up to %d, got dk=%d dv=%d" % (MAX_HEAD_DIM, dk, dv))
+    return code, dk, dv
+
+
+def linattn_forward(q, k, v, log_decay, state=None, *, scale=None, want_state=True, out=None, out_state=None,
+                    ws=None):
+    """Linear attention with a decay per head over whole sequences:
+    S_t = e^g S_{t-1} + k_t^T v_t, o_t = scale q_t S_t, g = log_decay[head].
+
+    q, k [B, L, H, dk], v [B, L, H, dv], fp32 or bf16, any strides with a dense
+    last dimension; log_decay [H] fp32; state [B, H, dk, dv] fp32 or None.
+    scale defaults to dk^-0.5.  Returns (o [B, L, H, dv], final state or None
+    unless want_state).  out_state may be `state` itself."""
+    lib = load_library()
+    code, dk, dv = _linattn_check(q, v, True)
+    B, L, H, _ = q.shape
+    dev = q.device
+    kshape, vshape, sshape = (B, L, H, dk), (B, L, H, dv), (B, H, dk, dv)
+    st = _linattn_views((q, k, v), (kshape, kshape, vshape), ("q", "k", "v"), q.dtype, dev)
+    _need_typed(log_decay, (H,), torch.float32, "log_decay", dev)
+    if state is not None:
+        _need_typed(state, sshape, torch.float32, "state", dev)
+    if out is None:
+        out = torch.empty(vshape, dtype=q.dtype, device=dev)
+    else:
+        _need_typed(out, vshape, q.dtype, "out", dev)
+    if out_state is not None:
+        _need_typed(out_state, sshape, torch.float32, "out_state", dev)
+    elif want_state:
+        out_state = torch.empty(sshape, dtype=torch.float32, device=dev)
+    buf, n = _workspace_of(lib.pararnn_linattn_workspace_bytes(0, code, B, L, H, dk, dv), dev, ws)
+    _check(lib.pararnn_linattn_forward(code, B, L, H, dk, dv, _ptr(q), _ptr(k), _ptr(v), st, _ptr(log_decay),
+                                       _ptr(state), dk ** -0.5 if scale is None else scale, _ptr(out),
+                                       _ptr(out_state), _ptr(buf), n, _stream(dev)), "pararnn_linattn_forward")
+    return out, out_state
+
+
+def linattn_backward(q, k, v, log_decay, grad_o, state=None, grad_state=None, *, scale=None, want_state=None,
+                     ws=None):
+    """Gradients of linattn_forward for dLoss/do = grad_o and dLoss/d(final
+    state) = grad_state (None: zeros).  Returns (dq, dk, dv, dstate), dstate
+    None unless want_state (default: whether a state is given).  log_decay is
+    a constant of the model and gets no gradient."""
+    lib = load_library()
+    code, dk, dv = _linattn_check(q, v, True)
+    B, L, H, _ = q.shape
+    dev = q.device
+    kshape, vshape, sshape = (B, L, H, dk), (B, L, H, dv), (B, H, dk, dv)
+    st = _linattn_views((q, k, v, grad_o), (kshape, kshape, vshape, vshape), ("q", "k", "v", "grad_o"), q.dtype, dev)
+    _need_typed(log_decay, (H,), torch.float32, "log_decay", dev)
+    for t, name in ((state, "state"), (grad_state, "grad_state")):
+        if t is not None:
+            _need_typed(t, sshape, torch.float32, name, dev)
+    if want_state is None:
+        want_state = state is not None
+    gq, gk = (torch.empty(kshape, dtype=q.dtype, device=dev) for _ in range(2))
+    gv = torch.empty(vshape, dtype=q.dtype, device=dev)
+    gs = torch.empty(sshape, dtype=torch.float32, device=dev) if want_state else None
+    buf, n = _workspace_of(lib.pararnn_linattn_workspace_bytes(1, code, B, L, H, dk, dv), dev, ws)
+    _check(lib.pararnn_linattn_backward(code, B, L, H, dk, dv, _ptr(q), _ptr(k), _ptr(v), _ptr(grad_o), st,
+                                        _ptr(log_decay), _ptr(state), _ptr(grad_state),
+                                        dk ** -0.5 if scale is None else scale, _ptr(gq), _ptr(gk), _ptr(gv),
+                                        _ptr(gs), _ptr(buf), n, _stream(dev)), "pararnn_linattn_backward")
+    return gq, gk, gv, gs
+
+
+def linattn_step(q, k, v, log_decay, state, *, scale=None, out=None, out_state=None):
+    """One token of linattn_forward (decoding): q, k [B, H, dk], v [B, H, dv],
+    state [B, H, dk, dv].  Returns (o [B, H, dv], new state); out_state may be
+    `state` itself."""
+    lib = load_library()
+    code, dk, dv = _linattn_check(q, v, False)
+    B, H, _ = q.shape
+    dev = q.device
+    kshape, vshape, sshape = (B, H, dk), (B, H, dv), (B, H, dk, dv)
+    st = _linattn_views((q, k, v), (kshape, kshape, vshape), ("q", "k", "v"), q.dtype, dev)
+    _need_typed(log_decay, (H,), torch.float32, "log_decay", dev)
+    _need_typed(state, sshape, torch.float32, "state", dev)
+    if out is None:
+        out = torch.empty(vshape, dtype=q.dtype, device=dev)
+    else:
+        _need_typed(out, vshape, q.dtype, "out", dev)
+    if out_state is None:
+        out_state = torch.empty(sshape, dtype=torch.float32, device=dev)
+    else:
+        _need_typed(out_state, sshape, torch.float32, "out_state", dev)
+    _check(lib.pararnn_linattn_step(code, B, H, dk, dv, _ptr(q), _ptr(k), _ptr(v), st, _ptr(log_decay), _ptr(state),
+                                    dk ** -0.5 if scale is None else scale, _ptr(out), _ptr(out_state),
+                                    _stream(dev)), "pararnn_linattn_step")
+    return out, out_state
+
+
+def _rows(x, name):
+    """(rows, D) of a tensor normalised over its last dimension."""
+    D = x.shape[-1] if x.dim() else 0
+    if x.numel() == 0:
+        raise PararnnError("%s is empty: %s" % (name, tuple(x.shape)))
+    return x.numel() // D, D
+
+
+def layernorm_forward(x, weight=None, bias=None, residual=None, *, eps=1e-5, out=None, out_sum=None):
+    """Layer norm over the last dimension, after an optional residual sum:
+    s = x + residual (in x's type), y = (s - mean) rstd weight + bias.
+
+    x, residual [..., D] fp32 or bf16; weight, bias [D] fp32 or None.  Returns
+    (y, s, mean, rstd): s is x itself without a residual, mean and rstd [...]
+    fp32 are what layernorm_backward takes."""
+    lib = load_library()
+    code = _type_code(x, "x")
+    rows, D = _rows(x, "x")
+    dev, shape = x.device, x.shape
+    _need_typed(x, shape, x.dtype, "x", dev)
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _need_typed(t, (D,), torch.float32, name, dev)
+    y = torch.empty_like(x) if out is None else out
+    if out is not None:
+        _need_typed(out, shape, x.dtype, "out", dev)
+    s = None
+    if residual is not None:
+        _need_typed(residual, shape, x.dtype, "residual", dev)
+        s = torch.empty_like(x) if out_sum is None else out_sum
+        _need_typed(s, shape, x.dtype, "out_sum", dev)
+    elif out_sum is not None:
+        raise ValueError("out_sum is given without a residual")
+    mean, rstd = (torch.empty(shape[:-1], dtype=torch.float32, device=dev) for _ in range(2))
+    _check(lib.pararnn_layernorm_forward(code, rows, D, _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), eps,
+                                         _ptr(s), _ptr(y), _ptr(mean), _ptr(rstd), _stream(dev)),
+           "pararnn_layernorm_forward")
+    return y, x if s is None else s, mean, rstd
+
+
+def layernorm_backward(s, weight, mean, rstd, grad_y, grad_sum=None, *, want_w=True, want_b=True, ws=None):
+    """Gradients of layernorm_forward: s, mean, rstd are its results, grad_sum
+    (None: zero) what reaches the sum past the norm.  Returns (dx, dweight,
+    dbias); dx is the gradient of x and of the residual alike."""
+    lib = load_library()
+    code = _type_code(s, "s")
+    rows, D = _rows(s, "s")
+    dev, shape = s.device, s.shape
+    _need_typed(s, shape, s.dtype, "s", dev)
+    _need_typed(grad_y, shape, s.dtype, "grad_y", dev)
+    if grad_sum is not None:
+        _need_typed(grad_sum, shape, s.dtype, "grad_sum", dev)
+    if weight is not None:
+        _need_typed(weight, (D,), torch.float32, "weight", dev)
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _need_typed(t, shape[:-1], torch.float32, name, dev)
+    dx = torch.empty_like(s)
+    gw = torch.empty(D, dtype=torch.float32, device=dev) if want_w else None
+    gb = torch.empty(D, dtype=torch.float32, device=dev) if want_b else None
+    buf, n = _workspace_of(lib.pararnn_layernorm_workspace_bytes(rows, D), dev, ws) if want_w or want_b else (None, 0)
+    _check(lib.pararnn_layernorm_backward(code, rows, D, _ptr(s), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(grad_y),
+                                          _ptr(grad_sum), _ptr(dx), _ptr(gw), _ptr(gb), _ptr(buf), n, _stream(dev)),
+           "pararnn_layernorm_backward")
+    return dx, gw, gb
+
+
+def _ids(ids, device):
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
+    if ids.device != device:
+        raise ValueError("ids is on %s, expected %s" % (ids.device, device))
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    if ids.numel() == 0:
+        raise PararnnError("ids is empty")
+    return ids.numel(), ids.element_size()
+
+
+def embedding_forward(ids, table, *, scale=1.0, out=None):
+    """scale * table[ids]: ids [...] int32 or int64, table [V, D] fp32 or bf16;
+    returns [..., D].  An id outside [0, V) gives a row of NaN."""
+    lib = load_library()
+    code = _type_code(table, "table")
+    dev = table.device
+    if table.dim() != 2 or table.numel() == 0:
+        raise ValueError("table must be [V, D], got %s" % (tuple(table.shape),))
+    V, D = table.shape
+    _need_typed(table, (V, D), table.dtype, "table", dev)
+    N, nb = _ids(ids, dev)
+    if out is None:
+        out = torch.empty((*ids.shape, D), dtype=table.dtype, device=dev)
+    else:
+        _need_typed(out, (*ids.shape, D), table.dtype, "out", dev)
+    _check(lib.pararnn_embedding_forward(code, N, V, D, _ptr(ids), nb, _ptr(table), scale, _ptr(out), _stream(dev)),
+           "pararnn_embedding_forward")
+    return out
+
+
+def embedding_backward(ids, grad, num_rows, *, scale=1.0, padding_idx=None, out=None, ws=None):
+    """Gradient of embedding_forward's table: [num_rows, D] in grad's type,
+    row r = scale * the sum of grad over the positions where ids is r (in
+    their order), zeros elsewhere and at padding_idx."""
+    lib = load_library()
+    code = _type_code(grad, "grad")
+    dev = grad.device
+    N, nb = _ids(ids, dev)
+    if grad.dim() < 1 or grad.shape[-1] == 0:
+        raise ValueError("grad must be [..., D]")
+    D, V = grad.shape[-1], int(num_rows)
+    _need_typed(grad, (*ids.shape, D), grad.dtype, "grad", dev)
+    if V < 1:
+        raise PararnnError("num_rows must be positive, got %d" % V)
+    if padding_idx is not None and not 0 <= padding_idx < V:
+        raise ValueError("padding_idx must be in [0, %d), got %s" % (V, padding_idx))
+    if out is None:
+        out = torch.empty((V, D), dtype=grad.dtype, device=dev)
+    else:
+        _need_typed(out, (V, D), grad.dtype, "out", dev)
+    n = lib.pararnn_embedding_workspace_bytes(N, V, D)
+    if n == 0:
+        raise PararnnError("invalid sizes N=%d V=%d D=%d" % (N, V, D))
+    buf, n = _workspace_of(n, dev, ws)
+    _check(lib.pararnn_embedding_backward(code, N, V, D, _ptr(ids), nb, _ptr(grad), scale,
+                                          -1 if padding_idx is None else padding_idx, _ptr(out), _ptr(buf), n,
+                                          _stream(dev)), "pararnn_embedding_backward")
+    return out

@@ -123,6 +123,55 @@ size_t lstm_fwd_ws(int64_t B, int64_t L, int64_t H, int32_t cap) {
     return chain_ws(kCfgLstmChain, 2, B, L, H, cap).total;
 }
 
+// ---- operators around the recurrences: sizes and operand strides
+constexpr int64_t kMaxHeadDim = 256;
+
+bool type_ok(int32_t dtype) { return dtype == PARARNN_F32 || dtype == PARARNN_BF16; }
+
+bool linattn_dims_ok(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk, int64_t dv) {
+    if (!type_ok(dtype) || dk < 1 || dk > kMaxHeadDim || dv < 1 || dv > kMaxHeadDim) return false;
+    // at most 3 walks of 4 column blocks a (batch row, head)
+    return dims_ok(B, L, H) && dims_ok(B, L, H * kMaxHeadDim) && grid_ok((B * H + 7) * 12);
+}
+
+LinattnArgs linattn_shape(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk, int64_t dv) {
+    LinattnArgs a{};
+    a.bf16 = dtype == PARARNN_BF16;
+    a.B = B;
+    a.L = L;
+    a.H = H;
+    a.dk = (int)dk;
+    a.dv = (int)dv;
+    return a;
+}
+
+// Operands q, k, v (and grad_o) with their strides over (batch row, position,
+// head), dense if none are given; false where a pointer is not aligned to its
+// elements or a stride is negative.
+bool linattn_inputs(LinattnArgs &a, const void *const *in, int n, const int64_t *strides) {
+    const void **to[4] = {&a.q, &a.k, &a.v, &a.grad_o};
+    for (int i = 0; i < n; ++i) {
+        *to[i] = in[i];
+        if (!aligned(in[i], a.bf16 ? 2 : 4)) return false;
+        const int64_t d = i < 2 ? a.dk : a.dv;
+        for (int j = 0; j < 3; ++j) {
+            a.st[i][j] = strides ? strides[i * 3 + j] : (j == 0 ? a.L * a.H * d : j == 1 ? a.H * d : d);
+            if (a.st[i][j] < 0) return false;
+        }
+    }
+    return true;
+}
+
+bool layernorm_dims_ok(int32_t dtype, int64_t rows, int64_t D) {
+    return type_ok(dtype) && dims_ok(rows, D, 1) && D < ((int64_t)1 << 24);
+}
+
+bool embedding_dims_ok(int32_t dtype, int64_t N, int64_t V, int64_t D) {
+    const int64_t most = (int64_t)1 << 30;
+    return type_ok(dtype) && dims_ok(N, D, 1) && dims_ok(V, D, 1) && N < most && V < most && D < ((int64_t)1 << 24) &&
+           grid_ok((N / 16 + 1) * (D / 64 + 1) + V / 256 + 1);
+}
+
 }  // namespace
 
 extern "C" {
@@ -376,6 +425,123 @@ int pararnn_adjoint_backward(int32_t cell, int64_t B, int64_t L, int64_t H, cons
     if (!grid_ok(scan_shape(kCfgLstmAdj, B, L, H).ntiles)) return PARARNN_ERR_INVALID;
     if (ws_bytes < lstm_adjoint_ws(B, L, H) || !aligned(ws, 256)) return PARARNN_ERR_INVALID;
     return status_of(lstm_adjoint(a, Ws{static_cast<char *>(ws), ws_bytes}, s));
+}
+
+// ---------------------------------------------------------------- operators around the recurrences
+size_t pararnn_linattn_workspace_bytes(int32_t backward, int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk,
+                                       int64_t dv) {
+    if (!linattn_dims_ok(dtype, B, L, H, dk, dv)) return 0;
+    return linattn_ws(linattn_shape(dtype, B, L, H, dk, dv), backward != 0);
+}
+
+int pararnn_linattn_forward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk, int64_t dv, const void *q,
+                            const void *k, const void *v, const int64_t *strides, const float *log_decay,
+                            const float *state, float scale, void *o, float *out_state, void *ws, size_t ws_bytes,
+                            void *stream) {
+    if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
+    if (!linattn_dims_ok(dtype, B, L, H, dk, dv) || !q || !k || !v || !log_decay || !o) return PARARNN_ERR_INVALID;
+    LinattnArgs a = linattn_shape(dtype, B, L, H, dk, dv);
+    const void *in[3] = {q, k, v};
+    if (!linattn_inputs(a, in, 3, strides)) return PARARNN_ERR_INVALID;
+    if (!ws || ws_bytes < linattn_ws(a, false) || !aligned(ws, 256)) return PARARNN_ERR_INVALID;
+    a.log_decay = log_decay;
+    a.state = state;
+    a.scale = scale;
+    a.o = o;
+    a.out_state = out_state;
+    return status_of(linattn_forward(a, Ws{static_cast<char *>(ws), ws_bytes}, static_cast<hipStream_t>(stream)));
+}
+
+int pararnn_linattn_backward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk, int64_t dv, const void *q,
+                             const void *k, const void *v, const void *grad_o, const int64_t *strides,
+                             const float *log_decay, const float *state, const float *grad_out_state, float scale,
+                             void *grad_q, void *grad_k, void *grad_v, float *grad_state, void *ws, size_t ws_bytes,
+                             void *stream) {
+    if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
+    if (!linattn_dims_ok(dtype, B, L, H, dk, dv) || !q || !k || !v || !grad_o || !log_decay || !grad_q || !grad_k ||
+        !grad_v)
+        return PARARNN_ERR_INVALID;
+    LinattnArgs a = linattn_shape(dtype, B, L, H, dk, dv);
+    const void *in[4] = {q, k, v, grad_o};
+    if (!linattn_inputs(a, in, 4, strides)) return PARARNN_ERR_INVALID;
+    if (!ws || ws_bytes < linattn_ws(a, true) || !aligned(ws, 256)) return PARARNN_ERR_INVALID;
+    a.log_decay = log_decay;
+    a.state = state;
+    a.scale = scale;
+    a.grad_out_state = grad_out_state;
+    a.grad_q = grad_q;
+    a.grad_k = grad_k;
+    a.grad_v = grad_v;
+    a.grad_state = grad_state;
+    return status_of(linattn_backward(a, Ws{static_cast<char *>(ws), ws_bytes}, static_cast<hipStream_t>(stream)));
+}
+
+int pararnn_linattn_step(int32_t dtype, int64_t B, int64_t H, int64_t dk, int64_t dv, const void *q, const void *k,
+                         const void *v, const int64_t *strides, const float *log_decay, const float *state, float scale,
+                         void *o, float *out_state, void *stream) {
+    if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
+    if (!linattn_dims_ok(dtype, B, 1, H, dk, dv) || !q || !k || !v || !log_decay || !state || !o || !out_state)
+        return PARARNN_ERR_INVALID;
+    LinattnArgs a = linattn_shape(dtype, B, 1, H, dk, dv);
+    const void *in[3] = {q, k, v};
+    if (!linattn_inputs(a, in, 3, strides)) return PARARNN_ERR_INVALID;
+    a.log_decay = log_decay;
+    a.state = state;
+    a.scale = scale;
+    a.o = o;
+    a.out_state = out_state;
+    return status_of(linattn_step(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t pararnn_layernorm_workspace_bytes(int64_t rows, int64_t D) {
+    if (!layernorm_dims_ok(PARARNN_F32, rows, D)) return 0;
+    return kScratchOffset + (size_t)layernorm_parts(rows, D) * 2 * (size_t)D * sizeof(float);
+}
+
+int pararnn_layernorm_forward(int32_t dtype, int64_t rows, int64_t D, const void *x, const void *residual,
+                              const float *weight, const float *bias, float eps, void *sum, void *y, float *mean,
+                              float *rstd, void *stream) {
+    if (!layernorm_dims_ok(dtype, rows, D) || !x || !y || (residual != nullptr) != (sum != nullptr))
+        return PARARNN_ERR_INVALID;
+    if (!(eps >= 0.0f)) return PARARNN_ERR_INVALID;
+    const LayernormFwdArgs a{dtype == PARARNN_BF16, rows, D, x, residual, weight, bias, eps, sum, y, mean, rstd};
+    return status_of(layernorm_forward(a, static_cast<hipStream_t>(stream)));
+}
+
+int pararnn_layernorm_backward(int32_t dtype, int64_t rows, int64_t D, const void *s, const float *weight,
+                               const float *mean, const float *rstd, const void *grad_y, const void *grad_sum,
+                               void *grad_x, float *grad_weight, float *grad_bias, void *ws, size_t ws_bytes,
+                               void *stream) {
+    if (!layernorm_dims_ok(dtype, rows, D) || !s || !mean || !rstd || !grad_y || !grad_x) return PARARNN_ERR_INVALID;
+    if ((grad_weight || grad_bias) &&
+        (!ws || ws_bytes < pararnn_layernorm_workspace_bytes(rows, D) || !aligned(ws, 256)))
+        return PARARNN_ERR_INVALID;
+    const LayernormBwdArgs a{dtype == PARARNN_BF16, rows, D, s, weight, mean, rstd, grad_y, grad_sum, grad_x,
+                             grad_weight, grad_bias};
+    return status_of(layernorm_backward(a, Ws{static_cast<char *>(ws), ws_bytes}, static_cast<hipStream_t>(stream)));
+}
+
+int pararnn_embedding_forward(int32_t dtype, int64_t N, int64_t V, int64_t D, const void *ids, int32_t id_bytes,
+                              const void *table, float scale, void *out, void *stream) {
+    if (!embedding_dims_ok(dtype, N, V, D) || (id_bytes != 4 && id_bytes != 8) || !ids || !table || !out)
+        return PARARNN_ERR_INVALID;
+    const EmbeddingArgs a{dtype == PARARNN_BF16, id_bytes == 8, N, V, D, -1, ids, table, scale, out};
+    return status_of(embedding_forward(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t pararnn_embedding_workspace_bytes(int64_t N, int64_t V, int64_t D) {
+    return embedding_dims_ok(PARARNN_F32, N, V, D) ? embedding_ws(N, D) : 0;
+}
+
+int pararnn_embedding_backward(int32_t dtype, int64_t N, int64_t V, int64_t D, const void *ids, int32_t id_bytes,
+                               const void *grad, float scale, int64_t padding_idx, void *grad_table, void *ws,
+                               size_t ws_bytes, void *stream) {
+    if (!embedding_dims_ok(dtype, N, V, D) || (id_bytes != 4 && id_bytes != 8) || !ids || !grad || !grad_table)
+        return PARARNN_ERR_INVALID;
+    if (padding_idx < -1 || padding_idx >= V) return PARARNN_ERR_INVALID;
+    if (!ws || ws_bytes < embedding_ws(N, D) || !aligned(ws, 256)) return PARARNN_ERR_INVALID;
+    const EmbeddingArgs a{dtype == PARARNN_BF16, id_bytes == 8, N, V, D, padding_idx, ids, grad, scale, grad_table};
+    return status_of(embedding_backward(a, Ws{static_cast<char *>(ws), ws_bytes}, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

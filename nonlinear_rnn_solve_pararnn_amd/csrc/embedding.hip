@@ -1,0 +1,463 @@
+// embedding.hip -- embedding lookup with scaling, and its gradient by sorted
+// tokens.
+//
+//   out[n] = scale table[ids[n]]
+//   dtable[r] = scale * sum over n with ids[n] = r, in ascending n, of grad[n]
+//
+// The lookup is a gather of whole rows, bound by memory.  The gradient sorts
+// the (id, position) pairs by a stable radix sort, cuts the sorted list into
+// chunks of equal length and adds each run of equal ids within a chunk: a
+// natural text's most frequent token has thousands of rows, so the work is
+// split by sorted positions, not by table rows.  Runs that cross chunks leave
+// fp32 partial sums that a second kernel adds in order.  There are no
+// floating-point atomics: the result depends on the inputs alone.
+#include "launch.hpp"
+#include "rows.hpp"
+
+namespace prn {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// An id as a sort key: ids outside the table become V, which sorts last.
+__device__ __forceinline__ uint32_t id_key(const void *ids, int wide, int64_t n, int64_t V) {
+    const int64_t id = wide ? static_cast<const int64_t *>(ids)[n] : (int64_t)static_cast<const int32_t *>(ids)[n];
+    return id >= 0 && id < V ? (uint32_t)id : (uint32_t)V;
+}
+
+// ---------------------------------------------------------------- lookup
+struct EmbFwdArgs {
+    int64_t N, V;
+    int D, wide, lanes;  // lanes (a power of two) share a row
+    const void *ids, *table;
+    float scale;
+    void *out;
+};
+
+constexpr int kLookRows = 4;  // rows whose loads a thread keeps in flight
+
+template <typename T, int V>
+__global__ __launch_bounds__(kThreads) void emb_lookup_kernel(EmbFwdArgs a) {
+    const int li = threadIdx.x & (a.lanes - 1);
+    const int per = kThreads / a.lanes;  // rows a workgroup takes at once
+    const int64_t n0 = (int64_t)blockIdx.x * per * kLookRows + threadIdx.x / a.lanes;
+    uint32_t key[kLookRows];
+#pragma unroll
+    for (int r = 0; r < kLookRows; ++r) {
+        const int64_t n = n0 + (int64_t)r * per;
+        key[r] = n < a.N ? id_key(a.ids, a.wide, n, a.V) : (uint32_t)a.V;
+    }
+    const float bad = __uint_as_float(0x7fc00000u);
+    for (int c = li * V; c < a.D; c += a.lanes * V) {
+        float f[kLookRows][V];
+#pragma unroll
+        for (int r = 0; r < kLookRows; ++r) {
+            if (key[r] < (uint32_t)a.V) load_vec<T, V>(static_cast<const T *>(a.table) + (int64_t)key[r] * a.D + c, f[r]);
+            else
+#pragma unroll
+                for (int i = 0; i < V; ++i) f[r][i] = bad;
+        }
+#pragma unroll
+        for (int r = 0; r < kLookRows; ++r) {
+            const int64_t n = n0 + (int64_t)r * per;
+            if (n >= a.N) continue;
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[r][i] *= a.scale;
+            store_vec<T, V>(static_cast<T *>(a.out) + n * a.D + c, f[r]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- sort
+constexpr int kBins = 256;          // 8 bits of the key a pass
+constexpr int kSmallN = 8192;       // sorted by one workgroup in LDS
+constexpr int kSmallThreads = 1024;
+constexpr int kMaxTiles = 128;      // workgroups of a pass over a longer list
+
+// Lanes of the wave whose digit equals this lane's (valid lanes only).
+__device__ __forceinline__ uint64_t same_digit(uint32_t d, bool valid) {
+    uint64_t m = __ballot(valid);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+        const uint64_t one = __ballot((d >> b) & 1u);
+        m &= ((d >> b) & 1u) ? one : ~one;
+    }
+    return m;
+}
+
+// Place of this lane's element among those of its digit: the wave's counter
+// of the digit, advanced by the wave's elements, plus the lanes before it.
+__device__ __forceinline__ uint32_t take_place(uint32_t *counter, uint32_t d, bool valid) {
+    const uint64_t m = same_digit(d, valid);
+    const int lane = threadIdx.x & 63;
+    const int first = valid ? __ffsll((unsigned long long)m) - 1 : lane;
+    uint32_t base = 0;
+    if (valid && lane == first) base = atomicAdd(&counter[d], (uint32_t)__popcll(m));
+    base = __shfl(base, first, 64);
+    return base + (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
+}
+
+// Exclusive sum of one value per thread over the first 256 threads of a
+// workgroup (all of its threads call this).
+__device__ __forceinline__ uint32_t scan256(uint32_t v, uint32_t *tmp) {
+    const int t = threadIdx.x, lane = t & 63;
+    uint32_t inc = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = __shfl_up(inc, d, 64);
+        if (lane >= d) inc += o;
+    }
+    if (t < kBins && lane == 63) tmp[t >> 6] = inc;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int w = 0; w < (t >> 6) && w < 4; ++w) before += tmp[w];
+    __syncthreads();
+    return before + inc - v;
+}
+
+struct SortArgs {
+    int64_t N, V;
+    int wide, passes;
+    const void *ids;
+    uint32_t *key[2], *pos[2];
+    uint32_t *hist;  // [tiles][256]
+    int64_t tile;    // elements a workgroup (a multiple of 256)
+};
+
+__global__ __launch_bounds__(kSmallThreads) void emb_sort_small_kernel(SortArgs a) {
+    __shared__ uint32_t key[2][kSmallN];
+    __shared__ uint16_t pos[2][kSmallN];
+    __shared__ uint32_t cnt[16][kBins];
+    __shared__ uint32_t tmp[4];
+    const int t = threadIdx.x, w = t >> 6, lane = t & 63;
+    const int N = (int)a.N;
+    const int per = (N + 1023) / 1024 * 64;  // elements a wave
+    for (int n = t; n < N; n += kSmallThreads) {
+        key[0][n] = id_key(a.ids, a.wide, n, a.V);
+        pos[0][n] = (uint16_t)n;
+    }
+    int cur = 0;
+    for (int p = 0; p < a.passes; ++p) {
+        for (int i = t; i < 16 * kBins; i += kSmallThreads) cnt[i / kBins][i % kBins] = 0;
+        __syncthreads();
+        const int lo = w * per, hi = min(N, lo + per);
+        for (int n = lo + lane; n < hi; n += 64) atomicAdd(&cnt[w][(key[cur][n] >> (8 * p)) & 255u], 1u);
+        __syncthreads();
+        uint32_t total = 0;
+        if (t < kBins)
+            for (int v = 0; v < 16; ++v) total += cnt[v][t];
+        uint32_t run = scan256(total, tmp);
+        if (t < kBins)
+            for (int v = 0; v < 16; ++v) {
+                const uint32_t c = cnt[v][t];
+                cnt[v][t] = run;
+                run += c;
+            }
+        __syncthreads();
+        for (int n0 = lo; n0 < hi; n0 += 64) {
+            const int n = n0 + lane;
+            const bool valid = n < hi;
+            const uint32_t k = valid ? key[cur][n] : 0u;
+            const uint32_t to = take_place(cnt[w], (k >> (8 * p)) & 255u, valid);
+            if (valid) {
+                key[cur ^ 1][to] = k;
+                pos[cur ^ 1][to] = pos[cur][n];
+            }
+        }
+        cur ^= 1;
+        __syncthreads();
+    }
+    for (int n = t; n < N; n += kSmallThreads) {
+        a.key[0][n] = key[cur][n];
+        a.pos[0][n] = pos[cur][n];
+    }
+}
+
+__device__ __forceinline__ uint32_t key_at(const SortArgs &a, int p, int64_t n) {
+    return p == 0 ? id_key(a.ids, a.wide, n, a.V) : a.key[(p - 1) & 1][n];
+}
+
+// Digit counts of each workgroup's elements in pass p.
+__global__ __launch_bounds__(kThreads) void emb_hist_kernel(SortArgs a, int p) {
+    __shared__ uint32_t cnt[kBins];
+    cnt[threadIdx.x] = 0;
+    __syncthreads();
+    const int64_t lo = (int64_t)blockIdx.x * a.tile, hi = min(a.N, lo + a.tile);
+    for (int64_t n = lo + threadIdx.x; n < hi; n += kThreads) atomicAdd(&cnt[(key_at(a, p, n) >> (8 * p)) & 255u], 1u);
+    __syncthreads();
+    a.hist[(int64_t)blockIdx.x * kBins + threadIdx.x] = cnt[threadIdx.x];
+}
+
+// Moves each workgroup's elements to their places in pass p, keeping the
+// order of equal digits: wave w takes the w-th quarter of the tile in order.
+__global__ __launch_bounds__(kThreads) void emb_scatter_kernel(SortArgs a, int p) {
+    __shared__ uint32_t cnt[4][kBins];
+    __shared__ uint32_t tmp[4];
+    const int t = threadIdx.x, w = t >> 6, lane = t & 63;
+    const int64_t end = min(a.N, ((int64_t)blockIdx.x + 1) * a.tile);
+    const int64_t lo = (int64_t)blockIdx.x * a.tile + w * (a.tile / 4), hi = min(end, lo + a.tile / 4);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) cnt[v][t] = 0;
+    __syncthreads();
+    for (int64_t n = lo + lane; n < hi; n += 64) atomicAdd(&cnt[w][(key_at(a, p, n) >> (8 * p)) & 255u], 1u);
+    uint32_t before = 0, total = 0;
+#pragma unroll 8
+    for (int g = 0; g < (int)gridDim.x; ++g) {
+        const uint32_t c = a.hist[(int64_t)g * kBins + t];
+        total += c;
+        before += g < (int)blockIdx.x ? c : 0u;
+    }
+    uint32_t run = scan256(total, tmp) + before;  // its barriers also order the counts above
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        const uint32_t c = cnt[v][t];
+        cnt[v][t] = run;
+        run += c;
+    }
+    __syncthreads();
+    for (int64_t n0 = lo; n0 < hi; n0 += 64) {
+        const int64_t n = n0 + lane;
+        const bool valid = n < hi;
+        const uint32_t k = valid ? key_at(a, p, n) : 0u;
+        const uint32_t pos = p == 0 ? (uint32_t)n : (valid ? a.pos[(p - 1) & 1][n] : 0u);
+        const uint32_t to = take_place(cnt[w], (k >> (8 * p)) & 255u, valid);
+        if (valid) {
+            a.key[p & 1][to] = k;
+            a.pos[p & 1][to] = pos;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- sums
+struct EmbSumArgs {
+    int64_t N, V, pad;  // pad: the row whose gradient stays zero, or -1
+    int D;
+    const uint32_t *key, *pos;
+    const void *grad;
+    float scale;
+    void *out;
+    float *part;     // [chunks][2][D]: sums of a run that came from the chunk before, of one that goes on
+    int run;         // sorted positions a chunk (at most 64)
+    int64_t chunks, cols;      // column blocks of 64 * V
+    int64_t sum_blocks;        // workgroups of the sums; the others write zero rows
+};
+
+constexpr int kBatch = 8;  // rows whose loads are in flight
+
+template <typename T, int V>
+__device__ __forceinline__ void emb_zero_rows(const EmbSumArgs &a, int64_t block) {
+    // a wave takes 64 table rows: each lane looks for its row among the
+    // sorted ids, then the wave writes the rows that no id names
+    const int lane = threadIdx.x & 63;
+    const int64_t row0 = (block * 4 + (threadIdx.x >> 6)) * 64;
+    if (row0 >= a.V) return;
+    const int64_t row = row0 + lane;
+    int64_t lo = 0, hi = a.N;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if ((int64_t)a.key[mid] < row) lo = mid + 1;
+        else hi = mid;
+    }
+    const bool named = lo < a.N && (int64_t)a.key[lo] == row && row != a.pad;
+    uint64_t empty = __ballot(row < a.V && !named);
+    float z[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) z[i] = 0.0f;
+    while (empty != 0) {
+        const int r = __ffsll((unsigned long long)empty) - 1;
+        empty &= empty - 1;
+        for (int c = lane * V; c < a.D; c += 64 * V) store_vec<T, V>(static_cast<T *>(a.out) + (row0 + r) * a.D + c, z);
+    }
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(kThreads) void emb_sum_kernel(EmbSumArgs a) {
+    if ((int64_t)blockIdx.x >= a.sum_blocks) {
+        emb_zero_rows<T, V>(a, (int64_t)blockIdx.x - a.sum_blocks);
+        return;
+    }
+    const int lane = threadIdx.x & 63;
+    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (item >= a.chunks * a.cols) return;
+    const int64_t chunk = item / a.cols;
+    const int c = (int)(item - chunk * a.cols) * 64 * V + lane * V;
+    const int64_t n0 = chunk * a.run;
+    const int cnt = (int)min((int64_t)a.run, a.N - n0);
+    const uint32_t mykey = a.key[n0 + min(lane, cnt - 1)], mypos = a.pos[n0 + min(lane, cnt - 1)];
+    const uint32_t none = 0xffffffffu;  // above every key
+    const uint32_t prev = n0 > 0 ? a.key[n0 - 1] : none;
+    const uint32_t next = n0 + cnt < a.N ? a.key[n0 + cnt] : none;
+    const bool in = c < a.D;
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    bool from_start = true;  // the current run began at the chunk's first position
+    uint32_t cur = __builtin_amdgcn_readlane(mykey, 0);
+    auto flush = [&](bool to_end) {
+        if (cur < (uint32_t)a.V && (int64_t)cur != a.pad && in) {
+            const bool head = from_start && prev == cur, tail = to_end && next == cur;
+            if (head || tail) {
+                float *p = a.part + ((chunk * 2 + (head ? 0 : 1)) * a.D + c);
+#pragma unroll
+                for (int i = 0; i < V; ++i) p[i] = acc[i];
+            } else {
+                float f[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) f[i] = acc[i] * a.scale;
+                store_vec<T, V>(static_cast<T *>(a.out) + (int64_t)cur * a.D + c, f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    };
+    for (int b = 0; b < cnt; b += kBatch) {
+        float f[kBatch][V];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int64_t at = (int64_t)__builtin_amdgcn_readlane(mypos, min(b + u, cnt - 1));
+            if (in) load_vec<T, V>(static_cast<const T *>(a.grad) + at * a.D + c, f[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (b + u < cnt) {
+                const uint32_t k = __builtin_amdgcn_readlane(mykey, b + u);
+                if (k != cur) {
+                    flush(false);
+                    cur = k;
+                    from_start = false;
+                }
+                if (in)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] += f[u][i];
+            }
+        }
+    }
+    flush(true);
+}
+
+// Runs that cross chunks: the wave of the chunk where such a run begins adds
+// its partial sums in order.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void emb_join_kernel(EmbSumArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (item >= a.chunks * a.cols) return;
+    const int64_t chunk = item / a.cols;
+    const int c = (int)(item - chunk * a.cols) * 64 + lane;
+    const int64_t n0 = chunk * a.run, n1 = n0 + a.run;  // n1: the next chunk's first position
+    if (n1 >= a.N) return;
+    const uint32_t k = a.key[n1];
+    if (a.key[n1 - 1] != k || k >= (uint32_t)a.V || (int64_t)k == a.pad) return;
+    if (a.key[n0] == k && n0 > 0 && a.key[n0 - 1] == k) return;  // begins earlier
+    int64_t lo = n1, hi = a.N;  // the first position past the run
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (a.key[mid] <= k) lo = mid + 1;
+        else hi = mid;
+    }
+    const int64_t last = (lo - 1) / a.run;
+    if (c >= a.D) return;
+    float acc = a.part[(chunk * 2 + 1) * a.D + c];
+#pragma unroll 8
+    for (int64_t q = chunk + 1; q <= last; ++q) acc += a.part[q * 2 * a.D + c];
+    static_cast<T *>(a.out)[(int64_t)k * a.D + c] = (T)(acc * a.scale);
+}
+
+// Layout of the gradient's scratch.
+struct EmbWs {
+    int tiles, run;
+    int64_t tile, chunks;
+    size_t key[2], pos[2], hist, part, total;
+};
+EmbWs emb_ws(int64_t N, int64_t D) {
+    EmbWs w;
+    size_t off = kScratchOffset;
+    auto take = [&](size_t n) {
+        const size_t at = off;
+        off += (n + 255) / 256 * 256;
+        return at;
+    };
+    const bool small = N <= kSmallN;
+    w.tile = std::max<int64_t>(2048, ((N + kMaxTiles - 1) / kMaxTiles + 255) / 256 * 256);
+    w.tiles = (int)((N + w.tile - 1) / w.tile);
+    w.run = N <= 16384 ? 16 : 64;
+    w.chunks = (N + w.run - 1) / w.run;
+    for (int i = 0; i < 2; ++i) {
+        w.key[i] = i == 0 || !small ? take((size_t)N * 4) : w.key[0];
+        w.pos[i] = i == 0 || !small ? take((size_t)N * 4) : w.pos[0];
+    }
+    w.hist = take((size_t)w.tiles * kBins * 4);
+    w.part = take((size_t)w.chunks * 2 * (size_t)D * 4);
+    w.total = off;
+    return w;
+}
+
+template <typename T, int V>
+hipError_t emb_sums(EmbSumArgs &a, hipStream_t s) {
+    a.cols = (a.D + 64 * V - 1) / (64 * V);
+    a.sum_blocks = (a.chunks * a.cols + 3) / 4;
+    const int64_t zero = (a.V + 255) / 256;
+    emb_sum_kernel<T, V><<<(unsigned)(a.sum_blocks + zero), kThreads, 0, s>>>(a);
+    a.cols = (a.D + 63) / 64;
+    emb_join_kernel<T><<<(unsigned)((a.chunks * a.cols + 3) / 4), kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t embedding_ws(int64_t N, int64_t D) { return emb_ws(N, D).total; }
+
+hipError_t embedding_forward(const EmbeddingArgs &q, hipStream_t s) {
+    const int es = q.bf16 ? 2 : 4, vec = 16 / es;
+    const bool al = q.D % vec == 0 && aligned16(q.table) && aligned16(q.out);
+    const int64_t vecs = al ? q.D / vec : q.D;
+    int lanes = 1;
+    while (lanes < 64 && lanes < vecs) lanes *= 2;
+    const EmbFwdArgs a{q.N, q.V, (int)q.D, q.wide_ids, lanes, q.ids, q.table, q.scale, q.out};
+    const int64_t per = (int64_t)kThreads / lanes * kLookRows;
+    const unsigned grid = (unsigned)((q.N + per - 1) / per);
+    if (q.bf16) {
+        if (al) emb_lookup_kernel<bf16, 8><<<grid, kThreads, 0, s>>>(a);
+        else emb_lookup_kernel<bf16, 1><<<grid, kThreads, 0, s>>>(a);
+    } else {
+        if (al) emb_lookup_kernel<float, 4><<<grid, kThreads, 0, s>>>(a);
+        else emb_lookup_kernel<float, 1><<<grid, kThreads, 0, s>>>(a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t embedding_backward(const EmbeddingArgs &q, const Ws &ws, hipStream_t s) {
+    const EmbWs w = emb_ws(q.N, q.D);
+    SortArgs o{};
+    o.N = q.N;
+    o.V = q.V;
+    o.wide = q.wide_ids;
+    o.ids = q.ids;
+    o.tile = w.tile;
+    o.hist = reinterpret_cast<uint32_t *>(ws.p + w.hist);
+    for (int i = 0; i < 2; ++i) {
+        o.key[i] = reinterpret_cast<uint32_t *>(ws.p + w.key[i]);
+        o.pos[i] = reinterpret_cast<uint32_t *>(ws.p + w.pos[i]);
+    }
+    o.passes = 1;
+    while (o.passes < 4 && (q.V >> (8 * o.passes)) != 0) ++o.passes;  // V itself is a key
+    int at = 0;
+    if (q.N <= kSmallN) {
+        emb_sort_small_kernel<<<1, kSmallThreads, 0, s>>>(o);
+    } else {
+        for (int p = 0; p < o.passes; ++p) {
+            emb_hist_kernel<<<w.tiles, kThreads, 0, s>>>(o, p);
+            emb_scatter_kernel<<<w.tiles, kThreads, 0, s>>>(o, p);
+        }
+        at = (o.passes - 1) & 1;
+    }
+    EmbSumArgs a{q.N, q.V, q.padding, (int)q.D, o.key[at], o.pos[at], q.table, q.scale, q.out,
+                 reinterpret_cast<float *>(ws.p + w.part), w.run, w.chunks, 0, 0};
+    const int vec = q.bf16 ? 8 : 4;
+    const bool al = q.D % vec == 0 && aligned16(q.table) && aligned16(q.out);
+    if (q.bf16) return al ? emb_sums<bf16, 8>(a, s) : emb_sums<bf16, 1>(a, s);
+    return al ? emb_sums<float, 4>(a, s) : emb_sums<float, 1>(a, s);
+}
+
+}  // namespace prn
