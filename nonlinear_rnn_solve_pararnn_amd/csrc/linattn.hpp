@@ -35,6 +35,7 @@ struct Walk {
     int d1, d2;
     int rev, e;
     float wi, wo, wt;
+    int out4;           // rows of out may be stored four elements at a time
 };
 
 struct WalkArgs {
@@ -43,6 +44,9 @@ struct WalkArgs {
     int64_t B, L, H;
     const float *log_decay;
     int nblk;   // column blocks of 64 a walk, at most
+    int segs;          // pieces of the sequence that are walked side by side
+    int64_t seg_len;   // positions a piece (a multiple of the chunk)
+    float *seg_state;  // T of every piece, in the walk's register layout
     int vec;    // every operand row is 16-byte aligned and a whole number of vectors
 };
 
