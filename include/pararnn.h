@@ -360,8 +360,8 @@ enum { PARARNN_F32 = 0, PARARNN_BF16 = 1 };
  * state itself).  log_decay: [H] fp32.  1 <= dk, dv <= 256 (above:
  * PARARNN_ERR_UNSUPPORTED).
  * strides: HOST array of {batch row, position, head} strides in elements for
- * q, k and v in turn (9 values), not negative; the last dimension is dense.
- * NULL: dense tensors.  Operands whose rows are 16-byte aligned move faster.
+ * q, k and v in turn (9 values), not negative, a position's below 2^22; the
+ * last dimension is dense.  NULL: dense tensors (H max(dk, dv) < 2^22).  Operands whose rows are 16-byte aligned move faster.
  * A value that is not finite at position t of q, k or v affects no output
  * before t; from t on the affected outputs are not finite (an infinity may
  * come out as NaN).

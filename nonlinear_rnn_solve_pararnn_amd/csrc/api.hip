@@ -128,10 +128,13 @@ constexpr int64_t kMaxHeadDim = 256;
 
 bool type_ok(int32_t dtype) { return dtype == PARARNN_F32 || dtype == PARARNN_BF16; }
 
+constexpr int64_t kMaxRowBytes = (int64_t)1 << 24;  // a chunk of 64 rows stays within 32-bit offsets
+
 bool linattn_dims_ok(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk, int64_t dv) {
     if (!type_ok(dtype) || dk < 1 || dk > kMaxHeadDim || dv < 1 || dv > kMaxHeadDim) return false;
     // at most 3 walks of 4 column blocks a (batch row, head)
-    return dims_ok(B, L, H) && dims_ok(B, L, H * kMaxHeadDim) && grid_ok((B * H + 7) * 12);
+    return dims_ok(B, L, H) && dims_ok(B, L, H * kMaxHeadDim) && grid_ok((B * H + 7) * 12) &&
+           H * std::max(dk, dv) * 4 < kMaxRowBytes;
 }
 
 LinattnArgs linattn_shape(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk, int64_t dv) {
@@ -147,7 +150,7 @@ LinattnArgs linattn_shape(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_
 
 // Operands q, k, v (and grad_o) with their strides over (batch row, position,
 // head), dense if none are given; false where a pointer is not aligned to its
-// elements or a stride is negative.
+// elements, or a stride is negative or (of a position) too large.
 bool linattn_inputs(LinattnArgs &a, const void *const *in, int n, const int64_t *strides) {
     const void **to[4] = {&a.q, &a.k, &a.v, &a.grad_o};
     for (int i = 0; i < n; ++i) {
@@ -156,7 +159,7 @@ bool linattn_inputs(LinattnArgs &a, const void *const *in, int n, const int64_t 
         const int64_t d = i < 2 ? a.dk : a.dv;
         for (int j = 0; j < 3; ++j) {
             a.st[i][j] = strides ? strides[i * 3 + j] : (j == 0 ? a.L * a.H * d : j == 1 ? a.H * d : d);
-            if (a.st[i][j] < 0) return false;
+            if (a.st[i][j] < 0 || (j == 1 && a.st[i][j] * 4 >= kMaxRowBytes)) return false;
         }
     }
     return true;

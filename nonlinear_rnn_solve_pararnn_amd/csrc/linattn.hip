@@ -41,37 +41,6 @@ WalkPlan walk_plan(const LinattnArgs &p, bool backward) {
     return w;
 }
 
-template <typename T, int D1>
-void walk_launch(const WalkArgs &a, hipStream_t s) {
-    constexpr int C = sizeof(T) == 2 ? 64 : 32;
-    const int64_t pairs = (a.B * a.H + 7) / 8 * 8 * a.walks * a.nblk;
-    if (a.segs > 1) {
-        walk::walk_kernel<T, D1, C, true><<<(unsigned)(pairs * (a.segs - 1)), kThreads, 0, s>>>(a);
-        const int64_t tiles = (int64_t)a.walks * a.B * a.H * a.nblk * 4 * (D1 / 16);
-        walk::join_kernel<D1><<<(unsigned)((tiles + 3) / 4), kThreads, 0, s>>>(a);
-    }
-    walk::walk_kernel<T, D1, C, false><<<(unsigned)(pairs * a.segs), kThreads, 0, s>>>(a);
-}
-
-template <typename T>
-hipError_t run_walks(WalkArgs &a, const WalkPlan &w, const Ws &ws, hipStream_t s) {
-    a.walks = w.walks;
-    a.nblk = w.nblk;
-    a.segs = w.segs;
-    a.seg_len = w.seg_len;
-    a.seg_state = reinterpret_cast<float *>(ws.p + kScratchOffset);
-    for (int i = 0; i < a.walks; ++i)
-        a.w[i].out4 = a.w[i].d2 % 4 == 0 && aligned_to(a.w[i].out, 4 * sizeof(T));
-    switch (w.d1) {
-        case 32: walk_launch<T, 32>(a, s); break;
-        case 64: walk_launch<T, 64>(a, s); break;
-        case 96: walk_launch<T, 96>(a, s); break;
-        case 128: walk_launch<T, 128>(a, s); break;
-        default: walk_launch<T, 256>(a, s); break;
-    }
-    return hipGetLastError();
-}
-
 bool view_vec(const WalkView &v, int d, int es) {
     const int64_t n = 16 / es;
     return d % n == 0 && aligned16(v.p) && v.sb % n == 0 && v.st % n == 0 && v.sh % n == 0;
@@ -83,6 +52,43 @@ bool walks_vec(const WalkArgs &a, int es) {
         if (!view_vec(a.w[i].X, a.w[i].d1, es) || !view_vec(a.w[i].Y, a.w[i].d1, es) || !view_vec(a.w[i].Z, a.w[i].d2, es))
             return false;
     return true;
+}
+
+template <typename T, int D1, bool VEC>
+void walk_launch(const WalkArgs &a, hipStream_t s) {
+    constexpr int C = sizeof(T) == 2 ? 64 : 32;
+    const int64_t pairs = (a.B * a.H + 7) / 8 * 8 * a.walks * a.nblk;
+    if (a.segs > 1) {
+        walk::walk_kernel<T, D1, C, VEC, true><<<(unsigned)(pairs * (a.segs - 1)), kThreads, 0, s>>>(a);
+        const int64_t tiles = (int64_t)a.walks * a.B * a.H * a.nblk * 4 * (D1 / 16);
+        walk::join_kernel<D1><<<(unsigned)((tiles + 3) / 4), kThreads, 0, s>>>(a);
+    }
+    walk::walk_kernel<T, D1, C, VEC, false><<<(unsigned)(pairs * a.segs), kThreads, 0, s>>>(a);
+}
+
+template <typename T, bool VEC>
+void walk_width_launch(const WalkArgs &a, int d1, hipStream_t s) {
+    switch (d1) {
+        case 32: walk_launch<T, 32, VEC>(a, s); break;
+        case 64: walk_launch<T, 64, VEC>(a, s); break;
+        case 96: walk_launch<T, 96, VEC>(a, s); break;
+        case 128: walk_launch<T, 128, VEC>(a, s); break;
+        default: walk_launch<T, 256, VEC>(a, s); break;
+    }
+}
+
+template <typename T>
+hipError_t run_walks(WalkArgs &a, const WalkPlan &w, const Ws &ws, hipStream_t s) {
+    a.walks = w.walks;
+    a.nblk = w.nblk;
+    a.segs = w.segs;
+    a.seg_len = w.seg_len;
+    a.seg_state = reinterpret_cast<float *>(ws.p + kScratchOffset);
+    for (int i = 0; i < a.walks; ++i)
+        a.w[i].out4 = a.w[i].d2 % 4 == 0 && aligned_to(a.w[i].out, 4 * sizeof(T));
+    if (walks_vec(a, sizeof(T))) walk_width_launch<T, true>(a, w.d1, s);
+    else walk_width_launch<T, false>(a, w.d1, s);
+    return hipGetLastError();
 }
 
 // ---------------------------------------------------------------- single token
@@ -173,7 +179,6 @@ hipError_t linattn_forward(const LinattnArgs &p, const Ws &ws, hipStream_t s) {
     const WalkView q{p.q, p.st[0][0], p.st[0][1], p.st[0][2]}, k{p.k, p.st[1][0], p.st[1][1], p.st[1][2]},
         v{p.v, p.st[2][0], p.st[2][1], p.st[2][2]};
     a.w[0] = {q, k, v, p.o, p.state, p.out_state, p.dv, 1, p.dk, p.dv, 0, 0, p.scale, p.scale, 1.0f, 0};
-    a.vec = walks_vec(a, p.bf16 ? 2 : 4);
     const WalkPlan w = walk_plan(p, false);
     return p.bf16 ? run_walks<bf16>(a, w, ws, s) : run_walks<float>(a, w, ws, s);
 }
@@ -190,7 +195,6 @@ hipError_t linattn_backward(const LinattnArgs &p, const Ws &ws, hipStream_t s) {
     a.w[0] = {g, v, k, p.grad_q, p.state, nullptr, 1, p.dv, p.dv, p.dk, 0, 0, p.scale, p.scale, 1.0f, 0};
     a.w[1] = {v, g, q, p.grad_k, p.grad_out_state, nullptr, 1, p.dv, p.dv, p.dk, 1, 1, p.scale, 1.0f, p.scale, 0};
     a.w[2] = {k, q, g, p.grad_v, p.grad_out_state, p.grad_state, p.dv, 1, p.dk, p.dv, 1, 1, p.scale, 1.0f, p.scale, 0};
-    a.vec = walks_vec(a, p.bf16 ? 2 : 4);
     const WalkPlan w = walk_plan(p, true);
     return p.bf16 ? run_walks<bf16>(a, w, ws, s) : run_walks<float>(a, w, ws, s);
 }

@@ -47,7 +47,6 @@ struct WalkArgs {
     int segs;          // pieces of the sequence that are walked side by side
     int64_t seg_len;   // positions a piece (a multiple of the chunk)
     float *seg_state;  // T of every piece, in the walk's register layout
-    int vec;    // every operand row is 16-byte aligned and a whole number of vectors
 };
 
 // The head's decay, kept finite so that 0 * g is 0.

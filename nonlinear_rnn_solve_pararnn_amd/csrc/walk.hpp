@@ -123,51 +123,83 @@ __device__ __forceinline__ float plane_sum(const bf16x8 (&p)[N], int i) {
     return v;
 }
 
-// Eight elements of an operand row as loaded.
-template <typename T>
-struct Raw {
-    T v[8];
+// Buffer accesses: an offset at or past `bytes` reads zeros and writes nothing.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00020000);
+}
+constexpr uint32_t kNowhere = 0x80000000u;  // above every buffer's size, also after a chunk's bytes are taken off
+
+// Rows of one operand as a walk sees them, from column c0 on.
+struct Rows {
+    const char *p;      // row 0 of the sequence
+    int64_t row_bytes;  // below 2^24 (checked on the host)
+    uint32_t tail;      // bytes of a row from p on
+    int64_t L;
+    int rev;
+
+    // Bytes and address of the chunk of cnt positions from p0.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk(int64_t p0, int cnt) const {
+        return buffer_of(p + (rev ? L - p0 - cnt : p0) * row_bytes, (uint32_t)(cnt - 1) * (uint32_t)row_bytes + tail);
+    }
+    // Offset of a chunk's row r in it, if the chunk is whole; (C - cnt) * row_bytes less in a reversed shorter one.
+    __device__ __forceinline__ uint32_t row_at(int r, int C) const { return (uint32_t)(rev ? C - 1 - r : r) * (uint32_t)row_bytes; }
+    __device__ __forceinline__ uint32_t shift(int cnt, int C) const { return rev ? (uint32_t)(C - cnt) * (uint32_t)row_bytes : 0u; }
 };
+template <typename T>
+__device__ __forceinline__ Rows rows_of(const WalkView &v, int64_t b, int64_t h, int64_t L, int rev, int c0, int d) {
+    return {static_cast<const char *>(v.p) + (b * v.sb + h * v.sh + c0) * (int64_t)sizeof(T), v.st * (int64_t)sizeof(T),
+            (uint32_t)(d - c0) * (uint32_t)sizeof(T), L, rev};
+}
 
-// A thread's share of one tile of W columns, loaded ahead of its use.
-template <typename T, int W, int C>
+// A thread's share of one tile of W columns (groups of 8 elements), loaded
+// ahead of its use.  VEC: rows are 16-byte aligned and whole numbers of
+// 16-byte pieces; otherwise elements are loaded one by one.
+template <typename T, int W, int C, bool VEC>
 struct Ahead {
-    static constexpr int kGroups = W / 8, kN = (C * kGroups + kThreads - 1) / kThreads;
-    Raw<T> r[kN];
+    static constexpr int kGroups = W / 8, kN = (C * kGroups + kThreads - 1) / kThreads, kV = 16 / (int)sizeof(T);
+    struct alignas(16) {
+        T v[8];
+    } r[kN];
+    uint32_t at[kN];   // offsets in a whole chunk
+    int left;          // columns the operand has
 
-    // Positions p0 + row of the walk, columns c0 .. of d; zeros past the ends.
-    __device__ __forceinline__ void load(const WalkView &v, int64_t base, int64_t L, int rev, int64_t p0, int64_t end,
-                                         int c0, int d, int vec) {
-        const T *src = static_cast<const T *>(v.p) + base + c0;
+    __device__ __forceinline__ void init(const Rows &v) {
+        left = (int)(v.tail / sizeof(T));
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
             const int i = threadIdx.x + n * kThreads, row = i / kGroups, c = (i - row * kGroups) * 8;
-            const int64_t p = p0 + row;
-            const T *at = src + (rev ? L - 1 - p : p) * v.st + c;
-            const bool ok = row < C && p < end;
-            if (vec) {
-                constexpr int kV = 16 / (int)sizeof(T);
-#pragma unroll
-                for (int h = 0; h < 8 / kV; ++h) {
-                    u32x4 x = {0u, 0u, 0u, 0u};
-                    if (ok && c0 + c + h * kV < d) x = *reinterpret_cast<const u32x4 *>(at + h * kV);
-                    *reinterpret_cast<u32x4 *>(&r[n].v[h * kV]) = x;
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) r[n].v[k] = ok && c0 + c + k < d ? at[k] : (T)0.0f;
-            }
+            at[n] = row < C && c < left ? v.row_at(row, C) + c * (uint32_t)sizeof(T) : kNowhere;
         }
     }
-
-    // Whether any element is infinite or NaN.
-    __device__ __forceinline__ bool odd() const {
-        bool bad = false;
+    // Positions p0 .. p0 + cnt of the walk; zeros past the ends.
+    __device__ __forceinline__ void load(const Rows &v, int64_t p0, int cnt) {
+        const __amdgpu_buffer_rsrc_t buf = v.chunk(p0, cnt);
+        const uint32_t shift = v.shift(cnt, C);
 #pragma unroll
-        for (int n = 0; n < kN; ++n)
+        for (int n = 0; n < kN; ++n) {
+            const uint32_t o = at[n] - shift;
+            if constexpr (VEC) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) bad = bad || abs_bits((float)r[n].v[k]) >= kInfBits;
-        return bad;
+                for (int h = 0; h < 8 / kV; ++h) {
+                    // the second half of a group may lie past the row's end
+                    const uint32_t oh = h == 0 ? o : ((int)((threadIdx.x + n * kThreads) % kGroups) * 8 + h * kV < left ? o + 16 * h : kNowhere);
+                    *reinterpret_cast<u32x4 *>(&r[n].v[h * kV]) = __builtin_amdgcn_raw_buffer_load_b128(buf, oh, 0, 0);
+                }
+            } else {
+                const int c = (int)((threadIdx.x + n * kThreads) % kGroups) * 8;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t ok = c + k < left ? o + k * (uint32_t)sizeof(T) : kNowhere;
+                    if constexpr (sizeof(T) == 2) {
+                        const uint16_t x = __builtin_amdgcn_raw_buffer_load_b16(buf, ok, 0, 0);
+                        r[n].v[k] = *reinterpret_cast<const T *>(&x);
+                    } else {
+                        const uint32_t x = __builtin_amdgcn_raw_buffer_load_b32(buf, ok, 0, 0);
+                        r[n].v[k] = *reinterpret_cast<const T *>(&x);
+                    }
+                }
+            }
+        }
     }
 
     __device__ __forceinline__ void store(bf16 *lds) const {
@@ -226,14 +258,13 @@ __device__ __forceinline__ f32x4 *seg_state(const WalkArgs &a, const Where &w, i
 __device__ __forceinline__ int state_row(int t, int q, int r) { return 32 * (t >> 1) + 8 * q + 4 * (t & 1) + r; }
 
 // STATE: only the segment's own part of T (from zero), for the join.
-template <typename T, int D1, int C, bool STATE>
+template <typename T, int D1, int C, bool VEC, bool STATE>
 __global__ __launch_bounds__(kThreads, D1 > 128 ? 1 : 2) void walk_kernel(WalkArgs a) {
     constexpr int kP = kPlanes<T>;                 // planes of X, Y, Z, P
     constexpr int kS = kP == 1 ? 1 : 3;            // planes of the operand copy of T
     constexpr int NA = D1 / 16, NT = D1 / 32, NS = C / 32, NI = C / 16;
     constexpr int kPX = C * kTileRow<D1>, kPZ = C * kTileRow<kNB>, kPP = C * kTileRow<C>;
     __shared__ __align__(16) bf16 X[STATE ? 8 : kP * kPX], Y[kP * kPX], Z[kP * kPZ], P[STATE ? 8 : kP * kPP];
-    __shared__ int64_t odd_at;
     const Where wh = where(a, STATE ? a.segs - 1 : a.segs);
     if (!wh.any) return;
     const Walk &w = a.w[wh.walk];
@@ -260,8 +291,8 @@ __global__ __launch_bounds__(kThreads, D1 > 128 ? 1 : 2) void walk_kernel(WalkAr
     }
 
     // decays: of P's elements in tiles on the diagonal and one below it, of a
-    // row's share of T, of eight consecutive positions' shares of T
-    float dec_d[4], dec_o[4], dec_row[NI], dec_8[8], dec_q[NS];
+    // row's share of T, of the positions' shares of T
+    float dec_d[4], dec_o[4], dec_row[NI], dec_z[NS][8];
     const float dec16 = fast_exp2(16.0f * g2);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -272,12 +303,11 @@ __global__ __launch_bounds__(kThreads, D1 > 128 ? 1 : 2) void walk_kernel(WalkAr
 #pragma unroll
     for (int it = 0; it < NI; ++it) dec_row[it] = w.wo * fast_exp2(g2 * (float)(16 * it + m + 1 - w.e));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dec_8[i] = fast_exp2(g2 * (float)(7 - i));
+    for (int s = 0; s < NS; ++s)
 #pragma unroll
-    for (int s = 0; s < NS; ++s) dec_q[s] = w.wt * fast_exp2(g2 * (float)(C - 8 - 32 * s - 8 * q + w.e));
+        for (int i = 0; i < 8; ++i) dec_z[s][i] = w.wt * fast_exp2(g2 * (float)(C - 1 - 32 * s - 8 * q - i + w.e));
     const float em1_full = walk_em1(g, C);
 
-    if (threadIdx.x == 0) odd_at = -1;
     if constexpr (!STATE) {
         // the tiles of P right of the diagonal that share a 32-wide read with it stay zero
         for (int i = threadIdx.x; i < kP * kPP / 8; i += kThreads) {
@@ -286,13 +316,25 @@ __global__ __launch_bounds__(kThreads, D1 > 128 ? 1 : 2) void walk_kernel(WalkAr
         }
     }
 
-    const int64_t bx = wh.b * w.X.sb + wh.h * w.X.sh, by = wh.b * w.Y.sb + wh.h * w.Y.sh,
-                  bz = wh.b * w.Z.sb + wh.h * w.Z.sh;
-    Ahead<T, D1, C> ax, ay;
-    Ahead<T, kNB, C> az;
-    if (!STATE) ax.load(w.X, bx, a.L, w.rev, begin, end, 0, w.d1, a.vec);
-    ay.load(w.Y, by, a.L, w.rev, begin, end, 0, w.d1, a.vec);
-    az.load(w.Z, bz, a.L, w.rev, begin, end, c0, w.d2, a.vec);
+    const Rows rx = rows_of<T>(w.X, wh.b, wh.h, a.L, w.rev, 0, w.d1), ry = rows_of<T>(w.Y, wh.b, wh.h, a.L, w.rev, 0, w.d1),
+               rz = rows_of<T>(w.Z, wh.b, wh.h, a.L, w.rev, c0, w.d2);
+    const Rows ro = rows_of<T>({w.out, a.L * a.H * w.d2, a.H * w.d2, w.d2}, wh.b, wh.h, a.L, w.rev, c0, w.d2);
+    Ahead<T, D1, C, VEC> ax, ay;
+    Ahead<T, kNB, C, VEC> az;
+    const int first = (int)min((int64_t)C, end - begin);
+    if (!STATE) {
+        ax.init(rx);
+        ax.load(rx, begin, first);
+    }
+    ay.init(ry);
+    ay.load(ry, begin, first);
+    az.init(rz);
+    az.load(rz, begin, first);
+    uint32_t out_at[NI];  // this lane's row of each 16-row tile of out, four columns from its own
+    const int oc = wave * 16 + 4 * q;
+#pragma unroll
+    for (int it = 0; it < NI; ++it)
+        out_at[it] = c0 + oc < w.d2 ? ro.row_at(16 * it + m, C) + oc * (uint32_t)sizeof(T) : kNowhere;
 
     for (int64_t p0 = begin; p0 < end; p0 += C) {
         const int cnt = (int)min((int64_t)C, end - p0);
@@ -300,11 +342,11 @@ __global__ __launch_bounds__(kThreads, D1 > 128 ? 1 : 2) void walk_kernel(WalkAr
         if (!STATE) ax.store(X);
         ay.store(Y);
         az.store(Z);
-        if (!STATE && az.odd()) odd_at = p0;
         if (p0 + C < end) {
-            if (!STATE) ax.load(w.X, bx, a.L, w.rev, p0 + C, end, 0, w.d1, a.vec);
-            ay.load(w.Y, by, a.L, w.rev, p0 + C, end, 0, w.d1, a.vec);
-            az.load(w.Z, bz, a.L, w.rev, p0 + C, end, c0, w.d2, a.vec);
+            const int next = (int)min((int64_t)C, end - p0 - C);
+            if (!STATE) ax.load(rx, p0 + C, next);
+            ay.load(ry, p0 + C, next);
+            az.load(rz, p0 + C, next);
         }
         lds_barrier();
 
@@ -393,7 +435,7 @@ __global__ __launch_bounds__(kThreads, D1 > 128 ? 1 : 2) void walk_kernel(WalkAr
             float f[8];
             if (cnt == C) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = plane_sum(z[s], i) * (dec_8[i] * dec_q[s]);
+                for (int i = 0; i < 8; ++i) f[i] = plane_sum(z[s], i) * dec_z[s][i];
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -418,7 +460,8 @@ __global__ __launch_bounds__(kThreads, D1 > 128 ? 1 : 2) void walk_kernel(WalkAr
 
         if constexpr (!STATE) {
             lds_barrier();  // P is whole
-            const bool odd = odd_at == p0;
+            // an infinity or NaN of Z has made T so, in its column's every row
+            const bool odd = __any(abs_bits(S[0][0]) >= kInfBits);
             if (odd) {
                 // values of Z that are not finite must not reach earlier
                 // positions through a zero of P: they are left out here and
@@ -455,21 +498,24 @@ __global__ __launch_bounds__(kThreads, D1 > 128 ? 1 : 2) void walk_kernel(WalkAr
                                 o[it][r] = fmaf((float)P[tile_at<C>(16 * it + m, j >> 3) + (j & 7)], zv, o[it][r]);
                     }
             }
-            const int cc = c0 + wave * 16 + 4 * q;
+            const __amdgpu_buffer_rsrc_t buf = ro.chunk(p0, cnt);
+            const uint32_t shift = ro.shift(cnt, C);
 #pragma unroll
             for (int it = 0; it < NI; ++it) {
-                const int64_t p = p0 + 16 * it + m;
-                if (p >= end) continue;
-                T *to = static_cast<T *>(w.out) + ((wh.b * a.L + (w.rev ? a.L - 1 - p : p)) * a.H + wh.h) * w.d2 + cc;
+                VecT<T, 4> v;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v.v[r] = (T)o[it][r];
+                const uint32_t at = out_at[it] - shift;
                 if (w.out4) {
-                    if (cc < w.d2) {
-                        const float f[4] = {o[it][0], o[it][1], o[it][2], o[it][3]};
-                        store_vec<T, 4>(to, f);
-                    }
+                    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b64(*reinterpret_cast<u32x2 *>(&v), buf, at, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<u32x4 *>(&v), buf, at, 0, 0);
                 } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (cc + r < w.d2) to[r] = (T)o[it][r];
+                    for (int r = 0; r < 4; ++r) {
+                        const uint32_t ar = c0 + oc + r < w.d2 ? at + r * (uint32_t)sizeof(T) : kNowhere;
+                        if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(*reinterpret_cast<uint16_t *>(&v.v[r]), buf, ar, 0, 0);
+                        else __builtin_amdgcn_raw_buffer_store_b32(*reinterpret_cast<uint32_t *>(&v.v[r]), buf, ar, 0, 0);
+                    }
                 }
             }
         }
