@@ -33,7 +33,7 @@ WalkPlan walk_plan(const LinattnArgs &p, bool backward) {
     const int C = walk_chunk(p.bf16);
     const int64_t chunks = (p.L + C - 1) / C, groups = p.B * p.H * w.nblk * w.walks;
     const int64_t want = 2 * (int64_t)device_cu_count();
-    int64_t segs = groups * 2 > want ? 1 : std::min<int64_t>((want + groups - 1) / groups, chunks / 4);
+    int64_t segs = groups * 2 >= want ? 1 : std::min<int64_t>((want + groups - 1) / groups, chunks / 4);
     if (segs < 2) segs = 1;
     w.seg_len = (chunks + segs - 1) / segs * C;
     w.segs = (int)((p.L + w.seg_len - 1) / w.seg_len);
@@ -59,11 +59,12 @@ void walk_launch(const WalkArgs &a, hipStream_t s) {
     constexpr int C = sizeof(T) == 2 ? 64 : 32;
     const int64_t pairs = (a.B * a.H + 7) / 8 * 8 * a.walks * a.nblk;
     if (a.segs > 1) {
-        walk::walk_kernel<T, D1, C, VEC, true><<<(unsigned)(pairs * (a.segs - 1)), kThreads, 0, s>>>(a);
+        walk::walk_kernel<T, D1, C, VEC, walk::Part::State, false><<<(unsigned)(pairs * (a.segs - 1)), kThreads, 0, s>>>(a);
         const int64_t tiles = (int64_t)a.walks * a.B * a.H * a.nblk * 4 * (D1 / 16);
         walk::join_kernel<D1><<<(unsigned)((tiles + 3) / 4), kThreads, 0, s>>>(a);
     }
-    walk::walk_kernel<T, D1, C, VEC, false><<<(unsigned)(pairs * a.segs), kThreads, 0, s>>>(a);
+    constexpr bool kPipe = false;
+    walk::walk_kernel<T, D1, C, VEC, walk::Part::Whole, kPipe><<<(unsigned)(pairs * a.segs), kThreads, 0, s>>>(a);
 }
 
 template <typename T, bool VEC>

@@ -43,8 +43,8 @@ template <typename T> constexpr int kPlanes = sizeof(T) == 2 ? 1 : 3;
 // 16 lanes fall on different banks; other widths are padded by one group.
 template <int W>
 __device__ __forceinline__ int tile_at(int row, int grp) {
-    if (W == 128 || W == 256) return row * W + ((grp ^ (((row & 3) << 2) | ((row >> 2) & 3))) << 3);
-    if (W == 64) return row * W + ((grp ^ ((((row >> 1) & 1) << 2) | ((row >> 2) & 3))) << 3);
+    if (W == 128 || W == 256) return row * W + ((grp ^ (((row & 3) << 2) | (-(row >> 2) & 3))) << 3);
+    if (W == 64) return row * W + ((grp ^ ((((row >> 1) & 1) << 2) | (-(row >> 2) & 3))) << 3);
     return row * (W + 8) + (grp << 3);
 }
 template <int W> constexpr int kTileRow = (W == 64 || W == 128 || W == 256) ? W : W + 8;
@@ -129,26 +129,30 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint3
 }
 constexpr uint32_t kNowhere = 0x80000000u;  // above every buffer's size, also after a chunk's bytes are taken off
 
-// Rows of one operand as a walk sees them, from column c0 on.
+// Rows of one operand as a walk's segment sees them, from column c0 on, in
+// chunks of C positions.
 struct Rows {
-    const char *p;      // row 0 of the sequence
-    int64_t row_bytes;  // below 2^24 (checked on the host)
-    uint32_t tail;      // bytes of a row from p on
-    int64_t L;
+    const char *p;       // the first chunk, if it is whole: its lowest address
+    int64_t step;        // bytes from a chunk to the next one
+    uint32_t row_bytes;  // below 2^24 (checked on the host)
+    uint32_t tail;       // bytes of a row from p on
     int rev;
 
-    // Bytes and address of the chunk of cnt positions from p0.
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk(int64_t p0, int cnt) const {
-        return buffer_of(p + (rev ? L - p0 - cnt : p0) * row_bytes, (uint32_t)(cnt - 1) * (uint32_t)row_bytes + tail);
+    // Address and bytes of chunk i of cnt positions (none: nothing to read or write).
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk(int i, int cnt, int C) const {
+        return buffer_of(p + i * step + (rev ? (C - cnt) * (int64_t)row_bytes : 0),
+                         cnt == 0 ? 0u : (uint32_t)(cnt - 1) * row_bytes + tail);
     }
-    // Offset of a chunk's row r in it, if the chunk is whole; (C - cnt) * row_bytes less in a reversed shorter one.
-    __device__ __forceinline__ uint32_t row_at(int r, int C) const { return (uint32_t)(rev ? C - 1 - r : r) * (uint32_t)row_bytes; }
-    __device__ __forceinline__ uint32_t shift(int cnt, int C) const { return rev ? (uint32_t)(C - cnt) * (uint32_t)row_bytes : 0u; }
+    // Offset of a chunk's row r in it, if the chunk is whole; shift() less in a shorter one.
+    __device__ __forceinline__ uint32_t row_at(int r, int C) const { return (uint32_t)(rev ? C - 1 - r : r) * row_bytes; }
+    __device__ __forceinline__ uint32_t shift(int cnt, int C) const { return rev ? (uint32_t)(C - cnt) * row_bytes : 0u; }
 };
 template <typename T>
-__device__ __forceinline__ Rows rows_of(const WalkView &v, int64_t b, int64_t h, int64_t L, int rev, int c0, int d) {
-    return {static_cast<const char *>(v.p) + (b * v.sb + h * v.sh + c0) * (int64_t)sizeof(T), v.st * (int64_t)sizeof(T),
-            (uint32_t)(d - c0) * (uint32_t)sizeof(T), L, rev};
+__device__ __forceinline__ Rows rows_of(const WalkView &v, int64_t b, int64_t h, int64_t L, int64_t begin, int C, int rev,
+                                        int c0, int d) {
+    const int64_t row = v.st * (int64_t)sizeof(T);
+    const char *p = static_cast<const char *>(v.p) + (b * v.sb + h * v.sh + c0) * (int64_t)sizeof(T);
+    return {p + (rev ? L - begin - C : begin) * row, rev ? -row * C : row * C, (uint32_t)row, (uint32_t)((d - c0) * (int)sizeof(T)), rev};
 }
 
 // A thread's share of one tile of W columns (groups of 8 elements), loaded
@@ -160,24 +164,28 @@ struct Ahead {
     struct alignas(16) {
         T v[8];
     } r[kN];
-    uint32_t at[kN];   // offsets in a whole chunk
-    int left;          // columns the operand has
+    // Where the groups of a row divide the threads, a thread's pieces are the
+    // same columns kThreads / kGroups rows apart and one offset tells them all.
+    static constexpr bool kEven = kThreads % kGroups == 0;
+    static constexpr int kStep = kThreads / kGroups;
+    uint32_t at[kEven ? 1 : kN];  // offsets in a whole chunk
+    int left;                     // columns the operand has
 
     __device__ __forceinline__ void init(const Rows &v) {
         left = (int)(v.tail / sizeof(T));
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
+        for (int n = 0; n < (kEven ? 1 : kN); ++n) {
             const int i = threadIdx.x + n * kThreads, row = i / kGroups, c = (i - row * kGroups) * 8;
             at[n] = row < C && c < left ? v.row_at(row, C) + c * (uint32_t)sizeof(T) : kNowhere;
         }
     }
-    // Positions p0 .. p0 + cnt of the walk; zeros past the ends.
-    __device__ __forceinline__ void load(const Rows &v, int64_t p0, int cnt) {
-        const __amdgpu_buffer_rsrc_t buf = v.chunk(p0, cnt);
+    // The cnt positions of chunk i; zeros past the ends.
+    __device__ __forceinline__ void load(const Rows &v, int chunk, int cnt) {
+        const __amdgpu_buffer_rsrc_t buf = v.chunk(chunk, cnt, C);
         const uint32_t shift = v.shift(cnt, C);
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
-            const uint32_t o = at[n] - shift;
+            const uint32_t o = kEven ? at[0] + ((uint32_t)(v.rev ? -n : n) * kStep * v.row_bytes - shift) : at[kEven ? 0 : n] - shift;
             if constexpr (VEC) {
 #pragma unroll
                 for (int h = 0; h < 8 / kV; ++h) {
@@ -223,9 +231,11 @@ struct Ahead {
     }
 };
 
-// Which part of the work a workgroup does.
+// Which part of the work a workgroup does (every count fits 31 bits: the
+// grid does).  The divisions run on the vector unit; their results are put
+// back into scalar registers, where addresses and branches want them.
 struct Where {
-    int64_t bh, b, h;
+    int bh, b, h;
     int walk, blk, seg;
     bool any;
 };
@@ -233,17 +243,18 @@ struct Where {
 // same rows: consecutive workgroups go to the 8 XCDs in turn, so all blocks of
 // one pair meet in one L2.
 __device__ __forceinline__ Where where(const WalkArgs &a, int segs) {
-    const int64_t per = (int64_t)a.walks * a.nblk * segs;
-    const int64_t grp = (int64_t)blockIdx.x / (8 * per), rest = (int64_t)blockIdx.x - grp * 8 * per;
+    auto scalar = [](uint32_t x) { return (int)__builtin_amdgcn_readfirstlane(x); };
+    const uint32_t per = (uint32_t)(a.walks * a.nblk * segs), heads = (uint32_t)a.H;
+    const uint32_t grp = blockIdx.x / (8 * per), rest = blockIdx.x - grp * 8 * per;
+    const uint32_t bh = grp * 8 + (rest & 7), sub = rest >> 3, pair = sub / (uint32_t)segs, walk = pair / (uint32_t)a.nblk;
     Where w;
-    w.bh = grp * 8 + (rest & 7);
-    const int sub = (int)(rest >> 3), pair = sub / segs;
-    w.seg = sub - pair * segs;
-    w.walk = pair / a.nblk;
-    w.blk = pair - w.walk * a.nblk;
-    w.b = w.bh / a.H;
-    w.h = w.bh - w.b * a.H;
-    w.any = w.bh < a.B * a.H && w.blk * kNB < a.w[w.walk].d2;
+    w.bh = scalar(bh);
+    w.b = scalar(bh / heads);
+    w.h = w.bh - w.b * (int)heads;
+    w.seg = scalar(sub - pair * (uint32_t)segs);
+    w.walk = scalar(walk);
+    w.blk = scalar(pair - walk * (uint32_t)a.nblk);
+    w.any = w.bh < (int)(a.B * a.H) && w.blk * kNB < a.w[w.walk].d2;
     return w;
 }
 
@@ -251,31 +262,55 @@ __device__ __forceinline__ Where where(const WalkArgs &a, int segs) {
 // `wave` of a block, tile by tile.
 template <int D1>
 __device__ __forceinline__ f32x4 *seg_state(const WalkArgs &a, const Where &w, int seg, int wave) {
-    const int64_t slot = (((int64_t)w.walk * a.B * a.H + w.bh) * a.nblk + w.blk) * a.segs + seg;
+    const int64_t slot = ((w.walk * a.B * a.H + w.bh) * a.nblk + w.blk) * a.segs + seg;
     return reinterpret_cast<f32x4 *>(a.seg_state) + (slot * 4 + wave) * (D1 / 16) * 64;
 }
 // Row of T that register r of tile t holds in lanes of group q.
 __device__ __forceinline__ int state_row(int t, int q, int r) { return 32 * (t >> 1) + 8 * q + 4 * (t & 1) + r; }
 
-// STATE: only the segment's own part of T (from zero), for the join.
-template <typename T, int D1, int C, bool VEC, bool STATE>
-__global__ __launch_bounds__(kThreads, D1 > 128 ? 1 : 2) void walk_kernel(WalkArgs a) {
+// Bytes of LDS of a walk's workgroup that keeps `stages` chunks.
+template <typename T, int D1, int C>
+constexpr int walk_lds(int stages, int ps) {
+    return 4 * C + 2 * kPlanes<T> * C * (stages * (2 * kTileRow<D1> + kTileRow<kNB>) + ps * kTileRow<C>);
+}
+// Chunks in LDS: three where they fit the CU's 160 KB, else one.
+template <typename T, int D1, int C>
+constexpr bool kPiped = walk_lds<T, D1, C>(3, 2) <= 160 * 1024;
+
+enum class Part {
+    Whole,  // outputs and T
+    State   // only the segment's own part of T (from zero), for the join
+};
+
+// Three chunks in LDS (PIPE): while chunk i is walked, the P of chunk i + 1 is
+// formed and chunk i + 2 is written to LDS from the registers that it was
+// loaded into a chunk earlier, so one barrier a chunk is enough and the parts
+// of an iteration are independent of each other.  With one chunk in LDS the
+// parts follow each other with three barriers, and other workgroups of the CU
+// fill the waits.
+template <typename T, int D1, int C, bool VEC, Part PART, bool PIPE>
+__global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kernel(WalkArgs a) {
+    constexpr bool kOut = PART == Part::Whole;
     constexpr int kP = kPlanes<T>;                 // planes of X, Y, Z, P
     constexpr int kS = kP == 1 ? 1 : 3;            // planes of the operand copy of T
     constexpr int NA = D1 / 16, NT = D1 / 32, NS = C / 32, NI = C / 16;
-    constexpr int kPX = C * kTileRow<D1>, kPZ = C * kTileRow<kNB>, kPP = C * kTileRow<C>;
-    __shared__ __align__(16) bf16 X[STATE ? 8 : kP * kPX], Y[kP * kPX], Z[kP * kPZ], P[STATE ? 8 : kP * kPP];
-    const Where wh = where(a, STATE ? a.segs - 1 : a.segs);
+    constexpr int kPX = C * kTileRow<D1>, kPZ = C * kTileRow<kNB>, kPP = C * kTileRow<C>;  // elements of a plane
+    constexpr int kStages = PIPE ? 3 : 1, kPs = PIPE ? 2 : 1;
+    __shared__ __align__(16) bf16 X[kOut ? kStages * kP * kPX : 8], Y[kStages * kP * kPX], Z[kStages * kP * kPZ],
+        P[kOut ? kPs * kP * kPP : 8];
+    __shared__ __align__(16) float dec_z[C];
+    const Where wh = where(a, kOut ? a.segs : a.segs - 1);
     if (!wh.any) return;
     const Walk &w = a.w[wh.walk];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
     const int tr_i = m >> 2, tr_c = m & 3;         // this lane's row and column group in a transposing read
     const int c0 = wh.blk * kNB, col = c0 + wave * 16 + m;
     const float g = walk_gate(a.log_decay, wh.h), g2 = g * kLog2e;
     const int64_t begin = (int64_t)wh.seg * a.seg_len, end = min(a.L, begin + a.seg_len);
+    const int chunks = (int)((end - begin + C - 1) / C), last = (int)(end - begin - (int64_t)(chunks - 1) * C);
 
     f32x4 S[NA];
-    if (!STATE && a.segs > 1) {
+    if (kOut && a.segs > 1) {
         const f32x4 *src = seg_state<D1>(a, wh, wh.seg, wave) + lane;
 #pragma unroll
         for (int t = 0; t < NA; ++t) S[t] = src[t * 64];
@@ -285,14 +320,14 @@ __global__ __launch_bounds__(kThreads, D1 > 128 ? 1 : 2) void walk_kernel(WalkAr
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = state_row(t, q, r);
-                S[t][r] = !STATE && w.init != nullptr && col < w.d2 && row < w.d1
-                              ? w.init[wh.bh * w.d1 * w.d2 + (int64_t)row * w.im + (int64_t)col * w.in] : 0.0f;
+                S[t][r] = kOut && w.init != nullptr && col < w.d2 && row < w.d1
+                              ? w.init[(int64_t)wh.bh * w.d1 * w.d2 + (int64_t)row * w.im + (int64_t)col * w.in] : 0.0f;
             }
     }
 
     // decays: of P's elements in tiles on the diagonal and one below it, of a
-    // row's share of T, of the positions' shares of T
-    float dec_d[4], dec_o[4], dec_row[NI], dec_z[NS][8];
+    // row's share of T, and (in LDS) of the positions' shares of T
+    float dec_d[4], dec_o[4], dec_row[NI];
     const float dec16 = fast_exp2(16.0f * g2);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -302,226 +337,317 @@ __global__ __launch_bounds__(kThreads, D1 > 128 ? 1 : 2) void walk_kernel(WalkAr
     }
 #pragma unroll
     for (int it = 0; it < NI; ++it) dec_row[it] = w.wo * fast_exp2(g2 * (float)(16 * it + m + 1 - w.e));
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dec_z[s][i] = w.wt * fast_exp2(g2 * (float)(C - 1 - 32 * s - 8 * q - i + w.e));
+    if (threadIdx.x < C) dec_z[threadIdx.x] = w.wt * fast_exp2(g2 * (float)(C - 1 - (int)threadIdx.x + w.e));
     const float em1_full = walk_em1(g, C);
 
-    if constexpr (!STATE) {
+    if constexpr (kOut) {
         // the tiles of P right of the diagonal that share a 32-wide read with it stay zero
-        for (int i = threadIdx.x; i < kP * kPP / 8; i += kThreads) {
+        for (int i = threadIdx.x; i < kPs * kP * kPP / 8; i += kThreads) {
             const bf16x8 z = {};
             *reinterpret_cast<bf16x8 *>(&P[i * 8]) = z;
         }
     }
 
-    const Rows rx = rows_of<T>(w.X, wh.b, wh.h, a.L, w.rev, 0, w.d1), ry = rows_of<T>(w.Y, wh.b, wh.h, a.L, w.rev, 0, w.d1),
-               rz = rows_of<T>(w.Z, wh.b, wh.h, a.L, w.rev, c0, w.d2);
-    const Rows ro = rows_of<T>({w.out, a.L * a.H * w.d2, a.H * w.d2, w.d2}, wh.b, wh.h, a.L, w.rev, c0, w.d2);
+    auto rows = [&](const WalkView &v, int from, int d) { return rows_of<T>(v, wh.b, wh.h, a.L, begin, C, w.rev, from, d); };
+    const Rows rx = rows(w.X, 0, w.d1), ry = rows(w.Y, 0, w.d1), rz = rows(w.Z, c0, w.d2),
+               ro = rows({w.out, a.L * a.H * w.d2, a.H * w.d2, w.d2}, c0, w.d2);
     Ahead<T, D1, C, VEC> ax, ay;
     Ahead<T, kNB, C, VEC> az;
-    const int first = (int)min((int64_t)C, end - begin);
-    if (!STATE) {
-        ax.init(rx);
-        ax.load(rx, begin, first);
-    }
+    if (kOut) ax.init(rx);
     ay.init(ry);
-    ay.load(ry, begin, first);
     az.init(rz);
-    az.load(rz, begin, first);
-    uint32_t out_at[NI];  // this lane's row of each 16-row tile of out, four columns from its own
     const int oc = wave * 16 + 4 * q;
-#pragma unroll
-    for (int it = 0; it < NI; ++it)
-        out_at[it] = c0 + oc < w.d2 ? ro.row_at(16 * it + m, C) + oc * (uint32_t)sizeof(T) : kNowhere;
+    // this lane's row of the first 16-row tile of out, four columns from its own
+    const uint32_t out_at = c0 + oc < w.d2 ? ro.row_at(m, C) + oc * (uint32_t)sizeof(T) : kNowhere;
+    const uint32_t out_step = (uint32_t)(w.rev ? -16 : 16) * ro.row_bytes;
 
-    for (int64_t p0 = begin; p0 < end; p0 += C) {
-        const int cnt = (int)min((int64_t)C, end - p0);
-        lds_barrier();  // the last chunk's reads are done
-        if (!STATE) ax.store(X);
-        ay.store(Y);
-        az.store(Z);
-        if (p0 + C < end) {
-            const int next = (int)min((int64_t)C, end - p0 - C);
-            if (!STATE) ax.load(rx, p0 + C, next);
-            ay.load(ry, p0 + C, next);
-            az.load(rz, p0 + C, next);
-        }
-        lds_barrier();
-
-        f32x4 o[NI];
-        if constexpr (!STATE) {
-            // P, a tile's transpose at a time (a lane's results are then four
-            // consecutive j); the NI (NI + 1) / 2 tiles go round the waves
-            constexpr int kTiles = NI * (NI + 1) / 2;
+    auto positions = [&](int i) { return i < chunks - 1 ? C : i == chunks - 1 ? last : 0; };
+    auto load = [&](int i) {  // chunk i (past the last one: zeros) into registers
+        const int cnt = positions(i);
+        if (kOut) ax.load(rx, i, cnt);
+        ay.load(ry, i, cnt);
+        az.load(rz, i, cnt);
+    };
+    auto put = [&](int stage) {
+        if (kOut) ax.store(X + stage * kP * kPX);
+        ay.store(Y + stage * kP * kPX);
+        az.store(Z + stage * kP * kPZ);
+    };
+    // The products of a chunk run as one sequence of batches, each a few
+    // operand reads and the matrix instructions that use them, with the reads
+    // of batch k + 1 issued before the products of batch k (the compiler,
+    // short of registers, would put every read right before its use and wait):
+    //   P of chunk i + 1 or i: the tiles below and on the diagonal go round
+    //     the waves (the last one is formed more than once if they don't come
+    //     out even), each as its transpose, so that a lane's four results are
+    //     consecutive j;
+    //   the rows' share of T, transposed (lane m is position 16 it + m,
+    //     registers are four columns);
+    //   T over the chunk.
+    constexpr int kTiles = NI * (NI + 1) / 2, kMine = (kTiles + 3) / 4;
+    constexpr int kU1 = kP == 1 ? 2 : 1, kU3 = kP == 1 ? 4 : 2;          // units a batch
+    constexpr int kB1 = kOut ? (kMine * NT + kU1 - 1) / kU1 : 0, kB2 = kOut ? NT : 0,
+                  kB3s = (NA + kU3 - 1) / kU3, kB3 = NS * kB3s;
+    constexpr int kFrags = (kP == 1 ? 4 : 6);
+    static_assert(NI * kP <= kFrags && 2 * kU1 * kP <= kFrags && kU3 * kP <= kFrags, "a batch fits its buffer");
+    struct Frags {
+        bf16x8 v[kFrags];
+    };
+    int my_it[kMine], my_jt[kMine];
 #pragma unroll
-            for (int k = 0; k < (kTiles + 3) / 4; ++k) {
-                const int tile = wave + 4 * k;
-                if (tile < kTiles) {
-                    const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3, jt = tile - it * (it + 1) / 2;
-                    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < kMine; ++k) {
+        const int tile = min(wave + 4 * k, kTiles - 1);
+        my_it[k] = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
+        my_jt[k] = tile - my_it[k] * (my_it[k] + 1) / 2;
+    }
+    auto products = [&](const bf16 *Xp, const bf16 *Yp, bf16 *Ps, const bf16 *Xs, const bf16 *Ys, const bf16 *Zs, int cnt,
+                        bool whole, bf16x8 (&z)[NS][kP], f32x4 (&o)[NI]) {
+        Frags buf[2];
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        bf16x8 zw[3];
+        auto read = [&](int k, Frags &f) {
+            if (k < kB1) {
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        bf16x8 y[kP], x[kP];
+                for (int u = 0; u < kU1; ++u) {
+                    const int unit = k * kU1 + u, mine = unit / NT, t = unit % NT;
+                    if (unit < kMine * NT)
 #pragma unroll
                         for (int p = 0; p < kP; ++p) {
-                            y[p] = read_row(&Y[p * kPX + tile_at<D1>(jt * 16 + m, 4 * t + q)]);
-                            x[p] = read_row(&X[p * kPX + tile_at<D1>(it * 16 + m, 4 * t + q)]);
+                            f.v[(2 * u) * kP + p] = read_row(&Yp[p * kPX + tile_at<D1>(my_jt[mine] * 16 + m, 4 * t + q)]);
+                            f.v[(2 * u + 1) * kP + p] = read_row(&Xp[p * kPX + tile_at<D1>(my_it[mine] * 16 + m, 4 * t + q)]);
                         }
-                        acc = mfma_planes(y, x, acc);
+                }
+            } else if (k < kB1 + kB2) {
+                const int t = k - kB1;
+#pragma unroll
+                for (int it = 0; it < NI; ++it)
+#pragma unroll
+                    for (int p = 0; p < kP; ++p)
+                        f.v[it * kP + p] = read_row(&Xs[p * kPX + tile_at<D1>(it * 16 + m, 4 * t + q)]);
+            } else {
+                const int s = (k - kB1 - kB2) / kB3s, t0 = (k - kB1 - kB2) % kB3s * kU3;
+#pragma unroll
+                for (int u = 0; u < kU3; ++u)
+                    if (t0 + u < NA)
+#pragma unroll
+                        for (int p = 0; p < kP; ++p) {
+                            const int t = t0 + u, row = 32 * s + 8 * q + tr_i, grp = 4 * (t >> 1) + tr_c, in = 4 * (t & 1);
+                            f.v[u * kP + p] = join(read_tr(&Ys[p * kPX + tile_at<D1>(row, grp) + in]),
+                                                   read_tr(&Ys[p * kPX + tile_at<D1>(row + 4, grp) + in]));
+                        }
+            }
+        };
+        auto use = [&](int k, const Frags &f) {
+            if (k < kB1) {
+#pragma unroll
+                for (int u = 0; u < kU1; ++u) {
+                    const int unit = k * kU1 + u, mine = unit / NT, t = unit % NT;
+                    if (unit >= kMine * NT) continue;
+                    bf16x8 y[kP], x[kP];
+#pragma unroll
+                    for (int p = 0; p < kP; ++p) {
+                        y[p] = f.v[(2 * u) * kP + p];
+                        x[p] = f.v[(2 * u + 1) * kP + p];
                     }
+                    acc = mfma_planes(y, x, acc);
+                    if (t != NT - 1) continue;
+                    const int it = my_it[mine], jt = my_jt[mine];
                     const float far = it - jt == 3 ? dec16 * dec16 : it - jt == 2 ? dec16 : 1.0f;
-                    float f[4];
+                    float v[8] = {};
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        f[r] = it == jt ? acc[r] * dec_d[r] : acc[r] * (dec_o[r] * far);
-                        if (it == jt && m < 4 * q + r) f[r] = 0.0f;  // whatever Y holds there
+                        v[r] = acc[r] * (it == jt ? dec_d[r] : dec_o[r] * far);
+                        if (it == jt && m < 4 * q + r) v[r] = 0.0f;  // whatever Y holds there
+                        acc[r] = 0.0f;
                     }
-                    bf16 *to = &P[tile_at<C>(it * 16 + m, 2 * jt + (q >> 1)) + 4 * (q & 1)];
-                    if constexpr (kP == 1) {
-                        VecT<bf16, 4> v;
+                    bf16x8 pv[kP];
+                    to_planes(v, pv);
+                    bf16 *to = &Ps[tile_at<C>(it * 16 + m, 2 * jt + (q >> 1)) + 4 * (q & 1)];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) v.v[r] = (bf16)f[r];
-                        *reinterpret_cast<VecT<bf16, 4> *>(to) = v;
-                    } else {
-                        const float f8[8] = {f[0], f[1], f[2], f[3], 0.0f, 0.0f, 0.0f, 0.0f};
-                        bf16x8 p[3];
-                        split3(f8, p);
-#pragma unroll
-                        for (int k2 = 0; k2 < 3; ++k2)
-                            *reinterpret_cast<u32x2 *>(to + k2 * kPP) = *reinterpret_cast<const u32x2 *>(&p[k2]);
-                    }
+                    for (int p = 0; p < kP; ++p) *reinterpret_cast<u32x2 *>(to + p * kPP) = *reinterpret_cast<const u32x2 *>(&pv[p]);
                 }
-            }
-            // the rows' share of T, transposed: lane m is position 16 it + m, registers four columns
-#pragma unroll
-            for (int it = 0; it < NI; ++it) o[it] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float f[8] = {S[2 * t][0],     S[2 * t][1],     S[2 * t][2],     S[2 * t][3],
+            } else if (k < kB1 + kB2) {
+                const int t = k - kB1;
+                const float v[8] = {S[2 * t][0],     S[2 * t][1],     S[2 * t][2],     S[2 * t][3],
                                     S[2 * t + 1][0], S[2 * t + 1][1], S[2 * t + 1][2], S[2 * t + 1][3]};
                 bf16x8 sp[kS];
-                to_planes(f, sp);
+                to_planes(v, sp);
 #pragma unroll
                 for (int it = 0; it < NI; ++it) {
                     bf16x8 x[kP];
 #pragma unroll
-                    for (int p = 0; p < kP; ++p) x[p] = read_row(&X[p * kPX + tile_at<D1>(it * 16 + m, 4 * t + q)]);
-                    o[it] = mfma_planes(sp, x, o[it]);
+                    for (int p = 0; p < kP; ++p) x[p] = f.v[it * kP + p];
+                    o[it] = mfma_planes(sp, x, t == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : o[it]);
                 }
+                if (t == NT - 1)
+#pragma unroll
+                    for (int it = 0; it < NI; ++it)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) o[it][r] *= dec_row[it];
+            } else {
+                const int s = (k - kB1 - kB2) / kB3s, t0 = (k - kB1 - kB2) % kB3s * kU3;
+                if (k == kB1 + kB2) {
+                    const float em1 = whole ? em1_full : walk_em1(g, cnt);
+#pragma unroll
+                    for (int t = 0; t < NA; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) S[t][r] = fmaf(S[t][r], em1, S[t][r]);
+                }
+                if (t0 == 0) {
+                    float v[8];
+                    if (whole) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = plane_sum(z[s], i) * dec_z[32 * s + 8 * q + i];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int n = cnt - 1 - (32 * s + 8 * q + i);
+                            v[i] = n >= 0 ? plane_sum(z[s], i) * (w.wt * fast_exp2(g2 * (float)(n + w.e))) : 0.0f;
+                        }
+                    }
+                    split3(v, zw);
+                }
+#pragma unroll
+                for (int u = 0; u < kU3; ++u)
+                    if (t0 + u < NA) {
+                        bf16x8 y[kP];
+#pragma unroll
+                        for (int p = 0; p < kP; ++p) y[p] = f.v[u * kP + p];
+                        S[t0 + u] = mfma_planes(y, zw, S[t0 + u]);
+                    }
             }
+        };
 #pragma unroll
-            for (int it = 0; it < NI; ++it)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[it][r] *= dec_row[it];
-        }
-
-        // T over the chunk
-        const float em1 = cnt == C ? em1_full : walk_em1(g, cnt);
-#pragma unroll
-        for (int t = 0; t < NA; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[t][r] = fmaf(S[t][r], em1, S[t][r]);
-        bf16x8 z[NS][kP];
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
                 const int row = 32 * s + 8 * q + tr_i, grp = 2 * wave + (tr_c >> 1), in = 4 * (tr_c & 1);
-                z[s][p] = join(read_tr(&Z[p * kPZ + tile_at<kNB>(row, grp) + in]),
-                               read_tr(&Z[p * kPZ + tile_at<kNB>(row + 4, grp) + in]));
+                z[s][p] = join(read_tr(&Zs[p * kPZ + tile_at<kNB>(row, grp) + in]),
+                               read_tr(&Zs[p * kPZ + tile_at<kNB>(row + 4, grp) + in]));
             }
-            float f[8];
-            if (cnt == C) {
+        read(0, buf[0]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = plane_sum(z[s], i) * dec_z[s][i];
-            } else {
+        for (int k = 0; k < kB1 + kB2 + kB3; ++k) {
+            if (k + 1 < kB1 + kB2 + kB3) read(k + 1, buf[(k + 1) & 1]);
+            __builtin_amdgcn_sched_barrier(0);
+            use(k, buf[k & 1]);
+        }
+    };
+    // out += P Z.  Values of Z that are not finite must not reach earlier
+    // positions through a zero of P: then (their columns of T have become so)
+    // they are left out of the product and added to the positions from their own on.
+    auto within = [&](const bf16 *Ps, const bf16 *Zs, int cnt, bf16x8 (&z)[NS][kP], f32x4 (&o)[NI]) {
+        bf16x8 pr[NI][NS][kP];
+#pragma unroll
+        for (int it = 0; it < NI; ++it)
+#pragma unroll
+            for (int s = 0; s <= it / 2; ++s)
+#pragma unroll
+                for (int p = 0; p < kP; ++p) pr[it][s][p] = read_row(&Ps[p * kPP + tile_at<C>(it * 16 + m, 4 * s + q)]);
+        const bool odd = __any(abs_bits(S[0][0]) >= kInfBits);
+        if (odd) {
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int n = cnt - 1 - (32 * s + 8 * q + i);
-                    f[i] = n >= 0 ? plane_sum(z[s], i) * (w.wt * fast_exp2(g2 * (float)(n + w.e))) : 0.0f;
-                }
-            }
-            bf16x8 zw[3];
-            split3(f, zw);
+                    const bool bad = abs_bits((float)z[s][0][i]) >= kInfBits;
 #pragma unroll
-            for (int t = 0; t < NA; ++t) {
-                bf16x8 y[kP];
-#pragma unroll
-                for (int p = 0; p < kP; ++p) {
-                    const int row = 32 * s + 8 * q + tr_i, grp = 4 * (t >> 1) + tr_c, in = 4 * (t & 1);
-                    y[p] = join(read_tr(&Y[p * kPX + tile_at<D1>(row, grp) + in]),
-                                read_tr(&Y[p * kPX + tile_at<D1>(row + 4, grp) + in]));
+                    for (int p = 0; p < kP; ++p)
+                        if (bad) z[s][p][i] = (bf16)0.0f;
                 }
-                S[t] = mfma_planes(y, zw, S[t]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int it = 0; it < NI; ++it)
+#pragma unroll
+            for (int s = 0; s <= it / 2; ++s) o[it] = mfma_planes(z[s], pr[it][s], o[it]);
+        if (odd) {
+#pragma unroll 1
+            for (int j = 0; j < cnt; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int c = oc + r;
+                    const float zv = (float)Zs[tile_at<kNB>(j, c >> 3) + (c & 7)];  // the first plane is as little finite
+                    if (abs_bits(zv) < kInfBits) continue;
+#pragma unroll
+                    for (int it = 0; it < NI; ++it)
+                        if (j <= 16 * it + m)
+                            o[it][r] = fmaf((float)Ps[tile_at<C>(16 * it + m, j >> 3) + (j & 7)], zv, o[it][r]);
+                }
+        }
+    };
+    auto write = [&](int i, int cnt, const f32x4 (&o)[NI]) {
+        const __amdgpu_buffer_rsrc_t buf = ro.chunk(i, cnt, C);
+        const uint32_t shift = ro.shift(cnt, C);
+#pragma unroll
+        for (int it = 0; it < NI; ++it) {
+            VecT<T, 4> v;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v.v[r] = (T)o[it][r];
+            const uint32_t at = out_at + ((uint32_t)it * out_step - shift);
+            if (w.out4) {
+                if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b64(*reinterpret_cast<u32x2 *>(&v), buf, at, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<u32x4 *>(&v), buf, at, 0, 0);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint32_t ar = c0 + oc + r < w.d2 ? at + r * (uint32_t)sizeof(T) : kNowhere;
+                    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(*reinterpret_cast<uint16_t *>(&v.v[r]), buf, ar, 0, 0);
+                    else __builtin_amdgcn_raw_buffer_store_b32(*reinterpret_cast<uint32_t *>(&v.v[r]), buf, ar, 0, 0);
+                }
             }
         }
+    };
 
-        if constexpr (!STATE) {
-            lds_barrier();  // P is whole
-            // an infinity or NaN of Z has made T so, in its column's every row
-            const bool odd = __any(abs_bits(S[0][0]) >= kInfBits);
-            if (odd) {
-                // values of Z that are not finite must not reach earlier
-                // positions through a zero of P: they are left out here and
-                // added to the positions from their own on below
-#pragma unroll
-                for (int s = 0; s < NS; ++s)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const bool bad = abs_bits((float)z[s][0][i]) >= kInfBits;
-#pragma unroll
-                        for (int p = 0; p < kP; ++p)
-                            if (bad) z[s][p][i] = (bf16)0.0f;
-                    }
-            }
-#pragma unroll
-            for (int it = 0; it < NI; ++it)
-#pragma unroll
-                for (int s = 0; s <= it / 2; ++s) {
-                    bf16x8 pr[kP];
-#pragma unroll
-                    for (int p = 0; p < kP; ++p) pr[p] = read_row(&P[p * kPP + tile_at<C>(it * 16 + m, 4 * s + q)]);
-                    o[it] = mfma_planes(z[s], pr, o[it]);
-                }
-            if (odd) {
-                for (int j = 0; j < cnt; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int c = wave * 16 + 4 * q + r;
-                        const float zv = (float)Z[tile_at<kNB>(j, c >> 3) + (c & 7)];  // the first plane is as little finite
-                        if (abs_bits(zv) < kInfBits) continue;
-#pragma unroll
-                        for (int it = 0; it < NI; ++it)
-                            if (j <= 16 * it + m)
-                                o[it][r] = fmaf((float)P[tile_at<C>(16 * it + m, j >> 3) + (j & 7)], zv, o[it][r]);
-                    }
-            }
-            const __amdgpu_buffer_rsrc_t buf = ro.chunk(p0, cnt);
-            const uint32_t shift = ro.shift(cnt, C);
-#pragma unroll
-            for (int it = 0; it < NI; ++it) {
-                VecT<T, 4> v;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v.v[r] = (T)o[it][r];
-                const uint32_t at = out_at[it] - shift;
-                if (w.out4) {
-                    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b64(*reinterpret_cast<u32x2 *>(&v), buf, at, 0, 0);
-                    else __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<u32x4 *>(&v), buf, at, 0, 0);
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const uint32_t ar = c0 + oc + r < w.d2 ? at + r * (uint32_t)sizeof(T) : kNowhere;
-                        if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(*reinterpret_cast<uint16_t *>(&v.v[r]), buf, ar, 0, 0);
-                        else __builtin_amdgcn_raw_buffer_store_b32(*reinterpret_cast<uint32_t *>(&v.v[r]), buf, ar, 0, 0);
-                    }
-                }
+    if constexpr (PIPE) {
+        load(0);
+        put(0);
+        load(1);
+        put(1);
+        load(2);
+        lds_barrier();
+        form_first(X, Y, P);
+        lds_barrier();
+        int cur = 0, nxt = 1, far = 2;  // stages of chunks i, i + 1, i + 2
+        auto step = [&](int i, bool whole) {
+            put(far);
+            load(i + 3);
+            const int cnt = whole ? C : positions(i);
+            const bf16 *Xs = X + cur * kP * kPX, *Ys = Y + cur * kP * kPX, *Zs = Z + cur * kP * kPZ;
+            bf16 *Pc = P + (i & 1) * kP * kPP, *Pn = P + (~i & 1) * kP * kPP;
+            f32x4 o[NI];
+            bf16x8 z[NS][kP];
+            products(X + nxt * kP * kPX, Y + nxt * kP * kPX, Pn, Xs, Ys, Zs, cnt, whole, z, o);
+            within(Pc, Zs, cnt, z, o);
+            write(i, cnt, o);
+            lds_barrier();
+            const int old = cur;
+            cur = nxt;
+            nxt = far;
+            far = old;
+        };
+        for (int i = 0; i < chunks - 1; ++i) step(i, true);
+        step(chunks - 1, false);
+    } else {
+        load(0);
+        for (int i = 0; i < chunks; ++i) {
+            const int cnt = positions(i);
+            lds_barrier();  // the last chunk's reads are done
+            put(0);
+            load(i + 1);
+            lds_barrier();
+            f32x4 o[NI];
+            bf16x8 z[NS][kP];
+            products(X, Y, P, X, Y, Z, cnt, cnt == C, z, o);
+            if constexpr (kOut) {
+                lds_barrier();  // P is whole
+                within(P, Z, cnt, z, o);
+                write(i, cnt, o);
             }
         }
     }
 
-    if constexpr (STATE) {
+    if constexpr (!kOut) {
         f32x4 *dst = seg_state<D1>(a, wh, wh.seg, wave) + lane;
 #pragma unroll
         for (int t = 0; t < NA; ++t) dst[t * 64] = S[t];
@@ -531,7 +657,7 @@ __global__ __launch_bounds__(kThreads, D1 > 128 ? 1 : 2) void walk_kernel(WalkAr
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = state_row(t, q, r);
-                if (row < w.d1) w.fin[wh.bh * w.d1 * w.d2 + (int64_t)row * w.im + (int64_t)col * w.in] = S[t][r];
+                if (row < w.d1) w.fin[(int64_t)wh.bh * w.d1 * w.d2 + (int64_t)row * w.im + (int64_t)col * w.in] = S[t][r];
             }
     }
 }
@@ -547,7 +673,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(WalkArgs a) {
     const int64_t blk_of = item / (4 * NA);
     Where wh;
     wh.blk = (int)(blk_of % a.nblk);
-    wh.bh = blk_of / a.nblk % (a.B * a.H);
+    wh.bh = (int)(blk_of / a.nblk % (a.B * a.H));
     wh.walk = (int)(blk_of / a.nblk / (a.B * a.H));
     const Walk &w = a.w[wh.walk];
     if (wh.blk * kNB >= w.d2) return;
@@ -558,7 +684,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(WalkArgs a) {
     for (int r = 0; r < 4; ++r) {
         const int row = state_row(t, q, r);
         s[r] = w.init != nullptr && col < w.d2 && row < w.d1
-                   ? w.init[wh.bh * w.d1 * w.d2 + (int64_t)row * w.im + (int64_t)col * w.in] : 0.0f;
+                   ? w.init[(int64_t)wh.bh * w.d1 * w.d2 + (int64_t)row * w.im + (int64_t)col * w.in] : 0.0f;
     }
     f32x4 *at = seg_state<D1>(a, wh, 0, wave) + t * 64 + lane;
     const int64_t step = 4 * NA * 64;
