@@ -69,6 +69,32 @@ __global__ __launch_bounds__(kThreads) void emb_lookup_kernel(EmbFwdArgs a) {
     }
 }
 
+// ---------------------------------------------------------------- zero rows
+// Every row of the gradient is cleared while the ids are sorted (a share in
+// each launch of the sort, by workgroups of their own): the sort has work for
+// few CUs, and rows that no id names need no search.  Named rows are written
+// twice for that, at most N of V + N.
+struct ZeroArgs {
+    char *out;
+    int64_t bytes;
+    int first;  // workgroups of the launch before those that clear
+};
+constexpr int kZeroBlocks = 1024;
+
+__device__ __forceinline__ void zero_share(const ZeroArgs &z, int share, int shares) {
+    // 16-byte pieces [lo, hi) of this share; the first also takes what is left at either end
+    const int64_t head = min(z.bytes, (int64_t)((16 - ((uintptr_t)z.out & 15)) & 15)), whole = (z.bytes - head) / 16;
+    uint4 *v = reinterpret_cast<uint4 *>(z.out + head);
+    const int64_t lo = whole * share / shares, hi = whole * (share + 1) / shares;
+    const int64_t me = (int64_t)((int)blockIdx.x - z.first) * blockDim.x + threadIdx.x;
+    const int64_t all = (int64_t)((int)gridDim.x - z.first) * blockDim.x;
+    for (int64_t i = lo + me; i < hi; i += all) v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (share == 0) {
+        if (me < head) z.out[me] = 0;
+        if (me < z.bytes - head - whole * 16) z.out[head + whole * 16 + me] = 0;
+    }
+}
+
 // ---------------------------------------------------------------- sort
 constexpr int kBins = 256;          // 8 bits of the key a pass
 constexpr int kSmallN = 8192;       // sorted by one workgroup in LDS
@@ -125,7 +151,11 @@ struct SortArgs {
     int64_t tile;    // elements a workgroup (a multiple of 256)
 };
 
-__global__ __launch_bounds__(kSmallThreads) void emb_sort_small_kernel(SortArgs a) {
+__global__ __launch_bounds__(kSmallThreads) void emb_sort_small_kernel(SortArgs a, ZeroArgs zero) {
+    if ((int)blockIdx.x >= zero.first) {
+        zero_share(zero, 0, 1);
+        return;
+    }
     __shared__ uint32_t key[2][kSmallN];
     __shared__ uint16_t pos[2][kSmallN];
     __shared__ uint32_t cnt[16][kBins];
@@ -133,9 +163,19 @@ __global__ __launch_bounds__(kSmallThreads) void emb_sort_small_kernel(SortArgs 
     const int t = threadIdx.x, w = t >> 6, lane = t & 63;
     const int N = (int)a.N;
     const int per = (N + 1023) / 1024 * 64;  // elements a wave
-    for (int n = t; n < N; n += kSmallThreads) {
-        key[0][n] = id_key(a.ids, a.wide, n, a.V);
-        pos[0][n] = (uint16_t)n;
+    uint32_t own[kSmallN / kSmallThreads];
+#pragma unroll
+    for (int u = 0; u < kSmallN / kSmallThreads; ++u) {
+        const int n = t + u * kSmallThreads;
+        own[u] = n < N ? id_key(a.ids, a.wide, n, a.V) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < kSmallN / kSmallThreads; ++u) {
+        const int n = t + u * kSmallThreads;
+        if (n < N) {
+            key[0][n] = own[u];
+            pos[0][n] = (uint16_t)n;
+        }
     }
     int cur = 0;
     for (int p = 0; p < a.passes; ++p) {
@@ -179,7 +219,11 @@ __device__ __forceinline__ uint32_t key_at(const SortArgs &a, int p, int64_t n) 
 }
 
 // Digit counts of each workgroup's elements in pass p.
-__global__ __launch_bounds__(kThreads) void emb_hist_kernel(SortArgs a, int p) {
+__global__ __launch_bounds__(kThreads) void emb_hist_kernel(SortArgs a, int p, ZeroArgs zero) {
+    if ((int)blockIdx.x >= zero.first) {
+        zero_share(zero, 2 * p, 2 * a.passes);
+        return;
+    }
     __shared__ uint32_t cnt[kBins];
     cnt[threadIdx.x] = 0;
     __syncthreads();
@@ -191,7 +235,11 @@ __global__ __launch_bounds__(kThreads) void emb_hist_kernel(SortArgs a, int p) {
 
 // Moves each workgroup's elements to their places in pass p, keeping the
 // order of equal digits: wave w takes the w-th quarter of the tile in order.
-__global__ __launch_bounds__(kThreads) void emb_scatter_kernel(SortArgs a, int p) {
+__global__ __launch_bounds__(kThreads) void emb_scatter_kernel(SortArgs a, int p, ZeroArgs zero) {
+    if ((int)blockIdx.x >= zero.first) {
+        zero_share(zero, 2 * p + 1, 2 * a.passes);
+        return;
+    }
     __shared__ uint32_t cnt[4][kBins];
     __shared__ uint32_t tmp[4];
     const int t = threadIdx.x, w = t >> 6, lane = t & 63;
@@ -202,8 +250,8 @@ __global__ __launch_bounds__(kThreads) void emb_scatter_kernel(SortArgs a, int p
     __syncthreads();
     for (int64_t n = lo + lane; n < hi; n += 64) atomicAdd(&cnt[w][(key_at(a, p, n) >> (8 * p)) & 255u], 1u);
     uint32_t before = 0, total = 0;
-#pragma unroll 8
-    for (int g = 0; g < (int)gridDim.x; ++g) {
+#pragma unroll 16
+    for (int g = 0; g < zero.first; ++g) {
         const uint32_t c = a.hist[(int64_t)g * kBins + t];
         total += c;
         before += g < (int)blockIdx.x ? c : 0u;
@@ -239,44 +287,13 @@ struct EmbSumArgs {
     void *out;
     float *part;     // [chunks][2][D]: sums of a run that came from the chunk before, of one that goes on
     int run;         // sorted positions a chunk (at most 64)
-    int64_t chunks, cols;      // column blocks of 64 * V
-    int64_t sum_blocks;        // workgroups of the sums; the others write zero rows
+    int64_t chunks, cols;  // column blocks of 64 * V (of 64 in the join)
 };
 
 constexpr int kBatch = 8;  // rows whose loads are in flight
 
 template <typename T, int V>
-__device__ __forceinline__ void emb_zero_rows(const EmbSumArgs &a, int64_t block) {
-    // a wave takes 64 table rows: each lane looks for its row among the
-    // sorted ids, then the wave writes the rows that no id names
-    const int lane = threadIdx.x & 63;
-    const int64_t row0 = (block * 4 + (threadIdx.x >> 6)) * 64;
-    if (row0 >= a.V) return;
-    const int64_t row = row0 + lane;
-    int64_t lo = 0, hi = a.N;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if ((int64_t)a.key[mid] < row) lo = mid + 1;
-        else hi = mid;
-    }
-    const bool named = lo < a.N && (int64_t)a.key[lo] == row && row != a.pad;
-    uint64_t empty = __ballot(row < a.V && !named);
-    float z[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) z[i] = 0.0f;
-    while (empty != 0) {
-        const int r = __ffsll((unsigned long long)empty) - 1;
-        empty &= empty - 1;
-        for (int c = lane * V; c < a.D; c += 64 * V) store_vec<T, V>(static_cast<T *>(a.out) + (row0 + r) * a.D + c, z);
-    }
-}
-
-template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void emb_sum_kernel(EmbSumArgs a) {
-    if ((int64_t)blockIdx.x >= a.sum_blocks) {
-        emb_zero_rows<T, V>(a, (int64_t)blockIdx.x - a.sum_blocks);
-        return;
-    }
     const int lane = threadIdx.x & 63;
     const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (item >= a.chunks * a.cols) return;
@@ -359,7 +376,7 @@ __global__ __launch_bounds__(kThreads) void emb_join_kernel(EmbSumArgs a) {
     const int64_t last = (lo - 1) / a.run;
     if (c >= a.D) return;
     float acc = a.part[(chunk * 2 + 1) * a.D + c];
-#pragma unroll 8
+#pragma unroll 16
     for (int64_t q = chunk + 1; q <= last; ++q) acc += a.part[q * 2 * a.D + c];
     static_cast<T *>(a.out)[(int64_t)k * a.D + c] = (T)(acc * a.scale);
 }
@@ -379,7 +396,7 @@ EmbWs emb_ws(int64_t N, int64_t D) {
         return at;
     };
     const bool small = N <= kSmallN;
-    w.tile = std::max<int64_t>(2048, ((N + kMaxTiles - 1) / kMaxTiles + 255) / 256 * 256);
+    w.tile = std::max<int64_t>(1024, ((N + kMaxTiles - 1) / kMaxTiles + 255) / 256 * 256);
     w.tiles = (int)((N + w.tile - 1) / w.tile);
     w.run = N <= 16384 ? 16 : 64;
     w.chunks = (N + w.run - 1) / w.run;
@@ -396,9 +413,7 @@ EmbWs emb_ws(int64_t N, int64_t D) {
 template <typename T, int V>
 hipError_t emb_sums(EmbSumArgs &a, hipStream_t s) {
     a.cols = (a.D + 64 * V - 1) / (64 * V);
-    a.sum_blocks = (a.chunks * a.cols + 3) / 4;
-    const int64_t zero = (a.V + 255) / 256;
-    emb_sum_kernel<T, V><<<(unsigned)(a.sum_blocks + zero), kThreads, 0, s>>>(a);
+    emb_sum_kernel<T, V><<<(unsigned)((a.chunks * a.cols + 3) / 4), kThreads, 0, s>>>(a);
     a.cols = (a.D + 63) / 64;
     emb_join_kernel<T><<<(unsigned)((a.chunks * a.cols + 3) / 4), kThreads, 0, s>>>(a);
     return hipGetLastError();
@@ -442,18 +457,21 @@ hipError_t embedding_backward(const EmbeddingArgs &q, const Ws &ws, hipStream_t 
     }
     o.passes = 1;
     while (o.passes < 4 && (q.V >> (8 * o.passes)) != 0) ++o.passes;  // V itself is a key
+    ZeroArgs zero{static_cast<char *>(q.out), q.V * q.D * (q.bf16 ? 2 : 4), w.tiles};
+    const int blocks = (int)std::min<int64_t>((zero.bytes + 16383) / 16384, kZeroBlocks);
     int at = 0;
     if (q.N <= kSmallN) {
-        emb_sort_small_kernel<<<1, kSmallThreads, 0, s>>>(o);
+        zero.first = 1;
+        emb_sort_small_kernel<<<1 + blocks, kSmallThreads, 0, s>>>(o, zero);
     } else {
         for (int p = 0; p < o.passes; ++p) {
-            emb_hist_kernel<<<w.tiles, kThreads, 0, s>>>(o, p);
-            emb_scatter_kernel<<<w.tiles, kThreads, 0, s>>>(o, p);
+            emb_hist_kernel<<<w.tiles + blocks, kThreads, 0, s>>>(o, p, zero);
+            emb_scatter_kernel<<<w.tiles + blocks, kThreads, 0, s>>>(o, p, zero);
         }
         at = (o.passes - 1) & 1;
     }
     EmbSumArgs a{q.N, q.V, q.padding, (int)q.D, o.key[at], o.pos[at], q.table, q.scale, q.out,
-                 reinterpret_cast<float *>(ws.p + w.part), w.run, w.chunks, 0, 0};
+                 reinterpret_cast<float *>(ws.p + w.part), w.run, w.chunks, 0};
     const int vec = q.bf16 ? 8 : 4;
     const bool al = q.D % vec == 0 && aligned16(q.table) && aligned16(q.out);
     if (q.bf16) return al ? emb_sums<bf16, 8>(a, s) : emb_sums<bf16, 1>(a, s);

@@ -22,15 +22,21 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sum over the W waves that share a row; buf holds one float a wave, and
-// alternates between calls (`half`) so that one barrier per sum is enough.
+// Sums over the W waves that share a row.  buf holds a pair a wave, and
+// alternates between calls (`half`) so that one barrier a call is enough.
 template <int W>
-__device__ __forceinline__ float row_sum(float v, float (&buf)[2][4], int half) {
-    v = wave_sum(v);
-    if (W == 1) return v;
-    if ((threadIdx.x & 63) == 0) buf[half][threadIdx.x >> 6] = v;
+__device__ __forceinline__ float2 row_sums(float a, float b, float2 (&buf)[2][4], int half) {
+    a = lanes_sum(a);
+    b = lanes_sum(b);
+    if (W == 1) return make_float2(a, b);
+    if ((threadIdx.x & 63) == 0) buf[half][threadIdx.x >> 6] = make_float2(a, b);
     __syncthreads();
-    return (buf[half][0] + buf[half][1]) + (buf[half][2] + buf[half][3]);
+    const float2 p = buf[half][0], q = buf[half][1], r = buf[half][2], t = buf[half][3];
+    return make_float2((p.x + q.x) + (r.x + t.x), (p.y + q.y) + (r.y + t.y));
+}
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float2 (&buf)[2][4], int half) {
+    return row_sums<W>(v, 0.0f, buf, half).x;
 }
 
 struct LnFwdArgs {
@@ -46,7 +52,7 @@ struct LnFwdArgs {
 template <typename T, int V, int W, int E>
 __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
     constexpr int NV = E / V, kRows = 4 / W;
-    __shared__ float buf[2][4];
+    __shared__ float2 buf[2][4];
     const int li = W == 1 ? (threadIdx.x & 63) : threadIdx.x;
     const int64_t step = (int64_t)gridDim.x * kRows;
     const float n = (float)a.D;
@@ -112,7 +118,7 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
 // Rows too long for the registers: one workgroup a row, read three times.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ln_fwd_long_kernel(LnFwdArgs a) {
-    __shared__ float buf[2][4];
+    __shared__ float2 buf[2][4];
     const float n = (float)a.D;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         const int64_t base = row * a.D;
@@ -157,58 +163,81 @@ struct LnBwdArgs {
     float *part;  // [gridDim.x][2][D] partial dw, db, or null
 };
 
+// The workgroups keep their columns' dw and db in registers over all their
+// rows, so there are only as many partial sums as workgroups; the few waves
+// that leaves on a CU keep memory busy by loading a row ahead.
 template <typename T, int V, int W, int E>
 __global__ __launch_bounds__(kThreads) void ln_bwd_kernel(LnBwdArgs a) {
     constexpr int NV = E / V, kRows = 4 / W;
-    __shared__ float buf[2][4], buf2[2][4];
+    __shared__ float2 buf[2][4];
     __shared__ float comb[W == 1 ? 3 * 64 * V : 1];
     const int li = W == 1 ? (threadIdx.x & 63) : threadIdx.x;
     const int64_t step = (int64_t)gridDim.x * kRows;
     const float n = (float)a.D;
-    float gw[NV][V], gb[NV][V];
+    const T *s = static_cast<const T *>(a.s), *dy = static_cast<const T *>(a.dy), *ds = static_cast<const T *>(a.ds);
+    float w[NV][V], gw[NV][V], gb[NV][V];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) gw[j][i] = gb[j][i] = 0.0f;
-    int half = 0;
-    for (int64_t row = (int64_t)blockIdx.x * kRows + (W == 1 ? threadIdx.x >> 6 : 0); row < a.rows; row += step) {
-        const int64_t base = row * a.D;
-        const float mu = a.mean[row], rstd = a.rstd[row];
+        for (int i = 0; i < V; ++i) {
+            const int c = (li + j * 64 * W) * V + i;
+            w[j][i] = c < a.D ? (a.w != nullptr ? a.w[c] : 1.0f) : 0.0f;
+            gw[j][i] = gb[j][i] = 0.0f;
+        }
+    struct Row {
+        VecT<T, V> s[NV], dy[NV], ds[NV];
+        float mu, rstd;
+    };
+    Row next;
+    auto load = [&](int64_t row) {
+        next.mu = a.mean[row];
+        next.rstd = a.rstd[row];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (li + j * 64 * W) * V;
+            if (c < a.D) {
+                const int64_t at = row * a.D + c;
+                next.s[j] = *reinterpret_cast<const VecT<T, V> *>(s + at);
+                next.dy[j] = *reinterpret_cast<const VecT<T, V> *>(dy + at);
+                if (ds != nullptr) next.ds[j] = *reinterpret_cast<const VecT<T, V> *>(ds + at);
+            }
+        }
+    };
+    int64_t row = (int64_t)blockIdx.x * kRows + (W == 1 ? threadIdx.x >> 6 : 0);
+    if (row < a.rows) load(row);
+    for (int half = 0; row < a.rows; row += step, half ^= 1) {
+        const Row cur = next;
+        if (row + step < a.rows) load(row + step);
         float xh[NV][V], g[NV][V];
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (li + j * 64 * W) * V;
             if (c < a.D) {
-                load_vec<T, V>(static_cast<const T *>(a.s) + base + c, xh[j]);
-                load_vec<T, V>(static_cast<const T *>(a.dy) + base + c, g[j]);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    xh[j][i] = (xh[j][i] - mu) * rstd;
-                    gw[j][i] = fmaf(g[j][i], xh[j][i], gw[j][i]);
-                    gb[j][i] += g[j][i];
-                    g[j][i] *= a.w != nullptr ? a.w[c + i] : 1.0f;
+                    const float d = (float)cur.dy[j].v[i];
+                    xh[j][i] = ((float)cur.s[j].v[i] - cur.mu) * cur.rstd;
+                    gw[j][i] = fmaf(d, xh[j][i], gw[j][i]);
+                    gb[j][i] += d;
+                    g[j][i] = d * w[j][i];
                     s1 += g[j][i];
                     s2 = fmaf(g[j][i], xh[j][i], s2);
                 }
             }
         }
-        const float c1 = row_sum<W>(s1, buf, half) / n;
-        const float c2 = row_sum<W>(s2, buf2, half) / n;
-        half ^= 1;
+        const float2 sums = row_sums<W>(s1, s2, buf, half);
+        const float c1 = sums.x / n, c2 = sums.y / n;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (li + j * 64 * W) * V;
             if (c < a.D) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) g[j][i] = rstd * (g[j][i] - fmaf(xh[j][i], c2, c1));
-                if (a.ds != nullptr) {
-                    float r[V];
-                    load_vec<T, V>(static_cast<const T *>(a.ds) + base + c, r);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) g[j][i] += r[i];
+                for (int i = 0; i < V; ++i) {
+                    g[j][i] = cur.rstd * (g[j][i] - fmaf(xh[j][i], c2, c1));
+                    if (ds != nullptr) g[j][i] += (float)cur.ds[j].v[i];
                 }
-                store_vec<T, V>(static_cast<T *>(a.dx) + base + c, g[j]);
+                store_vec<T, V>(static_cast<T *>(a.dx) + row * a.D + c, g[j]);
             }
         }
     }
@@ -244,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_kernel(LnBwdArgs a) {
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ln_bwd_long_kernel(LnBwdArgs a) {
-    __shared__ float buf[2][4], buf2[2][4];
+    __shared__ float2 buf[2][4];
     const float n = (float)a.D;
     int half = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -259,8 +288,8 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_long_kernel(LnBwdArgs a) {
             s1 += g;
             s2 = fmaf(g, ((float)s[c] - mu) * rstd, s2);
         }
-        const float c1 = row_sum<4>(s1, buf, half) / n;
-        const float c2 = row_sum<4>(s2, buf2, half) / n;
+        const float2 c = row_sums<4>(s1, s2, buf, half);
+        const float c1 = c.x / n, c2 = c.y / n;
         half ^= 1;
         for (int c = threadIdx.x; c < a.D; c += kThreads) {
             const float g = (float)dy[c] * (a.w != nullptr ? a.w[c] : 1.0f);
@@ -309,7 +338,7 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_short_kernel(LnBwdArgs a) {
 #pragma unroll
     for (int i = 0; i < 2 * kShortRow; ++i) {
         const int c = i >> 1;
-        const float v = wave_sum(i & 1 ? gb[c] : gw[c]);
+        const float v = lanes_sum(i & 1 ? gb[c] : gw[c]);
         if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
         __syncthreads();
         if (threadIdx.x == 0 && c < a.D) part[(i & 1) * a.D + c] = (buf[0] + buf[1]) + (buf[2] + buf[3]);

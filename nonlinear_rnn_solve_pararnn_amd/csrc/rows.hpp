@@ -36,4 +36,20 @@ __device__ __forceinline__ void store_vec(T *p, const float (&f)[V]) {
     *reinterpret_cast<VecT<T, V> *>(p) = x;
 }
 
+// Sum over the 64 lanes of a wave, in every lane: neighbours within rows of
+// 16, then across rows, on the vector unit (no LDS traffic).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float add_dpp(float v) {
+    return v + __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, ROWS, 0xf, false));
+}
+__device__ __forceinline__ float lanes_sum(float v) {
+    v = add_dpp<0x111, 0xf>(v);  // row_shr:1
+    v = add_dpp<0x112, 0xf>(v);  // row_shr:2
+    v = add_dpp<0x114, 0xf>(v);  // row_shr:4
+    v = add_dpp<0x118, 0xf>(v);  // row_shr:8: lane 15 of a row has the row's sum
+    v = add_dpp<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
+    v = add_dpp<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
 }  // namespace prn
