@@ -73,7 +73,9 @@ __global__ __launch_bounds__(kThreads) void emb_lookup_kernel(EmbFwdArgs a) {
 // Every row of the gradient is cleared while the ids are sorted (a share in
 // each launch of the sort, by workgroups of their own): the sort has work for
 // few CUs, and rows that no id names need no search.  Named rows are written
-// twice for that, at most N of V + N.
+// twice for that, at most N of V + N.  The stores are streamed: kept in the
+// caches as ordinary ones are, their way to memory costs the sums that follow
+// (65536 x 2048 bf16: 93 us instead of 78).
 struct ZeroArgs {
     char *out;
     int64_t bytes;
@@ -84,11 +86,17 @@ constexpr int kZeroBlocks = 1024;
 __device__ __forceinline__ void zero_share(const ZeroArgs &z, int share, int shares) {
     // 16-byte pieces [lo, hi) of this share; the first also takes what is left at either end
     const int64_t head = min(z.bytes, (int64_t)((16 - ((uintptr_t)z.out & 15)) & 15)), whole = (z.bytes - head) / 16;
-    uint4 *v = reinterpret_cast<uint4 *>(z.out + head);
+    u32x4 *v = reinterpret_cast<u32x4 *>(z.out + head);
+    const u32x4 zero = {0u, 0u, 0u, 0u};
     const int64_t lo = whole * share / shares, hi = whole * (share + 1) / shares;
     const int64_t me = (int64_t)((int)blockIdx.x - z.first) * blockDim.x + threadIdx.x;
     const int64_t all = (int64_t)((int)gridDim.x - z.first) * blockDim.x;
-    for (int64_t i = lo + me; i < hi; i += all) v[i] = make_uint4(0u, 0u, 0u, 0u);
+    int64_t i = lo + me;
+    for (; i + 3 * all < hi; i += 4 * all) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) __builtin_nontemporal_store(zero, v + i + u * all);
+    }
+    for (; i < hi; i += all) __builtin_nontemporal_store(zero, v + i);
     if (share == 0) {
         if (me < head) z.out[me] = 0;
         if (me < z.bytes - head - whole * 16) z.out[head + whole * 16 + me] = 0;
@@ -97,7 +105,7 @@ __device__ __forceinline__ void zero_share(const ZeroArgs &z, int share, int sha
 
 // ---------------------------------------------------------------- sort
 constexpr int kBins = 256;          // 8 bits of the key a pass
-constexpr int kSmallN = 8192;       // sorted by one workgroup in LDS
+constexpr int kSmallN = 2048;       // sorted by one workgroup in LDS
 constexpr int kSmallThreads = 1024;
 constexpr int kMaxTiles = 128;      // workgroups of a pass over a longer list
 
@@ -110,18 +118,6 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t d, bool valid) {
         m &= ((d >> b) & 1u) ? one : ~one;
     }
     return m;
-}
-
-// Place of this lane's element among those of its digit: the wave's counter
-// of the digit, advanced by the wave's elements, plus the lanes before it.
-__device__ __forceinline__ uint32_t take_place(uint32_t *counter, uint32_t d, bool valid) {
-    const uint64_t m = same_digit(d, valid);
-    const int lane = threadIdx.x & 63;
-    const int first = valid ? __ffsll((unsigned long long)m) - 1 : lane;
-    uint32_t base = 0;
-    if (valid && lane == first) base = atomicAdd(&counter[d], (uint32_t)__popcll(m));
-    base = __shfl(base, first, 64);
-    return base + (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
 }
 
 // Exclusive sum of one value per thread over the first 256 threads of a
@@ -151,66 +147,97 @@ struct SortArgs {
     int64_t tile;    // elements a workgroup (a multiple of 256)
 };
 
+// A wave's places for up to U groups of 64 elements in their order: the
+// counters' additions of one wave are done in the order they are issued, so
+// none waits for the one before it.
+template <int U>
+__device__ __forceinline__ void take_places(uint32_t *counter, const uint32_t (&d)[U], int count, uint32_t (&to)[U]) {
+    const int lane = threadIdx.x & 63;
+    uint64_t same[U];
+    uint32_t base[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const bool valid = u * 64 + lane < count;
+        same[u] = same_digit(d[u], valid);
+        base[u] = 0;
+        if (valid && lane == __ffsll((unsigned long long)same[u]) - 1) base[u] = atomicAdd(&counter[d[u]], (uint32_t)__popcll(same[u]));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int first = same[u] != 0 ? __ffsll((unsigned long long)same[u]) - 1 : lane;
+        to[u] = __shfl(base[u], first, 64) + (uint32_t)__popcll(same[u] & ((1ull << lane) - 1ull));
+    }
+}
+
+// The whole list in one workgroup: wave w keeps the elements [w per, (w + 1) per) in order.
 __global__ __launch_bounds__(kSmallThreads) void emb_sort_small_kernel(SortArgs a, ZeroArgs zero) {
     if ((int)blockIdx.x >= zero.first) {
         zero_share(zero, 0, 1);
         return;
     }
-    __shared__ uint32_t key[2][kSmallN];
-    __shared__ uint16_t pos[2][kSmallN];
-    __shared__ uint32_t cnt[16][kBins];
+    constexpr int U = kSmallN / kSmallThreads, NW = kSmallThreads / 64;
+    __shared__ uint32_t key[kSmallN];
+    __shared__ uint16_t pos[kSmallN];
+    __shared__ uint32_t cnt[NW][kBins];
     __shared__ uint32_t tmp[4];
     const int t = threadIdx.x, w = t >> 6, lane = t & 63;
     const int N = (int)a.N;
-    const int per = (N + 1023) / 1024 * 64;  // elements a wave
-    uint32_t own[kSmallN / kSmallThreads];
+    const int per = (N + kSmallThreads - 1) / kSmallThreads * 64, lo = w * per, count = max(0, min(N - lo, per));
+    uint32_t k[U], d[U], to[U];
+    uint16_t q[U];
 #pragma unroll
-    for (int u = 0; u < kSmallN / kSmallThreads; ++u) {
-        const int n = t + u * kSmallThreads;
-        own[u] = n < N ? id_key(a.ids, a.wide, n, a.V) : 0u;
+    for (int u = 0; u < U; ++u) {
+        const int n = u * 64 + lane;
+        k[u] = n < count ? id_key(a.ids, a.wide, lo + n, a.V) : 0u;
+        q[u] = (uint16_t)(lo + n);
     }
-#pragma unroll
-    for (int u = 0; u < kSmallN / kSmallThreads; ++u) {
-        const int n = t + u * kSmallThreads;
-        if (n < N) {
-            key[0][n] = own[u];
-            pos[0][n] = (uint16_t)n;
-        }
-    }
-    int cur = 0;
     for (int p = 0; p < a.passes; ++p) {
-        for (int i = t; i < 16 * kBins; i += kSmallThreads) cnt[i / kBins][i % kBins] = 0;
+#pragma unroll
+        for (int i = 0; i < NW * kBins / kSmallThreads; ++i) (&cnt[0][0])[t + i * kSmallThreads] = 0;
+        if (p > 0)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u * 64 + lane < count) {
+                    k[u] = key[lo + u * 64 + lane];
+                    q[u] = pos[lo + u * 64 + lane];
+                }
         __syncthreads();
-        const int lo = w * per, hi = min(N, lo + per);
-        for (int n = lo + lane; n < hi; n += 64) atomicAdd(&cnt[w][(key[cur][n] >> (8 * p)) & 255u], 1u);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            d[u] = (k[u] >> (8 * p)) & 255u;
+            if (u * 64 + lane < count) atomicAdd(&cnt[w][d[u]], 1u);
+        }
         __syncthreads();
-        uint32_t total = 0;
+        uint32_t c[NW], total = 0;
         if (t < kBins)
-            for (int v = 0; v < 16; ++v) total += cnt[v][t];
+#pragma unroll
+            for (int v = 0; v < NW; ++v) c[v] = cnt[v][t];
+#pragma unroll
+        for (int v = 0; v < NW; ++v) total += t < kBins ? c[v] : 0u;
         uint32_t run = scan256(total, tmp);
         if (t < kBins)
-            for (int v = 0; v < 16; ++v) {
-                const uint32_t c = cnt[v][t];
+#pragma unroll
+            for (int v = 0; v < NW; ++v) {
                 cnt[v][t] = run;
-                run += c;
+                run += c[v];
             }
         __syncthreads();
-        for (int n0 = lo; n0 < hi; n0 += 64) {
-            const int n = n0 + lane;
-            const bool valid = n < hi;
-            const uint32_t k = valid ? key[cur][n] : 0u;
-            const uint32_t to = take_place(cnt[w], (k >> (8 * p)) & 255u, valid);
-            if (valid) {
-                key[cur ^ 1][to] = k;
-                pos[cur ^ 1][to] = pos[cur][n];
+        take_places<U>(cnt[w], d, count, to);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u * 64 + lane < count) {
+                key[to[u]] = k[u];
+                pos[to[u]] = q[u];
             }
-        }
-        cur ^= 1;
         __syncthreads();
     }
-    for (int n = t; n < N; n += kSmallThreads) {
-        a.key[0][n] = key[cur][n];
-        a.pos[0][n] = pos[cur][n];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int n = t + u * kSmallThreads;
+        if (n < N) {
+            a.key[0][n] = key[n];
+            a.pos[0][n] = pos[n];
+        }
     }
 }
 
@@ -264,16 +291,25 @@ __global__ __launch_bounds__(kThreads) void emb_scatter_kernel(SortArgs a, int p
         run += c;
     }
     __syncthreads();
-    for (int64_t n0 = lo; n0 < hi; n0 += 64) {
-        const int64_t n = n0 + lane;
-        const bool valid = n < hi;
-        const uint32_t k = valid ? key_at(a, p, n) : 0u;
-        const uint32_t pos = p == 0 ? (uint32_t)n : (valid ? a.pos[(p - 1) & 1][n] : 0u);
-        const uint32_t to = take_place(cnt[w], (k >> (8 * p)) & 255u, valid);
-        if (valid) {
-            a.key[p & 1][to] = k;
-            a.pos[p & 1][to] = pos;
+    constexpr int U = 4;
+    for (int64_t n0 = lo; n0 < hi; n0 += U * 64) {
+        const int count = (int)min(hi - n0, (int64_t)U * 64);
+        uint32_t k[U], q[U], d[U], to[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t n = n0 + u * 64 + lane;
+            const bool valid = u * 64 + lane < count;
+            k[u] = valid ? key_at(a, p, n) : 0u;
+            q[u] = p == 0 ? (uint32_t)n : (valid ? a.pos[(p - 1) & 1][n] : 0u);
+            d[u] = (k[u] >> (8 * p)) & 255u;
         }
+        take_places<U>(cnt[w], d, count, to);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u * 64 + lane < count) {
+                a.key[p & 1][to[u]] = k[u];
+                a.pos[p & 1][to[u]] = q[u];
+            }
     }
 }
 
@@ -287,10 +323,11 @@ struct EmbSumArgs {
     void *out;
     float *part;     // [chunks][2][D]: sums of a run that came from the chunk before, of one that goes on
     int run;         // sorted positions a chunk (at most 64)
-    int64_t chunks, cols;  // column blocks of 64 * V (of 64 in the join)
+    int64_t chunks, cols;  // column blocks of 64 * V
 };
 
-constexpr int kBatch = 8;  // rows whose loads are in flight
+constexpr int kBatch = 8;         // rows whose loads are in flight
+constexpr uint32_t kNoKey = ~0u;  // above every key
 
 template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void emb_sum_kernel(EmbSumArgs a) {
@@ -302,9 +339,8 @@ __global__ __launch_bounds__(kThreads) void emb_sum_kernel(EmbSumArgs a) {
     const int64_t n0 = chunk * a.run;
     const int cnt = (int)min((int64_t)a.run, a.N - n0);
     const uint32_t mykey = a.key[n0 + min(lane, cnt - 1)], mypos = a.pos[n0 + min(lane, cnt - 1)];
-    const uint32_t none = 0xffffffffu;  // above every key
-    const uint32_t prev = n0 > 0 ? a.key[n0 - 1] : none;
-    const uint32_t next = n0 + cnt < a.N ? a.key[n0 + cnt] : none;
+    const uint32_t prev = n0 > 0 ? a.key[n0 - 1] : kNoKey;
+    const uint32_t next = n0 + cnt < a.N ? a.key[n0 + cnt] : kNoKey;
     const bool in = c < a.D;
     float acc[V];
 #pragma unroll
@@ -332,8 +368,8 @@ __global__ __launch_bounds__(kThreads) void emb_sum_kernel(EmbSumArgs a) {
         float f[kBatch][V];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int64_t at = (int64_t)__builtin_amdgcn_readlane(mypos, min(b + u, cnt - 1));
-            if (in) load_vec<T, V>(static_cast<const T *>(a.grad) + at * a.D + c, f[u]);
+            const int64_t row = (int64_t)__builtin_amdgcn_readlane(mypos, min(b + u, cnt - 1));
+            if (in) load_vec<T, V>(static_cast<const T *>(a.grad) + row * a.D + c, f[u]);
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
@@ -354,31 +390,47 @@ __global__ __launch_bounds__(kThreads) void emb_sum_kernel(EmbSumArgs a) {
 }
 
 // Runs that cross chunks: the wave of the chunk where such a run begins adds
-// its partial sums in order.
-template <typename T>
+// its partial sums in order, V columns a lane.
+template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void emb_join_kernel(EmbSumArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (item >= a.chunks * a.cols) return;
     const int64_t chunk = item / a.cols;
-    const int c = (int)(item - chunk * a.cols) * 64 + lane;
+    const int c = (int)(item - chunk * a.cols) * 64 * V + lane * V;
     const int64_t n0 = chunk * a.run, n1 = n0 + a.run;  // n1: the next chunk's first position
     if (n1 >= a.N) return;
-    const uint32_t k = a.key[n1];
-    if (a.key[n1 - 1] != k || k >= (uint32_t)a.V || (int64_t)k == a.pad) return;
-    if (a.key[n0] == k && n0 > 0 && a.key[n0 - 1] == k) return;  // begins earlier
-    int64_t lo = n1, hi = a.N;  // the first position past the run
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (a.key[mid] <= k) lo = mid + 1;
-        else hi = mid;
+    const uint32_t k = a.key[n1], end = a.key[n1 - 1], begin = a.key[n0], before = n0 > 0 ? a.key[n0 - 1] : kNoKey;
+    if (end != k || k >= (uint32_t)a.V || (int64_t)k == a.pad) return;
+    if (begin == k && before == k) return;  // the run begins earlier
+    int64_t past = chunk + 1;  // the first chunk that does not begin with the run's id
+    while (true) {
+        const int64_t q = past + lane;
+        const uint64_t ends = __ballot(q >= a.chunks || a.key[min(q, a.chunks - 1) * a.run] != k);
+        if (ends != 0) {
+            past += __ffsll((unsigned long long)ends) - 1;
+            break;
+        }
+        past += 64;
     }
-    const int64_t last = (lo - 1) / a.run;
     if (c >= a.D) return;
-    float acc = a.part[(chunk * 2 + 1) * a.D + c];
-#pragma unroll 16
-    for (int64_t q = chunk + 1; q <= last; ++q) acc += a.part[q * 2 * a.D + c];
-    static_cast<T *>(a.out)[(int64_t)k * a.D + c] = (T)(acc * a.scale);
+    float acc[V];
+    load_vec<float, V>(a.part + (chunk * 2 + 1) * a.D + c, acc);
+    constexpr int U = 8;
+    for (int64_t q0 = chunk + 1; q0 < past; q0 += U) {
+        float f[U][V];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (q0 + u < past) load_vec<float, V>(a.part + (q0 + u) * 2 * a.D + c, f[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (q0 + u < past)
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] += f[u][i];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] *= a.scale;
+    store_vec<T, V>(static_cast<T *>(a.out) + (int64_t)k * a.D + c, acc);
 }
 
 // Layout of the gradient's scratch.
@@ -396,9 +448,13 @@ EmbWs emb_ws(int64_t N, int64_t D) {
         return at;
     };
     const bool small = N <= kSmallN;
-    w.tile = std::max<int64_t>(1024, ((N + kMaxTiles - 1) / kMaxTiles + 255) / 256 * 256);
+    w.tile = std::max<int64_t>(512, ((N + kMaxTiles - 1) / kMaxTiles + 255) / 256 * 256);
     w.tiles = (int)((N + w.tile - 1) / w.tile);
-    w.run = N <= 16384 ? 16 : 64;
+    // chunks of up to 64 entries (one a lane), shorter where the sums would not
+    // fill the CUs (65536 x 2048 bf16: 64 entries 91 us + 10 us for the joins,
+    // 32 entries 94 + 17)
+    const int64_t per_cu = N * ((D + 511) / 512) / (4 * device_cu_count());
+    w.run = per_cu >= 64 ? 64 : per_cu >= 32 ? 32 : 16;
     w.chunks = (N + w.run - 1) / w.run;
     for (int i = 0; i < 2; ++i) {
         w.key[i] = i == 0 || !small ? take((size_t)N * 4) : w.key[0];
@@ -414,8 +470,9 @@ template <typename T, int V>
 hipError_t emb_sums(EmbSumArgs &a, hipStream_t s) {
     a.cols = (a.D + 64 * V - 1) / (64 * V);
     emb_sum_kernel<T, V><<<(unsigned)((a.chunks * a.cols + 3) / 4), kThreads, 0, s>>>(a);
-    a.cols = (a.D + 63) / 64;
-    emb_join_kernel<T><<<(unsigned)((a.chunks * a.cols + 3) / 4), kThreads, 0, s>>>(a);
+    constexpr int J = V == 1 ? 1 : 4;
+    a.cols = (a.D + 64 * J - 1) / (64 * J);
+    emb_join_kernel<T, J><<<(unsigned)((a.chunks * a.cols + 3) / 4), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -461,8 +518,8 @@ hipError_t embedding_backward(const EmbeddingArgs &q, const Ws &ws, hipStream_t 
     const int blocks = (int)std::min<int64_t>((zero.bytes + 16383) / 16384, kZeroBlocks);
     int at = 0;
     if (q.N <= kSmallN) {
-        zero.first = 1;
-        emb_sort_small_kernel<<<1 + blocks, kSmallThreads, 0, s>>>(o, zero);
+        zero.first = 1;  // a workgroup here fills a CU
+        emb_sort_small_kernel<<<1 + std::min(blocks, device_cu_count() - 1), kSmallThreads, 0, s>>>(o, zero);
     } else {
         for (int p = 0; p < o.passes; ++p) {
             emb_hist_kernel<<<w.tiles + blocks, kThreads, 0, s>>>(o, p, zero);

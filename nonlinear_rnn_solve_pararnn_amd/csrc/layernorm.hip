@@ -64,12 +64,13 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
         for (int j = 0; j < NV; ++j) {
             const int c = (li + j * 64 * W) * V;
             if (c < a.D) {
-                load_vec<T, V>(static_cast<const T *>(a.x) + base + c, f[j]);
-                if (a.res != nullptr) {
-                    float r[V];
-                    load_vec<T, V>(static_cast<const T *>(a.res) + base + c, r);
+                const VecT<T, V> x = load_once<T, V>(static_cast<const T *>(a.x) + base + c);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) f[j][i] = (float)(T)(f[j][i] + r[i]);
+                for (int i = 0; i < V; ++i) f[j][i] = (float)x.v[i];
+                if (a.res != nullptr) {
+                    const VecT<T, V> r = load_once<T, V>(static_cast<const T *>(a.res) + base + c);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) f[j][i] = (float)(T)(f[j][i] + (float)r.v[i]);
                     store_vec<T, V>(static_cast<T *>(a.s) + base + c, f[j]);
                 }
             } else {
@@ -197,9 +198,9 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_kernel(LnBwdArgs a) {
             const int c = (li + j * 64 * W) * V;
             if (c < a.D) {
                 const int64_t at = row * a.D + c;
-                next.s[j] = *reinterpret_cast<const VecT<T, V> *>(s + at);
-                next.dy[j] = *reinterpret_cast<const VecT<T, V> *>(dy + at);
-                if (ds != nullptr) next.ds[j] = *reinterpret_cast<const VecT<T, V> *>(ds + at);
+                next.s[j] = load_once<T, V>(s + at);
+                next.dy[j] = load_once<T, V>(dy + at);
+                if (ds != nullptr) next.ds[j] = load_once<T, V>(ds + at);
             }
         }
     };
@@ -388,7 +389,7 @@ __global__ __launch_bounds__(1024) void ln_reduce_kernel(const float *part, int 
 
 template <typename T, int V>
 void ln_fwd_launch(const LnFwdArgs &a, hipStream_t s) {
-    const int64_t cap = (int64_t)device_cu_count() * 8;
+    const int64_t cap = (int64_t)1 << 30;
     const int g1 = (int)std::min<int64_t>((a.rows + 3) / 4, cap), g4 = (int)std::min<int64_t>(a.rows, cap);
     if (a.D <= 512) ln_fwd_kernel<T, V, 1, 8><<<g1, kThreads, 0, s>>>(a);
     else if (a.D <= 1024) ln_fwd_kernel<T, V, 1, 16><<<g1, kThreads, 0, s>>>(a);

@@ -27,6 +27,21 @@ __device__ __forceinline__ void load_vec(const T *p, float (&f)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = (float)x.v[i];
 }
+// Elements that a launch reads exactly once (streamed past the caches, like
+// ld_once); 16-byte vectors, ordinary loads of single elements.
+template <typename T, int V>
+__device__ __forceinline__ VecT<T, V> load_once(const T *p) {
+    if constexpr (sizeof(T) * V == 16) {
+        union {
+            u32x4 w;
+            VecT<T, V> v;
+        } x;
+        x.w = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+        return x.v;
+    } else {
+        return *reinterpret_cast<const VecT<T, V> *>(p);
+    }
+}
 // Rounds to T (bf16: to nearest, ties to even).
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T *p, const float (&f)[V]) {
