@@ -167,13 +167,18 @@ def _workspace(op, B, L, H, device, max_iter=1, ws=None):
     return _workspace_of(n, device, ws)
 
 
+def _raw_stream(device: torch.device) -> int:
+    """The device's current HIP stream as an integer (a stream object costs more than a small kernel's launch)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _workspace_of(n: int, device, ws=None):
     """The caller's workspace if one is given, else the stream's, of at least n bytes."""
     if ws is not None:
         if ws.device != device or ws.numel() * ws.element_size() < n or ws.data_ptr() % 256:
             raise ValueError("workspace too small, misaligned or on the wrong device")
         return ws, ws.numel() * ws.element_size()
-    key = (device, torch.cuda.current_stream(device).cuda_stream)
+    key = (device, _raw_stream(device))
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < n:
         buf = new_workspace(n, device)
@@ -506,6 +511,10 @@ _DTYPES = {torch.float32: 0, torch.bfloat16: 1}   # PARARNN_F32, PARARNN_BF16
 MAX_HEAD_DIM = 256
 
 
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _type_code(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
@@ -537,11 +546,11 @@ def _linattn_views(tensors, shapes, names, dtype, device):
     for t, shape, name in zip(tensors, shapes, names):
         if not isinstance(t, torch.Tensor):
             raise TypeError("%s must be a torch.Tensor" % name)
-        if t.dtype != dtype:
-            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-        if t.device != device:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-        if t.shape != shape:
+        if t.dtype != dtype or t.device != device or t.shape != shape:
+            if t.dtype != dtype:
+                raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+            if t.device != device:
+                raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
             raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
         if not t.is_contiguous():
             dense = False
@@ -587,7 +596,7 @@ def linattn_forward(q, k, v, log_decay, state=None, *, scale=None, want_state=Tr
     if state is not None:
         _need_typed(state, sshape, torch.float32, "state", dev)
     if out is None:
-        out = torch.empty(vshape, dtype=q.dtype, device=dev)
+        out = torch.empty_like(v, memory_format=torch.contiguous_format)
     else:
         _need_typed(out, vshape, q.dtype, "out", dev)
     if out_state is not None:
@@ -595,9 +604,9 @@ def linattn_forward(q, k, v, log_decay, state=None, *, scale=None, want_state=Tr
     elif want_state:
         out_state = torch.empty(sshape, dtype=torch.float32, device=dev)
     buf, n = _workspace_of(lib.pararnn_linattn_workspace_bytes(0, code, B, L, H, dk, dv), dev, ws)
-    _check(lib.pararnn_linattn_forward(code, B, L, H, dk, dv, _ptr(q), _ptr(k), _ptr(v), st, _ptr(log_decay),
-                                       _ptr(state), dk ** -0.5 if scale is None else scale, _ptr(out),
-                                       _ptr(out_state), _ptr(buf), n, _stream(dev)), "pararnn_linattn_forward")
+    _check(lib.pararnn_linattn_forward(code, B, L, H, dk, dv, _at(q), _at(k), _at(v), st, _at(log_decay),
+                                       _at(state), dk ** -0.5 if scale is None else scale, _at(out),
+                                       _at(out_state), _at(buf), n, _raw_stream(dev)), "pararnn_linattn_forward")
     return out, out_state
 
 
@@ -619,14 +628,13 @@ def linattn_backward(q, k, v, log_decay, grad_o, state=None, grad_state=None, *,
             _need_typed(t, sshape, torch.float32, name, dev)
     if want_state is None:
         want_state = state is not None
-    gq, gk = (torch.empty(kshape, dtype=q.dtype, device=dev) for _ in range(2))
-    gv = torch.empty(vshape, dtype=q.dtype, device=dev)
+    gq, gk, gv = (torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k, v))
     gs = torch.empty(sshape, dtype=torch.float32, device=dev) if want_state else None
     buf, n = _workspace_of(lib.pararnn_linattn_workspace_bytes(1, code, B, L, H, dk, dv), dev, ws)
-    _check(lib.pararnn_linattn_backward(code, B, L, H, dk, dv, _ptr(q), _ptr(k), _ptr(v), _ptr(grad_o), st,
-                                        _ptr(log_decay), _ptr(state), _ptr(grad_state),
-                                        dk ** -0.5 if scale is None else scale, _ptr(gq), _ptr(gk), _ptr(gv),
-                                        _ptr(gs), _ptr(buf), n, _stream(dev)), "pararnn_linattn_backward")
+    _check(lib.pararnn_linattn_backward(code, B, L, H, dk, dv, _at(q), _at(k), _at(v), _at(grad_o), st,
+                                        _at(log_decay), _at(state), _at(grad_state),
+                                        dk ** -0.5 if scale is None else scale, _at(gq), _at(gk), _at(gv),
+                                        _at(gs), _at(buf), n, _raw_stream(dev)), "pararnn_linattn_backward")
     return gq, gk, gv, gs
 
 
@@ -643,16 +651,16 @@ def linattn_step(q, k, v, log_decay, state, *, scale=None, out=None, out_state=N
     _need_typed(log_decay, (H,), torch.float32, "log_decay", dev)
     _need_typed(state, sshape, torch.float32, "state", dev)
     if out is None:
-        out = torch.empty(vshape, dtype=q.dtype, device=dev)
+        out = torch.empty_like(v, memory_format=torch.contiguous_format)
     else:
         _need_typed(out, vshape, q.dtype, "out", dev)
     if out_state is None:
         out_state = torch.empty(sshape, dtype=torch.float32, device=dev)
     else:
         _need_typed(out_state, sshape, torch.float32, "out_state", dev)
-    _check(lib.pararnn_linattn_step(code, B, H, dk, dv, _ptr(q), _ptr(k), _ptr(v), st, _ptr(log_decay), _ptr(state),
-                                    dk ** -0.5 if scale is None else scale, _ptr(out), _ptr(out_state),
-                                    _stream(dev)), "pararnn_linattn_step")
+    _check(lib.pararnn_linattn_step(code, B, H, dk, dv, _at(q), _at(k), _at(v), st, _at(log_decay), _at(state),
+                                    dk ** -0.5 if scale is None else scale, _at(out), _at(out_state),
+                                    _raw_stream(dev)), "pararnn_linattn_step")
     return out, out_state
 
 
@@ -689,9 +697,10 @@ def layernorm_forward(x, weight=None, bias=None, residual=None, *, eps=1e-5, out
         _need_typed(s, shape, x.dtype, "out_sum", dev)
     elif out_sum is not None:
         raise ValueError("out_sum is given without a residual")
-    mean, rstd = (torch.empty(shape[:-1], dtype=torch.float32, device=dev) for _ in range(2))
-    _check(lib.pararnn_layernorm_forward(code, rows, D, _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), eps,
-                                         _ptr(s), _ptr(y), _ptr(mean), _ptr(rstd), _stream(dev)),
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    rstd = torch.empty_like(mean)
+    _check(lib.pararnn_layernorm_forward(code, rows, D, _at(x), _at(residual), _at(weight), _at(bias), eps,
+                                         _at(s), _at(y), _at(mean), _at(rstd), _raw_stream(dev)),
            "pararnn_layernorm_forward")
     return y, x if s is None else s, mean, rstd
 
@@ -716,8 +725,8 @@ def layernorm_backward(s, weight, mean, rstd, grad_y, grad_sum=None, *, want_w=T
     gw = torch.empty(D, dtype=torch.float32, device=dev) if want_w else None
     gb = torch.empty(D, dtype=torch.float32, device=dev) if want_b else None
     buf, n = _workspace_of(lib.pararnn_layernorm_workspace_bytes(rows, D), dev, ws) if want_w or want_b else (None, 0)
-    _check(lib.pararnn_layernorm_backward(code, rows, D, _ptr(s), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(grad_y),
-                                          _ptr(grad_sum), _ptr(dx), _ptr(gw), _ptr(gb), _ptr(buf), n, _stream(dev)),
+    _check(lib.pararnn_layernorm_backward(code, rows, D, _at(s), _at(weight), _at(mean), _at(rstd), _at(grad_y),
+                                          _at(grad_sum), _at(dx), _at(gw), _at(gb), _at(buf), n, _raw_stream(dev)),
            "pararnn_layernorm_backward")
     return dx, gw, gb
 
@@ -751,7 +760,7 @@ def embedding_forward(ids, table, *, scale=1.0, out=None):
         out = torch.empty((*ids.shape, D), dtype=table.dtype, device=dev)
     else:
         _need_typed(out, (*ids.shape, D), table.dtype, "out", dev)
-    _check(lib.pararnn_embedding_forward(code, N, V, D, _ptr(ids), nb, _ptr(table), scale, _ptr(out), _stream(dev)),
+    _check(lib.pararnn_embedding_forward(code, N, V, D, _at(ids), nb, _at(table), scale, _at(out), _raw_stream(dev)),
            "pararnn_embedding_forward")
     return out
 
@@ -780,7 +789,7 @@ def embedding_backward(ids, grad, num_rows, *, scale=1.0, padding_idx=None, out=
     if n == 0:
         raise PararnnError("invalid sizes N=%d V=%d D=%d" % (N, V, D))
     buf, n = _workspace_of(n, dev, ws)
-    _check(lib.pararnn_embedding_backward(code, N, V, D, _ptr(ids), nb, _ptr(grad), scale,
-                                          -1 if padding_idx is None else padding_idx, _ptr(out), _ptr(buf), n,
-                                          _stream(dev)), "pararnn_embedding_backward")
+    _check(lib.pararnn_embedding_backward(code, N, V, D, _at(ids), nb, _at(grad), scale,
+                                          -1 if padding_idx is None else padding_idx, _at(out), _at(buf), n,
+                                          _raw_stream(dev)), "pararnn_embedding_backward")
     return out
