@@ -11,33 +11,36 @@ constexpr int kThreads = 256;
 // Width of the state's rows a walk is built for.
 int walk_width(int d1) { return d1 <= 32 ? 32 : d1 <= 64 ? 64 : d1 <= 96 ? 96 : d1 <= 128 ? 128 : 256; }
 
-// Positions a chunk: 64 for bf16; 32 for fp32, whose three planes would
-// otherwise leave room for one workgroup a CU.
-int walk_chunk(bool bf) { return bf ? 64 : 32; }
-
 struct WalkPlan {
-    int d1, nblk, walks, segs;
+    int d1, nblk, walks, segs, chunk;
     int64_t seg_len;
     size_t bytes;  // segment states
 };
 
-// Pieces of the sequence.  A walk is sequential, so few (batch row, head,
-// column block) walks leave most CUs idle; the sequence is then cut into
-// pieces whose own states are found first and joined.
+// A walk is sequential, so few (batch row, head, column block) walks leave
+// CUs idle.  Below one walk a CU the sequence is cut into segments whose own
+// states are found first and joined, as many as keep two workgroups on every
+// CU in one round (B=1, L=32771, H=8, 64x128 fp32: 32 segments 214 us, 48 244,
+// 64 230); from one walk a CU on the second reading of Y and Z costs more than
+// it gains (B=8, L=2048, H=16, 128x128 bf16: 101 us whole, 118 in two).
 WalkPlan walk_plan(const LinattnArgs &p, bool backward) {
+    auto blocks = [](int cols) { return (cols + walk::kNB - 1) / walk::kNB; };
     WalkPlan w;
     w.walks = backward ? 3 : 1;
-    const int cols = backward ? std::max(p.dk, p.dv) : p.dv;
     w.d1 = walk_width(backward ? std::max(p.dk, p.dv) : p.dk);
-    w.nblk = (cols + walk::kNB - 1) / walk::kNB;
-    const int C = walk_chunk(p.bf16);
-    const int64_t chunks = (p.L + C - 1) / C, groups = p.B * p.H * w.nblk * w.walks;
-    const int64_t want = 2 * (int64_t)device_cu_count();
-    int64_t segs = groups * 2 >= want ? 1 : std::min<int64_t>((want + groups - 1) / groups, chunks / 4);
+    w.nblk = backward ? blocks(std::max(p.dk, p.dv)) : blocks(p.dv);
+    const int64_t cus = device_cu_count(), pairs = p.B * p.H;
+    const int64_t groups = pairs * (backward ? 2 * blocks(p.dk) + blocks(p.dv) : blocks(p.dv));
+    // fp32: 32 positions, as three planes of 64 would leave room for one
+    // workgroup a CU; bf16: see kWgs
+    w.chunk = p.bf16 && groups <= 2 * cus ? 64 : 32;
+    const int C = w.chunk;
+    const int64_t chunks = (p.L + C - 1) / C;
+    int64_t segs = groups >= cus ? 1 : std::min<int64_t>(2 * cus / groups, chunks / 4);
     if (segs < 2) segs = 1;
     w.seg_len = (chunks + segs - 1) / segs * C;
     w.segs = (int)((p.L + w.seg_len - 1) / w.seg_len);
-    w.bytes = w.segs > 1 ? (size_t)groups * w.segs * 4 * (w.d1 / 16) * 64 * 16 : 0;
+    w.bytes = w.segs > 1 ? (size_t)pairs * w.walks * w.nblk * w.segs * 4 * (w.d1 / 16) * 64 * 16 : 0;
     return w;
 }
 
@@ -54,28 +57,32 @@ bool walks_vec(const WalkArgs &a, int es) {
     return true;
 }
 
-template <typename T, int D1, bool VEC>
+template <typename T, int D1, int C, bool VEC>
 void walk_launch(const WalkArgs &a, hipStream_t s) {
-    constexpr int C = sizeof(T) == 2 ? 64 : 32;
     const int64_t pairs = (a.B * a.H + 7) / 8 * 8 * a.walks * a.nblk;
     if (a.segs > 1) {
-        walk::walk_kernel<T, D1, C, VEC, walk::Part::State, false><<<(unsigned)(pairs * (a.segs - 1)), kThreads, 0, s>>>(a);
+        walk::walk_kernel<T, D1, C, VEC, walk::Part::State><<<(unsigned)(pairs * (a.segs - 1)), walk::kThreads, 0, s>>>(a);
         const int64_t tiles = (int64_t)a.walks * a.B * a.H * a.nblk * 4 * (D1 / 16);
-        walk::join_kernel<D1><<<(unsigned)((tiles + 3) / 4), kThreads, 0, s>>>(a);
+        walk::join_kernel<D1><<<(unsigned)tiles, walk::kThreads, 0, s>>>(a);
     }
-    constexpr bool kPipe = false;
-    walk::walk_kernel<T, D1, C, VEC, walk::Part::Whole, kPipe><<<(unsigned)(pairs * a.segs), kThreads, 0, s>>>(a);
+    walk::walk_kernel<T, D1, C, VEC, walk::Part::Whole><<<(unsigned)(pairs * a.segs), walk::kThreads, 0, s>>>(a);
 }
 
-template <typename T, bool VEC>
+template <typename T, int C, bool VEC>
 void walk_width_launch(const WalkArgs &a, int d1, hipStream_t s) {
     switch (d1) {
-        case 32: walk_launch<T, 32, VEC>(a, s); break;
-        case 64: walk_launch<T, 64, VEC>(a, s); break;
-        case 96: walk_launch<T, 96, VEC>(a, s); break;
-        case 128: walk_launch<T, 128, VEC>(a, s); break;
-        default: walk_launch<T, 256, VEC>(a, s); break;
+        case 32: walk_launch<T, 32, C, VEC>(a, s); break;
+        case 64: walk_launch<T, 64, C, VEC>(a, s); break;
+        case 96: walk_launch<T, 96, C, VEC>(a, s); break;
+        case 128: walk_launch<T, 128, C, VEC>(a, s); break;
+        default: walk_launch<T, 256, C, VEC>(a, s); break;
     }
+}
+
+template <typename T, int C>
+void walk_vec_launch(const WalkArgs &a, int d1, hipStream_t s) {
+    if (walks_vec(a, sizeof(T))) walk_width_launch<T, C, true>(a, d1, s);
+    else walk_width_launch<T, C, false>(a, d1, s);
 }
 
 template <typename T>
@@ -87,8 +94,13 @@ hipError_t run_walks(WalkArgs &a, const WalkPlan &w, const Ws &ws, hipStream_t s
     a.seg_state = reinterpret_cast<float *>(ws.p + kScratchOffset);
     for (int i = 0; i < a.walks; ++i)
         a.w[i].out4 = a.w[i].d2 % 4 == 0 && aligned_to(a.w[i].out, 4 * sizeof(T));
-    if (walks_vec(a, sizeof(T))) walk_width_launch<T, true>(a, w.d1, s);
-    else walk_width_launch<T, false>(a, w.d1, s);
+    if constexpr (sizeof(T) == 2) {
+        if (w.chunk == 64) {
+            walk_vec_launch<T, 64>(a, w.d1, s);
+            return hipGetLastError();
+        }
+    }
+    walk_vec_launch<T, 32>(a, w.d1, s);
     return hipGetLastError();
 }
 

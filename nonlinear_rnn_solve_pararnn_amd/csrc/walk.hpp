@@ -268,36 +268,27 @@ __device__ __forceinline__ f32x4 *seg_state(const WalkArgs &a, const Where &w, i
 // Row of T that register r of tile t holds in lanes of group q.
 __device__ __forceinline__ int state_row(int t, int q, int r) { return 32 * (t >> 1) + 8 * q + 4 * (t & 1) + r; }
 
-// Bytes of LDS of a walk's workgroup that keeps `stages` chunks.
+// Workgroups a CU that the registers are shared out for.  Where a launch has
+// more than two a CU, bf16 takes chunks of 32 positions, whose smaller tiles
+// leave room for three (backward at B=8, L=2048, H=16, 128x128: 225 us instead
+// of 255 with chunks of 64); with one or two a CU the longer chunk, with half
+// as many barriers, is ahead (forward there: 101 us, 109 with 32).
 template <typename T, int D1, int C>
-constexpr int walk_lds(int stages, int ps) {
-    return 4 * C + 2 * kPlanes<T> * C * (stages * (2 * kTileRow<D1> + kTileRow<kNB>) + ps * kTileRow<C>);
-}
-// Chunks in LDS: three where they fit the CU's 160 KB, else one.
-template <typename T, int D1, int C>
-constexpr bool kPiped = walk_lds<T, D1, C>(3, 2) <= 160 * 1024;
+constexpr int kWgs = D1 > 128 ? 1 : sizeof(T) == 2 && C == 32 ? 3 : 2;
 
 enum class Part {
     Whole,  // outputs and T
     State   // only the segment's own part of T (from zero), for the join
 };
 
-// Three chunks in LDS (PIPE): while chunk i is walked, the P of chunk i + 1 is
-// formed and chunk i + 2 is written to LDS from the registers that it was
-// loaded into a chunk earlier, so one barrier a chunk is enough and the parts
-// of an iteration are independent of each other.  With one chunk in LDS the
-// parts follow each other with three barriers, and other workgroups of the CU
-// fill the waits.
-template <typename T, int D1, int C, bool VEC, Part PART, bool PIPE>
-__global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kernel(WalkArgs a) {
+template <typename T, int D1, int C, bool VEC, Part PART>
+__global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkArgs a) {
     constexpr bool kOut = PART == Part::Whole;
     constexpr int kP = kPlanes<T>;                 // planes of X, Y, Z, P
     constexpr int kS = kP == 1 ? 1 : 3;            // planes of the operand copy of T
     constexpr int NA = D1 / 16, NT = D1 / 32, NS = C / 32, NI = C / 16;
     constexpr int kPX = C * kTileRow<D1>, kPZ = C * kTileRow<kNB>, kPP = C * kTileRow<C>;  // elements of a plane
-    constexpr int kStages = PIPE ? 3 : 1, kPs = PIPE ? 2 : 1;
-    __shared__ __align__(16) bf16 X[kOut ? kStages * kP * kPX : 8], Y[kStages * kP * kPX], Z[kStages * kP * kPZ],
-        P[kOut ? kPs * kP * kPP : 8];
+    __shared__ __align__(16) bf16 X[kOut ? kP * kPX : 8], Y[kP * kPX], Z[kP * kPZ], P[kOut ? kP * kPP : 8];
     __shared__ __align__(16) float dec_z[C];
     const Where wh = where(a, kOut ? a.segs : a.segs - 1);
     if (!wh.any) return;
@@ -342,7 +333,7 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
 
     if constexpr (kOut) {
         // the tiles of P right of the diagonal that share a 32-wide read with it stay zero
-        for (int i = threadIdx.x; i < kPs * kP * kPP / 8; i += kThreads) {
+        for (int i = threadIdx.x; i < kP * kPP / 8; i += kThreads) {
             const bf16x8 z = {};
             *reinterpret_cast<bf16x8 *>(&P[i * 8]) = z;
         }
@@ -368,16 +359,18 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
         ay.load(ry, i, cnt);
         az.load(rz, i, cnt);
     };
-    auto put = [&](int stage) {
-        if (kOut) ax.store(X + stage * kP * kPX);
-        ay.store(Y + stage * kP * kPX);
-        az.store(Z + stage * kP * kPZ);
+    auto put = [&]() {
+        if (kOut) ax.store(X);
+        ay.store(Y);
+        az.store(Z);
     };
+    load(0);
+
     // The products of a chunk run as one sequence of batches, each a few
     // operand reads and the matrix instructions that use them, with the reads
     // of batch k + 1 issued before the products of batch k (the compiler,
     // short of registers, would put every read right before its use and wait):
-    //   P of chunk i + 1 or i: the tiles below and on the diagonal go round
+    //   P: the tiles below and on the diagonal go round
     //     the waves (the last one is formed more than once if they don't come
     //     out even), each as its transpose, so that a lane's four results are
     //     consecutive j;
@@ -385,10 +378,11 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
     //     registers are four columns);
     //   T over the chunk.
     constexpr int kTiles = NI * (NI + 1) / 2, kMine = (kTiles + 3) / 4;
-    constexpr int kU1 = kP == 1 ? 2 : 1, kU3 = kP == 1 ? 4 : 2;          // units a batch
+    constexpr bool kLong = kP == 1 && C == 64;                             // longer batches, where the registers allow
+    constexpr int kU1 = kLong ? 2 : 1, kU3 = kLong ? 4 : 2;                // units a batch
     constexpr int kB1 = kOut ? (kMine * NT + kU1 - 1) / kU1 : 0, kB2 = kOut ? NT : 0,
                   kB3s = (NA + kU3 - 1) / kU3, kB3 = NS * kB3s;
-    constexpr int kFrags = (kP == 1 ? 4 : 6);
+    constexpr int kFrags = kLong ? 4 : 2 * kP;
     static_assert(NI * kP <= kFrags && 2 * kU1 * kP <= kFrags && kU3 * kP <= kFrags, "a batch fits its buffer");
     struct Frags {
         bf16x8 v[kFrags];
@@ -400,8 +394,17 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
         my_it[k] = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
         my_jt[k] = tile - my_it[k] * (my_it[k] + 1) / 2;
     }
-    auto products = [&](const bf16 *Xp, const bf16 *Yp, bf16 *Ps, const bf16 *Xs, const bf16 *Ys, const bf16 *Zs, int cnt,
-                        bool whole, bf16x8 (&z)[NS][kP], f32x4 (&o)[NI]) {
+    auto products = [&](int cnt, bool whole, bf16x8 (&z)[NS][kP], f32x4 (&o)[NI]) {
+        // rows 16 it + m are laid out like rows m; with bf16 the offsets are hidden
+        // from the compiler, which would keep every sum with them in a register
+        // (20 of the 38 that it then spills)
+        int y_off[kMine], x_off[kMine];
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+            y_off[k] = __builtin_amdgcn_readfirstlane(my_jt[k] * 16 * kTileRow<D1>);
+            x_off[k] = __builtin_amdgcn_readfirstlane(my_it[k] * 16 * kTileRow<D1>);
+            if constexpr (kP == 1) asm volatile("" : "+s"(y_off[k]), "+s"(x_off[k]));
+        }
         Frags buf[2];
         f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
         bf16x8 zw[3];
@@ -413,8 +416,8 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
                     if (unit < kMine * NT)
 #pragma unroll
                         for (int p = 0; p < kP; ++p) {
-                            f.v[(2 * u) * kP + p] = read_row(&Yp[p * kPX + tile_at<D1>(my_jt[mine] * 16 + m, 4 * t + q)]);
-                            f.v[(2 * u + 1) * kP + p] = read_row(&Xp[p * kPX + tile_at<D1>(my_it[mine] * 16 + m, 4 * t + q)]);
+                            f.v[(2 * u) * kP + p] = read_row(&Y[p * kPX + tile_at<D1>(m, 4 * t + q) + y_off[mine]]);
+                            f.v[(2 * u + 1) * kP + p] = read_row(&X[p * kPX + tile_at<D1>(m, 4 * t + q) + x_off[mine]]);
                         }
                 }
             } else if (k < kB1 + kB2) {
@@ -423,7 +426,7 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
                 for (int it = 0; it < NI; ++it)
 #pragma unroll
                     for (int p = 0; p < kP; ++p)
-                        f.v[it * kP + p] = read_row(&Xs[p * kPX + tile_at<D1>(it * 16 + m, 4 * t + q)]);
+                        f.v[it * kP + p] = read_row(&X[p * kPX + tile_at<D1>(it * 16 + m, 4 * t + q)]);
             } else {
                 const int s = (k - kB1 - kB2) / kB3s, t0 = (k - kB1 - kB2) % kB3s * kU3;
 #pragma unroll
@@ -432,8 +435,8 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
 #pragma unroll
                         for (int p = 0; p < kP; ++p) {
                             const int t = t0 + u, row = 32 * s + 8 * q + tr_i, grp = 4 * (t >> 1) + tr_c, in = 4 * (t & 1);
-                            f.v[u * kP + p] = join(read_tr(&Ys[p * kPX + tile_at<D1>(row, grp) + in]),
-                                                   read_tr(&Ys[p * kPX + tile_at<D1>(row + 4, grp) + in]));
+                            f.v[u * kP + p] = join(read_tr(&Y[p * kPX + tile_at<D1>(row, grp) + in]),
+                                                   read_tr(&Y[p * kPX + tile_at<D1>(row + 4, grp) + in]));
                         }
             }
         };
@@ -462,7 +465,7 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
                     }
                     bf16x8 pv[kP];
                     to_planes(v, pv);
-                    bf16 *to = &Ps[tile_at<C>(it * 16 + m, 2 * jt + (q >> 1)) + 4 * (q & 1)];
+                    bf16 *to = &P[tile_at<C>(it * 16 + m, 2 * jt + (q >> 1)) + 4 * (q & 1)];
 #pragma unroll
                     for (int p = 0; p < kP; ++p) *reinterpret_cast<u32x2 *>(to + p * kPP) = *reinterpret_cast<const u32x2 *>(&pv[p]);
                 }
@@ -522,8 +525,8 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
                 const int row = 32 * s + 8 * q + tr_i, grp = 2 * wave + (tr_c >> 1), in = 4 * (tr_c & 1);
-                z[s][p] = join(read_tr(&Zs[p * kPZ + tile_at<kNB>(row, grp) + in]),
-                               read_tr(&Zs[p * kPZ + tile_at<kNB>(row + 4, grp) + in]));
+                z[s][p] = join(read_tr(&Z[p * kPZ + tile_at<kNB>(row, grp) + in]),
+                               read_tr(&Z[p * kPZ + tile_at<kNB>(row + 4, grp) + in]));
             }
         read(0, buf[0]);
 #pragma unroll
@@ -536,14 +539,14 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
     // out += P Z.  Values of Z that are not finite must not reach earlier
     // positions through a zero of P: then (their columns of T have become so)
     // they are left out of the product and added to the positions from their own on.
-    auto within = [&](const bf16 *Ps, const bf16 *Zs, int cnt, bf16x8 (&z)[NS][kP], f32x4 (&o)[NI]) {
+    auto within = [&](int cnt, bf16x8 (&z)[NS][kP], f32x4 (&o)[NI]) {
         bf16x8 pr[NI][NS][kP];
 #pragma unroll
         for (int it = 0; it < NI; ++it)
 #pragma unroll
             for (int s = 0; s <= it / 2; ++s)
 #pragma unroll
-                for (int p = 0; p < kP; ++p) pr[it][s][p] = read_row(&Ps[p * kPP + tile_at<C>(it * 16 + m, 4 * s + q)]);
+                for (int p = 0; p < kP; ++p) pr[it][s][p] = read_row(&P[p * kPP + tile_at<C>(it * 16 + m, 4 * s + q)]);
         const bool odd = __any(abs_bits(S[0][0]) >= kInfBits);
         if (odd) {
 #pragma unroll
@@ -567,12 +570,12 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int c = oc + r;
-                    const float zv = (float)Zs[tile_at<kNB>(j, c >> 3) + (c & 7)];  // the first plane is as little finite
+                    const float zv = (float)Z[tile_at<kNB>(j, c >> 3) + (c & 7)];  // the first plane is as little finite
                     if (abs_bits(zv) < kInfBits) continue;
 #pragma unroll
                     for (int it = 0; it < NI; ++it)
                         if (j <= 16 * it + m)
-                            o[it][r] = fmaf((float)Ps[tile_at<C>(16 * it + m, j >> 3) + (j & 7)], zv, o[it][r]);
+                            o[it][r] = fmaf((float)P[tile_at<C>(16 * it + m, j >> 3) + (j & 7)], zv, o[it][r]);
                 }
         }
     };
@@ -599,51 +602,19 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
         }
     };
 
-    if constexpr (PIPE) {
-        load(0);
-        put(0);
-        load(1);
-        put(1);
-        load(2);
+    for (int i = 0; i < chunks; ++i) {
+        const int cnt = positions(i);
+        lds_barrier();  // the last chunk's reads are done
+        put();
+        load(i + 1);
         lds_barrier();
-        form_first(X, Y, P);
-        lds_barrier();
-        int cur = 0, nxt = 1, far = 2;  // stages of chunks i, i + 1, i + 2
-        auto step = [&](int i, bool whole) {
-            put(far);
-            load(i + 3);
-            const int cnt = whole ? C : positions(i);
-            const bf16 *Xs = X + cur * kP * kPX, *Ys = Y + cur * kP * kPX, *Zs = Z + cur * kP * kPZ;
-            bf16 *Pc = P + (i & 1) * kP * kPP, *Pn = P + (~i & 1) * kP * kPP;
-            f32x4 o[NI];
-            bf16x8 z[NS][kP];
-            products(X + nxt * kP * kPX, Y + nxt * kP * kPX, Pn, Xs, Ys, Zs, cnt, whole, z, o);
-            within(Pc, Zs, cnt, z, o);
+        f32x4 o[NI];
+        bf16x8 z[NS][kP];
+        products(cnt, cnt == C, z, o);
+        if constexpr (kOut) {
+            lds_barrier();  // P is whole
+            within(cnt, z, o);
             write(i, cnt, o);
-            lds_barrier();
-            const int old = cur;
-            cur = nxt;
-            nxt = far;
-            far = old;
-        };
-        for (int i = 0; i < chunks - 1; ++i) step(i, true);
-        step(chunks - 1, false);
-    } else {
-        load(0);
-        for (int i = 0; i < chunks; ++i) {
-            const int cnt = positions(i);
-            lds_barrier();  // the last chunk's reads are done
-            put(0);
-            load(i + 1);
-            lds_barrier();
-            f32x4 o[NI];
-            bf16x8 z[NS][kP];
-            products(X, Y, P, X, Y, Z, cnt, cnt == C, z, o);
-            if constexpr (kOut) {
-                lds_barrier();  // P is whole
-                within(P, Z, cnt, z, o);
-                write(i, cnt, o);
-            }
         }
     }
 
@@ -662,44 +633,37 @@ __global__ __launch_bounds__(kThreads, PIPE || D1 > 128 ? 1 : 2) void walk_kerne
     }
 }
 
-// From every segment's own part of T to T before every segment, in place.
+// From every segment's own part of T to T before every segment, in place: a
+// workgroup a 16x16 tile, a thread an element.  Bound by latency (few
+// elements, one step a segment), so 16 segments' loads are in flight.
 template <int D1>
 __global__ __launch_bounds__(kThreads) void join_kernel(WalkArgs a) {
     constexpr int NA = D1 / 16;
-    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);  // one tile of one wave of one block
-    const int64_t tiles = (int64_t)a.walks * a.B * a.H * a.nblk * 4 * NA;
-    if (item >= tiles) return;
+    const uint32_t item = blockIdx.x, blk_of = item / (4 * NA), pairs = (uint32_t)(a.B * a.H);
     const int t = (int)(item % NA), wave = (int)(item / NA % 4);
-    const int64_t blk_of = item / (4 * NA);
     Where wh;
-    wh.blk = (int)(blk_of % a.nblk);
-    wh.bh = (int)(blk_of / a.nblk % (a.B * a.H));
-    wh.walk = (int)(blk_of / a.nblk / (a.B * a.H));
+    wh.blk = (int)(blk_of % (uint32_t)a.nblk);
+    wh.bh = (int)(blk_of / (uint32_t)a.nblk % pairs);
+    wh.walk = (int)(blk_of / (uint32_t)a.nblk / pairs);
     const Walk &w = a.w[wh.walk];
     if (wh.blk * kNB >= w.d2) return;
-    const int lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4, col = wh.blk * kNB + wave * 16 + m;
-    const float em1 = walk_em1(walk_gate(a.log_decay, wh.bh % a.H), a.seg_len);
-    f32x4 s;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int row = state_row(t, q, r);
-        s[r] = w.init != nullptr && col < w.d2 && row < w.d1
-                   ? w.init[(int64_t)wh.bh * w.d1 * w.d2 + (int64_t)row * w.im + (int64_t)col * w.in] : 0.0f;
-    }
-    f32x4 *at = seg_state<D1>(a, wh, 0, wave) + t * 64 + lane;
-    const int64_t step = 4 * NA * 64;
-    constexpr int U = 8;
+    const int lane = threadIdx.x >> 2, r = threadIdx.x & 3;  // whose register this element is
+    const int row = state_row(t, lane >> 4, r), col = wh.blk * kNB + wave * 16 + (lane & 15);
+    const float em1 = walk_em1(walk_gate(a.log_decay, wh.bh % (int)a.H), a.seg_len);
+    float s = w.init != nullptr && col < w.d2 && row < w.d1
+                  ? w.init[(int64_t)wh.bh * w.d1 * w.d2 + (int64_t)row * w.im + (int64_t)col * w.in] : 0.0f;
+    float *at = reinterpret_cast<float *>(seg_state<D1>(a, wh, 0, wave) + t * 64) + threadIdx.x;
+    const int64_t step = 4 * NA * 64 * 4;
+    constexpr int U = 16;
     for (int s0 = 0; s0 < a.segs; s0 += U) {
-        f32x4 own[U];
+        float own[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (s0 + u < a.segs - 1) own[u] = at[(s0 + u) * step];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s0 + u < a.segs) at[(s0 + u) * step] = s;
-            if (s0 + u < a.segs - 1)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) s[r] = fmaf(s[r], em1, s[r]) + own[u][r];
+            if (s0 + u < a.segs - 1) s = fmaf(s, em1, s) + own[u];
         }
     }
 }
