@@ -342,29 +342,36 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
     auto rows = [&](const WalkView &v, int from, int d) { return rows_of<T>(v, wh.b, wh.h, a.L, begin, C, w.rev, from, d); };
     const Rows rx = rows(w.X, 0, w.d1), ry = rows(w.Y, 0, w.d1), rz = rows(w.Z, c0, w.d2),
                ro = rows({w.out, a.L * a.H * w.d2, a.H * w.d2, w.d2}, c0, w.d2);
-    Ahead<T, D1, C, VEC> ax, ay;
-    Ahead<T, kNB, C, VEC> az;
+    // the pass that only carries T is bound by the loads' latency and has the
+    // registers to keep two chunks on their way
+    constexpr int kDepth = kOut ? 1 : 2;
+    Ahead<T, D1, C, VEC> ax, ay[kDepth];
+    Ahead<T, kNB, C, VEC> az[kDepth];
     if (kOut) ax.init(rx);
-    ay.init(ry);
-    az.init(rz);
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+        ay[d].init(ry);
+        az[d].init(rz);
+    }
     const int oc = wave * 16 + 4 * q;
     // this lane's row of the first 16-row tile of out, four columns from its own
     const uint32_t out_at = c0 + oc < w.d2 ? ro.row_at(m, C) + oc * (uint32_t)sizeof(T) : kNowhere;
     const uint32_t out_step = (uint32_t)(w.rev ? -16 : 16) * ro.row_bytes;
 
     auto positions = [&](int i) { return i < chunks - 1 ? C : i == chunks - 1 ? last : 0; };
-    auto load = [&](int i) {  // chunk i (past the last one: zeros) into registers
+    auto load = [&](int i, int d) {  // chunk i (past the last one: zeros) into registers
         const int cnt = positions(i);
         if (kOut) ax.load(rx, i, cnt);
-        ay.load(ry, i, cnt);
-        az.load(rz, i, cnt);
+        ay[d].load(ry, i, cnt);
+        az[d].load(rz, i, cnt);
     };
-    auto put = [&]() {
+    auto put = [&](int d) {
         if (kOut) ax.store(X);
-        ay.store(Y);
-        az.store(Z);
+        ay[d].store(Y);
+        az[d].store(Z);
     };
-    load(0);
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load(d, d);
 
     // The products of a chunk run as one sequence of batches, each a few
     // operand reads and the matrix instructions that use them, with the reads
@@ -602,11 +609,11 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
         }
     };
 
-    for (int i = 0; i < chunks; ++i) {
+    auto step = [&](int i, int d) {
         const int cnt = positions(i);
         lds_barrier();  // the last chunk's reads are done
-        put();
-        load(i + 1);
+        put(d);
+        load(i + kDepth, d);
         lds_barrier();
         f32x4 o[NI];
         bf16x8 z[NS][kP];
@@ -616,7 +623,11 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
             within(cnt, z, o);
             write(i, cnt, o);
         }
-    }
+    };
+    for (int i = 0; i < chunks; i += kDepth)
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d)
+            if (i + d < chunks) step(i + d, d);
 
     if constexpr (!kOut) {
         f32x4 *dst = seg_state<D1>(a, wh, wh.seg, wave) + lane;
