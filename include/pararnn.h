@@ -357,7 +357,7 @@ enum { PARARNN_F32 = 0, PARARNN_BF16 = 1 };
  *     S_t = e^g S_{t-1} + k_t^T v_t,   o_t = scale q_t S_t,   S_{-1} = state.
  * q, k: [B, L, H, dk]; v, o: [B, L, H, dv]; state, out_state: [B, H, dk, dv]
  * fp32 (state NULL: zeros; out_state NULL: not wanted; out_state may be
- * state itself).  log_decay: [H] fp32.  1 <= dk, dv <= 256 (above:
+ * state itself, but not overlap it otherwise).  log_decay: [H] fp32.  1 <= dk, dv <= 256 (above:
  * PARARNN_ERR_UNSUPPORTED).
  * strides: HOST array of {batch row, position, head} strides in elements for
  * q, k and v in turn (9 values), not negative, a position's below 2^22; the

@@ -165,6 +165,11 @@ bool linattn_inputs(LinattnArgs &a, const void *const *in, int n, const int64_t 
     return true;
 }
 
+// Whether the states' in- and output share memory without being the same.
+bool states_cross(const LinattnArgs &a, const float *in, const float *out) {
+    return in != out && overlaps(in, out, a.B * a.H * a.dk * a.dv);
+}
+
 bool layernorm_dims_ok(int32_t dtype, int64_t rows, int64_t D) {
     return type_ok(dtype) && dims_ok(rows, D, 1) && D < ((int64_t)1 << 24);
 }
@@ -447,6 +452,7 @@ int pararnn_linattn_forward(int32_t dtype, int64_t B, int64_t L, int64_t H, int6
     const void *in[3] = {q, k, v};
     if (!linattn_inputs(a, in, 3, strides)) return PARARNN_ERR_INVALID;
     if (!ws || ws_bytes < linattn_ws(a, false) || !aligned(ws, 256)) return PARARNN_ERR_INVALID;
+    if (states_cross(a, state, out_state)) return PARARNN_ERR_INVALID;
     a.log_decay = log_decay;
     a.state = state;
     a.scale = scale;
@@ -487,7 +493,7 @@ int pararnn_linattn_step(int32_t dtype, int64_t B, int64_t H, int64_t dk, int64_
         return PARARNN_ERR_INVALID;
     LinattnArgs a = linattn_shape(dtype, B, 1, H, dk, dv);
     const void *in[3] = {q, k, v};
-    if (!linattn_inputs(a, in, 3, strides)) return PARARNN_ERR_INVALID;
+    if (!linattn_inputs(a, in, 3, strides) || states_cross(a, state, out_state)) return PARARNN_ERR_INVALID;
     a.log_decay = log_decay;
     a.state = state;
     a.scale = scale;

@@ -470,6 +470,7 @@ template <typename T, int V>
 hipError_t emb_sums(EmbSumArgs &a, hipStream_t s) {
     a.cols = (a.D + 64 * V - 1) / (64 * V);
     emb_sum_kernel<T, V><<<(unsigned)((a.chunks * a.cols + 3) / 4), kThreads, 0, s>>>(a);
+    if (a.chunks == 1) return hipGetLastError();  // no run crosses chunks
     constexpr int J = V == 1 ? 1 : 4;
     a.cols = (a.D + 64 * J - 1) / (64 * J);
     emb_join_kernel<T, J><<<(unsigned)((a.chunks * a.cols + 3) / 4), kThreads, 0, s>>>(a);

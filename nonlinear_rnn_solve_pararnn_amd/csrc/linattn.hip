@@ -33,7 +33,7 @@ WalkPlan walk_plan(const LinattnArgs &p, bool backward) {
     const int64_t groups = pairs * (backward ? 2 * blocks(p.dk) + blocks(p.dv) : blocks(p.dv));
     // fp32: 32 positions, as three planes of 64 would leave room for one
     // workgroup a CU; bf16: see kWgs
-    w.chunk = p.bf16 && groups <= 2 * cus ? 64 : 32;
+    w.chunk = p.bf16 && groups <= 2 * cus && p.L > walk::kShort ? 64 : 32;
     const int C = w.chunk;
     const int64_t chunks = (p.L + C - 1) / C;
     int64_t segs = groups >= cus ? 1 : std::min<int64_t>(2 * cus / groups, chunks / 4);

@@ -16,10 +16,26 @@
 // Precision.  An fp32 number is three bf16 numbers of 8 bits each, exactly;
 // a product of two such sums takes the six products whose size is at least
 // 2^-16 of the first, which leaves an error of 2^-23 or so.  fp32 operands are
-// held as three planes throughout.  bf16 operands are one plane: exact as they
-// come, and the products X Y^T and Y^T (decayed Z) keep everything because the
-// decayed Z is split into three; P and the operand copy of T are rounded to
-// bf16 once, which puts an error the size of the result's own rounding on it.
+// held as three planes throughout.  bf16 operands are one plane, exact as they
+// come, and T is fp32 in both: the decayed Z that it adds up is split into
+// three planes, so the state of a bf16 model is as good as that of an fp32 one.
+// For the bf16 outputs alone, P and the copy of T that the rows are multiplied
+// with are rounded to bf16 once.  Sums of many such products are then off by
+// about as much as their own rounding; two planes each would cost 27% (forward
+// at B=8, L=2048, H=16, 128x128).  Where few terms are summed two planes are
+// taken: of T in heads of up to 32, of P in chunks of 32 positions, which all
+// short sequences have.
+//
+// What bounds it (B=8, L=2048, H=16, 128x128, bf16): 268 MB forward, 52 us at
+// the rate of a copy, 470 MB backward, 92 us; matrix instructions 18 us of the
+// forward pass.  It takes 90 us forward and 204 us backward.  Neither
+// memory (the loads and stores alone 71 us forward) nor the arithmetic (all
+// but the loads 84 us) fills the time; a workgroup's three barriers a chunk
+// leave both idle in turn.  Tried and not kept: three chunks in LDS and one
+// barrier (the accumulators then move between register files, 103 us forward,
+// 329 backward), two waves sharing 16 columns with half the positions each
+// (115, 337), workgroups of 32 columns (116, 365), outputs through LDS in whole
+// rows (98, 263).
 #pragma once
 
 #include "linattn.hpp"
@@ -110,9 +126,17 @@ __device__ __forceinline__ void round1(const float (&f)[8], bf16x8 (&p)[1]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[0][i] = (bf16)f[i];
 }
+__device__ __forceinline__ void split2(const float (&f)[8], bf16x8 (&p)[2]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        p[0][i] = (bf16)f[i];
+        p[1][i] = (bf16)(f[i] - (float)p[0][i]);
+    }
+}
 template <int N>
 __device__ __forceinline__ void to_planes(const float (&f)[8], bf16x8 (&p)[N]) {
     if constexpr (N == 3) split3(f, p);
+    else if constexpr (N == 2) split2(f, p);
     else round1(f, p);
 }
 template <int N>
@@ -272,7 +296,9 @@ __device__ __forceinline__ int state_row(int t, int q, int r) { return 32 * (t >
 // more than two a CU, bf16 takes chunks of 32 positions, whose smaller tiles
 // leave room for three (backward at B=8, L=2048, H=16, 128x128: 225 us instead
 // of 255 with chunks of 64); with one or two a CU the longer chunk, with half
-// as many barriers, is ahead (forward there: 101 us, 109 with 32).
+// as many barriers, is ahead (forward there: 101 us, 109 with 32), but for
+// sequences of up to kShort positions, where it makes no difference to the time.
+constexpr int64_t kShort = 256;
 template <typename T, int D1, int C>
 constexpr int kWgs = D1 > 128 ? 1 : sizeof(T) == 2 && C == 32 ? 3 : 2;
 
@@ -284,11 +310,12 @@ enum class Part {
 template <typename T, int D1, int C, bool VEC, Part PART>
 __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkArgs a) {
     constexpr bool kOut = PART == Part::Whole;
-    constexpr int kP = kPlanes<T>;                 // planes of X, Y, Z, P
-    constexpr int kS = kP == 1 ? 1 : 3;            // planes of the operand copy of T
+    constexpr int kP = kPlanes<T>;                 // planes of X, Y, Z
+    constexpr int kR = kP == 3 ? 3 : C == 64 ? 1 : 2;  // planes of P
+    constexpr int kS = kP == 3 ? 3 : D1 == 32 ? 2 : 1;  // planes of the operand copy of T
     constexpr int NA = D1 / 16, NT = D1 / 32, NS = C / 32, NI = C / 16;
     constexpr int kPX = C * kTileRow<D1>, kPZ = C * kTileRow<kNB>, kPP = C * kTileRow<C>;  // elements of a plane
-    __shared__ __align__(16) bf16 X[kOut ? kP * kPX : 8], Y[kP * kPX], Z[kP * kPZ], P[kOut ? kP * kPP : 8];
+    __shared__ __align__(16) bf16 X[kOut ? kP * kPX : 8], Y[kP * kPX], Z[kP * kPZ], P[kOut ? kR * kPP : 8];
     __shared__ __align__(16) float dec_z[C];
     const Where wh = where(a, kOut ? a.segs : a.segs - 1);
     if (!wh.any) return;
@@ -333,7 +360,7 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
 
     if constexpr (kOut) {
         // the tiles of P right of the diagonal that share a 32-wide read with it stay zero
-        for (int i = threadIdx.x; i < kP * kPP / 8; i += kThreads) {
+        for (int i = threadIdx.x; i < kR * kPP / 8; i += kThreads) {
             const bf16x8 z = {};
             *reinterpret_cast<bf16x8 *>(&P[i * 8]) = z;
         }
@@ -470,11 +497,11 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
                         if (it == jt && m < 4 * q + r) v[r] = 0.0f;  // whatever Y holds there
                         acc[r] = 0.0f;
                     }
-                    bf16x8 pv[kP];
+                    bf16x8 pv[kR];
                     to_planes(v, pv);
                     bf16 *to = &P[tile_at<C>(it * 16 + m, 2 * jt + (q >> 1)) + 4 * (q & 1)];
 #pragma unroll
-                    for (int p = 0; p < kP; ++p) *reinterpret_cast<u32x2 *>(to + p * kPP) = *reinterpret_cast<const u32x2 *>(&pv[p]);
+                    for (int p = 0; p < kR; ++p) *reinterpret_cast<u32x2 *>(to + p * kPP) = *reinterpret_cast<const u32x2 *>(&pv[p]);
                 }
             } else if (k < kB1 + kB2) {
                 const int t = k - kB1;
@@ -547,13 +574,13 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
     // positions through a zero of P: then (their columns of T have become so)
     // they are left out of the product and added to the positions from their own on.
     auto within = [&](int cnt, bf16x8 (&z)[NS][kP], f32x4 (&o)[NI]) {
-        bf16x8 pr[NI][NS][kP];
+        bf16x8 pr[NI][NS][kR];
 #pragma unroll
         for (int it = 0; it < NI; ++it)
 #pragma unroll
             for (int s = 0; s <= it / 2; ++s)
 #pragma unroll
-                for (int p = 0; p < kP; ++p) pr[it][s][p] = read_row(&P[p * kPP + tile_at<C>(it * 16 + m, 4 * s + q)]);
+                for (int p = 0; p < kR; ++p) pr[it][s][p] = read_row(&P[p * kPP + tile_at<C>(it * 16 + m, 4 * s + q)]);
         const bool odd = __any(abs_bits(S[0][0]) >= kInfBits);
         if (odd) {
 #pragma unroll
@@ -663,6 +690,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(WalkArgs a) {
     const float em1 = walk_em1(walk_gate(a.log_decay, wh.bh % (int)a.H), a.seg_len);
     float s = w.init != nullptr && col < w.d2 && row < w.d1
                   ? w.init[(int64_t)wh.bh * w.d1 * w.d2 + (int64_t)row * w.im + (int64_t)col * w.in] : 0.0f;
+    s = __builtin_canonicalizef(s);  // no signalling NaN (a launch tag) goes into the workspace
     float *at = reinterpret_cast<float *>(seg_state<D1>(a, wh, 0, wave) + t * 64) + threadIdx.x;
     const int64_t step = 4 * NA * 64 * 4;
     constexpr int U = 16;

@@ -95,6 +95,11 @@ def test_library_refuses_invalid_arguments(lib):
     assert lib.pararnn_linattn_forward(0, 1, 4, 4, 8, 8, f, f, f, bad, f, n, one, f, n, f, big, n) == -1
     assert lib.pararnn_linattn_forward(0, 1, 4, 4, 8, 8, f, f, f, n, f, n, one, f, n, f, 0, n) == -1     # workspace
     assert lib.pararnn_linattn_forward(0, 1, 4, 4, 8, 8, f, f, f, n, f, n, one, f, n, n, big, n) == -1
+    part = ctypes.c_void_p(0x10000 + 4)  # a state that overlaps its successor by all but one element
+    assert lib.pararnn_linattn_forward(0, 1, 4, 4, 8, 8, f, f, f, n, f, f, one, f, part, f, big, n) == -1
+    assert lib.pararnn_linattn_step(0, 1, 4, 8, 8, f, f, f, n, f, f, one, f, part, n) == -1
+    far = (ctypes.c_int64 * 9)(*([64, 1 << 22, 8] * 3))                          # a position's stride
+    assert lib.pararnn_linattn_forward(0, 1, 4, 4, 8, 8, f, f, f, far, f, n, one, f, n, f, big, n) == -1
     assert lib.pararnn_linattn_backward(0, 1, 4, 4, 8, 8, f, f, f, n, n, f, n, n, one, f, f, f, n, f, big, n) == -1
     assert lib.pararnn_linattn_step(0, 1, 4, 8, 8, f, f, f, n, f, n, one, f, f, n) == -1                 # no state
     assert lib.pararnn_layernorm_forward(0, 4, 0, f, n, n, n, one, n, f, n, n, n) == -1
