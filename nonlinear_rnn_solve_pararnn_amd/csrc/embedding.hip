@@ -105,7 +105,7 @@ __device__ __forceinline__ void zero_share(const ZeroArgs &z, int share, int sha
 
 // ---------------------------------------------------------------- sort
 constexpr int kBins = 256;          // 8 bits of the key a pass
-constexpr int kSmallN = 2048;       // sorted by one workgroup in LDS
+constexpr int kSmallN = 4096;       // sorted by one workgroup in LDS
 constexpr int kSmallThreads = 1024;
 constexpr int kMaxTiles = 128;      // workgroups of a pass over a longer list
 

@@ -49,6 +49,8 @@ struct LnFwdArgs {
     float *mean, *rstd;
 };
 
+// A workgroup keeps its columns' weight and bias in registers over its rows
+// and loads a row ahead.
 template <typename T, int V, int W, int E>
 __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
     constexpr int NV = E / V, kRows = 4 / W;
@@ -56,26 +58,51 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
     const int li = W == 1 ? (threadIdx.x & 63) : threadIdx.x;
     const int64_t step = (int64_t)gridDim.x * kRows;
     const float n = (float)a.D;
-    for (int64_t row = (int64_t)blockIdx.x * kRows + (W == 1 ? threadIdx.x >> 6 : 0); row < a.rows; row += step) {
+    const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
+    float w[NV][V], b[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = (li + j * 64 * W) * V + i;
+            w[j][i] = c < a.D && a.w != nullptr ? a.w[c] : 1.0f;
+            b[j][i] = c < a.D && a.b != nullptr ? a.b[c] : 0.0f;
+        }
+    struct Row {
+        VecT<T, V> x[NV], res[NV];
+    };
+    Row next;
+    auto load = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (li + j * 64 * W) * V;
+            if (c < a.D) {
+                next.x[j] = load_once<T, V>(x + row * a.D + c);
+                if (res != nullptr) next.res[j] = load_once<T, V>(res + row * a.D + c);
+            }
+        }
+    };
+    int64_t row = (int64_t)blockIdx.x * kRows + (W == 1 ? threadIdx.x >> 6 : 0);
+    if (row < a.rows) load(row);
+    for (; row < a.rows; row += step) {
         const int64_t base = row * a.D;
+        const Row cur = next;
+        if (row + step < a.rows) load(row + step);
         float f[NV][V];
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (li + j * 64 * W) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[j][i] = 0.0f;
             if (c < a.D) {
-                const VecT<T, V> x = load_once<T, V>(static_cast<const T *>(a.x) + base + c);
 #pragma unroll
-                for (int i = 0; i < V; ++i) f[j][i] = (float)x.v[i];
-                if (a.res != nullptr) {
-                    const VecT<T, V> r = load_once<T, V>(static_cast<const T *>(a.res) + base + c);
+                for (int i = 0; i < V; ++i) f[j][i] = (float)cur.x[j].v[i];
+                if (res != nullptr) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) f[j][i] = (float)(T)(f[j][i] + (float)r.v[i]);
+                    for (int i = 0; i < V; ++i) f[j][i] = (float)(T)(f[j][i] + (float)cur.res[j].v[i]);
                     store_vec<T, V>(static_cast<T *>(a.s) + base + c, f[j]);
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) f[j][i] = 0.0f;
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) sum += f[j][i];
@@ -102,14 +129,8 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
         for (int j = 0; j < NV; ++j) {
             const int c = (li + j * 64 * W) * V;
             if (c < a.D) {
-                float w[V], b[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    w[i] = a.w != nullptr ? a.w[c + i] : 1.0f;
-                    b[i] = a.b != nullptr ? a.b[c + i] : 0.0f;
-                }
-#pragma unroll
-                for (int i = 0; i < V; ++i) f[j][i] = fmaf(f[j][i] * rstd, w[i], b[i]);
+                for (int i = 0; i < V; ++i) f[j][i] = fmaf(f[j][i] * rstd, w[j][i], b[j][i]);
                 store_vec<T, V>(static_cast<T *>(a.y) + base + c, f[j]);
             }
         }
@@ -389,7 +410,7 @@ __global__ __launch_bounds__(1024) void ln_reduce_kernel(const float *part, int 
 
 template <typename T, int V>
 void ln_fwd_launch(const LnFwdArgs &a, hipStream_t s) {
-    const int64_t cap = (int64_t)1 << 30;
+    const int64_t cap = (int64_t)device_cu_count() * 4;
     const int g1 = (int)std::min<int64_t>((a.rows + 3) / 4, cap), g4 = (int)std::min<int64_t>(a.rows, cap);
     if (a.D <= 512) ln_fwd_kernel<T, V, 1, 8><<<g1, kThreads, 0, s>>>(a);
     else if (a.D <= 1024) ln_fwd_kernel<T, V, 1, 16><<<g1, kThreads, 0, s>>>(a);
