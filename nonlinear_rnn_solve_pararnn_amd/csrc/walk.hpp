@@ -163,9 +163,20 @@ struct Rows {
     int rev;
 
     // Address and bytes of chunk i of cnt positions (none: nothing to read or write).
+    __device__ __forceinline__ const char *at(int i, int cnt, int C) const {
+        return p + i * step + (rev ? (C - cnt) * (int64_t)row_bytes : 0);
+    }
+    __device__ __forceinline__ uint32_t bytes(int cnt) const { return cnt == 0 ? 0u : (uint32_t)(cnt - 1) * row_bytes + tail; }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk(int i, int cnt, int C) const {
-        return buffer_of(p + i * step + (rev ? (C - cnt) * (int64_t)row_bytes : 0),
-                         cnt == 0 ? 0u : (uint32_t)(cnt - 1) * row_bytes + tail);
+        return buffer_of(at(i, cnt, C), bytes(cnt));
+    }
+    // The same in whole words of memory, for rows of 2-byte elements that begin
+    // anywhere: `skew` bytes before the chunk's first element the buffer begins,
+    // and it ends with the word that holds the last one.
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_words(int i, int cnt, int C, uint32_t &skew) const {
+        const char *first = at(i, cnt, C);
+        skew = (uint32_t)(uintptr_t)first & 3u;
+        return buffer_of(first - skew, cnt == 0 ? 0u : (skew + bytes(cnt) + 3u) & ~3u);
     }
     // Offset of a chunk's row r in it, if the chunk is whole; shift() less in a shorter one.
     __device__ __forceinline__ uint32_t row_at(int r, int C) const { return (uint32_t)(rev ? C - 1 - r : r) * row_bytes; }
@@ -179,78 +190,124 @@ __device__ __forceinline__ Rows rows_of(const WalkView &v, int64_t b, int64_t h,
     return {p + (rev ? L - begin - C : begin) * row, rev ? -row * C : row * C, (uint32_t)row, (uint32_t)((d - c0) * (int)sizeof(T)), rev};
 }
 
-// A thread's share of one tile of W columns (groups of 8 elements), loaded
-// ahead of its use.  VEC: rows are 16-byte aligned and whole numbers of
-// 16-byte pieces; otherwise elements are loaded one by one.
-template <typename T, int W, int C, bool VEC>
-struct Ahead {
-    static constexpr int kGroups = W / 8, kN = (C * kGroups + kThreads - 1) / kThreads, kV = 16 / (int)sizeof(T);
-    struct alignas(16) {
-        T v[8];
-    } r[kN];
-    // Where the groups of a row divide the threads, a thread's pieces are the
+// A thread's groups of 8 elements of a tile of W columns.
+template <int W, int C>
+struct Groups {
+    static constexpr int kGroups = W / 8, kN = (C * kGroups + kThreads - 1) / kThreads;
+    // Where the groups of a row divide the threads, a thread's groups are the
     // same columns kThreads / kGroups rows apart and one offset tells them all.
     static constexpr bool kEven = kThreads % kGroups == 0;
     static constexpr int kStep = kThreads / kGroups;
     uint32_t at[kEven ? 1 : kN];  // offsets in a whole chunk
     int left;                     // columns the operand has
 
-    __device__ __forceinline__ void init(const Rows &v) {
-        left = (int)(v.tail / sizeof(T));
+    __device__ __forceinline__ void init(const Rows &v, int elem_bytes) {
+        left = (int)(v.tail / (uint32_t)elem_bytes);
 #pragma unroll
-        for (int n = 0; n < (kEven ? 1 : kN); ++n) {
-            const int i = threadIdx.x + n * kThreads, row = i / kGroups, c = (i - row * kGroups) * 8;
-            at[n] = row < C && c < left ? v.row_at(row, C) + c * (uint32_t)sizeof(T) : kNowhere;
-        }
+        for (int n = 0; n < (kEven ? 1 : kN); ++n)
+            at[n] = row(n) < C && column(n) < left ? v.row_at(row(n), C) + (uint32_t)(column(n) * elem_bytes) : kNowhere;
     }
+    __device__ __forceinline__ static int row(int n) { return (int)((threadIdx.x + n * kThreads) / kGroups); }
+    __device__ __forceinline__ static int column(int n) { return (int)((threadIdx.x + n * kThreads) % kGroups) * 8; }
+    __device__ __forceinline__ uint32_t offset(const Rows &v, int n, uint32_t shift) const {
+        return kEven ? at[0] + ((uint32_t)(v.rev ? -n : n) * kStep * v.row_bytes - shift) : at[kEven ? 0 : n] - shift;
+    }
+    // Group n, as the planes of its 8 elements, into an LDS tile.
+    template <int kP>
+    __device__ __forceinline__ static void put(bf16 *lds, int n, const bf16x8 (&p)[kP]) {
+        const int i = threadIdx.x + n * kThreads, r = i / kGroups, grp = i - r * kGroups;
+        if (C * kGroups % kThreads != 0 && r >= C) return;
+#pragma unroll
+        for (int k = 0; k < kP; ++k) *reinterpret_cast<bf16x8 *>(lds + k * C * kTileRow<W> + tile_at<W>(r, grp)) = p[k];
+    }
+};
+__device__ __forceinline__ void planes_of(const bf16 (&v)[8], bf16x8 (&p)[1]) { p[0] = *reinterpret_cast<const bf16x8 *>(&v[0]); }
+__device__ __forceinline__ void planes_of(const float (&v)[8], bf16x8 (&p)[3]) { split3(v, p); }
+
+// A thread's share of one tile, loaded ahead of its use.  VEC: rows are
+// 16-byte aligned and whole numbers of 16-byte pieces.
+template <typename T, int W, int C, bool VEC>
+struct Ahead {
+    Groups<W, C> g;
+    struct alignas(16) {
+        T v[8];
+    } r[Groups<W, C>::kN];
+
+    __device__ __forceinline__ void init(const Rows &v) { g.init(v, sizeof(T)); }
     // The cnt positions of chunk i; zeros past the ends.
     __device__ __forceinline__ void load(const Rows &v, int chunk, int cnt) {
+        constexpr int kV = 16 / (int)sizeof(T);
         const __amdgpu_buffer_rsrc_t buf = v.chunk(chunk, cnt, C);
         const uint32_t shift = v.shift(cnt, C);
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
-            const uint32_t o = kEven ? at[0] + ((uint32_t)(v.rev ? -n : n) * kStep * v.row_bytes - shift) : at[kEven ? 0 : n] - shift;
-            if constexpr (VEC) {
+        for (int n = 0; n < g.kN; ++n) {
+            const uint32_t o = g.offset(v, n, shift);
 #pragma unroll
-                for (int h = 0; h < 8 / kV; ++h) {
-                    // the second half of a group may lie past the row's end
-                    const uint32_t oh = h == 0 ? o : ((int)((threadIdx.x + n * kThreads) % kGroups) * 8 + h * kV < left ? o + 16 * h : kNowhere);
-                    *reinterpret_cast<u32x4 *>(&r[n].v[h * kV]) = __builtin_amdgcn_raw_buffer_load_b128(buf, oh, 0, 0);
-                }
-            } else {
-                const int c = (int)((threadIdx.x + n * kThreads) % kGroups) * 8;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t ok = c + k < left ? o + k * (uint32_t)sizeof(T) : kNowhere;
-                    if constexpr (sizeof(T) == 2) {
-                        const uint16_t x = __builtin_amdgcn_raw_buffer_load_b16(buf, ok, 0, 0);
-                        r[n].v[k] = *reinterpret_cast<const T *>(&x);
-                    } else {
-                        const uint32_t x = __builtin_amdgcn_raw_buffer_load_b32(buf, ok, 0, 0);
-                        r[n].v[k] = *reinterpret_cast<const T *>(&x);
-                    }
-                }
+            for (int h = 0; h < 8 / kV; ++h) {
+                // the second half of a group may lie past the row's end
+                const uint32_t oh = h == 0 ? o : (g.column(n) + h * kV < g.left ? o + 16 * h : kNowhere);
+                *reinterpret_cast<u32x4 *>(&r[n].v[h * kV]) = __builtin_amdgcn_raw_buffer_load_b128(buf, oh, 0, 0);
             }
         }
     }
+    __device__ __forceinline__ void store(const Rows &, bf16 *lds) const {
+#pragma unroll
+        for (int n = 0; n < g.kN; ++n) {
+            bf16x8 p[kPlanes<T>];
+            planes_of(r[n].v, p);
+            g.put(lds, n, p);
+        }
+    }
+};
 
-    __device__ __forceinline__ void store(bf16 *lds) const {
-        constexpr int kP = kPlanes<T>, kPlane = C * kTileRow<W>;
+// Rows that begin at any element: groups of fp32 are loaded from 4-byte
+// aligned addresses, groups of bf16 as the five words of memory that hold
+// them, and put straight when they go into LDS (forward at B=4, L=4000, H=8,
+// 77x101 bf16: 95 us, 138 with a load an element; 67 with 80x104).
+template <typename T, int W, int C>
+struct Ahead<T, W, C, false> {
+    Groups<W, C> g;
+    static constexpr bool kHalves = sizeof(T) == 2;
+    static constexpr int kWords = 2 * (int)sizeof(T);  // of a group
+    uint32_t r[Groups<W, C>::kN][kWords + 1];
+    uint32_t shift;                                    // of the loaded chunk's offsets, less the skew
+
+    __device__ __forceinline__ void init(const Rows &v) { g.init(v, sizeof(T)); }
+    __device__ __forceinline__ void load(const Rows &v, int chunk, int cnt) {
+        uint32_t skew = 0;
+        const __amdgpu_buffer_rsrc_t buf = kHalves ? v.chunk_words(chunk, cnt, C, skew) : v.chunk(chunk, cnt, C);
+        shift = v.shift(cnt, C) - skew;
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
-            const int i = threadIdx.x + n * kThreads, row = i / kGroups, grp = i - row * kGroups;
-            if (C * kGroups % kThreads != 0 && row >= C) continue;
-            bf16x8 p[kP];
-            if constexpr (kP == 1) {
-                p[0] = *reinterpret_cast<const bf16x8 *>(&r[n].v[0]);
-            } else {
-                float f[8];
+        for (int n = 0; n < g.kN; ++n) {
+            const uint32_t o = g.offset(v, n, shift) & ~3u;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] = (float)r[n].v[k];
-                split3(f, p);
+            for (int h = 0; h < kWords / 4; ++h) {
+                const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(buf, o + 16 * h, 0, 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) r[n][4 * h + k] = x[k];
             }
+            r[n][kWords] = kHalves ? __builtin_amdgcn_raw_buffer_load_b32(buf, o + 16, 0, 0) : 0u;
+        }
+    }
+    __device__ __forceinline__ void store(const Rows &v, bf16 *lds) const {
 #pragma unroll
-            for (int k = 0; k < kP; ++k) *reinterpret_cast<bf16x8 *>(lds + k * kPlane + tile_at<W>(row, grp)) = p[k];
+        for (int n = 0; n < g.kN; ++n) {
+            const uint32_t bits = kHalves ? (g.offset(v, n, shift) & 2u) << 3 : 0u;
+            const int valid = g.left - g.column(n);  // what follows the row's last column belongs to others
+            union {
+                uint32_t w[kWords];
+                T v[8];
+            } u;
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) {
+                constexpr int kPer = 4 / (int)sizeof(T);
+                uint32_t x = kHalves ? __builtin_amdgcn_alignbit(r[n][k + 1], r[n][k], bits) : r[n][k];
+                if (kHalves && valid == k * kPer + 1) x &= 0xffffu;
+                u.w[k] = valid <= k * kPer ? 0u : x;
+            }
+            bf16x8 p[kPlanes<T>];
+            planes_of(u.v, p);
+            g.put(lds, n, p);
         }
     }
 };
@@ -393,9 +450,9 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
         az[d].load(rz, i, cnt);
     };
     auto put = [&](int d) {
-        if (kOut) ax.store(X);
-        ay[d].store(Y);
-        az[d].store(Z);
+        if (kOut) ax.store(rx, X);
+        ay[d].store(ry, Y);
+        az[d].store(rz, Z);
     };
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) load(d, d);
