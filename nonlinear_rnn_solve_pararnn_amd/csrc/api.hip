@@ -6,6 +6,7 @@
 
 #include "pararnn.h"
 #include "launch.hpp"
+#include "sequence.hpp"
 
 using namespace prn;
 

@@ -11,8 +11,8 @@
 // split by sorted positions, not by table rows.  Runs that cross chunks leave
 // fp32 partial sums that a second kernel adds in order.  There are no
 // floating-point atomics: the result depends on the inputs alone.
-#include "launch.hpp"
 #include "rows.hpp"
+#include "sequence.hpp"
 
 namespace prn {
 

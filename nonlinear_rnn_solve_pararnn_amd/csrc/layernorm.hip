@@ -13,8 +13,8 @@
 // pass of the variance costs no traffic.  W waves share a row: one for rows
 // up to 1024 elements (no barrier), four above.  All statistics and sums are
 // fp32.
-#include "launch.hpp"
 #include "rows.hpp"
+#include "sequence.hpp"
 
 namespace prn {
 

@@ -15,8 +15,8 @@
 // weight 1 and the walk ends on the gradient of the initial state.
 #pragma once
 
-#include "launch.hpp"
 #include "rows.hpp"
+#include "sequence.hpp"
 
 namespace prn {
 
