@@ -357,11 +357,14 @@ enum { PARARNN_F32 = 0, PARARNN_BF16 = 1 };
  *     S_t = e^g S_{t-1} + k_t^T v_t,   o_t = scale q_t S_t,   S_{-1} = state.
  * q, k: [B, L, H, dk]; v, o: [B, L, H, dv]; state, out_state: [B, H, dk, dv]
  * fp32 (state NULL: zeros; out_state NULL: not wanted; out_state may be
- * state itself, but not overlap it otherwise).  log_decay: [H] fp32.  1 <= dk, dv <= 256 (above:
- * PARARNN_ERR_UNSUPPORTED).
+ * state itself, but not overlap it otherwise).  log_decay: [H] fp32.
+ * 1 <= dk, dv <= 256 (above: PARARNN_ERR_UNSUPPORTED).  B H is below 2^24, or
+ * 2^24 over the column blocks of 64 in dv (three times those of the wider of
+ * dk and dv in the backward pass).
  * strides: HOST array of {batch row, position, head} strides in elements for
  * q, k and v in turn (9 values), not negative, a position's below 2^22; the
- * last dimension is dense.  NULL: dense tensors (H max(dk, dv) < 2^22).  Operands whose rows are 16-byte aligned move faster.
+ * last dimension is dense.  NULL: dense tensors (H max(dk, dv) < 2^22).
+ * Operands whose rows are 16-byte aligned move faster.
  * A value that is not finite at position t of q, k or v affects no output
  * before t; from t on the affected outputs are not finite (an infinity may
  * come out as NaN).
@@ -381,7 +384,7 @@ int pararnn_linattn_forward(int32_t dtype, int64_t B, int64_t L, int64_t H, int6
  *     dstate = e^g D_0.
  * The log decay is a constant of the model and gets no gradient.
  * strides: as above for q, k, v and grad_o (12 values).  grad_state: NULL if
- * not wanted.
+ * not wanted; it must not overlap state or grad_out_state.
  */
 int pararnn_linattn_backward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk, int64_t dv,
                              const void *q, const void *k, const void *v, const void *grad_o,
@@ -418,6 +421,7 @@ int pararnn_layernorm_forward(int32_t dtype, int64_t rows, int64_t D, const void
  *     grad_x = rstd (g - mean(g) - xh mean(g xh)) + grad_sum
  * (the gradient of x and of the residual alike), grad_weight = sum over rows
  * of grad_y xh, grad_bias = sum over rows of grad_y, [D] fp32 each or NULL.
+ * grad_x may be grad_y or grad_sum itself.
  * ws: pararnn_layernorm_workspace_bytes (unused, may be NULL, when neither
  * weight nor bias gradient is wanted).
  */
@@ -430,7 +434,8 @@ int pararnn_layernorm_backward(int32_t dtype, int64_t rows, int64_t D, const voi
 /*
  * Embedding lookup: out[n] = scale table[ids[n]], table [V, D], out [N, D];
  * ids: int32 or int64 (id_bytes 4 or 8).  An id outside [0, V) reads nothing
- * and gives a row of NaN.  N, V < 2^30, D < 2^24.
+ * and gives a row of NaN.  N < 2^28 - 16, V < 2^30, D < 2^24,
+ * N D < 2^36.
  */
 int pararnn_embedding_forward(int32_t dtype, int64_t N, int64_t V, int64_t D, const void *ids,
                               int32_t id_bytes, const void *table, float scale, void *out, void *stream);

@@ -131,10 +131,18 @@ bool type_ok(int32_t dtype) { return dtype == PARARNN_F32 || dtype == PARARNN_BF
 
 constexpr int64_t kMaxRowBytes = (int64_t)1 << 24;  // a chunk of 64 rows stays within 32-bit offsets
 
-bool linattn_dims_ok(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk, int64_t dv) {
+// A launch counts its threads in 32 bits: workgroups of 256.
+bool blocks_ok(int64_t n) { return n < (int64_t)1 << 24; }
+
+// What a call launches: the walk of the outputs, the gradients' three, or the token's step.
+enum class LinattnPass { Forward, Backward, Step };
+
+bool linattn_dims_ok(LinattnPass pass, int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk, int64_t dv) {
     if (!type_ok(dtype) || dk < 1 || dk > kMaxHeadDim || dv < 1 || dv > kMaxHeadDim) return false;
-    // at most 3 walks of 4 column blocks a (batch row, head)
-    return dims_ok(B, L, H) && dims_ok(B, L, H * kMaxHeadDim) && grid_ok((B * H + 7) * 12) &&
+    auto blocks = [](int64_t cols) { return (cols + 63) / 64; };
+    // workgroups a (batch row, head); sequences are cut into segments only where there are few of them
+    const int64_t per = pass == LinattnPass::Forward ? blocks(dv) : pass == LinattnPass::Backward ? 3 * blocks(std::max(dk, dv)) : 1;
+    return dims_ok(B, L, H) && dims_ok(B, L, H * kMaxHeadDim) && blocks_ok((B * H + 7) * per) &&
            H * std::max(dk, dv) * 4 < kMaxRowBytes;
 }
 
@@ -177,8 +185,10 @@ bool layernorm_dims_ok(int32_t dtype, int64_t rows, int64_t D) {
 
 bool embedding_dims_ok(int32_t dtype, int64_t N, int64_t V, int64_t D) {
     const int64_t most = (int64_t)1 << 30;
+    // the lookup takes at least 16 rows a workgroup, the sums four times 64
+    // positions (fewer where that makes few workgroups) of at least 64 columns
     return type_ok(dtype) && dims_ok(N, D, 1) && dims_ok(V, D, 1) && N < most && V < most && D < ((int64_t)1 << 24) &&
-           grid_ok((N / 16 + 1) * (D / 64 + 1) + V / 256 + 1);
+           blocks_ok(N / 16 + 1) && blocks_ok((N / 64 + 1) * (D / 64 + 1) / 4 + 8192);
 }
 
 }  // namespace
@@ -439,7 +449,7 @@ int pararnn_adjoint_backward(int32_t cell, int64_t B, int64_t L, int64_t H, cons
 // ---------------------------------------------------------------- operators around the recurrences
 size_t pararnn_linattn_workspace_bytes(int32_t backward, int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk,
                                        int64_t dv) {
-    if (!linattn_dims_ok(dtype, B, L, H, dk, dv)) return 0;
+    if (!linattn_dims_ok(backward ? LinattnPass::Backward : LinattnPass::Forward, dtype, B, L, H, dk, dv)) return 0;
     return linattn_ws(linattn_shape(dtype, B, L, H, dk, dv), backward != 0);
 }
 
@@ -448,7 +458,8 @@ int pararnn_linattn_forward(int32_t dtype, int64_t B, int64_t L, int64_t H, int6
                             const float *state, float scale, void *o, float *out_state, void *ws, size_t ws_bytes,
                             void *stream) {
     if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
-    if (!linattn_dims_ok(dtype, B, L, H, dk, dv) || !q || !k || !v || !log_decay || !o) return PARARNN_ERR_INVALID;
+    if (!linattn_dims_ok(LinattnPass::Forward, dtype, B, L, H, dk, dv) || !q || !k || !v || !log_decay || !o)
+        return PARARNN_ERR_INVALID;
     LinattnArgs a = linattn_shape(dtype, B, L, H, dk, dv);
     const void *in[3] = {q, k, v};
     if (!linattn_inputs(a, in, 3, strides)) return PARARNN_ERR_INVALID;
@@ -468,13 +479,16 @@ int pararnn_linattn_backward(int32_t dtype, int64_t B, int64_t L, int64_t H, int
                              void *grad_q, void *grad_k, void *grad_v, float *grad_state, void *ws, size_t ws_bytes,
                              void *stream) {
     if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
-    if (!linattn_dims_ok(dtype, B, L, H, dk, dv) || !q || !k || !v || !grad_o || !log_decay || !grad_q || !grad_k ||
-        !grad_v)
+    if (!linattn_dims_ok(LinattnPass::Backward, dtype, B, L, H, dk, dv) || !q || !k || !v || !grad_o || !log_decay ||
+        !grad_q || !grad_k || !grad_v)
         return PARARNN_ERR_INVALID;
     LinattnArgs a = linattn_shape(dtype, B, L, H, dk, dv);
     const void *in[4] = {q, k, v, grad_o};
     if (!linattn_inputs(a, in, 4, strides)) return PARARNN_ERR_INVALID;
     if (!ws || ws_bytes < linattn_ws(a, true) || !aligned(ws, 256)) return PARARNN_ERR_INVALID;
+    // both states are read by walks beside the one that ends on grad_state
+    const int64_t n = B * H * dk * dv;
+    if (overlaps(state, grad_state, n) || overlaps(grad_out_state, grad_state, n)) return PARARNN_ERR_INVALID;
     a.log_decay = log_decay;
     a.state = state;
     a.scale = scale;
@@ -490,7 +504,7 @@ int pararnn_linattn_step(int32_t dtype, int64_t B, int64_t H, int64_t dk, int64_
                          const void *v, const int64_t *strides, const float *log_decay, const float *state, float scale,
                          void *o, float *out_state, void *stream) {
     if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
-    if (!linattn_dims_ok(dtype, B, 1, H, dk, dv) || !q || !k || !v || !log_decay || !state || !o || !out_state)
+    if (!linattn_dims_ok(LinattnPass::Step, dtype, B, 1, H, dk, dv) || !q || !k || !v || !log_decay || !state || !o || !out_state)
         return PARARNN_ERR_INVALID;
     LinattnArgs a = linattn_shape(dtype, B, 1, H, dk, dv);
     const void *in[3] = {q, k, v};

@@ -444,9 +444,9 @@ hipError_t ln_bwd(const LnBwdArgs &a, int G, float *gw, float *gb, hipStream_t s
     const bool vec = a.D % kVec<T> == 0 && aligned16(a.s) && aligned16(a.dy) && aligned16(a.dx) &&
                      (a.ds == nullptr || aligned16(a.ds));
     if (a.D > kLongRow) {
-        ln_bwd_long_kernel<T><<<(int)std::min<int64_t>(a.rows, (int64_t)device_cu_count() * 8), kThreads, 0, s>>>(a);
-        if (a.part != nullptr)
+        if (a.part != nullptr)  // first: it reads what grad_x may overwrite
             ln_bwd_cols_kernel<T><<<dim3((a.D + kThreads - 1) / kThreads, G), kThreads, 0, s>>>(a);
+        ln_bwd_long_kernel<T><<<(int)std::min<int64_t>(a.rows, (int64_t)device_cu_count() * 8), kThreads, 0, s>>>(a);
     } else if (a.D <= kShortRow) ln_bwd_short_kernel<T><<<G, kThreads, 0, s>>>(a);
     else if (vec) ln_bwd_launch<T, kVec<T>>(a, G, s);
     else ln_bwd_launch<T, 1>(a, G, s);

@@ -111,7 +111,7 @@ hipError_t run_walks(WalkArgs &a, const WalkPlan &w, const Ws &ws, hipStream_t s
 // partial products with q meet in shared memory.
 struct StepArgs {
     int64_t BH, H;
-    int dk, dv, cols, lanes;  // lanes (a power of two) threads over the columns
+    int dk, dv, lanes;  // lanes (a power of two) threads over the columns
     const void *q, *k, *v;
     int64_t qb, qh, kb, kh, vb, vh;
     const float *log_decay, *state;
@@ -217,7 +217,7 @@ hipError_t linattn_step(const LinattnArgs &p, hipStream_t s) {
     const int cols = al ? p.dv / 4 : p.dv;
     int lanes = 1;
     while (lanes < cols) lanes *= 2;
-    const StepArgs a{p.B * p.H, p.H, p.dk, p.dv, cols, lanes, p.q, p.k, p.v,
+    const StepArgs a{p.B * p.H, p.H, p.dk, p.dv, lanes, p.q, p.k, p.v,
                      p.st[0][0], p.st[0][2], p.st[1][0], p.st[1][2], p.st[2][0], p.st[2][2],
                      p.log_decay, p.state, p.scale, p.o, p.out_state};
     const unsigned grid = (unsigned)a.BH;

@@ -49,8 +49,11 @@ struct WalkArgs {
     float *seg_state;  // T of every piece, in the walk's register layout
 };
 
-// The head's decay, kept finite so that 0 * g is 0.
-__device__ __forceinline__ float walk_gate(const float *log_decay, int64_t h) { return fmaxf(log_decay[h], -1e30f); }
+// The head's decay, kept above -infinity so that 0 * g is 0 (a NaN stays one).
+__device__ __forceinline__ float walk_gate(const float *log_decay, int64_t h) {
+    const float g = log_decay[h];
+    return g < -1e30f ? -1e30f : g;
+}
 
 // e^(g n) - 1 in double, rounded once: the state is carried over a chunk as
 // T + T (e^(g n) - 1), whose rounding does not repeat from chunk to chunk the

@@ -203,6 +203,8 @@ class LinearAttention(torch.nn.Module):
         if x.dim() != 2 or x.shape[-1] != self.dim:
             raise ValueError("x must be [B, %d], got %s" % (self.dim, tuple(x.shape)))
         o, state = api.linattn_step(*self._project(x), self.log_decay, state, out_state=state)
+        if not state.is_inference():  # autograd learns of the change where the state was saved
+            torch.autograd.graph.increment_version(state)
         return F.linear(o.flatten(1), self.out), state
 
     def extra_repr(self):
