@@ -10,6 +10,7 @@ missing library raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -540,6 +541,12 @@ def _need_typed(t, shape, dtype, name, device):
         raise ValueError("%s must be contiguous" % name)
 
 
+@functools.lru_cache(maxsize=1024)
+def _linattn_ws(backward: int, *sizes) -> int:
+    """pararnn_linattn_workspace_bytes, which depends on the sizes alone (asked once per set of sizes)."""
+    return load_library().pararnn_linattn_workspace_bytes(backward, *sizes)
+
+
 def _linattn_views(tensors, shapes, names, dtype, device):
     """Checks the operands; the strides array the library takes, or None if all are dense."""
     dense = True
@@ -567,14 +574,15 @@ def _linattn_views(tensors, shapes, names, dtype, device):
 
 def _linattn_check(q, v, seq: bool):
     code = _type_code(q, "q")
-    if q.dim() != 3 + seq or not isinstance(v, torch.Tensor) or v.dim() != 3 + seq:
+    shape = q.shape
+    if len(shape) != 3 + seq or not isinstance(v, torch.Tensor) or v.dim() != 3 + seq:
         raise ValueError("q, k and v must be %s" % ("[B, L, H, d]" if seq else "[B, H, d]"))
-    dk, dv = q.shape[-1], v.shape[-1]
-    if q.numel() == 0 or dv == 0:
-        raise PararnnError("invalid sizes q %s, v %s" % (tuple(q.shape), tuple(v.shape)))
+    dk, dv = shape[-1], v.shape[-1]
+    if 0 in shape or dv == 0:
+        raise PararnnError("invalid sizes q %s, v %s" % (tuple(shape), tuple(v.shape)))
     if dk > MAX_HEAD_DIM or dv > MAX_HEAD_DIM:
         raise PararnnError("linear attention supports head sizes up to %d, got dk=%d dv=%d" % (MAX_HEAD_DIM, dk, dv))
-    return code, dk, dv
+    return code, dk, dv, shape
 
 
 def linattn_forward(q, k, v, log_decay, state=None, *, scale=None, want_state=True, out=None, out_state=None,
@@ -587,23 +595,23 @@ def linattn_forward(q, k, v, log_decay, state=None, *, scale=None, want_state=Tr
     scale defaults to dk^-0.5.  Returns (o [B, L, H, dv], final state or None
     unless want_state).  out_state may be `state` itself."""
     lib = load_library()
-    code, dk, dv = _linattn_check(q, v, True)
-    B, L, H, _ = q.shape
+    code, dk, dv, kshape = _linattn_check(q, v, True)
+    B, L, H, _ = kshape
     dev = q.device
-    kshape, vshape, sshape = (B, L, H, dk), (B, L, H, dv), (B, H, dk, dv)
+    vshape, sshape = (B, L, H, dv), (B, H, dk, dv)
     st = _linattn_views((q, k, v), (kshape, kshape, vshape), ("q", "k", "v"), q.dtype, dev)
     _need_typed(log_decay, (H,), torch.float32, "log_decay", dev)
     if state is not None:
         _need_typed(state, sshape, torch.float32, "state", dev)
     if out is None:
-        out = torch.empty_like(v, memory_format=torch.contiguous_format)
+        out = v.new_empty(vshape)
     else:
         _need_typed(out, vshape, q.dtype, "out", dev)
     if out_state is not None:
         _need_typed(out_state, sshape, torch.float32, "out_state", dev)
     elif want_state:
-        out_state = torch.empty(sshape, dtype=torch.float32, device=dev)
-    buf, n = _workspace_of(lib.pararnn_linattn_workspace_bytes(0, code, B, L, H, dk, dv), dev, ws)
+        out_state = log_decay.new_empty(sshape)
+    buf, n = _workspace_of(_linattn_ws(0, code, B, L, H, dk, dv), dev, ws)
     _check(lib.pararnn_linattn_forward(code, B, L, H, dk, dv, _at(q), _at(k), _at(v), st, _at(log_decay),
                                        _at(state), dk ** -0.5 if scale is None else scale, _at(out),
                                        _at(out_state), _at(buf), n, _raw_stream(dev)), "pararnn_linattn_forward")
@@ -617,10 +625,10 @@ def linattn_backward(q, k, v, log_decay, grad_o, state=None, grad_state=None, *,
     None unless want_state (default: whether a state is given).  log_decay is
     a constant of the model and gets no gradient."""
     lib = load_library()
-    code, dk, dv = _linattn_check(q, v, True)
-    B, L, H, _ = q.shape
+    code, dk, dv, kshape = _linattn_check(q, v, True)
+    B, L, H, _ = kshape
     dev = q.device
-    kshape, vshape, sshape = (B, L, H, dk), (B, L, H, dv), (B, H, dk, dv)
+    vshape, sshape = (B, L, H, dv), (B, H, dk, dv)
     st = _linattn_views((q, k, v, grad_o), (kshape, kshape, vshape, vshape), ("q", "k", "v", "grad_o"), q.dtype, dev)
     _need_typed(log_decay, (H,), torch.float32, "log_decay", dev)
     for t, name in ((state, "state"), (grad_state, "grad_state")):
@@ -630,7 +638,7 @@ def linattn_backward(q, k, v, log_decay, grad_o, state=None, grad_state=None, *,
         want_state = state is not None
     gq, gk, gv = (torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k, v))
     gs = torch.empty(sshape, dtype=torch.float32, device=dev) if want_state else None
-    buf, n = _workspace_of(lib.pararnn_linattn_workspace_bytes(1, code, B, L, H, dk, dv), dev, ws)
+    buf, n = _workspace_of(_linattn_ws(1, code, B, L, H, dk, dv), dev, ws)
     _check(lib.pararnn_linattn_backward(code, B, L, H, dk, dv, _at(q), _at(k), _at(v), _at(grad_o), st,
                                         _at(log_decay), _at(state), _at(grad_state),
                                         dk ** -0.5 if scale is None else scale, _at(gq), _at(gk), _at(gv),
@@ -643,19 +651,19 @@ def linattn_step(q, k, v, log_decay, state, *, scale=None, out=None, out_state=N
     state [B, H, dk, dv].  Returns (o [B, H, dv], new state); out_state may be
     `state` itself."""
     lib = load_library()
-    code, dk, dv = _linattn_check(q, v, False)
-    B, H, _ = q.shape
+    code, dk, dv, kshape = _linattn_check(q, v, False)
+    B, H, _ = kshape
     dev = q.device
-    kshape, vshape, sshape = (B, H, dk), (B, H, dv), (B, H, dk, dv)
+    vshape, sshape = (B, H, dv), (B, H, dk, dv)
     st = _linattn_views((q, k, v), (kshape, kshape, vshape), ("q", "k", "v"), q.dtype, dev)
     _need_typed(log_decay, (H,), torch.float32, "log_decay", dev)
     _need_typed(state, sshape, torch.float32, "state", dev)
     if out is None:
-        out = torch.empty_like(v, memory_format=torch.contiguous_format)
+        out = v.new_empty(vshape)
     else:
         _need_typed(out, vshape, q.dtype, "out", dev)
     if out_state is None:
-        out_state = torch.empty(sshape, dtype=torch.float32, device=dev)
+        out_state = log_decay.new_empty(sshape)
     else:
         _need_typed(out_state, sshape, torch.float32, "out_state", dev)
     _check(lib.pararnn_linattn_step(code, B, H, dk, dv, _at(q), _at(k), _at(v), st, _at(log_decay), _at(state),
