@@ -188,7 +188,7 @@ bool embedding_dims_ok(int32_t dtype, int64_t N, int64_t V, int64_t D) {
     // the lookup takes at least 16 rows a workgroup, the sums four times 64
     // positions (fewer where that makes few workgroups) of at least 64 columns
     return type_ok(dtype) && dims_ok(N, D, 1) && dims_ok(V, D, 1) && N < most && V < most && D < ((int64_t)1 << 24) &&
-           blocks_ok(N / 16 + 1) && blocks_ok((N / 64 + 1) * (D / 64 + 1) / 4 + 8192);
+           blocks_ok(N / 16 + 1) && blocks_ok((N / 64 + 1) * (D / 64 + 1) / 4 + 32768);
 }
 
 }  // namespace

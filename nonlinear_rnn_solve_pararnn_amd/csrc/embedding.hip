@@ -4,13 +4,22 @@
 //   out[n] = scale table[ids[n]]
 //   dtable[r] = scale * sum over n with ids[n] = r, in ascending n, of grad[n]
 //
-// The lookup is a gather of whole rows, bound by memory.  The gradient sorts
+// The lookup is a gather of whole rows, bound by memory: 32768 rows of
+// 50000x1024 bf16 in 18.5 us, 134 MB at 7.3 TB/s, as frequent rows come from
+// the caches.  The gradient sorts
 // the (id, position) pairs by a stable radix sort, cuts the sorted list into
 // chunks of equal length and adds each run of equal ids within a chunk: a
 // natural text's most frequent token has thousands of rows, so the work is
 // split by sorted positions, not by table rows.  Runs that cross chunks leave
 // fp32 partial sums that a second kernel adds in order.  There are no
 // floating-point atomics: the result depends on the inputs alone.
+// Measured: 8192 tokens into 32768x1024 fp32, 48 us (four launches of the sort
+// with the clearing beside them 33, sums 12, join 5; 168 MB move at the least,
+// 33 us at a copy's 5.1 TB/s); 65536 tokens into 50000x2048 bf16, 138 us
+// (51, 78, 9; 473 MB, 93 us).  Streaming the gradient's loads past the caches
+// takes 74 us instead of 78 for the sums of the second and 13.4 instead of
+// 11.8 for those of the first, whose gradient the caches still hold, and was
+// left out.
 #include "rows.hpp"
 #include "sequence.hpp"
 
@@ -37,8 +46,11 @@ struct EmbFwdArgs {
 
 constexpr int kLookRows = 4;  // rows whose loads a thread keeps in flight
 
-template <typename T, int V>
+// Rows that begin at any element: 65536 rows of 50000x2047 bf16 in 141 us
+// (210 an element at a time; 103 for 2048 columns).
+template <typename T, bool VEC>
 __global__ __launch_bounds__(kThreads) void emb_lookup_kernel(EmbFwdArgs a) {
+    constexpr int V = kVec<T>;
     const int li = threadIdx.x & (a.lanes - 1);
     const int per = kThreads / a.lanes;  // rows a workgroup takes at once
     const int64_t n0 = (int64_t)blockIdx.x * per * kLookRows + threadIdx.x / a.lanes;
@@ -49,11 +61,12 @@ __global__ __launch_bounds__(kThreads) void emb_lookup_kernel(EmbFwdArgs a) {
         key[r] = n < a.N ? id_key(a.ids, a.wide, n, a.V) : (uint32_t)a.V;
     }
     const float bad = __uint_as_float(0x7fc00000u);
-    for (int c = li * V; c < a.D; c += a.lanes * V) {
+    for (int c0 = li * V; c0 < a.D; c0 += a.lanes * V) {
+        const int c = group_at<T, VEC>(c0, a.D);
         float f[kLookRows][V];
 #pragma unroll
         for (int r = 0; r < kLookRows; ++r) {
-            if (key[r] < (uint32_t)a.V) load_vec<T, V>(static_cast<const T *>(a.table) + (int64_t)key[r] * a.D + c, f[r]);
+            if (key[r] < (uint32_t)a.V) load_group<T, VEC>(static_cast<const T *>(a.table) + (int64_t)key[r] * a.D + c, a.D, f[r]);
             else
 #pragma unroll
                 for (int i = 0; i < V; ++i) f[r][i] = bad;
@@ -64,7 +77,7 @@ __global__ __launch_bounds__(kThreads) void emb_lookup_kernel(EmbFwdArgs a) {
             if (n >= a.N) continue;
 #pragma unroll
             for (int i = 0; i < V; ++i) f[r][i] *= a.scale;
-            store_vec<T, V>(static_cast<T *>(a.out) + n * a.D + c, f[r]);
+            store_group<T, VEC>(static_cast<T *>(a.out) + n * a.D + c, a.D, f[r]);
         }
     }
 }
@@ -329,19 +342,22 @@ struct EmbSumArgs {
 constexpr int kBatch = 8;         // rows whose loads are in flight
 constexpr uint32_t kNoKey = ~0u;  // above every key
 
-template <typename T, int V>
+// A wave takes a chunk for 64 groups of columns (65536 tokens, 50000x2047 bf16:
+// the whole gradient 157 us, 271 an element at a time; 136 for 2048 columns).
+template <typename T, bool VEC>
 __global__ __launch_bounds__(kThreads) void emb_sum_kernel(EmbSumArgs a) {
+    constexpr int V = kVec<T>;
     const int lane = threadIdx.x & 63;
     const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     if (item >= a.chunks * a.cols) return;
     const int64_t chunk = item / a.cols;
-    const int c = (int)(item - chunk * a.cols) * 64 * V + lane * V;
+    const int c0 = (int)(item - chunk * a.cols) * 64 * V + lane * V, c = group_at<T, VEC>(c0, a.D);
     const int64_t n0 = chunk * a.run;
     const int cnt = (int)min((int64_t)a.run, a.N - n0);
     const uint32_t mykey = a.key[n0 + min(lane, cnt - 1)], mypos = a.pos[n0 + min(lane, cnt - 1)];
     const uint32_t prev = n0 > 0 ? a.key[n0 - 1] : kNoKey;
     const uint32_t next = n0 + cnt < a.N ? a.key[n0 + cnt] : kNoKey;
-    const bool in = c < a.D;
+    const bool in = c0 < a.D;
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
@@ -353,12 +369,13 @@ __global__ __launch_bounds__(kThreads) void emb_sum_kernel(EmbSumArgs a) {
             if (head || tail) {
                 float *p = a.part + ((chunk * 2 + (head ? 0 : 1)) * a.D + c);
 #pragma unroll
-                for (int i = 0; i < V; ++i) p[i] = acc[i];
+                for (int i = 0; i < V; ++i)
+                    if (VEC || i < a.D) p[i] = acc[i];
             } else {
                 float f[V];
 #pragma unroll
                 for (int i = 0; i < V; ++i) f[i] = acc[i] * a.scale;
-                store_vec<T, V>(static_cast<T *>(a.out) + (int64_t)cur * a.D + c, f);
+                store_group<T, VEC>(static_cast<T *>(a.out) + (int64_t)cur * a.D + c, a.D, f);
             }
         }
 #pragma unroll
@@ -369,7 +386,7 @@ __global__ __launch_bounds__(kThreads) void emb_sum_kernel(EmbSumArgs a) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int64_t row = (int64_t)__builtin_amdgcn_readlane(mypos, min(b + u, cnt - 1));
-            if (in) load_vec<T, V>(static_cast<const T *>(a.grad) + row * a.D + c, f[u]);
+            if (in) load_group<T, VEC>(static_cast<const T *>(a.grad) + row * a.D + c, a.D, f[u]);
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
@@ -450,11 +467,14 @@ EmbWs emb_ws(int64_t N, int64_t D) {
     const bool small = N <= kSmallN;
     w.tile = std::max<int64_t>(512, ((N + kMaxTiles - 1) / kMaxTiles + 255) / 256 * 256);
     w.tiles = (int)((N + w.tile - 1) / w.tile);
-    // chunks of up to 64 entries (one a lane), shorter where the sums would not
-    // fill the CUs (65536 x 2048 bf16: 64 entries 91 us + 10 us for the joins,
-    // 32 entries 94 + 17)
-    const int64_t per_cu = N * ((D + 511) / 512) / (4 * device_cu_count());
-    w.run = per_cu >= 64 ? 64 : per_cu >= 32 ? 32 : 16;
+    // chunks of up to 64 entries (one a lane), shorter where that makes fewer
+    // than four waves a SIMD.  65536 x 2048 bf16 (four with 64 entries): 91 us +
+    // 10 us for the joins, with 32 entries 94 + 17; 65536 x 128 bf16 (one with
+    // 64): the whole gradient 48 us, with 16 entries 36; 8192 x 1024 fp32 (one
+    // with 16): sums and joins 12 + 5, with 8 entries 12 + 8; 4000 x 256 bf16
+    // (a quarter with 16): the whole gradient 22 us, with 8 entries 19.
+    const int64_t per_simd = N * ((D + 511) / 512) / (4 * device_cu_count());
+    w.run = per_simd >= 256 ? 64 : per_simd >= 128 ? 32 : per_simd >= 16 ? 16 : 8;
     w.chunks = (N + w.run - 1) / w.run;
     for (int i = 0; i < 2; ++i) {
         w.key[i] = i == 0 || !small ? take((size_t)N * 4) : w.key[0];
@@ -466,12 +486,13 @@ EmbWs emb_ws(int64_t N, int64_t D) {
     return w;
 }
 
-template <typename T, int V>
+template <typename T, bool VEC>
 hipError_t emb_sums(EmbSumArgs &a, hipStream_t s) {
+    constexpr int V = kVec<T>;
     a.cols = (a.D + 64 * V - 1) / (64 * V);
-    emb_sum_kernel<T, V><<<(unsigned)((a.chunks * a.cols + 3) / 4), kThreads, 0, s>>>(a);
+    emb_sum_kernel<T, VEC><<<(unsigned)((a.chunks * a.cols + 3) / 4), kThreads, 0, s>>>(a);
     if (a.chunks == 1) return hipGetLastError();  // no run crosses chunks
-    constexpr int J = V == 1 ? 1 : 4;
+    constexpr int J = VEC ? 4 : 1;
     a.cols = (a.D + 64 * J - 1) / (64 * J);
     emb_join_kernel<T, J><<<(unsigned)((a.chunks * a.cols + 3) / 4), kThreads, 0, s>>>(a);
     return hipGetLastError();
@@ -484,18 +505,18 @@ size_t embedding_ws(int64_t N, int64_t D) { return emb_ws(N, D).total; }
 hipError_t embedding_forward(const EmbeddingArgs &q, hipStream_t s) {
     const int es = q.bf16 ? 2 : 4, vec = 16 / es;
     const bool al = q.D % vec == 0 && aligned16(q.table) && aligned16(q.out);
-    const int64_t vecs = al ? q.D / vec : q.D;
+    const int64_t vecs = (q.D + vec - 1) / vec;
     int lanes = 1;
     while (lanes < 64 && lanes < vecs) lanes *= 2;
     const EmbFwdArgs a{q.N, q.V, (int)q.D, q.wide_ids, lanes, q.ids, q.table, q.scale, q.out};
     const int64_t per = (int64_t)kThreads / lanes * kLookRows;
     const unsigned grid = (unsigned)((q.N + per - 1) / per);
     if (q.bf16) {
-        if (al) emb_lookup_kernel<bf16, 8><<<grid, kThreads, 0, s>>>(a);
-        else emb_lookup_kernel<bf16, 1><<<grid, kThreads, 0, s>>>(a);
+        if (al) emb_lookup_kernel<bf16, true><<<grid, kThreads, 0, s>>>(a);
+        else emb_lookup_kernel<bf16, false><<<grid, kThreads, 0, s>>>(a);
     } else {
-        if (al) emb_lookup_kernel<float, 4><<<grid, kThreads, 0, s>>>(a);
-        else emb_lookup_kernel<float, 1><<<grid, kThreads, 0, s>>>(a);
+        if (al) emb_lookup_kernel<float, true><<<grid, kThreads, 0, s>>>(a);
+        else emb_lookup_kernel<float, false><<<grid, kThreads, 0, s>>>(a);
     }
     return hipGetLastError();
 }
@@ -532,8 +553,8 @@ hipError_t embedding_backward(const EmbeddingArgs &q, const Ws &ws, hipStream_t 
                  reinterpret_cast<float *>(ws.p + w.part), w.run, w.chunks, 0};
     const int vec = q.bf16 ? 8 : 4;
     const bool al = q.D % vec == 0 && aligned16(q.table) && aligned16(q.out);
-    if (q.bf16) return al ? emb_sums<bf16, 8>(a, s) : emb_sums<bf16, 1>(a, s);
-    return al ? emb_sums<float, 4>(a, s) : emb_sums<float, 1>(a, s);
+    if (q.bf16) return al ? emb_sums<bf16, true>(a, s) : emb_sums<bf16, false>(a, s);
+    return al ? emb_sums<float, true>(a, s) : emb_sums<float, false>(a, s);
 }
 
 }  // namespace prn

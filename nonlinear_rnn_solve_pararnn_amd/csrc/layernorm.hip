@@ -13,6 +13,11 @@
 // pass of the variance costs no traffic.  W waves share a row: one for rows
 // up to 1024 elements (no barrier), four above.  All statistics and sums are
 // fp32.
+//
+// Measured: forward with residual, 32768x1024 fp32, 98 us (537 MB, 5.5 TB/s);
+// backward with dw and db, 8192x4096 bf16, 49 + 5 us (201 MB, 4.1 TB/s in the
+// first); a copy of 1 GiB runs at 5.1 TB/s.  Rows that are not whole 16-byte
+// vectors: 20000x1283 fp32 forward and backward 86 us each (4.8 TB/s forward).
 #include "rows.hpp"
 #include "sequence.hpp"
 
@@ -50,7 +55,8 @@ struct LnFwdArgs {
 };
 
 // A workgroup keeps its columns' weight and bias in registers over its rows
-// and loads a row ahead.
+// and loads a row ahead (32768x1024 fp32 with residual: 98 us, 109 with one
+// row a wave and the weights read again for each; 20000x1283: 86 us, 171).
 template <typename T, int V, int W, int E>
 __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
     constexpr int NV = E / V, kRows = 4 / W;
@@ -137,7 +143,9 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
     }
 }
 
-// Rows too long for the registers: one workgroup a row, read three times.
+// Rows too long for the registers (above 8192): one workgroup a row, read
+// three times, of which the caches hold the later two for rows of up to some
+// hundred thousand elements.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ln_fwd_long_kernel(LnFwdArgs a) {
     __shared__ float2 buf[2][4];

@@ -107,8 +107,10 @@ hipError_t run_walks(WalkArgs &a, const WalkPlan &w, const Ws &ws, hipStream_t s
 // ---------------------------------------------------------------- single token
 //   S' = e^g S + k^T v,  o = scale q S'
 // Reads and writes the state once and is bound by that.  One workgroup a
-// (batch row, head): threads are columns (V of them each) by rows, the rows'
-// partial products with q meet in shared memory.
+// (batch row, head): threads are columns (V of them each) by rows, eight rows'
+// loads in flight a thread, the rows' partial products with q meet in shared
+// memory.  B=128, H=16, 128x128: 53.7 us, 270 MB at 5.0 TB/s (a copy's rate);
+// B=1: 5.6 us, where 16 workgroups wait for one round trip to memory.
 struct StepArgs {
     int64_t BH, H;
     int dk, dv, lanes;  // lanes (a power of two) threads over the columns

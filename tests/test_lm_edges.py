@@ -90,3 +90,27 @@ def test_step_over_a_saved_state_is_noticed():
     with torch.inference_mode():
         s = torch.zeros(1, 2, 16, 16, device=DEV)
         mix.step(x[:, 0], s)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,D", [(9000, 9), (700, 15), (300, 1031), (33, 518), (2500, 8), (40, 3)])
+def test_embedding_rows_that_begin_anywhere(N, D, dtype):
+    """Integers small enough that every sum is exact in bf16: groups of columns
+    that overlap at a row's end, and tensors that begin inside a word."""
+    V = 1200
+    gen = torch.Generator().manual_seed(N + D)
+
+    def inside(*shape):
+        x = torch.randint(-2, 3, shape, generator=gen).to(dtype)
+        flat = torch.empty(x.numel() + 3, dtype=dtype, device=DEV)
+        return flat[3:].view(shape).copy_(x)
+
+    ids = torch.randperm(V * 8, generator=gen)[:N].remainder(V)  # at most 8 of one id: sums up to 16
+    table, grad, ids = inside(V, D), inside(N, D), ids.to(DEV)
+    assert torch.equal(api.embedding_forward(ids, table, scale=2.0), table[ids] * 2)
+    out = torch.full((V * D + 8,), 7.0, dtype=dtype, device=DEV)
+    got = api.embedding_backward(ids, grad, V, scale=2.0, out=out[5:5 + V * D].view(V, D))
+    want = torch.zeros(V, D, dtype=torch.float64).index_add_(0, ids.cpu(), grad.cpu().double()) * 2
+    assert torch.equal(got.cpu().double(), want)
+    assert (out[:5] == 7).all() and (out[5 + V * D:] == 7).all()
