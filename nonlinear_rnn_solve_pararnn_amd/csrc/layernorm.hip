@@ -15,9 +15,13 @@
 // fp32.
 //
 // Measured: forward with residual, 32768x1024 fp32, 98 us (537 MB, 5.5 TB/s);
-// backward with dw and db, 8192x4096 bf16, 49 + 5 us (201 MB, 4.1 TB/s in the
-// first); a copy of 1 GiB runs at 5.1 TB/s.  Rows that are not whole 16-byte
-// vectors: 20000x1283 fp32 forward and backward 86 us each (4.8 TB/s forward).
+// backward with a gradient of the sum, dw and db, 8192x4096 bf16, 49 + 5 us
+// (268 MB, 5.5 TB/s in the first); a copy of 1 GiB runs at 5.1 TB/s.  Rows that
+// are not whole 16-byte vectors move an element at a time: 20000x1283 fp32
+// forward and backward 86 us each (4.8 TB/s), bf16 57 and 73 us (3.6, 2.8).
+// Rows above 8192 elements are read several times by one workgroup each:
+// 4096x16384 fp32 forward 333, backward 410 us (3.2, 2.6 TB/s of its least
+// traffic).
 #include "rows.hpp"
 #include "sequence.hpp"
 
@@ -144,8 +148,7 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
 }
 
 // Rows too long for the registers (above 8192): one workgroup a row, read
-// three times, of which the caches hold the later two for rows of up to some
-// hundred thousand elements.
+// three times.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ln_fwd_long_kernel(LnFwdArgs a) {
     __shared__ float2 buf[2][4];
