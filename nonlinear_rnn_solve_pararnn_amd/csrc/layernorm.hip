@@ -18,7 +18,9 @@
 // backward with a gradient of the sum, dw and db, 8192x4096 bf16, 49 + 5 us
 // (268 MB, 5.5 TB/s in the first); a copy of 1 GiB runs at 5.1 TB/s.  Rows that
 // are not whole 16-byte vectors move an element at a time: 20000x1283 fp32
-// forward and backward 86 us each (4.8 TB/s), bf16 57 and 73 us (3.6, 2.8).
+// forward and backward 86 us each (4.8 TB/s), bf16 57 and 73 us (3.6, 2.8);
+// groups put together from whole words were no better here (fp32 99 and 80,
+// bf16 64 and 89), as that work sits between a row's loads and the next's.
 // Rows above 8192 elements are read several times by one workgroup each:
 // 4096x16384 fp32 forward 333, backward 410 us (3.2, 2.6 TB/s of its least
 // traffic).
