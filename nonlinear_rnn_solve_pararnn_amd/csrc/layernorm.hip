@@ -10,9 +10,9 @@
 // Both passes are bound by memory: a few operations per element against 2 to
 // 4 tensors moved.  A row therefore stays in registers from its one load to
 // its store (E elements a thread, in vectors of V), so the centred second
-// pass of the variance costs no traffic.  W waves share a row: one for rows
-// up to 1024 elements (no barrier), four above.  All statistics and sums are
-// fp32.
+// pass of the variance costs no traffic.  R threads share a row: 16 lanes for
+// rows up to 128 elements, a wave up to 1024 (no barrier), the workgroup
+// above.  All statistics and sums are fp32.
 //
 // Measured: forward with residual, 32768x1024 fp32, 98 us (537 MB, 5.5 TB/s);
 // backward with a gradient of the sum, dw and db, 8192x4096 bf16, 49 + 5 us
@@ -33,21 +33,23 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Sums over the W waves that share a row.  buf holds a pair a wave, and
-// alternates between calls (`half`) so that one barrier a call is enough.
-template <int W>
+// Sums over the R threads that share a row: 16 lanes, a wave, or the
+// workgroup, where buf holds a pair a wave and alternates between calls
+// (`half`) so that one barrier a call is enough.
+template <int R>
 __device__ __forceinline__ float2 row_sums(float a, float b, float2 (&buf)[2][4], int half) {
+    if (R == 16) return make_float2(lanes16_sum(a), lanes16_sum(b));
     a = lanes_sum(a);
     b = lanes_sum(b);
-    if (W == 1) return make_float2(a, b);
+    if (R == 64) return make_float2(a, b);
     if ((threadIdx.x & 63) == 0) buf[half][threadIdx.x >> 6] = make_float2(a, b);
     __syncthreads();
     const float2 p = buf[half][0], q = buf[half][1], r = buf[half][2], t = buf[half][3];
     return make_float2((p.x + q.x) + (r.x + t.x), (p.y + q.y) + (r.y + t.y));
 }
-template <int W>
+template <int R>
 __device__ __forceinline__ float row_sum(float v, float2 (&buf)[2][4], int half) {
-    return row_sums<W>(v, 0.0f, buf, half).x;
+    return row_sums<R>(v, 0.0f, buf, half).x;
 }
 
 struct LnFwdArgs {
@@ -63,11 +65,11 @@ struct LnFwdArgs {
 // A workgroup keeps its columns' weight and bias in registers over its rows
 // and loads a row ahead (32768x1024 fp32 with residual: 98 us, 109 with one
 // row a wave and the weights read again for each; 20000x1283: 86 us, 171).
-template <typename T, int V, int W, int E>
+template <typename T, int V, int R, int E>
 __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
-    constexpr int NV = E / V, kRows = 4 / W;
+    constexpr int NV = E / V, kRows = kThreads / R;
     __shared__ float2 buf[2][4];
-    const int li = W == 1 ? (threadIdx.x & 63) : threadIdx.x;
+    const int li = threadIdx.x & (R - 1);
     const int64_t step = (int64_t)gridDim.x * kRows;
     const float n = (float)a.D;
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.res);
@@ -76,7 +78,7 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = (li + j * 64 * W) * V + i;
+            const int c = (li + j * R) * V + i;
             w[j][i] = c < a.D && a.w != nullptr ? a.w[c] : 1.0f;
             b[j][i] = c < a.D && a.b != nullptr ? a.b[c] : 0.0f;
         }
@@ -87,14 +89,14 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
     auto load = [&](int64_t row) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (li + j * 64 * W) * V;
+            const int c = (li + j * R) * V;
             if (c < a.D) {
                 next.x[j] = load_once<T, V>(x + row * a.D + c);
                 if (res != nullptr) next.res[j] = load_once<T, V>(res + row * a.D + c);
             }
         }
     };
-    int64_t row = (int64_t)blockIdx.x * kRows + (W == 1 ? threadIdx.x >> 6 : 0);
+    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / R;
     if (row < a.rows) load(row);
     for (; row < a.rows; row += step) {
         const int64_t base = row * a.D;
@@ -104,7 +106,7 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (li + j * 64 * W) * V;
+            const int c = (li + j * R) * V;
 #pragma unroll
             for (int i = 0; i < V; ++i) f[j][i] = 0.0f;
             if (c < a.D) {
@@ -119,11 +121,11 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
 #pragma unroll
             for (int i = 0; i < V; ++i) sum += f[j][i];
         }
-        const float mu = row_sum<W>(sum, buf, 0) / n;
+        const float mu = row_sum<R>(sum, buf, 0) / n;
         float sq = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (li + j * 64 * W) * V;
+            const int c = (li + j * R) * V;
             if (c < a.D) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -132,14 +134,14 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
                 }
             }
         }
-        const float rstd = 1.0f / sqrtf(row_sum<W>(sq, buf, 1) / n + a.eps);
+        const float rstd = 1.0f / sqrtf(row_sum<R>(sq, buf, 1) / n + a.eps);
         if (li == 0) {
             if (a.mean != nullptr) a.mean[row] = mu;
             if (a.rstd != nullptr) a.rstd[row] = rstd;
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (li + j * 64 * W) * V;
+            const int c = (li + j * R) * V;
             if (c < a.D) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) f[j][i] = fmaf(f[j][i] * rstd, w[j][i], b[j][i]);
@@ -170,13 +172,13 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_long_kernel(LnFwdArgs a) {
             sum += v;
         }
         const T *src = r != nullptr ? s : x;  // each thread reads back what it wrote itself
-        const float mu = row_sum<4>(sum, buf, 0) / n;
+        const float mu = row_sum<256>(sum, buf, 0) / n;
         float sq = 0.0f;
         for (int c = threadIdx.x; c < a.D; c += kThreads) {
             const float d = (float)src[c] - mu;
             sq = fmaf(d, d, sq);
         }
-        const float rstd = 1.0f / sqrtf(row_sum<4>(sq, buf, 1) / n + a.eps);
+        const float rstd = 1.0f / sqrtf(row_sum<256>(sq, buf, 1) / n + a.eps);
         if (threadIdx.x == 0) {
             if (a.mean != nullptr) a.mean[row] = mu;
             if (a.rstd != nullptr) a.rstd[row] = rstd;
@@ -201,12 +203,12 @@ struct LnBwdArgs {
 // The workgroups keep their columns' dw and db in registers over all their
 // rows, so there are only as many partial sums as workgroups; the few waves
 // that leaves on a CU keep memory busy by loading a row ahead.
-template <typename T, int V, int W, int E>
+template <typename T, int V, int R, int E>
 __global__ __launch_bounds__(kThreads) void ln_bwd_kernel(LnBwdArgs a) {
-    constexpr int NV = E / V, kRows = 4 / W;
+    constexpr int NV = E / V, kRows = kThreads / R;
     __shared__ float2 buf[2][4];
-    __shared__ float comb[W == 1 ? 3 * 64 * V : 1];
-    const int li = W == 1 ? (threadIdx.x & 63) : threadIdx.x;
+    __shared__ float comb[kRows > 1 ? (kRows - 1) * R * V : 1];
+    const int li = threadIdx.x & (R - 1);
     const int64_t step = (int64_t)gridDim.x * kRows;
     const float n = (float)a.D;
     const T *s = static_cast<const T *>(a.s), *dy = static_cast<const T *>(a.dy), *ds = static_cast<const T *>(a.ds);
@@ -215,7 +217,7 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_kernel(LnBwdArgs a) {
     for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = (li + j * 64 * W) * V + i;
+            const int c = (li + j * R) * V + i;
             w[j][i] = c < a.D ? (a.w != nullptr ? a.w[c] : 1.0f) : 0.0f;
             gw[j][i] = gb[j][i] = 0.0f;
         }
@@ -229,7 +231,7 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_kernel(LnBwdArgs a) {
         next.rstd = a.rstd[row];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (li + j * 64 * W) * V;
+            const int c = (li + j * R) * V;
             if (c < a.D) {
                 const int64_t at = row * a.D + c;
                 next.s[j] = load_once<T, V>(s + at);
@@ -238,7 +240,7 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_kernel(LnBwdArgs a) {
             }
         }
     };
-    int64_t row = (int64_t)blockIdx.x * kRows + (W == 1 ? threadIdx.x >> 6 : 0);
+    int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / R;
     if (row < a.rows) load(row);
     for (int half = 0; row < a.rows; row += step, half ^= 1) {
         const Row cur = next;
@@ -247,7 +249,7 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_kernel(LnBwdArgs a) {
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (li + j * 64 * W) * V;
+            const int c = (li + j * R) * V;
             if (c < a.D) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -261,11 +263,11 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_kernel(LnBwdArgs a) {
                 }
             }
         }
-        const float2 sums = row_sums<W>(s1, s2, buf, half);
+        const float2 sums = row_sums<R>(s1, s2, buf, half);
         const float c1 = sums.x / n, c2 = sums.y / n;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (li + j * 64 * W) * V;
+            const int c = (li + j * R) * V;
             if (c < a.D) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -282,23 +284,24 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_kernel(LnBwdArgs a) {
     for (int q = 0; q < 2; ++q) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (li + j * 64 * W) * V;
+            const int c = (li + j * R) * V;
             float v[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) v[i] = q == 0 ? gw[j][i] : gb[j][i];
-            if (W == 1) {  // the four waves' sums, in their order
-                const int wv = threadIdx.x >> 6;
+            if (kRows > 1) {  // the sums of the rows side by side, in their order
+                const int grp = threadIdx.x / R;
                 __syncthreads();
-                if (wv > 0)
+                if (grp > 0)
 #pragma unroll
-                    for (int i = 0; i < V; ++i) comb[((wv - 1) * V + i) * 64 + li] = v[i];
+                    for (int i = 0; i < V; ++i) comb[((grp - 1) * V + i) * R + li] = v[i];
                 __syncthreads();
-                if (wv == 0)
+                if (grp == 0)
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        v[i] = ((v[i] + comb[i * 64 + li]) + comb[(V + i) * 64 + li]) + comb[(2 * V + i) * 64 + li];
+                    for (int g = 0; g < kRows - 1; ++g)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) v[i] += comb[(g * V + i) * R + li];
             }
-            if (c < a.D && (W != 1 || threadIdx.x < 64)) {
+            if (c < a.D && threadIdx.x < R) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) part[(int64_t)q * a.D + c + i] = v[i];
             }
@@ -323,7 +326,7 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_long_kernel(LnBwdArgs a) {
             s1 += g;
             s2 = fmaf(g, ((float)s[c] - mu) * rstd, s2);
         }
-        const float2 c = row_sums<4>(s1, s2, buf, half);
+        const float2 c = row_sums<256>(s1, s2, buf, half);
         const float c1 = c.x / n, c2 = c.y / n;
         half ^= 1;
         for (int c = threadIdx.x; c < a.D; c += kThreads) {
@@ -421,22 +424,32 @@ __global__ __launch_bounds__(1024) void ln_reduce_kernel(const float *part, int 
     }
 }
 
+// Rows up to kNarrow elements: 16 lanes each, four rows a wave (100000x64 fp32:
+// forward with residual 21 us, backward 24; 37 and 51 with a wave a row, of
+// which 16 lanes work; bf16 17 and 20, 42 and 51 so; 32768x128 fp32 14 and 16,
+// 17 and 23 so).
+constexpr int64_t kNarrow = 128;
+// Rows that a workgroup takes at once.
+int64_t rows_at_once(int64_t D) { return D <= kNarrow ? 16 : D <= 1024 ? 4 : 1; }
+
 template <typename T, int V>
 void ln_fwd_launch(const LnFwdArgs &a, hipStream_t s) {
     const int64_t cap = (int64_t)device_cu_count() * 4;
-    const int g1 = (int)std::min<int64_t>((a.rows + 3) / 4, cap), g4 = (int)std::min<int64_t>(a.rows, cap);
-    if (a.D <= 512) ln_fwd_kernel<T, V, 1, 8><<<g1, kThreads, 0, s>>>(a);
-    else if (a.D <= 1024) ln_fwd_kernel<T, V, 1, 16><<<g1, kThreads, 0, s>>>(a);
-    else if (a.D <= 4096) ln_fwd_kernel<T, V, 4, 16><<<g4, kThreads, 0, s>>>(a);
-    else ln_fwd_kernel<T, V, 4, 32><<<g4, kThreads, 0, s>>>(a);
+    const int g = (int)std::min<int64_t>((a.rows + rows_at_once(a.D) - 1) / rows_at_once(a.D), cap);
+    if (a.D <= kNarrow) ln_fwd_kernel<T, V, 16, 8><<<g, kThreads, 0, s>>>(a);
+    else if (a.D <= 512) ln_fwd_kernel<T, V, 64, 8><<<g, kThreads, 0, s>>>(a);
+    else if (a.D <= 1024) ln_fwd_kernel<T, V, 64, 16><<<g, kThreads, 0, s>>>(a);
+    else if (a.D <= 4096) ln_fwd_kernel<T, V, 256, 16><<<g, kThreads, 0, s>>>(a);
+    else ln_fwd_kernel<T, V, 256, 32><<<g, kThreads, 0, s>>>(a);
 }
 
 template <typename T, int V>
 void ln_bwd_launch(const LnBwdArgs &a, int G, hipStream_t s) {
-    if (a.D <= 512) ln_bwd_kernel<T, V, 1, 8><<<G, kThreads, 0, s>>>(a);
-    else if (a.D <= 1024) ln_bwd_kernel<T, V, 1, 16><<<G, kThreads, 0, s>>>(a);
-    else if (a.D <= 4096) ln_bwd_kernel<T, V, 4, 16><<<G, kThreads, 0, s>>>(a);
-    else ln_bwd_kernel<T, V, 4, 32><<<G, kThreads, 0, s>>>(a);
+    if (a.D <= kNarrow) ln_bwd_kernel<T, V, 16, 8><<<G, kThreads, 0, s>>>(a);
+    else if (a.D <= 512) ln_bwd_kernel<T, V, 64, 8><<<G, kThreads, 0, s>>>(a);
+    else if (a.D <= 1024) ln_bwd_kernel<T, V, 64, 16><<<G, kThreads, 0, s>>>(a);
+    else if (a.D <= 4096) ln_bwd_kernel<T, V, 256, 16><<<G, kThreads, 0, s>>>(a);
+    else ln_bwd_kernel<T, V, 256, 32><<<G, kThreads, 0, s>>>(a);
 }
 
 constexpr int64_t kLongRow = 8192;  // above it a row does not fit the registers
@@ -472,7 +485,7 @@ hipError_t ln_bwd(const LnBwdArgs &a, int G, float *gw, float *gb, hipStream_t s
 
 // Partials of the weight's gradient: one workgroup's rows each.
 int layernorm_parts(int64_t rows, int64_t D) {
-    const int64_t per = D <= kShortRow ? kThreads : D <= 1024 ? 4 : 1;  // rows a workgroup takes at once
+    const int64_t per = D <= kShortRow ? kThreads : rows_at_once(D);
     const int64_t cap = D > kLongRow ? 64 : (int64_t)device_cu_count() * 2;
     return (int)std::min<int64_t>((rows + per - 1) / per, cap);
 }

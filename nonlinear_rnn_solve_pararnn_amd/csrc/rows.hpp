@@ -142,4 +142,12 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
+// Sum over each row of 16 lanes, in every lane of it (rotations by 8, 4, 2, 1).
+__device__ __forceinline__ float lanes16_sum(float v) {
+    v = add_dpp<0x128, 0xf>(v);
+    v = add_dpp<0x124, 0xf>(v);
+    v = add_dpp<0x122, 0xf>(v);
+    return add_dpp<0x121, 0xf>(v);
+}
+
 }  // namespace prn

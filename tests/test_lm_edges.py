@@ -114,3 +114,15 @@ def test_embedding_rows_that_begin_anywhere(N, D, dtype):
     want = torch.zeros(V, D, dtype=torch.float64).index_add_(0, ids.cpu(), grad.cpu().double()) * 2
     assert torch.equal(got.cpu().double(), want)
     assert (out[:5] == 7).all() and (out[5 + V * D:] == 7).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,D", [(1, 5), (15, 16), (17, 65), (37, 100), (64, 127), (9001, 128), (33, 129)])
+def test_norm_of_short_rows(rows, D, dtype):
+    """Four rows a wave up to 128 elements, a row each above; tolerances as for every norm."""
+    from tests.test_gpu_layernorm import TYPES, check, make
+    T, tol = TYPES[dtype]
+    x, r, w, b, dy, ds = make(rows, D, T, seed=rows * 3 + D)
+    check(x, w, b, r, dy, ds, tol)
+    check(x, w, None, None, dy, None, tol)
