@@ -44,9 +44,11 @@ WalkPlan walk_plan(const LinattnArgs &p, bool backward) {
     return w;
 }
 
+// Rows that overlap are left to the loads of any alignment, whose rows past the
+// last position are cleared: here they would find elements of the last rows.
 bool view_vec(const WalkView &v, int d, int es) {
     const int64_t n = 16 / es;
-    return d % n == 0 && aligned16(v.p) && v.sb % n == 0 && v.st % n == 0 && v.sh % n == 0;
+    return d % n == 0 && aligned16(v.p) && v.sb % n == 0 && v.st % n == 0 && v.sh % n == 0 && (v.st >= d || v.st == 0);
 }
 
 // Whether every operand of every walk moves as 16-byte vectors.

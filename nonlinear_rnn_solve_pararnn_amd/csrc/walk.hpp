@@ -42,6 +42,7 @@
 #pragma once
 
 #include "linattn.hpp"
+#include "walk_rows.hpp"
 
 namespace prn {
 namespace walk {
@@ -50,7 +51,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kThreads = 256;
 constexpr int kNB = 64;  // columns of Z a workgroup
 
 template <typename T> constexpr int kPlanes = sizeof(T) == 2 ? 1 : 3;
@@ -153,76 +153,46 @@ __device__ __forceinline__ float plane_sum(const bf16x8 (&p)[N], int i) {
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00020000);
 }
-constexpr uint32_t kNowhere = 0x80000000u;  // above every buffer's size, also after a chunk's bytes are taken off
-
-// Rows of one operand as a walk's segment sees them, from column c0 on, in
-// chunks of C positions.
-struct Rows {
-    const char *p;       // the first chunk, if it is whole: its lowest address
-    int64_t step;        // bytes from a chunk to the next one
-    uint32_t row_bytes;  // below 2^24 (checked on the host)
-    uint32_t tail;       // bytes of a row from p on
-    int rev;
-
-    // Address and bytes of chunk i of cnt positions (none: nothing to read or write).
-    __device__ __forceinline__ const char *at(int i, int cnt, int C) const {
-        return p + i * step + (rev ? (C - cnt) * (int64_t)row_bytes : 0);
-    }
-    __device__ __forceinline__ uint32_t bytes(int cnt) const { return cnt == 0 ? 0u : (uint32_t)(cnt - 1) * row_bytes + tail; }
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk(int i, int cnt, int C) const {
-        return buffer_of(at(i, cnt, C), bytes(cnt));
-    }
-    // The same in whole words of memory, for rows of 2-byte elements that begin
-    // anywhere: `skew` bytes before the chunk's first element the buffer begins,
-    // and it ends with the word that holds the last one.
-    __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_words(int i, int cnt, int C, uint32_t &skew) const {
-        const char *first = at(i, cnt, C);
-        skew = (uint32_t)(uintptr_t)first & 3u;
-        return buffer_of(first - skew, cnt == 0 ? 0u : (skew + bytes(cnt) + 3u) & ~3u);
-    }
-    // Offset of a chunk's row r in it, if the chunk is whole; shift() less in a shorter one.
-    __device__ __forceinline__ uint32_t row_at(int r, int C) const { return (uint32_t)(rev ? C - 1 - r : r) * row_bytes; }
-    __device__ __forceinline__ uint32_t shift(int cnt, int C) const { return rev ? (uint32_t)(C - cnt) * row_bytes : 0u; }
-};
+// Chunk i of cnt positions; the same in whole words, `skew` bytes before it.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_of(const Rows &v, int i, int cnt, int C) {
+    return buffer_of(v.at(i, cnt, C), v.bytes(cnt));
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_words_of(const Rows &v, int i, int cnt, int C, uint32_t &skew) {
+    const char *first = v.at(i, cnt, C);
+    skew = Rows::word_skew(first);
+    return buffer_of(first - skew, v.word_bytes(skew, cnt));
+}
 template <typename T>
 __device__ __forceinline__ Rows rows_of(const WalkView &v, int64_t b, int64_t h, int64_t L, int64_t begin, int C, int rev,
                                         int c0, int d) {
-    const int64_t row = v.st * (int64_t)sizeof(T);
-    const char *p = static_cast<const char *>(v.p) + (b * v.sb + h * v.sh + c0) * (int64_t)sizeof(T);
-    return {p + (rev ? L - begin - C : begin) * row, rev ? -row * C : row * C, (uint32_t)row, (uint32_t)((d - c0) * (int)sizeof(T)), rev};
+    const char *first = static_cast<const char *>(v.p) + (b * v.sb + h * v.sh + c0) * (int64_t)sizeof(T);
+    return rows_from(first, v.st * (int64_t)sizeof(T), (uint32_t)((d - c0) * (int)sizeof(T)), L, begin, C, rev);
 }
 
-// A thread's groups of 8 elements of a tile of W columns.
-template <int W, int C>
-struct Groups {
-    static constexpr int kGroups = W / 8, kN = (C * kGroups + kThreads - 1) / kThreads;
-    // Where the groups of a row divide the threads, a thread's groups are the
-    // same columns kThreads / kGroups rows apart and one offset tells them all.
-    static constexpr bool kEven = kThreads % kGroups == 0;
-    static constexpr int kStep = kThreads / kGroups;
-    uint32_t at[kEven ? 1 : kN];  // offsets in a whole chunk
-    int left;                     // columns the operand has
-
-    __device__ __forceinline__ void init(const Rows &v, int elem_bytes) {
-        left = (int)(v.tail / (uint32_t)elem_bytes);
+// Group n of a thread, as the planes of its 8 elements, into an LDS tile.
+template <int W, int C, int kP>
+__device__ __forceinline__ void put_group(bf16 *lds, int thread, int n, const bf16x8 (&p)[kP]) {
+    constexpr int kGroups = Groups<W, C>::kGroups;
+    const int i = thread + n * kThreads, r = i / kGroups, grp = i - r * kGroups;
+    if (C * kGroups % kThreads != 0 && r >= C) return;
 #pragma unroll
-        for (int n = 0; n < (kEven ? 1 : kN); ++n)
-            at[n] = row(n) < C && column(n) < left ? v.row_at(row(n), C) + (uint32_t)(column(n) * elem_bytes) : kNowhere;
-    }
-    __device__ __forceinline__ static int row(int n) { return (int)((threadIdx.x + n * kThreads) / kGroups); }
-    __device__ __forceinline__ static int column(int n) { return (int)((threadIdx.x + n * kThreads) % kGroups) * 8; }
-    __device__ __forceinline__ uint32_t offset(const Rows &v, int n, uint32_t shift) const {
-        return kEven ? at[0] + ((uint32_t)(v.rev ? -n : n) * kStep * v.row_bytes - shift) : at[kEven ? 0 : n] - shift;
-    }
-    // Group n, as the planes of its 8 elements, into an LDS tile.
-    template <int kP>
-    __device__ __forceinline__ static void put(bf16 *lds, int n, const bf16x8 (&p)[kP]) {
-        const int i = threadIdx.x + n * kThreads, r = i / kGroups, grp = i - r * kGroups;
-        if (C * kGroups % kThreads != 0 && r >= C) return;
+    for (int k = 0; k < kP; ++k) *reinterpret_cast<bf16x8 *>(lds + k * C * kTileRow<W> + tile_at<W>(r, grp)) = p[k];
+}
+// Zeros over a thread's rows past the last position.
+template <int kP, int W, int C>
+__device__ __forceinline__ void clear_past(bf16 *lds, int thread, int cnt) {
+    uint32_t none = 0;
+    asm volatile("" : "+v"(none));  // or the zeros take registers in every chunk
+    bf16x8 zero[kP];
 #pragma unroll
-        for (int k = 0; k < kP; ++k) *reinterpret_cast<bf16x8 *>(lds + k * C * kTileRow<W> + tile_at<W>(r, grp)) = p[k];
+    for (int k = 0; k < kP; ++k) {
+        const u32x4 z = {none, none, none, none};
+        zero[k] = *reinterpret_cast<const bf16x8 *>(&z);
     }
-};
+#pragma unroll 1
+    for (int n = 0; n < Groups<W, C>::kN; ++n)
+        if (Groups<W, C>::past(thread, n, cnt)) put_group<W, C>(lds, thread, n, zero);
+}
 __device__ __forceinline__ void planes_of(const bf16 (&v)[8], bf16x8 (&p)[1]) { p[0] = *reinterpret_cast<const bf16x8 *>(&v[0]); }
 __device__ __forceinline__ void planes_of(const float (&v)[8], bf16x8 (&p)[3]) { split3(v, p); }
 
@@ -235,11 +205,11 @@ struct Ahead {
         T v[8];
     } r[Groups<W, C>::kN];
 
-    __device__ __forceinline__ void init(const Rows &v) { g.init(v, sizeof(T)); }
+    __device__ __forceinline__ void init(const Rows &v) { g.init(v, sizeof(T), threadIdx.x); }
     // The cnt positions of chunk i; zeros past the ends.
     __device__ __forceinline__ void load(const Rows &v, int chunk, int cnt) {
         constexpr int kV = 16 / (int)sizeof(T);
-        const __amdgpu_buffer_rsrc_t buf = v.chunk(chunk, cnt, C);
+        const __amdgpu_buffer_rsrc_t buf = chunk_of(v, chunk, cnt, C);
         const uint32_t shift = v.shift(cnt, C);
 #pragma unroll
         for (int n = 0; n < g.kN; ++n) {
@@ -257,7 +227,7 @@ struct Ahead {
         for (int n = 0; n < g.kN; ++n) {
             bf16x8 p[kPlanes<T>];
             planes_of(r[n].v, p);
-            g.put(lds, n, p);
+            put_group<W, C>(lds, threadIdx.x, n, p);
         }
     }
 };
@@ -274,10 +244,10 @@ struct Ahead<T, W, C, false> {
     uint32_t r[Groups<W, C>::kN][kWords + 1];
     uint32_t shift;                                    // of the loaded chunk's offsets, less the skew
 
-    __device__ __forceinline__ void init(const Rows &v) { g.init(v, sizeof(T)); }
+    __device__ __forceinline__ void init(const Rows &v) { g.init(v, sizeof(T), threadIdx.x); }
     __device__ __forceinline__ void load(const Rows &v, int chunk, int cnt) {
         uint32_t skew = 0;
-        const __amdgpu_buffer_rsrc_t buf = kHalves ? v.chunk_words(chunk, cnt, C, skew) : v.chunk(chunk, cnt, C);
+        const __amdgpu_buffer_rsrc_t buf = kHalves ? chunk_words_of(v, chunk, cnt, C, skew) : chunk_of(v, chunk, cnt, C);
         shift = v.shift(cnt, C) - skew;
 #pragma unroll
         for (int n = 0; n < g.kN; ++n) {
@@ -295,21 +265,19 @@ struct Ahead<T, W, C, false> {
 #pragma unroll
         for (int n = 0; n < g.kN; ++n) {
             const uint32_t bits = kHalves ? (g.offset(v, n, shift) & 2u) << 3 : 0u;
-            const int valid = g.left - g.column(n);  // what follows the row's last column belongs to others
+            const int valid = g.own(n);
             union {
                 uint32_t w[kWords];
                 T v[8];
             } u;
 #pragma unroll
             for (int k = 0; k < kWords; ++k) {
-                constexpr int kPer = 4 / (int)sizeof(T);
-                uint32_t x = kHalves ? __builtin_amdgcn_alignbit(r[n][k + 1], r[n][k], bits) : r[n][k];
-                if (kHalves && valid == k * kPer + 1) x &= 0xffffu;
-                u.w[k] = valid <= k * kPer ? 0u : x;
+                const uint32_t x = kHalves ? __builtin_amdgcn_alignbit(r[n][k + 1], r[n][k], bits) : r[n][k];
+                u.w[k] = g.own_word(x, k, sizeof(T), valid);
             }
             bf16x8 p[kPlanes<T>];
             planes_of(u.v, p);
-            g.put(lds, n, p);
+            put_group<W, C>(lds, threadIdx.x, n, p);
         }
     }
 };
@@ -675,7 +643,7 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
         }
     };
     auto write = [&](int i, int cnt, const f32x4 (&o)[NI]) {
-        const __amdgpu_buffer_rsrc_t buf = ro.chunk(i, cnt, C);
+        const __amdgpu_buffer_rsrc_t buf = chunk_of(ro, i, cnt, C);
         const uint32_t shift = ro.shift(cnt, C);
 #pragma unroll
         for (int it = 0; it < NI; ++it) {
@@ -702,6 +670,18 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
         lds_barrier();  // the last chunk's reads are done
         put(d);
         load(i + kDepth, d);
+        if constexpr (!VEC) {  // with VEC they have found nothing in the buffer (see view_vec)
+            if (cnt < C) {
+                // the thread's index is found again: kept for the one chunk that
+                // may be short it would take a register in all of them
+                uint32_t all = ~0u;
+                asm volatile("" : "+s"(all));
+                const int thread = wave * 64 + (int)__builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0));
+                if (kOut) clear_past<kP, D1, C>(X, thread, cnt);
+                clear_past<kP, D1, C>(Y, thread, cnt);
+                clear_past<kP, kNB, C>(Z, thread, cnt);
+            }
+        }
         lds_barrier();
         f32x4 o[NI];
         bf16x8 z[NS][kP];
