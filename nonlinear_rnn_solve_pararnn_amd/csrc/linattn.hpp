@@ -55,9 +55,22 @@ __device__ __forceinline__ float walk_gate(const float *log_decay, int64_t h) {
     return g < -1e30f ? -1e30f : g;
 }
 
-// e^(g n) - 1 in double, rounded once: the state is carried over a chunk as
-// T + T (e^(g n) - 1), whose rounding does not repeat from chunk to chunk the
-// way that of a factor near 1 does.
-__device__ __forceinline__ float walk_em1(float g, int64_t n) { return (float)expm1((double)g * (double)n); }
+// The state's factor over n positions, in double and rounded once.  Slow decays
+// are carried as T + T (e^(g n) - 1), whose rounding does not repeat from chunk
+// to chunk the way that of a factor near 1 does; where less than half is left,
+// e^(g n) itself is the factor, as what is left of T + T (e^(g n) - 1) would be
+// that factor's rounding error of 2^-25.
+struct Carry {
+    float f;
+    bool fast;
+    __device__ __forceinline__ float operator()(float t) const { return fast ? t * f : fmaf(t, f, t); }
+};
+__device__ __forceinline__ Carry walk_carry(float g, int64_t n) {
+    const double e = exp((double)g * (double)n);  // e - 1 is off by 2^-53 of T, whatever its size
+    const bool fast = e < 0.5;
+    const float f = (float)(fast ? e : e - 1.0);
+    // the same in every lane
+    return {__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(f))), (bool)__builtin_amdgcn_readfirstlane(fast)};
+}
 
 }  // namespace prn

@@ -4,7 +4,7 @@
 // Chunks of C positions.  Within a chunk, with the decays applied in fp32:
 //   P = (X Y^T) * wi e^(g(i-j)) on and below the diagonal,
 //   out = P Z + wo e^(g(i+1-e)) X T,
-//   T <- T + T (e^(gC) - 1) + sum_j Y_j^T (wt e^(g(C-1-j+e)) Z_j).
+//   T <- e^(gC) T + sum_j Y_j^T (wt e^(g(C-1-j+e)) Z_j).
 // One workgroup walks one segment of one (batch row, head) for 64 columns of
 // Z; wave w owns columns 16 w .. 16 w + 15 and keeps its [D1, 16] columns of T
 // in fp32 registers.  T is a matrix operand straight from there: in the
@@ -385,7 +385,7 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
 #pragma unroll
     for (int it = 0; it < NI; ++it) dec_row[it] = w.wo * fast_exp2(g2 * (float)(16 * it + m + 1 - w.e));
     if (threadIdx.x < C) dec_z[threadIdx.x] = w.wt * fast_exp2(g2 * (float)(C - 1 - (int)threadIdx.x + w.e));
-    const float em1_full = walk_em1(g, C);
+    const Carry carry_full = walk_carry(g, C), carry_last = last == C ? carry_full : walk_carry(g, last);
 
     if constexpr (kOut) {
         // the tiles of P right of the diagonal that share a 32-wide read with it stay zero
@@ -457,6 +457,18 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
         my_it[k] = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
         my_jt[k] = tile - my_it[k] * (my_it[k] + 1) / 2;
     }
+    auto carry_state = [&](bool whole) {
+        const Carry carry = whole ? carry_full : carry_last;
+        if (carry.fast) {
+            asm volatile("");  // a branch: the compiler would work out both and select
+#pragma unroll
+            for (int t = 0; t < NA; ++t) S[t] *= carry.f;
+        } else {
+            const f32x4 f = {carry.f, carry.f, carry.f, carry.f};
+#pragma unroll
+            for (int t = 0; t < NA; ++t) S[t] = __builtin_elementwise_fma(S[t], f, S[t]);
+        }
+    };
     auto products = [&](int cnt, bool whole, bf16x8 (&z)[NS][kP], f32x4 (&o)[NI]) {
         // rows 16 it + m are laid out like rows m; with bf16 the offsets are hidden
         // from the compiler, which would keep every sum with them in a register
@@ -552,13 +564,6 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
                         for (int r = 0; r < 4; ++r) o[it][r] *= dec_row[it];
             } else {
                 const int s = (k - kB1 - kB2) / kB3s, t0 = (k - kB1 - kB2) % kB3s * kU3;
-                if (k == kB1 + kB2) {
-                    const float em1 = whole ? em1_full : walk_em1(g, cnt);
-#pragma unroll
-                    for (int t = 0; t < NA; ++t)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) S[t][r] = fmaf(S[t][r], em1, S[t][r]);
-                }
                 if (t0 == 0) {
                     float v[8];
                     if (whole) {
@@ -592,10 +597,19 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
                                read_tr(&Z[p * kPZ + tile_at<kNB>(row + 4, grp) + in]));
             }
         read(0, buf[0]);
-#pragma unroll
-        for (int k = 0; k < kB1 + kB2 + kB3; ++k) {
+        auto ahead = [&](int k) {
             if (k + 1 < kB1 + kB2 + kB3) read(k + 1, buf[(k + 1) & 1]);
             __builtin_amdgcn_sched_barrier(0);
+        };
+#pragma unroll
+        for (int k = 0; k < kB1 + kB2; ++k) {
+            ahead(k);
+            use(k, buf[k & 1]);
+        }
+#pragma unroll
+        for (int k = kB1 + kB2; k < kB1 + kB2 + kB3; ++k) {
+            ahead(k);
+            if (k == kB1 + kB2) carry_state(whole);
             use(k, buf[k & 1]);
         }
     };
@@ -728,7 +742,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(WalkArgs a) {
     if (wh.blk * kNB >= w.d2) return;
     const int lane = threadIdx.x >> 2, r = threadIdx.x & 3;  // whose register this element is
     const int row = state_row(t, lane >> 4, r), col = wh.blk * kNB + wave * 16 + (lane & 15);
-    const float em1 = walk_em1(walk_gate(a.log_decay, wh.bh % (int)a.H), a.seg_len);
+    const Carry carry = walk_carry(walk_gate(a.log_decay, wh.bh % (int)a.H), a.seg_len);
     float s = w.init != nullptr && col < w.d2 && row < w.d1
                   ? w.init[(int64_t)wh.bh * w.d1 * w.d2 + (int64_t)row * w.im + (int64_t)col * w.in] : 0.0f;
     s = __builtin_canonicalizef(s);  // no signalling NaN (a launch tag) goes into the workspace
@@ -743,7 +757,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(WalkArgs a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s0 + u < a.segs) at[(s0 + u) * step] = s;
-            if (s0 + u < a.segs - 1) s = fmaf(s, em1, s) + own[u];
+            if (s0 + u < a.segs - 1) s = carry(s) + own[u];
         }
     }
 }
