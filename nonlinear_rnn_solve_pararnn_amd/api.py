@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import threading
 from typing import Optional, Sequence
 
 import torch
@@ -122,7 +123,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return ctypes.c_void_p(_raw_stream(device))
 
 
 def _need(t: torch.Tensor, shape, name: str, device=None):
@@ -144,10 +145,12 @@ def workspace_bytes(op: int, B: int, L: int, H: int, max_iter: int = 1) -> int:
     return int(load_library().pararnn_workspace_bytes(op, B, L, H, max_iter))
 
 
-# One zero-filled workspace per (device, stream), grown on demand.  The
-# library leaves a workspace ready for the next call of any entry point, so it
-# is cleared only when it is first allocated.
+# One zero-filled workspace per (device, stream, host thread), grown on demand.
+# The library leaves a workspace ready for the next call of any entry point, so
+# it is cleared only when it is first allocated.  Threads have their own: two
+# that issue on one stream may interleave the launches of their calls.
 _ws_cache = {}
+_WS_HEADER = 256   # bytes before an operator's scratch: a call that needs no more uses none of them
 
 
 def new_workspace(nbytes: int, device) -> torch.Tensor:
@@ -157,7 +160,7 @@ def new_workspace(nbytes: int, device) -> torch.Tensor:
 
 
 def release_workspaces():
-    """Drop the cached per-stream workspaces."""
+    """Drop the cached workspaces."""
     _ws_cache.clear()
 
 
@@ -173,13 +176,32 @@ def _raw_stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _workspace_of(n: int, device, ws=None):
-    """The caller's workspace if one is given, else the stream's, of at least n bytes."""
+def _capturing() -> bool:
+    """Whether the current stream's calls go into a HIP graph."""
+    return torch._C._cuda_isCurrentStreamCapturing()
+
+
+@functools.lru_cache(maxsize=None)
+def _no_scratch(device: torch.device) -> torch.Tensor:
+    """What calls that use no scratch are given: never read nor written."""
+    return new_workspace(_WS_HEADER, device)
+
+
+def _workspace_of(n: int, device, ws=None, scratch=False):
+    """The caller's workspace if one is given, else the one this thread keeps for
+    the stream, of at least n bytes.  A call that is being captured gets one of its
+    own from the graph's memory (cleared in the graph, unless it is only scratch):
+    replays must not depend on a buffer that a later call may replace or use."""
     if ws is not None:
         if ws.device != device or ws.numel() * ws.element_size() < n or ws.data_ptr() % 256:
             raise ValueError("workspace too small, misaligned or on the wrong device")
         return ws, ws.numel() * ws.element_size()
-    key = (device, _raw_stream(device))
+    if scratch and n <= _WS_HEADER:
+        return _no_scratch(device), _WS_HEADER
+    if _capturing():
+        buf = torch.empty(max(n, 256), dtype=torch.uint8, device=device) if scratch else new_workspace(n, device)
+        return buf, buf.numel()
+    key = (device.index, _raw_stream(device), threading.get_ident())
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < n:
         buf = new_workspace(n, device)
@@ -547,6 +569,12 @@ def _linattn_ws(backward: int, *sizes) -> int:
     return load_library().pararnn_linattn_workspace_bytes(backward, *sizes)
 
 
+@functools.lru_cache(maxsize=1024)
+def _layernorm_ws(rows: int, D: int) -> int:
+    """pararnn_layernorm_workspace_bytes, likewise."""
+    return load_library().pararnn_layernorm_workspace_bytes(rows, D)
+
+
 def _linattn_views(tensors, shapes, names, dtype, device):
     """Checks the operands; the strides array the library takes, or None if all are dense."""
     dense = True
@@ -611,7 +639,7 @@ def linattn_forward(q, k, v, log_decay, state=None, *, scale=None, want_state=Tr
         _need_typed(out_state, sshape, torch.float32, "out_state", dev)
     elif want_state:
         out_state = log_decay.new_empty(sshape)
-    buf, n = _workspace_of(_linattn_ws(0, code, B, L, H, dk, dv), dev, ws)
+    buf, n = _workspace_of(_linattn_ws(0, code, B, L, H, dk, dv), dev, ws, True)
     _check(lib.pararnn_linattn_forward(code, B, L, H, dk, dv, _at(q), _at(k), _at(v), st, _at(log_decay),
                                        _at(state), dk ** -0.5 if scale is None else scale, _at(out),
                                        _at(out_state), _at(buf), n, _raw_stream(dev)), "pararnn_linattn_forward")
@@ -638,7 +666,7 @@ def linattn_backward(q, k, v, log_decay, grad_o, state=None, grad_state=None, *,
         want_state = state is not None
     gq, gk, gv = (torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k, v))
     gs = torch.empty(sshape, dtype=torch.float32, device=dev) if want_state else None
-    buf, n = _workspace_of(_linattn_ws(1, code, B, L, H, dk, dv), dev, ws)
+    buf, n = _workspace_of(_linattn_ws(1, code, B, L, H, dk, dv), dev, ws, True)
     _check(lib.pararnn_linattn_backward(code, B, L, H, dk, dv, _at(q), _at(k), _at(v), _at(grad_o), st,
                                         _at(log_decay), _at(state), _at(grad_state),
                                         dk ** -0.5 if scale is None else scale, _at(gq), _at(gk), _at(gv),
@@ -732,7 +760,7 @@ def layernorm_backward(s, weight, mean, rstd, grad_y, grad_sum=None, *, want_w=T
     dx = torch.empty_like(s)
     gw = torch.empty(D, dtype=torch.float32, device=dev) if want_w else None
     gb = torch.empty(D, dtype=torch.float32, device=dev) if want_b else None
-    buf, n = _workspace_of(lib.pararnn_layernorm_workspace_bytes(rows, D), dev, ws) if want_w or want_b else (None, 0)
+    buf, n = _workspace_of(_layernorm_ws(rows, D), dev, ws, True) if want_w or want_b else (None, 0)
     _check(lib.pararnn_layernorm_backward(code, rows, D, _at(s), _at(weight), _at(mean), _at(rstd), _at(grad_y),
                                           _at(grad_sum), _at(dx), _at(gw), _at(gb), _at(buf), n, _raw_stream(dev)),
            "pararnn_layernorm_backward")
@@ -796,7 +824,7 @@ def embedding_backward(ids, grad, num_rows, *, scale=1.0, padding_idx=None, out=
     n = lib.pararnn_embedding_workspace_bytes(N, V, D)
     if n == 0:
         raise PararnnError("invalid sizes N=%d V=%d D=%d" % (N, V, D))
-    buf, n = _workspace_of(n, dev, ws)
+    buf, n = _workspace_of(n, dev, ws, True)
     _check(lib.pararnn_embedding_backward(code, N, V, D, _at(ids), nb, _at(grad), scale,
                                           -1 if padding_idx is None else padding_idx, _at(out), _at(buf), n,
                                           _raw_stream(dev)), "pararnn_embedding_backward")
