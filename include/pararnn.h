@@ -344,8 +344,9 @@ int pararnn_gru_forward_noalloc(int64_t B, int64_t L, int64_t H,
  * layer norm and the embedding lookup, each with its gradient.  Tensors are
  * fp32 or bf16 (`dtype`, all sequence tensors of a call alike); states,
  * decays, norm weights and statistics are always fp32, and so is every sum.
- * bf16 results are rounded once, to nearest even.  Outputs are dense and must
- * not alias inputs unless stated.  Workspaces follow the rules above and may
+ * bf16 results are rounded to nearest even, once but in linear attention,
+ * which says below what else it rounds.  Outputs are dense and must not alias
+ * inputs unless stated.  Workspaces follow the rules above and may
  * be shared with every other entry point.  Results do not depend on timing:
  * the same inputs give the same bits.
  */
@@ -368,6 +369,17 @@ enum { PARARNN_F32 = 0, PARARNN_BF16 = 1 };
  * A value that is not finite at position t of q, k or v affects no output
  * before t; from t on the affected outputs are not finite (an infinity may
  * come out as NaN).
+ * Precision: states are carried in fp32, with the relative accuracy of fp32
+ * whatever the decay.  fp32 products are formed of three parts of 8 bits, of
+ * which the three smallest of nine products are left out (2^-23 of a product).
+ * With bf16 tensors whole sequences round two things to bf16 on the way to an
+ * output or a gradient: the copy of the state that a row is multiplied with
+ * (heads above 32), and the weights of the positions within a chunk of 64;
+ * outputs are then off by about 2.3e-3 in the 2-norm, of which their own
+ * rounding is 1.7e-3.  States are not affected, nor is the single token's step.
+ * How long a chunk is (32 positions keep the weights to 16 bits) and how many
+ * pieces a sequence is walked in depend on L, on the head sizes and on B H, so
+ * the same row may come out with other last bits in a batch of another size.
  */
 size_t pararnn_linattn_workspace_bytes(int32_t backward, int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t dk,
                                        int64_t dv);

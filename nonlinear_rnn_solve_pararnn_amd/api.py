@@ -621,7 +621,9 @@ def linattn_forward(q, k, v, log_decay, state=None, *, scale=None, want_state=Tr
     q, k [B, L, H, dk], v [B, L, H, dv], fp32 or bf16, any strides with a dense
     last dimension; log_decay [H] fp32; state [B, H, dk, dv] fp32 or None.
     scale defaults to dk^-0.5.  Returns (o [B, L, H, dv], final state or None
-    unless want_state).  out_state may be `state` itself."""
+    unless want_state).  out_state may be `state` itself.  bf16 outputs carry one
+    or two roundings to bf16 on the way beside their own; states are fp32
+    throughout.  The last bits of a row may differ in a batch of another size."""
     lib = load_library()
     code, dk, dv, kshape = _linattn_check(q, v, True)
     B, L, H, _ = kshape

@@ -46,8 +46,8 @@ struct EmbFwdArgs {
 
 constexpr int kLookRows = 4;  // rows whose loads a thread keeps in flight
 
-// Rows that begin at any element: 65536 rows of 50000x2047 bf16 in 141 us
-// (210 an element at a time; 103 for 2048 columns).
+// Rows that begin at any element: 65536 rows of 50000x2047 bf16, uniform ids, in
+// 140 us (210 an element at a time; 109 for 2048 columns).
 template <typename T, bool VEC>
 __global__ __launch_bounds__(kThreads) void emb_lookup_kernel(EmbFwdArgs a) {
     constexpr int V = kVec<T>;
@@ -343,7 +343,8 @@ constexpr int kBatch = 8;         // rows whose loads are in flight
 constexpr uint32_t kNoKey = ~0u;  // above every key
 
 // A wave takes a chunk for 64 groups of columns (65536 tokens, 50000x2047 bf16:
-// the whole gradient 157 us, 271 an element at a time; 136 for 2048 columns).
+// the whole gradient 156 us; 139 for 2048 columns; an element at a time, uniform
+// ids, 271 where this takes 168).
 template <typename T, bool VEC>
 __global__ __launch_bounds__(kThreads) void emb_sum_kernel(EmbSumArgs a) {
     constexpr int V = kVec<T>;
@@ -472,7 +473,8 @@ EmbWs emb_ws(int64_t N, int64_t D) {
     // 10 us for the joins, with 32 entries 94 + 17; 65536 x 128 bf16 (one with
     // 64): the whole gradient 48 us, with 16 entries 36; 8192 x 1024 fp32 (one
     // with 16): sums and joins 12 + 5, with 8 entries 12 + 8; 4000 x 256 bf16
-    // (a quarter with 16): the whole gradient 22 us, with 8 entries 19.
+    // (a quarter with 16): the whole gradient 22 us, with 8 entries 19 (the whole
+    // gradients with uniform ids).
     const int64_t per_simd = N * ((D + 511) / 512) / (4 * device_cu_count());
     w.run = per_simd >= 256 ? 64 : per_simd >= 128 ? 32 : per_simd >= 16 ? 16 : 8;
     w.chunks = (N + w.run - 1) / w.run;

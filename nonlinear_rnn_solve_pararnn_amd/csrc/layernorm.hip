@@ -18,12 +18,13 @@
 // backward with a gradient of the sum, dw and db, 8192x4096 bf16, 49 + 5 us
 // (268 MB, 5.5 TB/s in the first); a copy of 1 GiB runs at 5.1 TB/s.  Rows that
 // are not whole 16-byte vectors move an element at a time: 20000x1283 fp32
-// forward and backward 86 us each (4.8 TB/s), bf16 57 and 73 us (3.6, 2.8);
-// groups put together from whole words were no better here (fp32 99 and 80,
-// bf16 64 and 89), as that work sits between a row's loads and the next's.
-// Rows above 8192 elements are read several times by one workgroup each:
-// 4096x16384 fp32 forward 333, backward 410 us (3.2, 2.6 TB/s of its least
-// traffic).
+// forward and backward 107 and 130 us (3.8, 3.2 TB/s), bf16 90 and 130 us (2.3,
+// 1.6); groups put together from whole words were no better here (one set of
+// tensors, in part from the caches: fp32 99 and 80 us where elements took 83 and
+// 90, bf16 64 and 89 where they took 60 and 80), as that work sits between a
+// row's loads and the next's.  Rows above 8192 elements are read several times
+// by one workgroup each: 4096x16384 fp32 forward 339, backward 451 us (3.2, 2.4
+// TB/s of its least traffic).
 #include "rows.hpp"
 #include "sequence.hpp"
 
@@ -64,7 +65,8 @@ struct LnFwdArgs {
 
 // A workgroup keeps its columns' weight and bias in registers over its rows
 // and loads a row ahead (32768x1024 fp32 with residual: 98 us, 109 with one
-// row a wave and the weights read again for each; 20000x1283: 86 us, 171).
+// row a wave and the weights read again for each; 20000x1283, one set of tensors
+// in part from the caches: 86 us, 171).
 template <typename T, int V, int R, int E>
 __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(LnFwdArgs a) {
     constexpr int NV = E / V, kRows = kThreads / R;
@@ -427,7 +429,7 @@ __global__ __launch_bounds__(1024) void ln_reduce_kernel(const float *part, int 
 // Rows up to kNarrow elements: 16 lanes each, four rows a wave (100000x64 fp32:
 // forward with residual 21 us, backward 24; 37 and 51 with a wave a row, of
 // which 16 lanes work; bf16 17 and 20, 42 and 51 so; 32768x128 fp32 14 and 16,
-// 17 and 23 so).
+// 17 and 23 so; one set of tensors).
 constexpr int64_t kNarrow = 128;
 // Rows that a workgroup takes at once.
 int64_t rows_at_once(int64_t D) { return D <= kNarrow ? 16 : D <= 1024 ? 4 : 1; }

@@ -20,9 +20,9 @@ struct WalkPlan {
 // A walk is sequential, so few (batch row, head, column block) walks leave
 // CUs idle.  Below one walk a CU the sequence is cut into segments whose own
 // states are found first and joined, as many as keep two workgroups on every
-// CU in one round (B=1, L=32771, H=8, 64x128 fp32: 32 segments 214 us, 48 244,
-// 64 230); from one walk a CU on the second reading of Y and Z costs more than
-// it gains (B=8, L=2048, H=16, 128x128 bf16: 101 us whole, 118 in two).
+// CU in one round (B=1, L=32771, H=8, 64x128 fp32: 32 segments 186 us, 48 199,
+// 64 194); from one walk a CU on the second reading of Y and Z costs more than
+// it gains (B=8, L=2048, H=16, 128x128 bf16: 95 us whole, 122 in two).
 WalkPlan walk_plan(const LinattnArgs &p, bool backward) {
     auto blocks = [](int cols) { return (cols + walk::kNB - 1) / walk::kNB; };
     WalkPlan w;
@@ -111,8 +111,8 @@ hipError_t run_walks(WalkArgs &a, const WalkPlan &w, const Ws &ws, hipStream_t s
 // Reads and writes the state once and is bound by that.  One workgroup a
 // (batch row, head): threads are columns (V of them each) by rows, eight rows'
 // loads in flight a thread, the rows' partial products with q meet in shared
-// memory.  B=128, H=16, 128x128: 53.7 us, 270 MB at 5.0 TB/s (a copy's rate);
-// B=1: 5.6 us, where 16 workgroups wait for one round trip to memory.
+// memory.  B=128, H=16, 128x128: 53.8 us, 270 MB at 5.0 TB/s (a copy's rate);
+// B=1: 5.4 us, where 16 workgroups wait for one round trip to memory.
 struct StepArgs {
     int64_t BH, H;
     int dk, dv, lanes;  // lanes (a power of two) threads over the columns

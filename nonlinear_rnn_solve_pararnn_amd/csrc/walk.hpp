@@ -21,24 +21,26 @@
 // three planes, so the state of a bf16 model is as good as that of an fp32 one.
 // For the bf16 outputs alone, P and the copy of T that the rows are multiplied
 // with are rounded to bf16 once.  Sums of many such products are then off by
-// about as much as their own rounding; two planes each would cost 27% (forward
-// at B=8, L=2048, H=16, 128x128).  Where few terms are summed two planes are
+// about as much as their own rounding (B=8, L=2048, H=16, 128x128: outputs and
+// gradients 2.3e-3 from 64 bits, of which the last rounding alone is 1.7e-3);
+// two planes each leave that rounding alone and cost 45% (forward there, 95 to
+// 138 us; backward at B=1, 58 to 64).  Where few terms are summed two planes are
 // taken: of T in heads of up to 32, of P in chunks of 32 positions, which all
 // short sequences have.
 //
 // (A first form of the kernel on fp32 matrix instructions, with bf16 tensors
-// widened, took 647 us where this one takes 90: B=8, L=2048, H=16, 128x128.)
+// widened, took 647 us where this one takes 92: B=8, L=2048, H=16, 128x128.)
 //
 // What bounds it (B=8, L=2048, H=16, 128x128, bf16): 268 MB forward, 52 us at
 // the rate of a copy, 470 MB backward, 92 us; matrix instructions 18 us of the
-// forward pass.  It takes 90 us forward and 204 us backward.  Neither
-// memory (the loads and stores alone 71 us forward) nor the arithmetic (all
-// but the loads 84 us) fills the time; a workgroup's three barriers a chunk
-// leave both idle in turn.  Tried and not kept: three chunks in LDS and one
-// barrier (the accumulators then move between register files, 103 us forward,
-// 329 backward), two waves sharing 16 columns with half the positions each
-// (115, 337), workgroups of 32 columns (116, 365), outputs through LDS in whole
-// rows (98, 263).
+// forward pass.  It takes 92 us forward and 197 us backward.  Neither
+// memory (the loads and stores alone 75 and 162 us) nor the arithmetic (all
+// but the loads 83 and 175) fills the time; a workgroup's three barriers a chunk
+// leave both idle in turn.  Tried and not kept, beside 102 us forward and 256
+// backward at the time: three chunks in LDS and one barrier (the accumulators
+// then move between register files, 103 and 329), two waves sharing 16 columns
+// with half the positions each (115, 337), workgroups of 32 columns (116, 365),
+// outputs through LDS in whole rows (98, 263).
 #pragma once
 
 #include "linattn.hpp"
@@ -235,7 +237,7 @@ struct Ahead {
 // Rows that begin at any element: groups of fp32 are loaded from 4-byte
 // aligned addresses, groups of bf16 as the five words of memory that hold
 // them, and put straight when they go into LDS (forward at B=4, L=4000, H=8,
-// 77x101 bf16: 95 us, 138 with a load an element; 67 with 80x104).
+// 77x101 bf16: 88 us, 138 with a load an element; 60 with 80x104).
 template <typename T, int W, int C>
 struct Ahead<T, W, C, false> {
     Groups<W, C> g;
@@ -321,13 +323,16 @@ __device__ __forceinline__ int state_row(int t, int q, int r) { return 32 * (t >
 
 // Workgroups a CU that the registers are shared out for.  Where a launch has
 // more than two a CU, bf16 takes chunks of 32 positions, whose smaller tiles
-// leave room for three (backward at B=8, L=2048, H=16, 128x128: 225 us instead
-// of 255 with chunks of 64); with one or two a CU the longer chunk, with half
-// as many barriers, is ahead (forward there: 101 us, 109 with 32), but for
-// sequences of up to kShort positions, where it makes no difference to the time.
+// leave room for three (backward at B=8, L=2048, H=16, 128x128: 202 us, 241
+// with chunks of 64); with one or two a CU the longer chunk, with half as many
+// barriers, is mostly ahead (backward at B=4, L=2048, H=16, 64x64: 77 us, 82 with
+// 32; at B=1, L=4096, H=16, 96x96: 81, 88; the training forward pass the same, 95
+// and 96), but for sequences of up to kShort positions, where it makes no
+// difference to the time.
 constexpr int64_t kShort = 256;
-// fp32 keeps two: with three, the walk of 64-wide heads spills 35 registers
-// (B=1, L=32771, H=8, 64x128: 181 to 200 us, 150 with two).
+// fp32 keeps two: with three, walks have fewer registers than their loads ahead
+// need (B=1, L=32771, H=8, 64x128: the call 186 us, 193 with three; backward at
+// B=3, L=1000, H=10, 48x80: 70, 79; at B=8, L=1024, H=8, 64x64: 81, 86).
 template <typename T, int D1, int C>
 constexpr int kWgs = D1 > 128 ? 1 : sizeof(T) == 2 && C == 32 ? 3 : 2;
 
@@ -470,15 +475,12 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1, C>)) void walk_kernel(WalkAr
         }
     };
     auto products = [&](int cnt, bool whole, bf16x8 (&z)[NS][kP], f32x4 (&o)[NI]) {
-        // rows 16 it + m are laid out like rows m; with bf16 the offsets are hidden
-        // from the compiler, which would keep every sum with them in a register
-        // (20 of the 38 that it then spills)
+        // rows 16 it + m are laid out like rows m
         int y_off[kMine], x_off[kMine];
 #pragma unroll
         for (int k = 0; k < kMine; ++k) {
             y_off[k] = __builtin_amdgcn_readfirstlane(my_jt[k] * 16 * kTileRow<D1>);
             x_off[k] = __builtin_amdgcn_readfirstlane(my_it[k] * 16 * kTileRow<D1>);
-            if constexpr (kP == 1) asm volatile("" : "+s"(y_off[k]), "+s"(x_off[k]));
         }
         Frags buf[2];
         f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
