@@ -13,6 +13,7 @@ import ctypes
 import functools
 import os
 import threading
+import weakref
 from typing import Optional, Sequence
 
 import torch
@@ -148,8 +149,20 @@ def workspace_bytes(op: int, B: int, L: int, H: int, max_iter: int = 1) -> int:
 # One zero-filled workspace per (device, stream, host thread), grown on demand.
 # The library leaves a workspace ready for the next call of any entry point, so
 # it is cleared only when it is first allocated.  Threads have their own: two
-# that issue on one stream may interleave the launches of their calls.
-_ws_cache = {}
+# that issue on one stream may interleave the launches of their calls.  A
+# thread's go when it ends.
+class _Kept(dict):
+    __hash__ = object.__hash__
+
+
+class _Thread(threading.local):
+    def __init__(self):
+        self.kept = _Kept()
+        _all_kept.add(self.kept)
+
+
+_all_kept = weakref.WeakSet()
+_thread = _Thread()
 _WS_HEADER = 256   # bytes before an operator's scratch: a call that needs no more uses none of them
 
 
@@ -161,7 +174,8 @@ def new_workspace(nbytes: int, device) -> torch.Tensor:
 
 def release_workspaces():
     """Drop the cached workspaces."""
-    _ws_cache.clear()
+    for kept in list(_all_kept):
+        kept.clear()
 
 
 def _workspace(op, B, L, H, device, max_iter=1, ws=None):
@@ -201,11 +215,11 @@ def _workspace_of(n: int, device, ws=None, scratch=False):
     if _capturing():
         buf = torch.empty(max(n, 256), dtype=torch.uint8, device=device) if scratch else new_workspace(n, device)
         return buf, buf.numel()
-    key = (device.index, _raw_stream(device), threading.get_ident())
-    buf = _ws_cache.get(key)
+    kept, key = _thread.kept, (device.index, _raw_stream(device))
+    buf = kept.get(key)
     if buf is None or buf.numel() < n:
         buf = new_workspace(n, device)
-        _ws_cache[key] = buf
+        kept[key] = buf
     return buf, buf.numel()
 
 

@@ -37,11 +37,11 @@ def test_captured_modules_after_larger_calls():
         run()
         run()
     torch.cuda.synchronize()
-    kept = {id(x) for x in api._ws_cache.values()}
+    kept = {id(x) for d in api._all_kept for x in d.values()}
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=side):
         out = run()
-    assert {id(x) for x in api._ws_cache.values()} == kept
+    assert {id(x) for d in api._all_kept for x in d.values()} == kept
     with torch.cuda.stream(side):
         larger()
     torch.cuda.synchronize()

@@ -1,6 +1,8 @@
 """Which workspace a call without one of its own gets (CPU: the stream and
 whether it is being captured are stood in for)."""
+import gc
 import threading
+import weakref
 
 import pytest
 import torch
@@ -15,8 +17,9 @@ def stream(monkeypatch):
     state = {"id": 7, "capturing": False}
     monkeypatch.setattr(api, "_raw_stream", lambda device: state["id"])
     monkeypatch.setattr(api, "_capturing", lambda: state["capturing"])
-    monkeypatch.setattr(api, "_ws_cache", {})
-    return state
+    api.release_workspaces()
+    yield state
+    api.release_workspaces()
 
 
 def test_kept_by_stream_and_grown(stream):
@@ -48,6 +51,30 @@ def test_threads_on_one_stream_do_not_share(stream):
         t.join()
     mine = api._workspace_of(1000, CPU)[0]
     assert len({x.data_ptr() for x in (*got.values(), mine)}) == 3
+    ended = [weakref.ref(x) for x in got.values()]
+    got.clear()
+    del threads, t
+    gc.collect()
+    assert all(x() is None for x in ended)  # a thread's workspaces go with it
+    assert api._workspace_of(1000, CPU)[0] is mine
+
+
+def test_release_reaches_every_thread(stream):
+    step, seen = threading.Barrier(2), []
+
+    def run():
+        seen.append(api._workspace_of(1000, CPU)[0])
+        step.wait()
+        step.wait()
+        seen.append(api._workspace_of(1000, CPU)[0])
+
+    t = threading.Thread(target=run)
+    t.start()
+    step.wait()
+    api.release_workspaces()
+    step.wait()
+    t.join()
+    assert seen[0] is not seen[1]
 
 
 def test_calls_without_scratch_share_what_nobody_touches(stream):
@@ -59,13 +86,13 @@ def test_calls_without_scratch_share_what_nobody_touches(stream):
 @pytest.mark.parametrize("args", [(), (None, True)])
 def test_a_captured_call_has_its_own(stream, args):
     before = api._workspace_of(1000, CPU)[0]
-    kept = dict(api._ws_cache)
+    kept = dict(api._thread.kept)
     stream["capturing"] = True
     a, n = api._workspace_of(1000, CPU, *args)
     b, _ = api._workspace_of(4000, CPU, *args)
     assert n >= 1000 and a.data_ptr() % 16 == 0
     assert len({x.data_ptr() for x in (before, a, b)}) == 3
-    assert api._ws_cache == kept and all(api._ws_cache[k] is kept[k] for k in kept)
+    assert api._thread.kept.keys() == kept.keys() and all(api._thread.kept[k] is kept[k] for k in kept)
     if not args:
         assert not a.any()
     ws = torch.empty(4096 + 256, dtype=torch.uint8)
