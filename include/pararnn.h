@@ -463,6 +463,111 @@ int pararnn_embedding_backward(int32_t dtype, int64_t N, int64_t V, int64_t D, c
                                int32_t id_bytes, const void *grad, float scale, int64_t padding_idx,
                                void *grad_table, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * The gated delta rule: for each batch row and head, with g_t <= 0 the log
+ * decay and b_t the write strength of the position,
+ *     S_t = e^(g_t) (I - b_t k_t^T k_t) S_{t-1} + b_t k_t^T v_t,
+ *     o_t = scale q_t S_t,   S_{-1} = state.
+ * It is meant for keys of about unit length and b in [0, 1] (or [0, 2]): for
+ * b |k|^2 above 2 the state grows along k.  A position with b = 0 and g = 0
+ * leaves the state as it is (padding).
+ * q, k: [B, L, Hk, dk]; v, o: [B, L, H, dv], Hk a divisor of H: head h shares
+ * q and k of head h / (H / Hk); log_decay, beta: [B, L, H] fp32; state,
+ * out_state: [B, H, dk, dv] fp32 (state NULL: zeros; out_state NULL: not
+ * wanted; out_state may be state itself, but not overlap it otherwise).
+ * 1 <= dk, dv <= 256 (above: PARARNN_ERR_UNSUPPORTED).  B H ceil(L / 32) is
+ * below 2^26 - 4 and B H below 2^24 over the column blocks of 64 in dv.
+ * strides: HOST array of {batch row, position, head} strides in elements for
+ * q, k, v, log_decay and beta in turn (15 values), not negative, those of
+ * positions in q, k and v below 2^22; the last dimension of q, k and v is
+ * dense.  NULL: dense tensors (H max(dk, dv) < 2^22).  Operands whose rows are
+ * 16-byte aligned move faster.
+ * A value that is not finite at position t of q changes o_t alone; in v it
+ * makes its column of o NaN from t on and that column of the final state; in
+ * k, log_decay or beta (a log decay of -infinity is one that forgets
+ * everything, and finite) it makes every output of the head from t on NaN and
+ * its final state.  No output before t is affected.  A key whose squares add
+ * up past fp32 counts as not finite.
+ * Precision: states and what they are computed from are carried in fp32 (products
+ * formed of three parts of 8 bits, of which the three smallest of nine
+ * products are left out: 2^-23 of a product).  With bf16 tensors an output's
+ * own products take the state and the positions' weights at 16 bits.
+ * A row's result depends neither on B nor on H.
+ */
+size_t pararnn_delta_workspace_bytes(int32_t backward, int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk,
+                                     int64_t dk, int64_t dv);
+int pararnn_delta_forward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
+                          const void *q, const void *k, const void *v, const float *log_decay, const float *beta,
+                          const int64_t *strides, const float *state, float scale, void *o, float *out_state,
+                          void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Its gradients for a loss with dLoss/do = grad_o ([B, L, H, dv]) and
+ * dLoss/d(final state) = grad_out_state ([B, H, dk, dv] or NULL for zeros):
+ * grad_q, grad_k [B, L, Hk, dk] (summed over the heads that share them),
+ * grad_v [B, L, H, dv], grad_log_decay and grad_beta [B, L, H] fp32 (either may
+ * be NULL) and grad_state [B, H, dk, dv] or NULL (it must not overlap state or
+ * grad_out_state).  strides: as above and those of grad_o after them (18
+ * values).  Where a value is not finite, the gradients are not defined.
+ */
+int pararnn_delta_backward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
+                           const void *q, const void *k, const void *v, const float *log_decay, const float *beta,
+                           const void *grad_o, const int64_t *strides, const float *state,
+                           const float *grad_out_state, float scale, void *grad_q, void *grad_k, void *grad_v,
+                           float *grad_log_decay, float *grad_beta, float *grad_state, void *ws, size_t ws_bytes,
+                           void *stream);
+
+/*
+ * One token of the recurrence (its form for decoding): q, k [B, Hk, dk], v, o
+ * [B, H, dv], log_decay, beta [B, H], state and out_state [B, H, dk, dv], both
+ * required; out_state may be state itself.  strides: as above with the
+ * positions' ignored, or NULL.  No workspace.
+ */
+int pararnn_delta_step(int32_t dtype, int64_t B, int64_t H, int64_t Hk, int64_t dk, int64_t dv, const void *q,
+                       const void *k, const void *v, const float *log_decay, const float *beta, const int64_t *strides,
+                       const float *state, float scale, void *o, float *out_state, void *stream);
+
+/*
+ * Norms of queries and keys for each head, with the position rotation in the
+ * same pass.  For every row x of d elements of q [B, L, Hq, d] and k
+ * [B, L, Hk, d] (k NULL and Hk = 0: q alone):
+ *     r = 1 / sqrt(mean(x^2) + eps)  (PARARNN_NORM_RMS) or
+ *     r = 1 / sqrt(sum(x^2) + eps)   (PARARNN_NORM_L2),   n = x r w,
+ * and the first R elements of n are turned in pairs by the position's angles:
+ *     y_c = n_c cos_i - n_c' sin_i,  y_c' = n_c' cos_i + n_c sin_i,
+ * with c, c' = i, i + R / 2, or 2 i, 2 i + 1 (interleaved).  weight: [d] fp32 of
+ * each tensor, or NULL for ones.  table: [P, R] fp32, a position's R / 2
+ * cosines and then its R / 2 sines; R even, R <= d; R = 0 (table NULL): no
+ * rotation.  positions: [B, L] int32 or int64 (position_bytes 4 or 8), or NULL
+ * for 0 .. L-1; a position outside [0, P) turns the rotated elements to NaN
+ * (and reads nothing).
+ * yq, yk: dense outputs in dtype; rq [B, L, Hq], rk [B, L, Hk]: r, fp32, or NULL.
+ * strides: HOST array of {batch row, position, head} strides of q and k (6
+ * values, not negative, last dimension dense) or NULL for dense tensors.
+ * 2 <= d <= 256 (above: PARARNN_ERR_UNSUPPORTED), eps >= 0, B L (Hq + Hk) < 2^28.
+ */
+enum { PARARNN_NORM_RMS = 0, PARARNN_NORM_L2 = 1 };
+int pararnn_headnorm_forward(int32_t dtype, int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d, const void *q,
+                             const void *k, const int64_t *strides, const float *wq, const float *wk,
+                             const float *table, int64_t P, int64_t R, const void *positions,
+                             int32_t position_bytes, int32_t kind, int32_t interleaved, float eps, void *yq, void *yk,
+                             float *rq, float *rk, void *stream);
+
+/*
+ * Its gradients: with the rotation undone on the gradients of the outputs (g),
+ *     dw = sum over rows of g x r,  dx = r (g w - x r m(g w x r)),
+ * m the mean or the sum.  strides: of q, k, grad_yq and grad_yk (12 values) or
+ * NULL; rq, rk: the forward pass's; grad_q, grad_k: dense; grad_wq, grad_wk: [d]
+ * fp32 or NULL (ws: unused, may be NULL, when both are).
+ */
+size_t pararnn_headnorm_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d);
+int pararnn_headnorm_backward(int32_t dtype, int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d, const void *q,
+                              const void *k, const void *grad_yq, const void *grad_yk, const int64_t *strides,
+                              const float *wq, const float *wk, const float *rq, const float *rk, const float *table,
+                              int64_t P, int64_t R, const void *positions, int32_t position_bytes, int32_t kind,
+                              int32_t interleaved, void *grad_q, void *grad_k, float *grad_wq, float *grad_wk,
+                              void *ws, size_t ws_bytes, void *stream);
+
 /* Short text for a status code (static storage). */
 const char *pararnn_status_string(int status);
 

@@ -33,7 +33,9 @@ EXPORTS = ("pararnn_workspace_bytes", "rnn_linscan_diag", "rnn_linscan_blk2", "r
            "pararnn_linattn_workspace_bytes", "pararnn_linattn_forward", "pararnn_linattn_backward",
            "pararnn_linattn_step", "pararnn_layernorm_workspace_bytes", "pararnn_layernorm_forward",
            "pararnn_layernorm_backward", "pararnn_embedding_forward",
-           "pararnn_embedding_workspace_bytes", "pararnn_embedding_backward")
+           "pararnn_embedding_workspace_bytes", "pararnn_embedding_backward",
+           "pararnn_delta_workspace_bytes", "pararnn_delta_forward", "pararnn_delta_backward", "pararnn_delta_step",
+           "pararnn_headnorm_forward", "pararnn_headnorm_workspace_bytes", "pararnn_headnorm_backward")
 NOALLOC_SCRATCH_BYTES = 64 << 20   # PARARNN_NOALLOC_SCRATCH_BYTES
 
 _lib = None
@@ -107,6 +109,22 @@ def load_library():
     lib.pararnn_embedding_backward.argtypes = [i32, i64, i64, i64, vp, i32, vp, ctypes.c_float, i64,
                                                vp, vp, sz, vp]
     lib.pararnn_embedding_backward.restype = ctypes.c_int
+    lib.pararnn_delta_workspace_bytes.argtypes = [i32, i32] + [i64] * 6
+    lib.pararnn_delta_workspace_bytes.restype = sz
+    lib.pararnn_delta_forward.argtypes = [i32] + [i64] * 6 + [vp] * 7 + [ctypes.c_float, vp, vp, vp, sz, vp]
+    lib.pararnn_delta_forward.restype = ctypes.c_int
+    lib.pararnn_delta_backward.argtypes = [i32] + [i64] * 6 + [vp] * 9 + [ctypes.c_float] + [vp] * 7 + [sz, vp]
+    lib.pararnn_delta_backward.restype = ctypes.c_int
+    lib.pararnn_delta_step.argtypes = [i32] + [i64] * 5 + [vp] * 7 + [ctypes.c_float, vp, vp, vp]
+    lib.pararnn_delta_step.restype = ctypes.c_int
+    lib.pararnn_headnorm_forward.argtypes = [i32] + [i64] * 5 + [vp] * 6 + [i64, i64, vp, i32, i32, i32,
+                                                                            ctypes.c_float] + [vp] * 5
+    lib.pararnn_headnorm_forward.restype = ctypes.c_int
+    lib.pararnn_headnorm_workspace_bytes.argtypes = [i64] * 5
+    lib.pararnn_headnorm_workspace_bytes.restype = sz
+    lib.pararnn_headnorm_backward.argtypes = [i32] + [i64] * 5 + [vp] * 10 + [i64, i64, vp, i32, i32, i32] \
+        + [vp] * 5 + [sz, vp]
+    lib.pararnn_headnorm_backward.restype = ctypes.c_int
     lib.pararnn_status_string.argtypes = [ctypes.c_int]
     lib.pararnn_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -783,17 +801,17 @@ def layernorm_backward(s, weight, mean, rstd, grad_y, grad_sum=None, *, want_w=T
     return dx, gw, gb
 
 
-def _ids(ids, device):
+def _ids(ids, device, name="ids"):
     if not isinstance(ids, torch.Tensor):
-        raise TypeError("ids must be a torch.Tensor")
+        raise TypeError("%s must be a torch.Tensor" % name)
     if ids.dtype not in (torch.int32, torch.int64):
-        raise TypeError("ids must be int32 or int64, got %s" % ids.dtype)
+        raise TypeError("%s must be int32 or int64, got %s" % (name, ids.dtype))
     if ids.device != device:
-        raise ValueError("ids is on %s, expected %s" % (ids.device, device))
+        raise ValueError("%s is on %s, expected %s" % (name, ids.device, device))
     if not ids.is_contiguous():
-        raise ValueError("ids must be contiguous")
+        raise ValueError("%s must be contiguous" % name)
     if ids.numel() == 0:
-        raise PararnnError("ids is empty")
+        raise PararnnError("%s is empty" % name)
     return ids.numel(), ids.element_size()
 
 
@@ -845,3 +863,272 @@ def embedding_backward(ids, grad, num_rows, *, scale=1.0, padding_idx=None, out=
                                           -1 if padding_idx is None else padding_idx, _at(out), _at(buf), n,
                                           _raw_stream(dev)), "pararnn_embedding_backward")
     return out
+
+
+# ---------------------------------------------------------------- the delta-rule mixer
+@functools.lru_cache(maxsize=1024)
+def _delta_ws(backward: int, *sizes) -> int:
+    """pararnn_delta_workspace_bytes, which depends on the sizes alone."""
+    return load_library().pararnn_delta_workspace_bytes(backward, *sizes)
+
+
+@functools.lru_cache(maxsize=1024)
+def _headnorm_ws(*sizes) -> int:
+    """pararnn_headnorm_workspace_bytes, likewise."""
+    return load_library().pararnn_headnorm_workspace_bytes(*sizes)
+
+
+def _views(operands, lead, device):
+    """Checks operands given as (tensor, name, shape, type) and returns the strides array the library takes (batch
+    row, position, head of each), or None if all are dense.  Leading dimensions are [B, L] or [B]; a tensor of more
+    than one dimension after them has a dense last one."""
+    dense = True
+    for t, name, shape, dtype in operands:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if t.dtype != dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if t.device != device:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+        if t.shape != shape:
+            raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+        if not t.is_contiguous():
+            dense = False
+            if len(shape) == lead + 2 and shape[-1] > 1 and t.stride(-1) != 1:
+                raise ValueError("the last dimension of %s must be dense" % name)
+    if dense:
+        return None
+    st = []
+    for t, _, _, _ in operands:
+        s = t.stride()
+        st += (s[0], s[1], s[2]) if lead == 2 else (s[0], 0, s[1])
+    return (ctypes.c_int64 * len(st))(*st)
+
+
+def _delta_check(q, v, log_decay, seq: bool):
+    code = _type_code(q, "q")
+    if q.dim() != 3 + seq or not isinstance(v, torch.Tensor) or v.dim() != 3 + seq:
+        raise ValueError("q, k and v must be %s" % ("[B, L, heads, d]" if seq else "[B, heads, d]"))
+    Hk, dk = q.shape[-2:]
+    H, dv = v.shape[-2:]
+    if 0 in q.shape or 0 in v.shape:
+        raise PararnnError("invalid sizes q %s, v %s" % (tuple(q.shape), tuple(v.shape)))
+    if H % Hk:
+        raise ValueError("the %d heads of v must be a multiple of the %d of q and k" % (H, Hk))
+    if dk > MAX_HEAD_DIM or dv > MAX_HEAD_DIM:
+        raise PararnnError("the delta rule supports head sizes up to %d, got dk=%d dv=%d" % (MAX_HEAD_DIM, dk, dv))
+    return code, H, Hk, dk, dv
+
+
+def delta_forward(q, k, v, log_decay, beta, state=None, *, scale=None, want_state=True, out=None, out_state=None,
+                  ws=None):
+    """The gated delta rule over whole sequences, g = log_decay, b = beta:
+    S_t = e^(g_t) (I - b_t k_t^T k_t) S_{t-1} + b_t k_t^T v_t, o_t = scale q_t S_t.
+
+    q, k [B, L, Hk, dk], v [B, L, H, dv], fp32 or bf16, any strides with a dense
+    last dimension; H is a multiple of Hk, and head h of v shares q and k of
+    head h // (H // Hk).  log_decay (at most 0), beta [B, L, H] fp32, any
+    strides; state [B, H, dk, dv] fp32 or None.  Keys are meant to be of about
+    unit length.  scale defaults to dk^-0.5.  Returns (o [B, L, H, dv], final
+    state or None unless want_state).  out_state may be `state` itself.  States
+    are carried in fp32; a position with beta = 0 and log_decay = 0 leaves them
+    as they are."""
+    lib = load_library()
+    code, H, Hk, dk, dv = _delta_check(q, v, log_decay, True)
+    B, L = q.shape[:2]
+    dev, T = q.device, q.dtype
+    kshape, vshape, gshape, sshape = q.shape, (B, L, H, dv), (B, L, H), (B, H, dk, dv)
+    st = _views(((q, "q", kshape, T), (k, "k", kshape, T), (v, "v", vshape, T),
+                 (log_decay, "log_decay", gshape, torch.float32), (beta, "beta", gshape, torch.float32)), 2, dev)
+    if state is not None:
+        _need_typed(state, sshape, torch.float32, "state", dev)
+    if out is None:
+        out = v.new_empty(vshape)
+    else:
+        _need_typed(out, vshape, T, "out", dev)
+    if out_state is not None:
+        _need_typed(out_state, sshape, torch.float32, "out_state", dev)
+    elif want_state:
+        out_state = log_decay.new_empty(sshape)
+    buf, n = _workspace_of(_delta_ws(0, code, B, L, H, Hk, dk, dv), dev, ws, True)
+    _check(lib.pararnn_delta_forward(code, B, L, H, Hk, dk, dv, _at(q), _at(k), _at(v), _at(log_decay), _at(beta), st,
+                                     _at(state), dk ** -0.5 if scale is None else scale, _at(out), _at(out_state),
+                                     _at(buf), n, _raw_stream(dev)), "pararnn_delta_forward")
+    return out, out_state
+
+
+def delta_backward(q, k, v, log_decay, beta, grad_o, state=None, grad_state=None, *, scale=None, want_state=None,
+                   ws=None):
+    """Gradients of delta_forward for dLoss/do = grad_o and dLoss/d(final state)
+    = grad_state (None: zeros).  Returns (dq, dk, dv, dlog_decay, dbeta, dstate):
+    dq and dk summed over the heads that share them, dlog_decay and dbeta fp32,
+    dstate None unless want_state (default: whether a state is given)."""
+    lib = load_library()
+    code, H, Hk, dk, dv = _delta_check(q, v, log_decay, True)
+    B, L = q.shape[:2]
+    dev, T = q.device, q.dtype
+    kshape, vshape, gshape, sshape = q.shape, (B, L, H, dv), (B, L, H), (B, H, dk, dv)
+    st = _views(((q, "q", kshape, T), (k, "k", kshape, T), (v, "v", vshape, T),
+                 (log_decay, "log_decay", gshape, torch.float32), (beta, "beta", gshape, torch.float32),
+                 (grad_o, "grad_o", vshape, T)), 2, dev)
+    for t, name in ((state, "state"), (grad_state, "grad_state")):
+        if t is not None:
+            _need_typed(t, sshape, torch.float32, name, dev)
+    if want_state is None:
+        want_state = state is not None
+    gq, gk, gv = (torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k, v))
+    gg, gb = (log_decay.new_empty(gshape) for _ in range(2))
+    gs = log_decay.new_empty(sshape) if want_state else None
+    buf, n = _workspace_of(_delta_ws(1, code, B, L, H, Hk, dk, dv), dev, ws, True)
+    _check(lib.pararnn_delta_backward(code, B, L, H, Hk, dk, dv, _at(q), _at(k), _at(v), _at(log_decay), _at(beta),
+                                      _at(grad_o), st, _at(state), _at(grad_state),
+                                      dk ** -0.5 if scale is None else scale, _at(gq), _at(gk), _at(gv), _at(gg),
+                                      _at(gb), _at(gs), _at(buf), n, _raw_stream(dev)), "pararnn_delta_backward")
+    return gq, gk, gv, gg, gb, gs
+
+
+def delta_step(q, k, v, log_decay, beta, state, *, scale=None, out=None, out_state=None):
+    """One token of delta_forward (decoding): q, k [B, Hk, dk], v [B, H, dv],
+    log_decay, beta [B, H], state [B, H, dk, dv].  Returns (o [B, H, dv], new
+    state); out_state may be `state` itself."""
+    lib = load_library()
+    code, H, Hk, dk, dv = _delta_check(q, v, log_decay, False)
+    B = q.shape[0]
+    dev, T = q.device, q.dtype
+    kshape, vshape, gshape, sshape = q.shape, (B, H, dv), (B, H), (B, H, dk, dv)
+    st = _views(((q, "q", kshape, T), (k, "k", kshape, T), (v, "v", vshape, T),
+                 (log_decay, "log_decay", gshape, torch.float32), (beta, "beta", gshape, torch.float32)), 1, dev)
+    _need_typed(state, sshape, torch.float32, "state", dev)
+    if out is None:
+        out = v.new_empty(vshape)
+    else:
+        _need_typed(out, vshape, T, "out", dev)
+    if out_state is None:
+        out_state = log_decay.new_empty(sshape)
+    else:
+        _need_typed(out_state, sshape, torch.float32, "out_state", dev)
+    _check(lib.pararnn_delta_step(code, B, H, Hk, dk, dv, _at(q), _at(k), _at(v), _at(log_decay), _at(beta), st,
+                                  _at(state), dk ** -0.5 if scale is None else scale, _at(out), _at(out_state),
+                                  _raw_stream(dev)), "pararnn_delta_step")
+    return out, out_state
+
+
+NORM_KINDS = {"rms": 0, "l2": 1}   # PARARNN_NORM_RMS, PARARNN_NORM_L2
+
+
+def _headnorm_check(q, k, weights, table, positions, kind):
+    """(type code, leading shape, B, L, Hq, Hk, d, R, P, bytes of a position); k may be None."""
+    code = _type_code(q, "q")
+    if q.dim() not in (3, 4) or (k is not None and (not isinstance(k, torch.Tensor) or k.dim() != q.dim())):
+        raise ValueError("q and k must be [B, L, heads, d] or [B, heads, d]")
+    if q.numel() == 0 or (k is not None and k.numel() == 0):
+        raise PararnnError("q or k is empty")
+    if kind not in NORM_KINDS:
+        raise ValueError("kind must be 'rms' or 'l2', got %r" % (kind,))
+    lead, d = q.shape[:-2], q.shape[-1]
+    if d > MAX_HEAD_DIM:
+        raise PararnnError("headnorm supports head sizes up to %d, got %d" % (MAX_HEAD_DIM, d))
+    if d < 2:
+        raise PararnnError("a head of one element has no norm")
+    Hq, Hk = q.shape[-2], 0 if k is None else k.shape[-2]
+    B, L = lead if len(lead) == 2 else (lead[0], 1)
+    for w, name in zip(weights, ("q_weight", "k_weight")):
+        if w is not None:
+            _need_typed(w, (d,), torch.float32, name, q.device)
+    P = R = nb = 0
+    if table is not None:
+        if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.numel() == 0:
+            raise ValueError("table must be a [positions, R] tensor")
+        P, R = table.shape
+        if R % 2 or R > d:
+            raise ValueError("table must have an even number of columns of at most %d, got %d" % (d, R))
+        _need_typed(table, (P, R), torch.float32, "table", q.device)
+        if positions is None:
+            if len(lead) == 1:
+                raise ValueError("positions must be given where there is no dimension of positions")
+            if L > P:
+                raise ValueError("table has %d positions, the sequence %d" % (P, L))
+        else:
+            nb = _ids(positions, q.device, "positions")[1]
+            if positions.shape != lead:
+                raise ValueError("positions has shape %s, expected %s" % (tuple(positions.shape), tuple(lead)))
+    elif positions is not None:
+        raise ValueError("positions are given without a table")
+    return code, lead, B, L, Hq, Hk, d, R, P, nb
+
+
+def headnorm_forward(q, k=None, q_weight=None, k_weight=None, table=None, positions=None, *, kind="rms", eps=1e-6,
+                     interleaved=False, out_q=None, out_k=None):
+    """Norms of queries and keys for each head, then the rotation by position:
+    n = x r w with r = 1 / sqrt(mean(x^2) + eps) ("rms") or 1 / sqrt(sum(x^2) +
+    eps) ("l2", unit length), and the first R elements of n turned in pairs
+    (i, i + R/2), or (2i, 2i + 1) if interleaved.
+
+    q [B, L, Hq, d] or [B, Hq, d], k alike with its own number of heads or None,
+    fp32 or bf16, any strides with a dense last dimension; weights [d] fp32 or
+    None; table [P, R] fp32 (a position's cosines, then its sines) or None for
+    no rotation; positions [B, L] (or [B]) int32 or int64, None for 0 .. L-1.  A
+    position outside the table turns the rotated elements to NaN.  Returns
+    (yq, yk, rq, rk), r fp32 being what headnorm_backward takes."""
+    lib = load_library()
+    code, lead, B, L, Hq, Hk, d, R, P, nb = _headnorm_check(q, k, (q_weight, k_weight), table, positions, kind)
+    dev, T = q.device, q.dtype
+    ops = [(q, "q", q.shape, T)]
+    if k is not None:
+        ops.append((k, "k", (*lead, Hk, d), T))
+    st = _views(ops, len(lead), dev)
+    if st is not None and k is None:
+        st = (ctypes.c_int64 * 6)(*st, 0, 0, 0)
+    if out_q is None:
+        out_q = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        _need_typed(out_q, q.shape, T, "out_q", dev)
+    if k is None:
+        if out_k is not None or k_weight is not None:
+            raise ValueError("out_k or k_weight is given without k")
+    elif out_k is None:
+        out_k = torch.empty_like(k, memory_format=torch.contiguous_format)
+    else:
+        _need_typed(out_k, k.shape, T, "out_k", dev)
+    rq = torch.empty((*lead, Hq), dtype=torch.float32, device=dev)
+    rk = None if k is None else torch.empty((*lead, Hk), dtype=torch.float32, device=dev)
+    _check(lib.pararnn_headnorm_forward(code, B, L, Hq, Hk, d, _at(q), _at(k), st, _at(q_weight), _at(k_weight),
+                                        _at(table), P, R, _at(positions), nb, NORM_KINDS[kind], interleaved, eps,
+                                        _at(out_q), _at(out_k), _at(rq), _at(rk), _raw_stream(dev)),
+           "pararnn_headnorm_forward")
+    return out_q, out_k, rq, rk
+
+
+def headnorm_backward(q, k, rq, rk, grad_q, grad_k=None, q_weight=None, k_weight=None, table=None, positions=None, *,
+                      kind="rms", interleaved=False, want_w=None, ws=None):
+    """Gradients of headnorm_forward for the gradients of its outputs; rq, rk
+    are its results.  Returns (dq, dk, dq_weight, dk_weight); the weights' are
+    None unless want_w (default: where a weight is given)."""
+    lib = load_library()
+    code, lead, B, L, Hq, Hk, d, R, P, nb = _headnorm_check(q, k, (q_weight, k_weight), table, positions, kind)
+    dev, T = q.device, q.dtype
+    ops = [(q, "q", q.shape, T)]
+    _need_typed(rq, (*lead, Hq), torch.float32, "rq", dev)
+    if k is not None:
+        ops += [(k, "k", (*lead, Hk, d), T), (grad_q, "grad_q", q.shape, T), (grad_k, "grad_k", (*lead, Hk, d), T)]
+        _need_typed(rk, (*lead, Hk), torch.float32, "rk", dev)
+    else:
+        if grad_k is not None or rk is not None or k_weight is not None:
+            raise ValueError("grad_k, rk or k_weight is given without k")
+        ops.append((grad_q, "grad_q", q.shape, T))
+    st = _views(ops, len(lead), dev)
+    if st is not None and k is None:
+        st = (ctypes.c_int64 * 12)(*st[:3], 0, 0, 0, *st[3:], 0, 0, 0)
+    dq = torch.empty_like(q, memory_format=torch.contiguous_format)
+    dk = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
+    want = [w is not None if want_w is None else want_w for w in (q_weight, k_weight)]
+    gwq, gwk = (torch.empty(d, dtype=torch.float32, device=dev) if w and t is not None else None
+                for w, t in zip(want, (q, k)))
+    buf, n = (None, 0)
+    if gwq is not None or gwk is not None:
+        buf, n = _workspace_of(_headnorm_ws(B, L, Hq, Hk, d), dev, ws, True)
+    _check(lib.pararnn_headnorm_backward(code, B, L, Hq, Hk, d, _at(q), _at(k), _at(grad_q), _at(grad_k), st,
+                                         _at(q_weight), _at(k_weight), _at(rq), _at(rk), _at(table), P, R,
+                                         _at(positions), nb, NORM_KINDS[kind], interleaved, _at(dq), _at(dk), _at(gwq),
+                                         _at(gwk), _at(buf), n, _raw_stream(dev)), "pararnn_headnorm_backward")
+    return dq, dk, gwq, gwk

@@ -6,6 +6,7 @@
 
 #include "pararnn.h"
 #include "launch.hpp"
+#include "mixer.hpp"
 #include "sequence.hpp"
 
 using namespace prn;
@@ -189,6 +190,97 @@ bool embedding_dims_ok(int32_t dtype, int64_t N, int64_t V, int64_t D) {
     // positions (fewer where that makes few workgroups) of at least 64 columns
     return type_ok(dtype) && dims_ok(N, D, 1) && dims_ok(V, D, 1) && N < most && V < most && D < ((int64_t)1 << 24) &&
            blocks_ok(N / 16 + 1) && blocks_ok((N / 64 + 1) * (D / 64 + 1) / 4 + 32768);
+}
+
+// ---- the delta-rule mixer's
+bool delta_dims_ok(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv) {
+    if (!type_ok(dtype) || dk < 1 || dk > kMaxHeadDim || dv < 1 || dv > kMaxHeadDim || Hk < 1 || H < Hk || H % Hk != 0) return false;
+    const int64_t blocks = (std::max(dk, dv) + 63) / 64;
+    return dims_ok(B, L, H) && dims_ok(B, L, H * kMaxHeadDim) && blocks_ok((B * H + 7) * blocks) && L < ((int64_t)1 << 31) &&
+           blocks_ok((B * H * ((L + 31) / 32) + 3) / 4) && H * std::max(dk, dv) * 4 < kMaxRowBytes;
+}
+
+// One operand [B, L, heads, d] with its strides (dense if none are given);
+// false where the pointer is not aligned to its elements, or a stride is
+// negative or (of a position, where rows are addressed in chunks) too large.
+bool head_view(HeadView &v, const void *p, size_t es, const int64_t *strides, int64_t L, int64_t heads, int64_t d, bool chunks) {
+    v.p = p;
+    if (!aligned(p, es)) return false;
+    const int64_t dense[3] = {L * heads * d, heads * d, d};
+    for (int j = 0; j < 3; ++j) {
+        v.st[j] = strides ? strides[j] : dense[j];
+        if (v.st[j] < 0 || (chunks && j == 1 && v.st[j] * 4 >= kMaxRowBytes)) return false;
+    }
+    return true;
+}
+
+struct DeltaIn {
+    const void *q, *k, *v;
+    const float *log_decay, *beta;
+    const void *grad_o;  // backward pass
+};
+bool delta_args(DeltaArgs &a, int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
+                const DeltaIn &in, const int64_t *strides) {
+    a = DeltaArgs{};
+    a.bf16 = dtype == PARARNN_BF16;
+    a.B = B;
+    a.L = L;
+    a.H = H;
+    a.Hk = Hk;
+    a.dk = (int)dk;
+    a.dv = (int)dv;
+    const size_t es = a.bf16 ? 2 : 4;
+    auto at = [&](int i) { return strides ? strides + 3 * i : nullptr; };
+    return head_view(a.q, in.q, es, at(0), L, Hk, dk, true) && head_view(a.k, in.k, es, at(1), L, Hk, dk, true) &&
+           head_view(a.v, in.v, es, at(2), L, H, dv, true) && head_view(a.log_decay, in.log_decay, 4, at(3), L, H, 1, false) &&
+           head_view(a.beta, in.beta, 4, at(4), L, H, 1, false) &&
+           (in.grad_o == nullptr || head_view(a.grad_o, in.grad_o, es, at(5), L, H, dv, true));
+}
+
+bool headnorm_dims_ok(int32_t dtype, int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d) {
+    return type_ok(dtype) && d >= 2 && d <= kMaxHeadDim && Hk >= 0 && dims_ok(B, L, Hq) && Hk < kMaxDim &&
+           (double)B * (double)L * ((double)Hq + (double)Hk) < (double)((int64_t)1 << 28);
+}
+
+struct Rotation {
+    const float *table;
+    int64_t P, R;
+    const void *positions;
+    int32_t position_bytes;
+};
+bool headnorm_args(HeadnormArgs &a, int32_t dtype, int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d, const void *const *in,
+                   int n, const int64_t *strides, const Rotation &rot, int32_t kind, int32_t interleaved) {
+    a = HeadnormArgs{};
+    a.bf16 = dtype == PARARNN_BF16;
+    a.B = B;
+    a.L = L;
+    a.Hq = Hq;
+    a.Hk = Hk;
+    a.d = (int)d;
+    if (kind != PARARNN_NORM_RMS && kind != PARARNN_NORM_L2) return false;
+    a.l2 = kind == PARARNN_NORM_L2;
+    a.interleaved = interleaved != 0;
+    if (rot.R < 0 || rot.R > d || rot.R % 2 != 0 || (rot.R > 0) != (rot.table != nullptr)) return false;
+    if (rot.R > 0) {
+        if (rot.P < 1 || rot.P > kMaxDim) return false;
+        if (rot.positions ? (rot.position_bytes != 4 && rot.position_bytes != 8) || !aligned(rot.positions, rot.position_bytes) : false) return false;
+        a.R = (int)rot.R;
+        a.table = rot.table;
+        a.P = rot.P;
+        a.positions = rot.positions;
+        a.wide = rot.position_bytes == 8;
+    }
+    const size_t es = a.bf16 ? 2 : 4;
+    for (int i = 0; i < n; ++i) {
+        const bool keys = i % 2 == 1;
+        HeadView &v = i < 2 ? a.x[i] : a.g[i - 2];
+        if (keys && Hk == 0) {
+            if (in[i] != nullptr) return false;
+            continue;
+        }
+        if (in[i] == nullptr || !head_view(v, in[i], es, strides ? strides + 3 * i : nullptr, L, keys ? Hk : Hq, d, false)) return false;
+    }
+    return true;
 }
 
 }  // namespace
@@ -566,6 +658,132 @@ int pararnn_embedding_backward(int32_t dtype, int64_t N, int64_t V, int64_t D, c
     if (!ws || ws_bytes < embedding_ws(N, D) || !aligned(ws, 256)) return PARARNN_ERR_INVALID;
     const EmbeddingArgs a{dtype == PARARNN_BF16, id_bytes == 8, N, V, D, padding_idx, ids, grad, scale, grad_table};
     return status_of(embedding_backward(a, Ws{static_cast<char *>(ws), ws_bytes}, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- the delta-rule mixer
+size_t pararnn_delta_workspace_bytes(int32_t backward, int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk,
+                                     int64_t dk, int64_t dv) {
+    if (!delta_dims_ok(dtype, B, L, H, Hk, dk, dv)) return 0;
+    DeltaArgs a;
+    delta_args(a, dtype, B, L, H, Hk, dk, dv, DeltaIn{}, nullptr);
+    return delta_ws(a, backward != 0);
+}
+
+int pararnn_delta_forward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
+                          const void *q, const void *k, const void *v, const float *log_decay, const float *beta,
+                          const int64_t *strides, const float *state, float scale, void *o, float *out_state,
+                          void *ws, size_t ws_bytes, void *stream) {
+    if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
+    if (!delta_dims_ok(dtype, B, L, H, Hk, dk, dv) || !q || !k || !v || !log_decay || !beta || !o) return PARARNN_ERR_INVALID;
+    DeltaArgs a;
+    if (!delta_args(a, dtype, B, L, H, Hk, dk, dv, DeltaIn{q, k, v, log_decay, beta, nullptr}, strides)) return PARARNN_ERR_INVALID;
+    if (!ws || ws_bytes < delta_ws(a, false) || !aligned(ws, 256)) return PARARNN_ERR_INVALID;
+    if (state != out_state && overlaps(state, out_state, B * H * dk * dv)) return PARARNN_ERR_INVALID;
+    a.state = state;
+    a.scale = scale;
+    a.o = o;
+    a.out_state = out_state;
+    return status_of(delta_forward(a, Ws{static_cast<char *>(ws), ws_bytes}, static_cast<hipStream_t>(stream)));
+}
+
+int pararnn_delta_backward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
+                           const void *q, const void *k, const void *v, const float *log_decay, const float *beta,
+                           const void *grad_o, const int64_t *strides, const float *state,
+                           const float *grad_out_state, float scale, void *grad_q, void *grad_k, void *grad_v,
+                           float *grad_log_decay, float *grad_beta, float *grad_state, void *ws, size_t ws_bytes,
+                           void *stream) {
+    if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
+    if (!delta_dims_ok(dtype, B, L, H, Hk, dk, dv) || !q || !k || !v || !log_decay || !beta || !grad_o || !grad_q || !grad_k || !grad_v)
+        return PARARNN_ERR_INVALID;
+    DeltaArgs a;
+    if (!delta_args(a, dtype, B, L, H, Hk, dk, dv, DeltaIn{q, k, v, log_decay, beta, grad_o}, strides)) return PARARNN_ERR_INVALID;
+    if (!ws || ws_bytes < delta_ws(a, true) || !aligned(ws, 256)) return PARARNN_ERR_INVALID;
+    const int64_t n = B * H * dk * dv;
+    if (overlaps(state, grad_state, n) || overlaps(grad_out_state, grad_state, n)) return PARARNN_ERR_INVALID;
+    a.state = state;
+    a.scale = scale;
+    a.grad_out_state = grad_out_state;
+    a.grad_q = grad_q;
+    a.grad_k = grad_k;
+    a.grad_v = grad_v;
+    a.grad_log_decay = grad_log_decay;
+    a.grad_beta = grad_beta;
+    a.grad_state = grad_state;
+    return status_of(delta_backward(a, Ws{static_cast<char *>(ws), ws_bytes}, static_cast<hipStream_t>(stream)));
+}
+
+int pararnn_delta_step(int32_t dtype, int64_t B, int64_t H, int64_t Hk, int64_t dk, int64_t dv, const void *q,
+                       const void *k, const void *v, const float *log_decay, const float *beta, const int64_t *strides,
+                       const float *state, float scale, void *o, float *out_state, void *stream) {
+    if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
+    if (!delta_dims_ok(dtype, B, 1, H, Hk, dk, dv) || !q || !k || !v || !log_decay || !beta || !state || !o || !out_state)
+        return PARARNN_ERR_INVALID;
+    DeltaArgs a;
+    if (!delta_args(a, dtype, B, 1, H, Hk, dk, dv, DeltaIn{q, k, v, log_decay, beta, nullptr}, strides)) return PARARNN_ERR_INVALID;
+    if (state != out_state && overlaps(state, out_state, B * H * dk * dv)) return PARARNN_ERR_INVALID;
+    a.state = state;
+    a.scale = scale;
+    a.o = o;
+    a.out_state = out_state;
+    return status_of(delta_step(a, static_cast<hipStream_t>(stream)));
+}
+
+int pararnn_headnorm_forward(int32_t dtype, int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d, const void *q,
+                             const void *k, const int64_t *strides, const float *wq, const float *wk,
+                             const float *table, int64_t P, int64_t R, const void *positions,
+                             int32_t position_bytes, int32_t kind, int32_t interleaved, float eps, void *yq, void *yk,
+                             float *rq, float *rk, void *stream) {
+    if (d > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
+    if (!headnorm_dims_ok(dtype, B, L, Hq, Hk, d) || !(eps >= 0.0f) || !yq || (Hk > 0) != (yk != nullptr)) return PARARNN_ERR_INVALID;
+    HeadnormArgs a;
+    const void *in[2] = {q, k};
+    if (!headnorm_args(a, dtype, B, L, Hq, Hk, d, in, 2, strides, Rotation{table, P, R, positions, position_bytes}, kind, interleaved))
+        return PARARNN_ERR_INVALID;
+    a.w[0] = wq;
+    a.w[1] = wk;
+    a.eps = eps;
+    a.y[0] = yq;
+    a.y[1] = yk;
+    a.r[0] = rq;
+    a.r[1] = rk;
+    return status_of(headnorm_forward(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t pararnn_headnorm_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d) {
+    if (!headnorm_dims_ok(PARARNN_F32, B, L, Hq, Hk, d)) return 0;
+    HeadnormArgs a{};
+    a.B = B;
+    a.L = L;
+    a.Hq = Hq;
+    a.Hk = Hk;
+    a.d = (int)d;
+    return headnorm_ws(a);
+}
+
+int pararnn_headnorm_backward(int32_t dtype, int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d, const void *q,
+                              const void *k, const void *grad_yq, const void *grad_yk, const int64_t *strides,
+                              const float *wq, const float *wk, const float *rq, const float *rk, const float *table,
+                              int64_t P, int64_t R, const void *positions, int32_t position_bytes, int32_t kind,
+                              int32_t interleaved, void *grad_q, void *grad_k, float *grad_wq, float *grad_wk,
+                              void *ws, size_t ws_bytes, void *stream) {
+    if (d > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
+    if (!headnorm_dims_ok(dtype, B, L, Hq, Hk, d) || !rq || !grad_q || (Hk > 0) != (grad_k != nullptr) || (Hk > 0 && !rk) ||
+        (Hk == 0 && grad_wk))
+        return PARARNN_ERR_INVALID;
+    HeadnormArgs a;
+    const void *in[4] = {q, k, grad_yq, grad_yk};
+    if (!headnorm_args(a, dtype, B, L, Hq, Hk, d, in, 4, strides, Rotation{table, P, R, positions, position_bytes}, kind, interleaved))
+        return PARARNN_ERR_INVALID;
+    if ((grad_wq || grad_wk) && (!ws || ws_bytes < headnorm_ws(a) || !aligned(ws, 256))) return PARARNN_ERR_INVALID;
+    a.w[0] = wq;
+    a.w[1] = wk;
+    a.r[0] = const_cast<float *>(rq);
+    a.r[1] = const_cast<float *>(rk);
+    a.y[0] = grad_q;
+    a.y[1] = grad_k;
+    a.gw[0] = grad_wq;
+    a.gw[1] = grad_wk;
+    return status_of(headnorm_backward(a, Ws{static_cast<char *>(ws), ws_bytes}, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,364 @@
+// headnorm.hip -- norms of queries and keys for each head, with the position
+// rotation in the same pass, and their gradients.
+//
+//   r = 1 / sqrt(m(x^2) + eps),  m the mean (RMS) or the sum (unit length),
+//   n = x r w,  y = n with its first R elements turned in pairs (c, c'):
+//   y_c = n_c cos - n_c' sin,  y_c' = n_c' cos + n_c sin.
+// Backward, with the rotation undone on the gradient first (g = Rot^T dy):
+//   dw = sum over rows of g x r,  dx = r (g w - x r m(g w x r)).
+//
+// Bound by memory: a row is read once (its partner elements again, from the
+// first-level cache) and written once.  A head's row is 16 lanes wide, so a
+// wave has four rows on their way and row sums stay on the vector unit; a group
+// of 16 lanes takes several heads of one position in turn, which share the
+// cosines and sines it has loaded.
+#include "mixer.hpp"
+#include "rows.hpp"
+
+namespace prn {
+
+namespace {
+
+constexpr int kThreads = 256, kLanes = 16, kGroups = kThreads / kLanes;
+
+struct Params {
+    HeadnormArgs a;
+    int64_t tokens;
+    int heads;     // heads a group takes in turn
+    int parts[2];  // groups a token's heads need: queries, keys
+    float *part;   // [gridDim.x][2][d] partial dw, or null
+};
+
+// The elements c = (lane + 16 j) V + i of a row.
+template <int V>
+__device__ __forceinline__ int column(int lane, int j) { return (lane + kLanes * j) * V; }
+
+// Where the rotation's partner of the V elements from c on begins.
+__device__ __forceinline__ int partner(const HeadnormArgs &a, int c) {
+    if (a.interleaved) return c ^ 1;
+    return c < a.R / 2 ? c + a.R / 2 : c - a.R / 2;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ VecT<T, V> load_row(const T *p) { return *reinterpret_cast<const VecT<T, V> *>(p); }
+
+// A group's share of the rotation: the cosine and the signed sine of each of
+// its elements (y_c = n_c cos + n_partner sin; back: the angle's opposite).
+template <int V, int NV>
+struct Turn {
+    float cos[NV][V], sin[NV][V];
+
+    __device__ __forceinline__ void load(const HeadnormArgs &a, int64_t token, int lane, bool back) {
+        if (a.R == 0) return;
+        int64_t pos;
+        if (a.positions == nullptr) pos = token % a.L;
+        else pos = a.wide ? static_cast<const int64_t *>(a.positions)[token] : (int64_t) static_cast<const int32_t *>(a.positions)[token];
+        const bool in = pos >= 0 && pos < a.P;
+        const float *row = a.table + (in ? pos : 0) * a.R;
+        const float nan = __builtin_nanf("");
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = column<V>(lane, j) + i;
+                if (c < a.R) {
+                    const bool second = a.interleaved ? (c & 1) : c >= a.R / 2;
+                    const int k = a.interleaved ? c >> 1 : second ? c - a.R / 2 : c;
+                    cos[j][i] = in ? row[k] : nan;
+                    sin[j][i] = in ? row[a.R / 2 + k] : nan;
+                    if (second == back) sin[j][i] = -sin[j][i];
+                }
+            }
+    }
+    // n turned: p holds the partners of n's elements.
+    __device__ __forceinline__ float operator()(const HeadnormArgs &a, int c, int j, int i, float n, float p) const {
+        return c < a.R ? fmaf(n, cos[j][i], p * sin[j][i]) : n;
+    }
+};
+
+// Partners of a row's elements in it (interleaved vectors hold their own).
+template <typename T, int V>
+__device__ __forceinline__ void load_partner(const HeadnormArgs &a, const T *row, int c, const VecT<T, V> &own, VecT<T, V> &to) {
+    if (c >= a.R) return;
+    if (V > 1 && a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) to.v[i] = own.v[i ^ 1];
+    } else {
+        to = load_row<T, V>(row + partner(a, c));
+    }
+}
+
+struct Item {
+    int64_t token;
+    int which, head, heads;  // queries or keys, the first head, how many
+};
+__device__ __forceinline__ Item item_of(const Params &p, int64_t n) {
+    const uint32_t per = (uint32_t)(p.parts[0] + p.parts[1]);
+    const uint32_t token = (uint32_t)n / per, part = (uint32_t)n - token * per;
+    Item it;
+    it.token = token;
+    it.which = part >= (uint32_t)p.parts[0];
+    const int H = (int)(it.which ? p.a.Hk : p.a.Hq);
+    it.head = (int)(part - (it.which ? p.parts[0] : 0)) * p.heads;
+    it.heads = min(p.heads, H - it.head);
+    return it;
+}
+template <typename T>
+__device__ __forceinline__ const T *row_of(const HeadView &v, int64_t b, int64_t t, int head) {
+    return static_cast<const T *>(v.p) + b * v.st[0] + t * v.st[1] + head * v.st[2];
+}
+
+template <typename T, int V, int NV>
+__global__ __launch_bounds__(kThreads) void headnorm_fwd_kernel(Params p) {
+    const HeadnormArgs &a = p.a;
+    const int lane = threadIdx.x & (kLanes - 1);
+    const int64_t items = p.tokens * (p.parts[0] + p.parts[1]);
+    const int64_t n = (int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes;
+    if (n >= items) return;
+    const Item it = item_of(p, n);
+    const int64_t b = it.token / a.L, t = it.token - b * a.L;
+    const int64_t H = it.which ? a.Hk : a.Hq;
+    const float *wp = it.which ? a.w[1] : a.w[0];
+    const HeadView x = it.which ? a.x[1] : a.x[0];
+    Turn<V, NV> turn;
+    turn.load(a, it.token, lane, false);
+    float w[NV][V], wp_of[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = column<V>(lane, j) + i;
+            w[j][i] = wp != nullptr && c < a.d ? wp[c] : 1.0f;
+            wp_of[j][i] = wp != nullptr && c < a.R ? wp[partner(a, c)] : 1.0f;
+        }
+    VecT<T, V> own[NV], other[NV];
+    auto load = [&](int head) {
+        const T *row = row_of<T>(x, b, t, head);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = column<V>(lane, j);
+            if (c < a.d) {
+                own[j] = load_row<T, V>(row + c);
+                load_partner<T, V>(a, row, c, own[j], other[j]);
+            }
+        }
+    };
+    load(it.head);
+    for (int h = 0; h < it.heads; ++h) {
+        float f[NV][V], o[NV][V], sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (column<V>(lane, j) < a.d)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    f[j][i] = (float)own[j].v[i];
+                    o[j][i] = (float)other[j].v[i];
+                    sum = fmaf(f[j][i], f[j][i], sum);
+                }
+        if (h + 1 < it.heads) load(it.head + h + 1);
+        sum = lanes16_sum(sum);
+        const float r = 1.0f / sqrtf((a.l2 ? sum : sum / (float)a.d) + a.eps);
+        const int64_t row = it.token * H + it.head + h;
+        if (lane == 0 && a.r[it.which] != nullptr) a.r[it.which][row] = r;
+        T *y = static_cast<T *>(it.which ? a.y[1] : a.y[0]) + row * a.d;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = column<V>(lane, j);
+            if (c < a.d) {
+                float v[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] = turn(a, c + i, j, i, f[j][i] * r * w[j][i], o[j][i] * r * wp_of[j][i]);
+                store_vec<T, V>(y + c, v);
+            }
+        }
+    }
+}
+
+template <typename T, int V, int NV>
+__global__ __launch_bounds__(kThreads) void headnorm_bwd_kernel(Params p) {
+    const HeadnormArgs &a = p.a;
+    const int lane = threadIdx.x & (kLanes - 1), grp = threadIdx.x / kLanes;
+    const int64_t items = p.tokens * (p.parts[0] + p.parts[1]);
+    float gw[2][NV][V] = {};
+    for (int64_t n = (int64_t)blockIdx.x * kGroups + grp; n < items; n += (int64_t)gridDim.x * kGroups) {
+        const Item it = item_of(p, n);
+        const int64_t b = it.token / a.L, t = it.token - b * a.L;
+        const int64_t H = it.which ? a.Hk : a.Hq;
+        const float *wp = it.which ? a.w[1] : a.w[0];
+        const HeadView x = it.which ? a.x[1] : a.x[0], g = it.which ? a.g[1] : a.g[0];
+        Turn<V, NV> turn;
+        turn.load(a, it.token, lane, true);
+        float w[NV][V];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int c = column<V>(lane, j) + i;
+                w[j][i] = wp != nullptr && c < a.d ? wp[c] : 1.0f;
+            }
+        VecT<T, V> own[NV], dy[NV], other[NV];
+        float r_of = 0.0f;
+        auto load = [&](int head) {
+            const T *row = row_of<T>(x, b, t, head), *grow = row_of<T>(g, b, t, head);
+            r_of = (it.which ? a.r[1] : a.r[0])[it.token * H + head];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = column<V>(lane, j);
+                if (c < a.d) {
+                    own[j] = load_row<T, V>(row + c);
+                    dy[j] = load_row<T, V>(grow + c);
+                    load_partner<T, V>(a, grow, c, dy[j], other[j]);
+                }
+            }
+        };
+        load(it.head);
+        for (int h = 0; h < it.heads; ++h) {
+            const float r = r_of;
+            float xh[NV][V], v[NV][V], sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = column<V>(lane, j);
+                if (c < a.d)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        xh[j][i] = (float)own[j].v[i] * r;
+                        const float gn = turn(a, c + i, j, i, (float)dy[j].v[i], (float)other[j].v[i]);
+                        const float part = gn * xh[j][i];
+                        gw[0][j][i] += it.which ? 0.0f : part;
+                        gw[1][j][i] += it.which ? part : 0.0f;
+                        v[j][i] = gn * w[j][i];
+                        sum = fmaf(v[j][i], xh[j][i], sum);
+                    }
+            }
+            if (h + 1 < it.heads) load(it.head + h + 1);
+            sum = lanes16_sum(sum);
+            if (!a.l2) sum /= (float)a.d;
+            T *out = static_cast<T *>(it.which ? a.y[1] : a.y[0]) + (it.token * H + it.head + h) * a.d;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = column<V>(lane, j);
+                if (c < a.d) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[j][i] = r * (v[j][i] - xh[j][i] * sum);
+                    store_vec<T, V>(out + c, v[j]);
+                }
+            }
+        }
+    }
+    if (p.part == nullptr) return;
+    // the groups' sums, in their order
+    __shared__ float buf[kGroups][kLanes * V];
+    float *part = p.part + (int64_t)blockIdx.x * 2 * a.d;
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < V; ++i) buf[grp][lane * V + i] = gw[which][j][i];
+            __syncthreads();
+            for (int k = threadIdx.x; k < kLanes * V; k += kThreads) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int m = 0; m < kGroups; ++m) sum += buf[m][k];
+                const int c = kLanes * V * j + k;
+                if (c < a.d) part[which * a.d + c] = sum;
+            }
+        }
+}
+
+// dw = sum of the G partials, always in the same order: 64 columns a workgroup, 16 threads a column.
+__global__ __launch_bounds__(1024) void headnorm_reduce_kernel(const float *part, int G, int d, float *gq, float *gk) {
+    __shared__ float buf[16][64];
+    const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + lane;
+    float *out = blockIdx.y == 0 ? gq : gk;
+    if (out == nullptr) return;
+    float v = 0.0f;
+    if (c < d) {
+#pragma unroll 8
+        for (int g = grp; g < G; g += 16) v += part[((int64_t)g * 2 + blockIdx.y) * d + c];
+    }
+    buf[grp][lane] = v;
+    __syncthreads();
+    if (grp == 0 && c < d) {
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v += buf[i][lane];
+        out[c] = v;
+    }
+}
+
+bool view_vec(const HeadView &v, int n) {
+    return aligned16(v.p) && v.st[0] % n == 0 && v.st[1] % n == 0 && v.st[2] % n == 0;
+}
+
+// Whether every row moves as 16-byte vectors whose rotation partners are one too.
+bool rows_vec(const HeadnormArgs &a, int es, bool back) {
+    const int n = 16 / es;
+    if (a.d % n != 0 || (!a.interleaved && a.R / 2 % n != 0)) return false;
+    for (int i = 0; i < (a.Hk ? 2 : 1); ++i)
+        if (!view_vec(a.x[i], n) || !aligned16(a.y[i]) || (back && !view_vec(a.g[i], n))) return false;
+    return true;
+}
+
+// Heads a group takes in turn: as many as leave four waves a SIMD.
+Params params(const HeadnormArgs &a) {
+    Params p{};
+    p.a = a;
+    p.tokens = a.B * a.L;
+    const int64_t rows = p.tokens * (a.Hq + a.Hk), want = (int64_t)device_cu_count() * kGroups * 4;
+    p.heads = (int)std::max<int64_t>(1, std::min<int64_t>(8, rows / want));
+    p.parts[0] = (int)((a.Hq + p.heads - 1) / p.heads);
+    p.parts[1] = (int)((a.Hk + p.heads - 1) / p.heads);
+    return p;
+}
+
+int64_t groups(const Params &p) { return (p.tokens * (p.parts[0] + p.parts[1]) + kGroups - 1) / kGroups; }
+
+// Workgroups of the backward pass, which keep the weights' gradients in registers over all their rows.
+int bwd_grid(const Params &p) { return (int)std::min<int64_t>(groups(p), (int64_t)device_cu_count() * 4); }
+
+template <typename T, int V, int NV>
+hipError_t launch(const Params &p, bool back, hipStream_t s) {
+    if (back) headnorm_bwd_kernel<T, V, NV><<<bwd_grid(p), kThreads, 0, s>>>(p);
+    else headnorm_fwd_kernel<T, V, NV><<<(unsigned)groups(p), kThreads, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run(const Params &p, bool back, hipStream_t s) {
+    const int d = p.a.d;
+    if (rows_vec(p.a, sizeof(T), back)) {
+        constexpr int V = kVec<T>;
+        if (d <= kLanes * V) return launch<T, V, 1>(p, back, s);
+        if (d <= kLanes * V * 2) return launch<T, V, 2>(p, back, s);
+        if constexpr (V == 4) return launch<T, V, 4>(p, back, s);
+    }
+    if (d <= kLanes * 4) return launch<T, 1, 4>(p, back, s);
+    if (d <= kLanes * 8) return launch<T, 1, 8>(p, back, s);
+    return launch<T, 1, 16>(p, back, s);
+}
+
+}  // namespace
+
+size_t headnorm_ws(const HeadnormArgs &a) {
+    return kScratchOffset + (size_t)bwd_grid(params(a)) * 2 * a.d * sizeof(float);
+}
+
+hipError_t headnorm_forward(const HeadnormArgs &a, hipStream_t s) {
+    const Params p = params(a);
+    return a.bf16 ? run<bf16>(p, false, s) : run<float>(p, false, s);
+}
+
+hipError_t headnorm_backward(const HeadnormArgs &a, const Ws &ws, hipStream_t s) {
+    Params p = params(a);
+    const bool want = a.gw[0] != nullptr || a.gw[1] != nullptr;
+    if (want) p.part = reinterpret_cast<float *>(ws.p + kScratchOffset);
+    const hipError_t e = a.bf16 ? run<bf16>(p, true, s) : run<float>(p, true, s);
+    if (e != hipSuccess || !want) return e;
+    headnorm_reduce_kernel<<<dim3((a.d + 63) / 64, 2), 1024, 0, s>>>(p.part, bwd_grid(p), a.d, a.gw[0], a.gw[1]);
+    return hipGetLastError();
+}
+
+}  // namespace prn
