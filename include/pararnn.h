@@ -476,7 +476,8 @@ int pararnn_embedding_backward(int32_t dtype, int64_t N, int64_t V, int64_t D, c
  * out_state: [B, H, dk, dv] fp32 (state NULL: zeros; out_state NULL: not
  * wanted; out_state may be state itself, but not overlap it otherwise).
  * 1 <= dk, dv <= 256 (above: PARARNN_ERR_UNSUPPORTED).  B H ceil(L / 32) is
- * below 2^26 - 4 and B H below 2^24 over the column blocks of 64 in dv.
+ * below 2^26 - 4 (backward 2^22, and where heads share keys B L Hk dk below
+ * 2^32) and B H below 2^23 over the blocks of 64 in the wider of dk and dv.
  * strides: HOST array of {batch row, position, head} strides in elements for
  * q, k, v, log_decay and beta in turn (15 values), not negative, those of
  * positions in q, k and v below 2^22; the last dimension of q, k and v is

@@ -193,11 +193,16 @@ bool embedding_dims_ok(int32_t dtype, int64_t N, int64_t V, int64_t D) {
 }
 
 // ---- the delta-rule mixer's
-bool delta_dims_ok(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv) {
+bool delta_dims_ok(LinattnPass pass, int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv) {
     if (!type_ok(dtype) || dk < 1 || dk > kMaxHeadDim || dv < 1 || dv > kMaxHeadDim || Hk < 1 || H < Hk || H % Hk != 0) return false;
     const int64_t blocks = (std::max(dk, dv) + 63) / 64;
-    return dims_ok(B, L, H) && dims_ok(B, L, H * kMaxHeadDim) && blocks_ok((B * H + 7) * blocks) && L < ((int64_t)1 << 31) &&
-           blocks_ok((B * H * ((L + 31) / 32) + 3) / 4) && H * std::max(dk, dv) * 4 < kMaxRowBytes;
+    if (!dims_ok(B, L, H) || !dims_ok(B, L, H * kMaxHeadDim) || !blocks_ok((B * H + 7) * blocks * 2) || L >= ((int64_t)1 << 31) ||
+        H * std::max(dk, dv) * 4 >= kMaxRowBytes)
+        return false;
+    const int64_t items = B * H * ((L + 31) / 32);
+    if (pass != LinattnPass::Backward) return blocks_ok((items + 3) / 4);
+    // workgroups of up to 1024 threads a span; sums over shared heads an element a thread
+    return items < (int64_t)1 << 22 && (H == Hk || blocks_ok((B * L * Hk * dk + 255) / 256));
 }
 
 // One operand [B, L, heads, d] with its strides (dense if none are given);
@@ -663,7 +668,7 @@ int pararnn_embedding_backward(int32_t dtype, int64_t N, int64_t V, int64_t D, c
 // ---------------------------------------------------------------- the delta-rule mixer
 size_t pararnn_delta_workspace_bytes(int32_t backward, int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk,
                                      int64_t dk, int64_t dv) {
-    if (!delta_dims_ok(dtype, B, L, H, Hk, dk, dv)) return 0;
+    if (!delta_dims_ok(backward ? LinattnPass::Backward : LinattnPass::Forward, dtype, B, L, H, Hk, dk, dv)) return 0;
     DeltaArgs a;
     delta_args(a, dtype, B, L, H, Hk, dk, dv, DeltaIn{}, nullptr);
     return delta_ws(a, backward != 0);
@@ -674,7 +679,8 @@ int pararnn_delta_forward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_
                           const int64_t *strides, const float *state, float scale, void *o, float *out_state,
                           void *ws, size_t ws_bytes, void *stream) {
     if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
-    if (!delta_dims_ok(dtype, B, L, H, Hk, dk, dv) || !q || !k || !v || !log_decay || !beta || !o) return PARARNN_ERR_INVALID;
+    if (!delta_dims_ok(LinattnPass::Forward, dtype, B, L, H, Hk, dk, dv) || !q || !k || !v || !log_decay || !beta || !o)
+        return PARARNN_ERR_INVALID;
     DeltaArgs a;
     if (!delta_args(a, dtype, B, L, H, Hk, dk, dv, DeltaIn{q, k, v, log_decay, beta, nullptr}, strides)) return PARARNN_ERR_INVALID;
     if (!ws || ws_bytes < delta_ws(a, false) || !aligned(ws, 256)) return PARARNN_ERR_INVALID;
@@ -693,7 +699,8 @@ int pararnn_delta_backward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64
                            float *grad_log_decay, float *grad_beta, float *grad_state, void *ws, size_t ws_bytes,
                            void *stream) {
     if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
-    if (!delta_dims_ok(dtype, B, L, H, Hk, dk, dv) || !q || !k || !v || !log_decay || !beta || !grad_o || !grad_q || !grad_k || !grad_v)
+    if (!delta_dims_ok(LinattnPass::Backward, dtype, B, L, H, Hk, dk, dv) || !q || !k || !v || !log_decay || !beta || !grad_o || !grad_q ||
+        !grad_k || !grad_v)
         return PARARNN_ERR_INVALID;
     DeltaArgs a;
     if (!delta_args(a, dtype, B, L, H, Hk, dk, dv, DeltaIn{q, k, v, log_decay, beta, grad_o}, strides)) return PARARNN_ERR_INVALID;
@@ -716,7 +723,7 @@ int pararnn_delta_step(int32_t dtype, int64_t B, int64_t H, int64_t Hk, int64_t 
                        const void *k, const void *v, const float *log_decay, const float *beta, const int64_t *strides,
                        const float *state, float scale, void *o, float *out_state, void *stream) {
     if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
-    if (!delta_dims_ok(dtype, B, 1, H, Hk, dk, dv) || !q || !k || !v || !log_decay || !beta || !state || !o || !out_state)
+    if (!delta_dims_ok(LinattnPass::Step, dtype, B, 1, H, Hk, dk, dv) || !q || !k || !v || !log_decay || !beta || !state || !o || !out_state)
         return PARARNN_ERR_INVALID;
     DeltaArgs a;
     if (!delta_args(a, dtype, B, 1, H, Hk, dk, dv, DeltaIn{q, k, v, log_decay, beta, nullptr}, strides)) return PARARNN_ERR_INVALID;

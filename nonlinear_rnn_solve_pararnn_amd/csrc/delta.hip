@@ -32,27 +32,6 @@ struct WalkArgs {
     const char *rec;
 };
 
-// (batch row, head) pairs in groups of 8, then everything that reads the same
-// rows: consecutive workgroups go to the 8 XCDs in turn, so all blocks of one
-// pair meet in one L2.
-struct Where {
-    int bh, b, h, blk;
-    bool any;
-};
-__device__ __forceinline__ Where where(const WalkArgs &a) {
-    auto scalar = [](uint32_t x) { return (int)__builtin_amdgcn_readfirstlane(x); };
-    const uint32_t per = (uint32_t)a.nblk, heads = (uint32_t)a.H;
-    const uint32_t grp = blockIdx.x / (8 * per), rest = blockIdx.x - grp * 8 * per;
-    const uint32_t bh = grp * 8 + (rest & 7);
-    Where w;
-    w.bh = scalar(bh);
-    w.b = scalar(bh / heads);
-    w.h = w.bh - w.b * (int)heads;
-    w.blk = scalar(rest >> 3);
-    w.any = w.bh < (int)(a.B * a.H);
-    return w;
-}
-
 // Part of the work of a chunk that every walk shares: eight numbers of a lane
 // (a column of its wave's, positions 8 q ..) with the first ones that are not
 // finite, and all after them, taken out.  Returns the first such position of
@@ -91,11 +70,11 @@ __global__ __launch_bounds__(kThreads, (kWgs<T, D1>)) void walk_kernel(WalkArgs 
     constexpr int kPX = C * kTileRow<D1>, kPZ = C * kTileRow<kNB>;
     __shared__ __align__(16) bf16 K[kP * kPX], Q[kP * kPX], V[kP * kPZ];
     __shared__ __align__(16) Gates gates;
-    const Where wh = where(a);
+    const Where wh = where(a.nblk, (int)(a.B * a.H), (int)a.H);
     if (!wh.any) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
     const int tr_i = m >> 2, tr_c = m & 3;  // this lane's row and column group in a transposing read
-    const int c0 = wh.blk * kNB, col = c0 + wave * 16 + m;
+    const int c0 = wh.sub * kNB, col = c0 + wave * 16 + m;
     const int last = (int)(a.L - (int64_t)(a.chunks - 1) * C);
 
     f32x4 S[NA];
@@ -396,14 +375,6 @@ int walk_width(int d1) { return d1 <= 32 ? 32 : d1 <= 64 ? 64 : d1 <= 128 ? 128 
 
 int blocks_of(int cols) { return (cols + kNB - 1) / kNB; }
 
-WalkView view_of(const HeadView &v) { return {v.p, v.st[0], v.st[1], v.st[2]}; }
-
-// Rows that overlap are left to the loads of any alignment (see linattn.hip).
-bool view_vec(const HeadView &v, int d, int es) {
-    const int64_t n = 16 / es;
-    return d % n == 0 && aligned16(v.p) && v.st[0] % n == 0 && v.st[1] % n == 0 && v.st[2] % n == 0 && (v.st[1] >= d || v.st[1] == 0);
-}
-
 int64_t chunks_of(int64_t L) { return (L + C - 1) / C; }
 
 template <typename T, int D1, bool VEC>
@@ -466,6 +437,7 @@ void step_launch(const DeltaArgs &p, const StepArgs &a, hipStream_t s) {
 }  // namespace delta
 
 size_t delta_ws(const DeltaArgs &p, bool backward) {
+    if (backward) return kScratchOffset + delta::back_ws(p);
     const size_t items = (size_t)(p.B * p.H * delta::chunks_of(p.L));
     const int64_t rec = p.bf16 ? delta::kRecord<bf16, false> : delta::kRecord<float, false>;
     return kScratchOffset + items * rec;
@@ -476,7 +448,7 @@ hipError_t delta_forward(const DeltaArgs &p, const Ws &ws, hipStream_t s) {
     return p.bf16 ? delta::forward_type<bf16>(p, scratch, s) : delta::forward_type<float>(p, scratch, s);
 }
 
-hipError_t delta_backward(const DeltaArgs &p, const Ws &ws, hipStream_t s) { return hipErrorNotSupported; }
+hipError_t delta_backward(const DeltaArgs &p, const Ws &ws, hipStream_t s) { return delta::backward(p, ws.p + kScratchOffset, s); }
 
 hipError_t delta_step(const DeltaArgs &p, hipStream_t s) {
     const delta::StepArgs a{p.H, (int)(p.H / p.Hk), p.dk, p.dv, delta::blocks_of(p.dv), p.q, p.k, p.v, p.log_decay, p.beta,

@@ -48,6 +48,40 @@ constexpr int kAtTt = kAtT + 6 * kTile, kAtPt = kAtTt + 6 * kTile;  // backward
 // result, tile by tile, are then eight consecutive positions of one lane.
 __device__ __forceinline__ int row_of(int u, int m) { return 8 * (m >> 2) + 4 * u + (m & 3); }
 
+// (batch row, head) pairs in groups of 8, then the `per` workgroups that read the
+// same rows: consecutive workgroups go to the 8 XCDs in turn, so all workgroups
+// of one pair meet in one L2.
+struct Where {
+    int bh, b, h, sub;
+    bool any;
+};
+__device__ __forceinline__ Where where(int per_, int pairs, int heads) {
+    auto scalar = [](uint32_t x) { return (int)__builtin_amdgcn_readfirstlane(x); };
+    const uint32_t per = (uint32_t)per_;
+    const uint32_t grp = blockIdx.x / (8 * per), rest = blockIdx.x - grp * 8 * per;
+    const uint32_t bh = grp * 8 + (rest & 7);
+    Where w;
+    w.bh = scalar(bh);
+    w.b = scalar(bh / (uint32_t)heads);
+    w.h = w.bh - w.b * heads;
+    w.sub = scalar(rest >> 3);
+    w.any = w.bh < pairs;
+    return w;
+}
+
+__host__ __device__ __forceinline__ WalkView view_of(const HeadView &v) { return {v.p, v.st[0], v.st[1], v.st[2]}; }
+
+// Whether rows move as 16-byte vectors.  Rows that overlap are left to the
+// loads of any alignment, whose rows past the last position are cleared.
+inline bool view_vec(const HeadView &v, int d, int es) {
+    const int64_t n = 16 / es;
+    return d % n == 0 && aligned16(v.p) && v.st[0] % n == 0 && v.st[1] % n == 0 && v.st[2] % n == 0 && (v.st[1] >= d || v.st[1] == 0);
+}
+
+// delta_back.hip
+size_t back_ws(const DeltaArgs &p);
+hipError_t backward(const DeltaArgs &p, char *scratch, hipStream_t s);
+
 struct PrepArgs {
     HeadView q, k, log_decay, beta;
     int64_t L, items;  // items: chunks of all (batch row, head) pairs

@@ -1,0 +1,748 @@
+// delta_back.hip -- gradients of the gated delta rule (formulas of a chunk:
+// delta.hpp).
+//
+// With do' = scale do, D the gradient of the state and u_t, dR_t = dLoss/d(u_t / b_t):
+//   dR = T^T (P^T do + r (K D)),  D <- f_last D + (f Q)^T do' - (f b K)^T dR,
+// which needs no S, as the walk that finds U and S needs no D: both run side by
+// side in one launch (back_walk_kernel), whole workgroups either way, and leave
+// U, dR and their states at the ends of every span of positions.  u_t and dR_t
+// belong to their position, not to the chunk they were found in, so the rest is
+// worked out in spans of any length (grad_kernel), all spans side by side.
+// With S before the span, D after it, dr = b dR and j < i in both sums,
+//   dv = dr,  db = dR.u / b,
+//   dq = scale f (do S^T) + MP K,  MP_ij = E_ij do'_i.u_j (j <= i),
+//   dk = r (U D^T) - f (dr S^T) + MP^T Q + (MA + MA^T) K,  MA_ij = -E_ij dr_i.u_j,
+//   dg_t = f_last <D, S> + sum of those products that e^(g_t) is part of: of rows
+//          from t on with S, of rows before t with D, of pairs i >= t > j.
+// The last line adds terms that the gate does take part in; the shorter
+// identity dg_t - dg_(t+1) = do_t.o_t - dv_t.v_t adds up others that cancel.
+//
+// Precision: walks as in the forward pass.  fp32 tensors: three planes of
+// everything.  bf16 tensors: S, D, U, dr, MP and MA to 16 bits (dg and db are fp32
+// results: 2^-17 of a term; dq and dk are differences where a key is written over).
+#include "delta.hpp"
+
+namespace prn {
+namespace delta {
+
+using walk::Ahead;
+using walk::kNB;
+using walk::kTileRow;
+using walk::mfma_planes;
+using walk::read_row;
+using walk::read_tr;
+using walk::Rows;
+using walk::split3;
+using walk::state_row;
+using walk::tile_at;
+using walk::u32x2;
+
+struct BackArgs {
+    HeadView q, k, v, grad_o, log_decay, beta;
+    const float *init, *fin;  // S before the first position, D after the last one; null for zeros
+    float *grad_init;         // or null
+    int64_t B, L, H, Hk;
+    int group, dk, dv, chunks, nblk, spans;
+    float scale;
+    const char *rec;
+    float *U, *dR;  // [B H][spans span][D]
+    float *S, *Dn;  // [B H][spans][D][D]: rows of dk, columns of dv
+    float *part_q, *part_k;  // [B, L, H, dk] where heads share q and k, or null
+    void *grad_q, *grad_k, *grad_v;
+    float *grad_g, *grad_b;
+    int out8, out4;  // rows of grad_v, and of grad_q and grad_k, may be stored eight or four elements at a time
+};
+
+// Positions a span of grad_kernel: as many as its operands in LDS allow.
+template <typename T, int D> constexpr int kSpan = sizeof(T) == 2 && D <= 128 ? 64 : 32;
+
+template <typename T, int D1>
+constexpr int kBackWgs = D1 > 128 || (sizeof(T) == 4 && D1 > 64) ? 1 : 2;
+
+// The two walks: workgroups that take S from the first chunk on, and those
+// that take D from the last one back.
+template <typename T, int D1, bool VEC>
+__global__ __launch_bounds__(walk::kThreads, (kBackWgs<T, D1>)) void back_walk_kernel(BackArgs a) {
+    constexpr int kP = kPlanes<T>, NA = D1 / 16, NT = D1 / 32, kSpanChunks = kSpan<T, D1> / C;
+    constexpr int kPX = C * kTileRow<D1>, kPZ = C * kTileRow<kNB>;
+    __shared__ __align__(16) bf16 K[kP * kPX], Q[kP * kPX], Z[kP * kPZ];
+    __shared__ __align__(16) Gates gates;
+    const Where wh = where(a.nblk * 2, (int)(a.B * a.H), (int)a.H);
+    if (!wh.any) return;
+    const bool down = wh.sub >= a.nblk;  // D
+    const int blk = down ? wh.sub - a.nblk : wh.sub;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
+    const int tr_i = m >> 2, tr_c = m & 3;
+    const int c0 = blk * kNB, col = c0 + wave * 16 + m;
+    const int last = (int)(a.L - (int64_t)(a.chunks - 1) * C);
+
+    const float *from = down ? a.fin : a.init;
+    f32x4 S[NA];
+#pragma unroll
+    for (int t = 0; t < NA; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = state_row(t, q, r);
+            const float s = from != nullptr && col < a.dv && row < a.dk ? from[((int64_t)wh.bh * a.dk + row) * a.dv + col] : 0.0f;
+            S[t][r] = __builtin_canonicalizef(s);  // no signalling NaN (a launch tag) goes into the workspace
+        }
+
+    const int hk = wh.h / a.group;
+    const WalkView zv = down ? view_of(a.grad_o) : view_of(a.v);
+    const Rows rq = walk::rows_of<T>(view_of(a.q), wh.b, hk, a.L, 0, C, 0, 0, a.dk), rk = walk::rows_of<T>(view_of(a.k), wh.b, hk, a.L, 0, C, 0, 0, a.dk),
+               rz = walk::rows_of<T>(zv, wh.b, wh.h, a.L, 0, C, 0, c0, a.dv);
+    const char *rec = a.rec + (int64_t)wh.bh * a.chunks * kRecord<T, true>;
+    const int64_t span_rows = (int64_t)a.spans * kSpan<T, D1>;
+    float *rows = (down ? a.dR : a.U) + (int64_t)wh.bh * span_rows * D1 + col;
+    float *states = (down ? a.Dn : a.S) + (int64_t)wh.bh * a.spans * D1 * D1 + col;
+
+    Ahead<T, D1, C, VEC> aq, ak;
+    Ahead<T, kNB, C, VEC> az;
+    aq.init(rq);
+    ak.init(rk);
+    az.init(rz);
+    float gate_ahead = 0.0f;
+    bf16x8 Ta[2][3], Pa[2][3];
+    auto chunk_of = [&](int i) { return down ? a.chunks - 1 - i : i; };
+    auto positions = [&](int c) { return c < a.chunks - 1 ? C : last; };
+    auto load = [&](int i) {
+        if (i >= a.chunks) return;
+        const int c = chunk_of(i), cnt = positions(c);
+        ak.load(rk, c, cnt);
+        az.load(rz, c, cnt);
+        const char *r = rec + (int64_t)c * kRecord<T, true>;
+        if (threadIdx.x < sizeof(Gates) / 4) gate_ahead = reinterpret_cast<const float *>(r)[threadIdx.x];
+        const char *tm = r + (down ? kAtTt : kAtT) + lane * 16;
+#pragma unroll
+        for (int n = 0; n < 6; ++n) Ta[n / 3][n % 3] = *reinterpret_cast<const bf16x8 *>(tm + n * kTile);
+        if (down) {
+            aq.load(rq, c, cnt);
+#pragma unroll
+            for (int n = 0; n < 6; ++n) Pa[n / 3][n % 3] = *reinterpret_cast<const bf16x8 *>(r + kAtPt + n * kTile + lane * 16);
+        }
+    };
+    load(0);
+
+    for (int i = 0; i < a.chunks; ++i) {
+        const int c = chunk_of(i), cnt = positions(c);
+        if (down ? c % kSpanChunks == kSpanChunks - 1 || i == 0 : c % kSpanChunks == 0) {
+            float *to = states + (int64_t)(c / kSpanChunks) * D1 * D1;
+#pragma unroll
+            for (int t = 0; t < NA; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) to[state_row(t, q, r) * D1] = S[t][r];
+        }
+        bf16x8 Tm[2][3], Pm[2][3];
+#pragma unroll
+        for (int n = 0; n < 6; ++n) {
+            Tm[n / 3][n % 3] = Ta[n / 3][n % 3];
+            Pm[n / 3][n % 3] = Pa[n / 3][n % 3];
+        }
+        lds_barrier();  // the last chunk's reads are done
+        ak.store(rk, K);
+        az.store(rz, Z);
+        if (down) aq.store(rq, Q);
+        if (threadIdx.x < sizeof(Gates) / 4) reinterpret_cast<float *>(&gates)[threadIdx.x] = gate_ahead;
+        load(i + 1);
+        if constexpr (!VEC) {
+            if (cnt < C) {
+                walk::clear_past<kP, D1, C>(K, threadIdx.x, cnt);
+                if (down) walk::clear_past<kP, D1, C>(Q, threadIdx.x, cnt);
+                walk::clear_past<kP, kNB, C>(Z, threadIdx.x, cnt);
+            }
+        }
+        lds_barrier();
+
+        f32x4 ks[2] = {};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float v[8] = {S[2 * t][0],     S[2 * t][1],     S[2 * t][2],     S[2 * t][3],
+                                S[2 * t + 1][0], S[2 * t + 1][1], S[2 * t + 1][2], S[2 * t + 1][3]};
+            bf16x8 sp[3];
+            split3(v, sp);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                bf16x8 kr[kP];
+#pragma unroll
+                for (int p = 0; p < kP; ++p) kr[p] = read_row(&K[p * kPX + tile_at<D1>(row_of(u, m), 4 * t + q)]);
+                ks[u] = mfma_planes(kr, sp, ks[u]);
+            }
+        }
+        bf16x8 z[kP];
+        {
+            const int grp = 2 * wave + (tr_c >> 1), in = 4 * (tr_c & 1);
+#pragma unroll
+            for (int p = 0; p < kP; ++p)
+                z[p] = walk::join(read_tr(&Z[p * kPZ + tile_at<kNB>(8 * q + tr_i, grp) + in]),
+                                  read_tr(&Z[p * kPZ + tile_at<kNB>(8 * q + tr_i + 4, grp) + in]));
+        }
+        float x[8];
+        bf16x8 xp[3];
+        const float *edge = down ? gates.r : gates.f;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) x[n] = edge[8 * q + n] * ks[n >> 2][n & 3];
+        if (down) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const f32x4 y = mfma_planes(Pm[u], z, f32x4{x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]});
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[4 * u + r] = y[r];
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) x[n] = gates.b[8 * q + n] * (walk::plane_sum(z, n) - x[n]);
+        }
+        split3(x, xp);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const f32x4 y = mfma_planes(Tm[u], xp, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[4 * u + r] = y[r];
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) rows[((int64_t)c * C + 8 * q + n) * D1] = x[n];
+
+        // what the chunk adds to the state: K^T (r U), or Q^T (f do') - K^T (f b dR)
+        const Carry carry{gates.carry, gates.fast != 0.0f};
+#pragma unroll
+        for (int n = 0; n < 8; ++n) x[n] *= down ? -gates.f[8 * q + n] * gates.b[8 * q + n] : gates.r[8 * q + n];
+        split3(x, xp);
+        bf16x8 wp[3];
+        if (down) {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) x[n] = a.scale * gates.f[8 * q + n] * walk::plane_sum(z, n);
+            split3(x, wp);
+        }
+#pragma unroll
+        for (int t = 0; t < NA; ++t) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[t][r] = carry(S[t][r]);
+            const int grp = 4 * (t >> 1) + tr_c, in = 4 * (t & 1);
+            auto across = [&](const bf16 *X, bf16x8 (&y)[kP]) {
+#pragma unroll
+                for (int p = 0; p < kP; ++p)
+                    y[p] = walk::join(read_tr(&X[p * kPX + tile_at<D1>(8 * q + tr_i, grp) + in]),
+                                      read_tr(&X[p * kPX + tile_at<D1>(8 * q + tr_i + 4, grp) + in]));
+            };
+            bf16x8 y[kP];
+            if (down) {
+                across(Q, y);
+                S[t] = mfma_planes(y, wp, S[t]);
+            }
+            across(K, y);
+            S[t] = mfma_planes(y, xp, S[t]);
+        }
+    }
+    if (down && a.grad_init != nullptr && col < a.dv) {
+#pragma unroll
+        for (int t = 0; t < NA; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = state_row(t, q, r);
+                if (row < a.dk) a.grad_init[((int64_t)wh.bh * a.dk + row) * a.dv + col] = S[t][r];
+            }
+    }
+}
+
+// ---------------------------------------------------------------- the rest, span by span
+// A wave owns 16 rows of S and D (16 elements of k and q) and the gradients of
+// those elements at all positions of the span; S and D go from memory straight
+// into operands, each element once.  LDS holds the rows of do, U and dr, then,
+// in their place, those of q and k and the matrices MP and MA + MA^T.
+template <int N>
+__device__ __forceinline__ void planes_to(const float (&v)[8], bf16x8 (&p)[N]) { walk::to_planes(v, p); }
+
+template <typename T, int D>
+struct GradLds {
+    static constexpr int kN = kSpan<T, D>, kP = kPlanes<T>, kU = kP == 3 ? 3 : 2, kM = kU, kWaves = D / 16;
+    static constexpr int kRowsX = kN * kTileRow<D>, kRowsM = kN * kTileRow<kN>;
+    struct First {
+        bf16 go[kP * kRowsX], u[kU * kRowsX], dr[kU * kRowsX];
+    };
+    struct Second {
+        bf16 k[kP * kRowsX], q[kP * kRowsX], mp[kM * kRowsM], ma[kM * kRowsM];
+    };
+    union alignas(16) {
+        First first;
+        Second second;
+    };
+    double G[kN];
+    float f[kN], r[kN], b[kN];
+    float y[kWaves][kN], x[kWaves][kN], z[kWaves];  // the waves' shares of a row's products with S and with D, and of <D, S>
+    float row[2][kN / 16][kN], col[2][kN / 16][kN]; // sums of pairs of either kind: of a row in a tile of columns, of a column in one of rows
+};
+
+template <typename T, int D, bool VEC>
+__global__ __launch_bounds__(D * 4) void grad_kernel(BackArgs a) {
+    using Lds = GradLds<T, D>;
+    constexpr int N = Lds::kN, kP = Lds::kP, kU = Lds::kU, kM = Lds::kM, kWaves = Lds::kWaves, kThreadsG = D * 4;
+    constexpr int kX = Lds::kRowsX, kMx = Lds::kRowsM, NI = N / 16, NS = N / 32, kTiles = NI * (NI + 1) / 2;
+    __shared__ Lds l;
+    const uint32_t bh = blockIdx.x / (uint32_t)a.spans, span = blockIdx.x - bh * (uint32_t)a.spans;
+    const int64_t b = bh / (uint32_t)a.H, h = bh - b * a.H, hk = h / a.group, begin = (int64_t)span * N;
+    const int cnt = (int)min((int64_t)N, a.L - begin);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
+    const int tr_i = m >> 2, tr_c = m & 3;
+    const int steps = a.nblk * 2;  // of 32 columns of dv
+
+    if (threadIdx.x < N) {
+        const int p = threadIdx.x;
+        auto gate = [&](const HeadView &v) { return static_cast<const float *>(v.p)[b * v.st[0] + (begin + p) * v.st[1] + h * v.st[2]]; };
+        float g = p < cnt ? gate(a.log_decay) : 0.0f;
+        const float beta = p < cnt ? gate(a.beta) : 0.0f;
+        if (g < -1e5f) g = -1e5f;
+        double sum = (double)g * 1.4426950408889634;
+#pragma unroll
+        for (int d = 1; d < N; d *= 2) {
+            const double up = __shfl_up(sum, d, N);
+            if (p >= d) sum += up;
+        }
+        const double whole = __shfl(sum, N - 1, N);
+        l.G[p] = sum;
+        l.f[p] = fast_exp2((float)sum);
+        l.r[p] = fast_exp2((float)(whole - sum));
+        l.b[p] = beta;
+    }
+    __syncthreads();
+
+    // rows of do, U and dr; dv and db on the way
+    {
+        constexpr int kGrp = D / 8, kRowsAt = kThreadsG / kGrp;
+        const int grp = threadIdx.x % kGrp, r0 = threadIdx.x / kGrp;
+        const T *gop = static_cast<const T *>(a.grad_o.p) + b * a.grad_o.st[0] + begin * a.grad_o.st[1] + h * a.grad_o.st[2];
+        const int64_t base = ((int64_t)bh * a.spans + span) * N;
+#pragma unroll
+        for (int n = 0; n < N / kRowsAt; ++n) {
+            const int row = r0 + n * kRowsAt, at = tile_at<D>(row, grp), c = grp * 8;
+            const bool in = row < cnt;
+            bf16x8 go[kP], up[kU], dp[kU];
+            load8<T, VEC>(gop + row * a.grad_o.st[1], c, a.dv, in, go);
+            float u[8] = {}, d[8] = {}, dot = 0.0f;
+            if (in && c < a.nblk * kNB) {
+                const float *us = a.U + (base + row) * D + c, *ds = a.dR + (base + row) * D + c;
+                *reinterpret_cast<f32x4 *>(&u[0]) = *reinterpret_cast<const f32x4 *>(us);
+                *reinterpret_cast<f32x4 *>(&u[4]) = *reinterpret_cast<const f32x4 *>(us + 4);
+                *reinterpret_cast<f32x4 *>(&d[0]) = *reinterpret_cast<const f32x4 *>(ds);
+                *reinterpret_cast<f32x4 *>(&d[4]) = *reinterpret_cast<const f32x4 *>(ds + 4);
+            }
+            const float beta = l.b[row];
+            const bool tiny = fabsf(beta) < kTinyBeta;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dot = fmaf(u[i], d[i], dot);
+                d[i] = tiny ? 0.0f : beta * d[i];
+            }
+#pragma unroll
+            for (int s = 1; s < kGrp; s *= 2) dot += __shfl_xor(dot, s, kGrp);
+            if (grp == 0 && in && a.grad_b != nullptr) a.grad_b[((int64_t)b * a.L + begin + row) * a.H + h] = dot / (tiny ? kTinyBeta : beta);
+            if (in) {
+                T *gv = static_cast<T *>(a.grad_v) + (((int64_t)b * a.L + begin + row) * a.H + h) * a.dv + c;
+                if (a.out8) {
+                    if (c < a.dv) {
+                        constexpr int kV = kVec<T>;
+#pragma unroll
+                        for (int o = 0; o < 8; o += kV) {
+                            float w[kV];
+#pragma unroll
+                            for (int i = 0; i < kV; ++i) w[i] = d[o + i];
+                            store_vec<T, kV>(gv + o, w);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c + i < a.dv) gv[i] = (T)d[i];
+                }
+            }
+            planes_to(u, up);
+            planes_to(d, dp);
+#pragma unroll
+            for (int p = 0; p < kP; ++p) *reinterpret_cast<bf16x8 *>(&l.first.go[p * kX + at]) = go[p];
+#pragma unroll
+            for (int p = 0; p < kU; ++p) {
+                *reinterpret_cast<bf16x8 *>(&l.first.u[p * kX + at]) = up[p];
+                *reinterpret_cast<bf16x8 *>(&l.first.dr[p * kX + at]) = dp[p];
+            }
+        }
+    }
+    __syncthreads();
+
+    // products with S and D: lane m is position 16 it + m, registers are elements 16 wave + 4 q ..
+    f32x4 aq[NI] = {}, as[NI] = {}, ad[NI] = {};
+    {
+        const int64_t state = (((int64_t)bh * a.spans + span) * D + wave * 16 + m) * D + 8 * q;
+        float z = 0.0f;
+        for (int t = 0; t < steps; ++t) {
+            float sv[8], dv[8];
+            const float *ss = a.S + state + 32 * t, *ds = a.Dn + state + 32 * t;
+            *reinterpret_cast<f32x4 *>(&sv[0]) = *reinterpret_cast<const f32x4 *>(ss);
+            *reinterpret_cast<f32x4 *>(&sv[4]) = *reinterpret_cast<const f32x4 *>(ss + 4);
+            *reinterpret_cast<f32x4 *>(&dv[0]) = *reinterpret_cast<const f32x4 *>(ds);
+            *reinterpret_cast<f32x4 *>(&dv[4]) = *reinterpret_cast<const f32x4 *>(ds + 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z = fmaf(sv[i], dv[i], z);
+            bf16x8 sp[kU], dp[kU];
+            planes_to(sv, sp);
+            planes_to(dv, dp);
+#pragma unroll
+            for (int it = 0; it < NI; ++it) {
+                const int at = tile_at<D>(16 * it + m, 4 * t + q);
+                bf16x8 go[kP], dr[kU], u[kU];
+#pragma unroll
+                for (int p = 0; p < kP; ++p) go[p] = read_row(&l.first.go[p * kX + at]);
+#pragma unroll
+                for (int p = 0; p < kU; ++p) {
+                    dr[p] = read_row(&l.first.dr[p * kX + at]);
+                    u[p] = read_row(&l.first.u[p * kX + at]);
+                }
+                aq[it] = mfma_planes(sp, go, aq[it]);
+                as[it] = mfma_planes(sp, dr, as[it]);
+                ad[it] = mfma_planes(dp, u, ad[it]);
+            }
+        }
+        z = lanes_sum(z);
+        if (lane == 0) l.z[wave] = z;
+    }
+    // raw do_i.u_j and dr_i.u_j, tiles on and below the diagonal, round the waves: a result's rows are i
+    constexpr int kUnits = 2 * kTiles, kMine = (kUnits + kWaves - 1) / kWaves;
+    f32x4 pair[kMine] = {};
+    auto unit_of = [&](int n) { return min(wave + n * kWaves, kUnits - 1); };
+    auto tile_of = [&](int unit, int &it, int &jt) {
+        const int tile = unit >= kTiles ? unit - kTiles : unit;
+        it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
+        jt = tile - it * (it + 1) / 2;
+    };
+#pragma unroll
+    for (int n = 0; n < kMine; ++n) {
+        const int unit = unit_of(n);
+        int it, jt;
+        tile_of(unit, it, jt);
+        const bool erase = unit >= kTiles;
+        for (int t = 0; t < steps; ++t) {
+            const int ai = tile_at<D>(16 * it + m, 4 * t + q), aj = tile_at<D>(16 * jt + m, 4 * t + q);
+            bf16x8 u[kU];
+#pragma unroll
+            for (int p = 0; p < kU; ++p) u[p] = read_row(&l.first.u[p * kX + aj]);
+            if (erase) {
+                bf16x8 x[kU];
+#pragma unroll
+                for (int p = 0; p < kU; ++p) x[p] = read_row(&l.first.dr[p * kX + ai]);
+                pair[n] = mfma_planes(x, u, pair[n]);
+            } else {
+                bf16x8 x[kP];
+#pragma unroll
+                for (int p = 0; p < kP; ++p) x[p] = read_row(&l.first.go[p * kX + ai]);
+                pair[n] = mfma_planes(x, u, pair[n]);
+            }
+        }
+    }
+    __syncthreads();
+
+    // rows of q and k in their place
+    {
+        constexpr int kGrp = D / 8, kRowsAt = kThreadsG / kGrp;
+        const int grp = threadIdx.x % kGrp, r0 = threadIdx.x / kGrp;
+        const T *kp = static_cast<const T *>(a.k.p) + b * a.k.st[0] + begin * a.k.st[1] + hk * a.k.st[2];
+        const T *qp = static_cast<const T *>(a.q.p) + b * a.q.st[0] + begin * a.q.st[1] + hk * a.q.st[2];
+#pragma unroll
+        for (int n = 0; n < N / kRowsAt; ++n) {
+            const int row = r0 + n * kRowsAt, at = tile_at<D>(row, grp);
+            bf16x8 x[kP], y[kP];
+            load8<T, VEC>(kp + row * a.k.st[1], grp * 8, a.dk, row < cnt, x);
+            load8<T, VEC>(qp + row * a.q.st[1], grp * 8, a.dk, row < cnt, y);
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+                *reinterpret_cast<bf16x8 *>(&l.second.k[p * kX + at]) = x[p];
+                *reinterpret_cast<bf16x8 *>(&l.second.q[p * kX + at]) = y[p];
+            }
+        }
+        // MP right of the diagonal
+        for (int i = threadIdx.x; i < kM * kMx / 8; i += kThreadsG) {
+            const bf16x8 zero = {};
+            *reinterpret_cast<bf16x8 *>(&l.second.mp[i * 8]) = zero;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kMine; ++n) {
+        if (wave + n * kWaves >= kUnits) continue;
+        const int unit = unit_of(n);
+        int it, jt;
+        tile_of(unit, it, jt);
+        const bool erase = unit >= kTiles;
+        const bf16 *left = erase ? l.second.k : l.second.q;
+        f32x4 dots = {};
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t) {
+            bf16x8 x[kP], y[kP];
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+                x[p] = read_row(&left[p * kX + tile_at<D>(16 * it + m, 4 * t + q)]);
+                y[p] = read_row(&l.second.k[p * kX + tile_at<D>(16 * jt + m, 4 * t + q)]);
+            }
+            dots = mfma_planes(x, y, dots);
+        }
+        float cols = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 16 * it + 4 * q + r, j = 16 * jt + m;
+            const float e = j <= i ? fast_exp2((float)(l.G[i] - l.G[j])) : 0.0f;
+            const float w = erase ? (j < i ? -e * pair[n][r] : 0.0f) : a.scale * e * pair[n][r];
+            const float both = j < i ? w * dots[r] : 0.0f;
+            cols += both;
+            const float rows = lanes16_sum(both);
+            if (m == 0) l.row[erase][jt][i] = rows;
+            float v[8] = {w};
+            bf16x8 p[kM];
+            planes_to(v, p);
+#pragma unroll
+            for (int k = 0; k < kM; ++k) {
+                if (j <= i) (erase ? l.second.ma : l.second.mp)[k * kMx + tile_at<N>(i, j >> 3) + (j & 7)] = p[k][0];
+                if (erase && j < i) l.second.ma[k * kMx + tile_at<N>(j, i >> 3) + (i & 7)] = p[k][0];
+            }
+        }
+        cols += __shfl_xor(cols, 16);
+        cols += __shfl_xor(cols, 32);
+        if (q == 0) l.col[erase][it][16 * jt + m] = cols;
+    }
+    __syncthreads();
+
+    // the products with S and D weighted; a row's products with them are the gates' share
+#pragma unroll
+    for (int it = 0; it < NI; ++it) {
+        const int pos = 16 * it + m, at = tile_at<D>(pos, 2 * wave + (q >> 1)) + 4 * (q & 1);
+        const float f = l.f[pos], r = l.r[pos];
+        float x = 0.0f, y = 0.0f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            float qv = 0.0f, kv = 0.0f;
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+                qv += (float)l.second.q[p * kX + at + n];
+                kv += (float)l.second.k[p * kX + at + n];
+            }
+            aq[it][n] *= f * a.scale;
+            as[it][n] *= f;
+            ad[it][n] *= r;
+            y = fmaf(qv, aq[it][n], fmaf(-kv, as[it][n], y));
+            x = fmaf(kv, ad[it][n], x);
+            ad[it][n] -= as[it][n];
+        }
+        x += __shfl_xor(x, 16);
+        y += __shfl_xor(y, 16);
+        x += __shfl_xor(x, 32);
+        y += __shfl_xor(y, 32);
+        if (q == 0) {
+            l.x[wave][pos] = x;
+            l.y[wave][pos] = y;
+        }
+    }
+    // the pairs: dq += MP K, dk += MP^T Q + (MA + MA^T) K
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        bf16x8 kt[kP], qt[kP];
+        const int row = 32 * s + 8 * q + tr_i, grp = 2 * wave + (tr_c >> 1), in = 4 * (tr_c & 1);
+#pragma unroll
+        for (int p = 0; p < kP; ++p) {
+            kt[p] = walk::join(read_tr(&l.second.k[p * kX + tile_at<D>(row, grp) + in]), read_tr(&l.second.k[p * kX + tile_at<D>(row + 4, grp) + in]));
+            qt[p] = walk::join(read_tr(&l.second.q[p * kX + tile_at<D>(row, grp) + in]), read_tr(&l.second.q[p * kX + tile_at<D>(row + 4, grp) + in]));
+        }
+#pragma unroll
+        for (int it = 0; it < NI; ++it) {
+            bf16x8 w[kM];
+            if (s <= it / 2) {
+#pragma unroll
+                for (int p = 0; p < kM; ++p) w[p] = read_row(&l.second.mp[p * kMx + tile_at<N>(16 * it + m, 4 * s + q)]);
+                aq[it] = mfma_planes(kt, w, aq[it]);
+            }
+            if (s >= it / 2) {
+                const int g2 = 2 * it + (tr_c >> 1);
+#pragma unroll
+                for (int p = 0; p < kM; ++p)
+                    w[p] = walk::join(read_tr(&l.second.mp[p * kMx + tile_at<N>(row, g2) + in]), read_tr(&l.second.mp[p * kMx + tile_at<N>(row + 4, g2) + in]));
+                ad[it] = mfma_planes(qt, w, ad[it]);
+            }
+#pragma unroll
+            for (int p = 0; p < kM; ++p) w[p] = read_row(&l.second.ma[p * kMx + tile_at<N>(16 * it + m, 4 * s + q)]);
+            ad[it] = mfma_planes(kt, w, ad[it]);
+        }
+    }
+    const int c = 16 * wave + 4 * q;
+#pragma unroll
+    for (int it = 0; it < NI; ++it) {
+        const int pos = 16 * it + m;
+        if (pos >= cnt) continue;
+        const int64_t row = b * a.L + begin + pos;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float v[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) v[n] = k ? ad[it][n] : aq[it][n];
+            if (a.part_q != nullptr) {
+                float *to = (k ? a.part_k : a.part_q) + (row * a.H + h) * a.dk + c;
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    if (c + n < a.dk) to[n] = v[n];
+            } else {
+                T *to = static_cast<T *>(k ? a.grad_k : a.grad_q) + (row * a.H + h) * a.dk + c;
+                if (a.out4) {
+                    if (c < a.dk) store_vec<T, 4>(to, v);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        if (c + n < a.dk) to[n] = (T)v[n];
+                }
+            }
+        }
+    }
+    if (a.grad_g == nullptr) return;
+    __syncthreads();
+    if (wave == 0) {
+        const int p = lane & (N - 1), t = p >> 4;
+        double x = 0.0, y = 0.0, z = 0.0;
+        for (int w = 0; w < kWaves; ++w) {
+            x += l.x[w][p];
+            y += l.y[w][p];
+            z += l.z[w];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+                if (n <= t) y += l.row[k][n][p];
+                if (n >= t) y -= l.col[k][n][p];
+            }
+        const double own = x;
+#pragma unroll
+        for (int d = 1; d < N; d *= 2) {
+            const double before = __shfl_up(x, d, N), after = __shfl_down(y, d, N);
+            if (p >= d) x += before;
+            if (p + d < N) y += after;
+        }
+        if (lane < cnt) a.grad_g[(b * a.L + begin + p) * a.H + h] = (float)((double)l.f[N - 1] * z + y + (x - own));
+    }
+}
+
+// Gradients of shared heads: out [rows, Hk, dk] = sums of part [rows, Hk, group, dk] over the group, in its order.
+template <typename T>
+__global__ __launch_bounds__(256) void share_kernel(const float *part_q, const float *part_k, void *out_q, void *out_k, int64_t n, int group, int dk) {
+    const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (at >= n) return;
+    const int64_t head = at / dk;
+    const float *src = (blockIdx.y ? part_k : part_q) + head * group * dk + (at - head * dk);
+    float sum = 0.0f;
+    for (int g = 0; g < group; ++g) sum += src[(int64_t)g * dk];
+    static_cast<T *>(blockIdx.y ? out_k : out_q)[at] = (T)sum;
+}
+
+namespace {
+
+int back_width(const DeltaArgs &p) {
+    const int d = std::max(p.dk, p.dv);
+    return d <= 64 ? 64 : d <= 128 ? 128 : 256;
+}
+
+// Where the parts of the workspace begin.
+struct BackPlan {
+    int64_t chunks, spans;
+    size_t rows, states, parts, total;  // bytes of U (and dR), of S (and D), of a shared head's part, of all
+    size_t u, dr, s, d, pq, pk;
+};
+BackPlan back_plan(const DeltaArgs &p) {
+    auto round = [](size_t n) { return (n + 255) / 256 * 256; };
+    BackPlan w{};
+    const int D = back_width(p);
+    const int64_t span = p.bf16 && D <= 128 ? 64 : 32, pairs = p.B * p.H;
+    w.chunks = (p.L + C - 1) / C;
+    w.spans = (p.L + span - 1) / span;
+    w.rows = (size_t)(pairs * w.spans * span) * D * 4;
+    w.states = (size_t)(pairs * w.spans) * D * D * 4;
+    w.parts = p.H > p.Hk ? round((size_t)(pairs * p.L) * p.dk * 4) : 0;
+    w.u = round((size_t)(pairs * w.chunks) * (p.bf16 ? kRecord<bf16, true> : kRecord<float, true>));
+    w.dr = w.u + w.rows;
+    w.s = w.dr + w.rows;
+    w.d = w.s + w.states;
+    w.pq = w.d + w.states;
+    w.pk = w.pq + w.parts;
+    w.total = w.pk + w.parts;
+    return w;
+}
+
+template <typename T, int D, bool VEC>
+hipError_t back_launch(const DeltaArgs &p, char *scratch, hipStream_t s) {
+    const BackPlan w = back_plan(p);
+    const int64_t pairs = p.B * p.H, items = pairs * w.chunks;
+    const int group = (int)(p.H / p.Hk);
+    const PrepArgs prep{p.q, p.k, p.log_decay, p.beta, p.L, items, (int)p.H, group, p.dk, (int)w.chunks, p.scale, scratch};
+    prep_kernel<T, D, VEC, true><<<(unsigned)((items + 3) / 4), 256, 0, s>>>(prep);
+    BackArgs a{};
+    a.q = p.q;
+    a.k = p.k;
+    a.v = p.v;
+    a.grad_o = p.grad_o;
+    a.log_decay = p.log_decay;
+    a.beta = p.beta;
+    a.init = p.state;
+    a.fin = p.grad_out_state;
+    a.grad_init = p.grad_state;
+    a.B = p.B;
+    a.L = p.L;
+    a.H = p.H;
+    a.Hk = p.Hk;
+    a.group = group;
+    a.dk = p.dk;
+    a.dv = p.dv;
+    a.chunks = (int)w.chunks;
+    a.nblk = (p.dv + kNB - 1) / kNB;
+    a.spans = (int)w.spans;
+    a.scale = p.scale;
+    a.rec = scratch;
+    a.U = reinterpret_cast<float *>(scratch + w.u);
+    a.dR = reinterpret_cast<float *>(scratch + w.dr);
+    a.S = reinterpret_cast<float *>(scratch + w.s);
+    a.Dn = reinterpret_cast<float *>(scratch + w.d);
+    if (w.parts) {
+        a.part_q = reinterpret_cast<float *>(scratch + w.pq);
+        a.part_k = reinterpret_cast<float *>(scratch + w.pk);
+    }
+    a.grad_q = p.grad_q;
+    a.grad_k = p.grad_k;
+    a.grad_v = p.grad_v;
+    a.grad_g = p.grad_log_decay;
+    a.grad_b = p.grad_beta;
+    a.out8 = p.dv % 8 == 0 && aligned16(p.grad_v);
+    a.out4 = p.dk % 4 == 0 && aligned_to(p.grad_q, 4 * sizeof(T)) && aligned_to(p.grad_k, 4 * sizeof(T));
+    back_walk_kernel<T, D, VEC><<<(unsigned)((pairs + 7) / 8 * 8 * a.nblk * 2), walk::kThreads, 0, s>>>(a);
+    grad_kernel<T, D, VEC><<<(unsigned)(pairs * w.spans), D * 4, 0, s>>>(a);
+    if (w.parts) {
+        const int64_t n = p.B * p.L * p.Hk * p.dk;
+        share_kernel<T><<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, s>>>(a.part_q, a.part_k, a.grad_q, a.grad_k, n, group, p.dk);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, bool VEC>
+hipError_t back_width_launch(const DeltaArgs &p, char *scratch, hipStream_t s) {
+    switch (back_width(p)) {
+        case 64: return back_launch<T, 64, VEC>(p, scratch, s);
+        case 128: return back_launch<T, 128, VEC>(p, scratch, s);
+        default: return back_launch<T, 256, VEC>(p, scratch, s);
+    }
+}
+
+template <typename T>
+hipError_t back_type(const DeltaArgs &p, char *scratch, hipStream_t s) {
+    const int es = sizeof(T);
+    const bool vec = view_vec(p.q, p.dk, es) && view_vec(p.k, p.dk, es) && view_vec(p.v, p.dv, es) && view_vec(p.grad_o, p.dv, es);
+    return vec ? back_width_launch<T, true>(p, scratch, s) : back_width_launch<T, false>(p, scratch, s);
+}
+
+}  // namespace
+
+size_t back_ws(const DeltaArgs &p) { return back_plan(p).total; }
+hipError_t backward(const DeltaArgs &p, char *scratch, hipStream_t s) {
+    return p.bf16 ? back_type<bf16>(p, scratch, s) : back_type<float>(p, scratch, s);
+}
+
+}  // namespace delta
+}  // namespace prn
