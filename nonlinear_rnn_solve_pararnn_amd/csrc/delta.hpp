@@ -78,9 +78,37 @@ inline bool view_vec(const HeadView &v, int d, int es) {
     return d % n == 0 && aligned16(v.p) && v.st[0] % n == 0 && v.st[1] % n == 0 && v.st[2] % n == 0 && (v.st[1] >= d || v.st[1] == 0);
 }
 
+// Width of the state's rows that a walk is built for.
+inline int walk_width(int dk) { return dk <= 32 ? 32 : dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }
+inline int64_t chunks_of(int64_t L) { return (L + C - 1) / C; }
+// delta.hip
+int segments(int64_t groups, int64_t chunks);
 // delta_back.hip
 size_t back_ws(const DeltaArgs &p);
 hipError_t backward(const DeltaArgs &p, char *scratch, hipStream_t s);
+
+// Sums of products of planes, smallest first, of N results side by side: each
+// matrix instruction waits for the one before it on its result.
+template <int N, int NA, int NB>
+__device__ __forceinline__ void mfma_each(const bf16x8 (&a)[N][NA], const bf16x8 (&b)[NB], f32x4 (&c)[N]) {
+#pragma unroll
+    for (int s = 2; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB)
+#pragma unroll
+                for (int n = 0; n < N; ++n) c[n] = walk::mfma(a[n][i], b[s - i], c[n]);
+}
+template <int N, int NA, int NB>
+__device__ __forceinline__ void mfma_each_right(const bf16x8 (&a)[NA], const bf16x8 (&b)[N][NB], f32x4 (&c)[N]) {
+#pragma unroll
+    for (int s = 2; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB)
+#pragma unroll
+                for (int n = 0; n < N; ++n) c[n] = walk::mfma(a[i], b[n][s - i], c[n]);
+}
 
 struct PrepArgs {
     HeadView q, k, log_decay, beta;

@@ -20,227 +20,112 @@
 // Precision: walks as in the forward pass.  fp32 tensors: three planes of
 // everything.  bf16 tensors: S, D, U, dr, MP and MA to 16 bits (dg and db are fp32
 // results: 2^-17 of a term; dq and dk are differences where a key is written over).
-#include "delta.hpp"
+#include "delta_walk.hpp"
 
 namespace prn {
 namespace delta {
 
-using walk::Ahead;
-using walk::kNB;
-using walk::kTileRow;
 using walk::mfma_planes;
-using walk::read_row;
-using walk::read_tr;
-using walk::Rows;
-using walk::split3;
-using walk::state_row;
-using walk::tile_at;
-using walk::u32x2;
 
 struct BackArgs {
     HeadView q, k, v, grad_o, log_decay, beta;
     const float *init, *fin;  // S before the first position, D after the last one; null for zeros
     float *grad_init;         // or null
-    int64_t B, L, H, Hk;
-    int group, dk, dv, chunks, nblk, spans;
+    int64_t L;
+    int pairs, H, group, dk, dv, chunks, nblk, nblk_k, spans, span_chunks, width;  // width: rows of a state in memory
     float scale;
     const char *rec;
-    float *U, *dR;  // [B H][spans span][D]
-    float *S, *Dn;  // [B H][spans][D][D]: rows of dk, columns of dv
+    float *U, *dR;  // [pairs][spans span][64 nblk]
+    float *S, *D;   // [pairs][spans][width][64 nblk]
     float *part_q, *part_k;  // [B, L, H, dk] where heads share q and k, or null
     void *grad_q, *grad_k, *grad_v;
     float *grad_g, *grad_b;
     int out8, out4;  // rows of grad_v, and of grad_q and grad_k, may be stored eight or four elements at a time
+    SegArgs seg;
 };
 
 // Positions a span of grad_kernel: as many as its operands in LDS allow.
-template <typename T, int D> constexpr int kSpan = sizeof(T) == 2 && D <= 128 ? 64 : 32;
+constexpr int span_of(bool bf16, int D) { return bf16 && D <= 128 ? 64 : 32; }
 
 template <typename T, int D1>
-constexpr int kBackWgs = D1 > 128 || (sizeof(T) == 4 && D1 > 64) ? 1 : 2;
+constexpr int kBackWgs = D1 >= 128 || (sizeof(T) == 4 && D1 >= 64) ? 1 : 2;
+
+template <typename T>
+__device__ __forceinline__ Job job_of(const BackArgs &a, const Where &wh) {
+    Job j{};
+    j.q = a.q;
+    j.k = a.k;
+    j.L = a.L;
+    j.b = wh.b;
+    j.h = wh.h;
+    j.hk = (int)__builtin_amdgcn_readfirstlane(wh.h / a.group);  // the division runs on the vector unit
+    j.dk = a.dk;
+    j.dv = a.dv;
+    j.all = a.chunks;
+    j.scale = a.scale;
+    j.rec = a.rec + (int64_t)wh.bh * a.chunks * kRecord<T, true>;
+    return j;
+}
 
 // The two walks: workgroups that take S from the first chunk on, and those
 // that take D from the last one back.
 template <typename T, int D1, bool VEC>
 __global__ __launch_bounds__(walk::kThreads, (kBackWgs<T, D1>)) void back_walk_kernel(BackArgs a) {
-    constexpr int kP = kPlanes<T>, NA = D1 / 16, NT = D1 / 32, kSpanChunks = kSpan<T, D1> / C;
-    constexpr int kPX = C * kTileRow<D1>, kPZ = C * kTileRow<kNB>;
-    __shared__ __align__(16) bf16 K[kP * kPX], Q[kP * kPX], Z[kP * kPZ];
-    __shared__ __align__(16) Gates gates;
-    const Where wh = where(a.nblk * 2, (int)(a.B * a.H), (int)a.H);
+    __shared__ WalkLds<T, D1> lds;
+    const Where wh = where(a.nblk * 2 * a.seg.n, a.pairs, a.H);
     if (!wh.any) return;
-    const bool down = wh.sub >= a.nblk;  // D
-    const int blk = down ? wh.sub - a.nblk : wh.sub;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
-    const int tr_i = m >> 2, tr_c = m & 3;
-    const int c0 = blk * kNB, col = c0 + wave * 16 + m;
-    const int last = (int)(a.L - (int64_t)(a.chunks - 1) * C);
-
-    const float *from = down ? a.fin : a.init;
-    f32x4 S[NA];
-#pragma unroll
-    for (int t = 0; t < NA; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = state_row(t, q, r);
-            const float s = from != nullptr && col < a.dv && row < a.dk ? from[((int64_t)wh.bh * a.dk + row) * a.dv + col] : 0.0f;
-            S[t][r] = __builtin_canonicalizef(s);  // no signalling NaN (a launch tag) goes into the workspace
-        }
-
-    const int hk = wh.h / a.group;
-    const WalkView zv = down ? view_of(a.grad_o) : view_of(a.v);
-    const Rows rq = walk::rows_of<T>(view_of(a.q), wh.b, hk, a.L, 0, C, 0, 0, a.dk), rk = walk::rows_of<T>(view_of(a.k), wh.b, hk, a.L, 0, C, 0, 0, a.dk),
-               rz = walk::rows_of<T>(zv, wh.b, wh.h, a.L, 0, C, 0, c0, a.dv);
-    const char *rec = a.rec + (int64_t)wh.bh * a.chunks * kRecord<T, true>;
-    const int64_t span_rows = (int64_t)a.spans * kSpan<T, D1>;
-    float *rows = (down ? a.dR : a.U) + (int64_t)wh.bh * span_rows * D1 + col;
-    float *states = (down ? a.Dn : a.S) + (int64_t)wh.bh * a.spans * D1 * D1 + col;
-
-    Ahead<T, D1, C, VEC> aq, ak;
-    Ahead<T, kNB, C, VEC> az;
-    aq.init(rq);
-    ak.init(rk);
-    az.init(rz);
-    float gate_ahead = 0.0f;
-    bf16x8 Ta[2][3], Pa[2][3];
-    auto chunk_of = [&](int i) { return down ? a.chunks - 1 - i : i; };
-    auto positions = [&](int c) { return c < a.chunks - 1 ? C : last; };
-    auto load = [&](int i) {
-        if (i >= a.chunks) return;
-        const int c = chunk_of(i), cnt = positions(c);
-        ak.load(rk, c, cnt);
-        az.load(rz, c, cnt);
-        const char *r = rec + (int64_t)c * kRecord<T, true>;
-        if (threadIdx.x < sizeof(Gates) / 4) gate_ahead = reinterpret_cast<const float *>(r)[threadIdx.x];
-        const char *tm = r + (down ? kAtTt : kAtT) + lane * 16;
-#pragma unroll
-        for (int n = 0; n < 6; ++n) Ta[n / 3][n % 3] = *reinterpret_cast<const bf16x8 *>(tm + n * kTile);
-        if (down) {
-            aq.load(rq, c, cnt);
-#pragma unroll
-            for (int n = 0; n < 6; ++n) Pa[n / 3][n % 3] = *reinterpret_cast<const bf16x8 *>(r + kAtPt + n * kTile + lane * 16);
-        }
-    };
-    load(0);
-
-    for (int i = 0; i < a.chunks; ++i) {
-        const int c = chunk_of(i), cnt = positions(c);
-        if (down ? c % kSpanChunks == kSpanChunks - 1 || i == 0 : c % kSpanChunks == 0) {
-            float *to = states + (int64_t)(c / kSpanChunks) * D1 * D1;
-#pragma unroll
-            for (int t = 0; t < NA; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) to[state_row(t, q, r) * D1] = S[t][r];
-        }
-        bf16x8 Tm[2][3], Pm[2][3];
-#pragma unroll
-        for (int n = 0; n < 6; ++n) {
-            Tm[n / 3][n % 3] = Ta[n / 3][n % 3];
-            Pm[n / 3][n % 3] = Pa[n / 3][n % 3];
-        }
-        lds_barrier();  // the last chunk's reads are done
-        ak.store(rk, K);
-        az.store(rz, Z);
-        if (down) aq.store(rq, Q);
-        if (threadIdx.x < sizeof(Gates) / 4) reinterpret_cast<float *>(&gates)[threadIdx.x] = gate_ahead;
-        load(i + 1);
-        if constexpr (!VEC) {
-            if (cnt < C) {
-                walk::clear_past<kP, D1, C>(K, threadIdx.x, cnt);
-                if (down) walk::clear_past<kP, D1, C>(Q, threadIdx.x, cnt);
-                walk::clear_past<kP, kNB, C>(Z, threadIdx.x, cnt);
-            }
-        }
-        lds_barrier();
-
-        f32x4 ks[2] = {};
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const float v[8] = {S[2 * t][0],     S[2 * t][1],     S[2 * t][2],     S[2 * t][3],
-                                S[2 * t + 1][0], S[2 * t + 1][1], S[2 * t + 1][2], S[2 * t + 1][3]};
-            bf16x8 sp[3];
-            split3(v, sp);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                bf16x8 kr[kP];
-#pragma unroll
-                for (int p = 0; p < kP; ++p) kr[p] = read_row(&K[p * kPX + tile_at<D1>(row_of(u, m), 4 * t + q)]);
-                ks[u] = mfma_planes(kr, sp, ks[u]);
-            }
-        }
-        bf16x8 z[kP];
-        {
-            const int grp = 2 * wave + (tr_c >> 1), in = 4 * (tr_c & 1);
-#pragma unroll
-            for (int p = 0; p < kP; ++p)
-                z[p] = walk::join(read_tr(&Z[p * kPZ + tile_at<kNB>(8 * q + tr_i, grp) + in]),
-                                  read_tr(&Z[p * kPZ + tile_at<kNB>(8 * q + tr_i + 4, grp) + in]));
-        }
-        float x[8];
-        bf16x8 xp[3];
-        const float *edge = down ? gates.r : gates.f;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) x[n] = edge[8 * q + n] * ks[n >> 2][n & 3];
-        if (down) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const f32x4 y = mfma_planes(Pm[u], z, f32x4{x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]});
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[4 * u + r] = y[r];
-            }
-        } else {
-#pragma unroll
-            for (int n = 0; n < 8; ++n) x[n] = gates.b[8 * q + n] * (walk::plane_sum(z, n) - x[n]);
-        }
-        split3(x, xp);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const f32x4 y = mfma_planes(Tm[u], xp, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[4 * u + r] = y[r];
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n) rows[((int64_t)c * C + 8 * q + n) * D1] = x[n];
-
-        // what the chunk adds to the state: K^T (r U), or Q^T (f do') - K^T (f b dR)
-        const Carry carry{gates.carry, gates.fast != 0.0f};
-#pragma unroll
-        for (int n = 0; n < 8; ++n) x[n] *= down ? -gates.f[8 * q + n] * gates.b[8 * q + n] : gates.r[8 * q + n];
-        split3(x, xp);
-        bf16x8 wp[3];
-        if (down) {
-#pragma unroll
-            for (int n = 0; n < 8; ++n) x[n] = a.scale * gates.f[8 * q + n] * walk::plane_sum(z, n);
-            split3(x, wp);
-        }
-#pragma unroll
-        for (int t = 0; t < NA; ++t) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[t][r] = carry(S[t][r]);
-            const int grp = 4 * (t >> 1) + tr_c, in = 4 * (t & 1);
-            auto across = [&](const bf16 *X, bf16x8 (&y)[kP]) {
-#pragma unroll
-                for (int p = 0; p < kP; ++p)
-                    y[p] = walk::join(read_tr(&X[p * kPX + tile_at<D1>(8 * q + tr_i, grp) + in]),
-                                      read_tr(&X[p * kPX + tile_at<D1>(8 * q + tr_i + 4, grp) + in]));
-            };
-            bf16x8 y[kP];
-            if (down) {
-                across(Q, y);
-                S[t] = mfma_planes(y, wp, S[t]);
-            }
-            across(K, y);
-            S[t] = mfma_planes(y, xp, S[t]);
-        }
+    const int part = (int)__builtin_amdgcn_readfirstlane(wh.sub / a.nblk), blk = wh.sub - part * a.nblk, seg = part >> 1;
+    Job j = job_of<T>(a, wh);
+    j.c0 = blk * kNB;
+    j.from = seg * a.seg.chunks;
+    j.to = min(j.from + a.seg.chunks, a.chunks);
+    j.row = a.nblk * kNB;
+    j.span_chunks = a.span_chunks;
+    const int64_t state = (int64_t)wh.bh * a.dk * a.dv, rows = (int64_t)wh.bh * a.spans * a.span_chunks * C * j.row,
+                  states = (int64_t)wh.bh * a.spans * D1 * j.row;
+    if (part & 1) {
+        j.v = a.grad_o;
+        if (a.seg.n > 1) j.init = seg_at<D1>(a.seg.D, a.seg, wh.bh, seg, a.seg.wide);
+        else if (a.fin != nullptr) j.init = {const_cast<float *>(a.fin) + state, a.dv, a.dk, a.dv};
+        if (a.grad_init != nullptr && seg == 0) j.fin = {a.grad_init + state, a.dv, a.dk, a.dv};
+        j.rows = a.dR + rows;
+        j.states = a.D + states;
+        walk_chunks<T, D1, VEC, Role::Grad, true>(j, lds);
+    } else {
+        j.v = a.v;
+        if (a.seg.n > 1) j.init = seg_at<D1>(a.seg.S, a.seg, wh.bh, seg, a.seg.wide);
+        else if (a.init != nullptr) j.init = {const_cast<float *>(a.init) + state, a.dv, a.dk, a.dv};
+        j.rows = a.U + rows;
+        j.states = a.S + states;
+        walk_chunks<T, D1, VEC, Role::State, true>(j, lds);
     }
-    if (down && a.grad_init != nullptr && col < a.dv) {
-#pragma unroll
-        for (int t = 0; t < NA; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = state_row(t, q, r);
-                if (row < a.dk) a.grad_init[((int64_t)wh.bh * a.dk + row) * a.dv + col] = S[t][r];
-            }
+}
+
+// The segments' own parts: of S, of D, and M.
+template <typename T, int D1, bool VEC>
+__global__ __launch_bounds__(walk::kThreads, (kBackWgs<T, D1>)) void back_segment_kernel(BackArgs a) {
+    __shared__ WalkLds<T, D1> lds;
+    const int per = 2 * a.nblk + a.nblk_k;
+    const Where wh = where(per * a.seg.n, a.pairs, a.H);
+    if (!wh.any) return;
+    const int seg = (int)__builtin_amdgcn_readfirstlane(wh.sub / per), blk = wh.sub - seg * per;
+    Job j = job_of<T>(a, wh);
+    j.from = seg * a.seg.chunks;
+    j.to = min(j.from + a.seg.chunks, a.chunks);
+    if (blk >= a.nblk && blk < 2 * a.nblk) {
+        if (seg == 0) return;
+        j.v = a.grad_o;
+        j.c0 = (blk - a.nblk) * kNB;
+        j.fin = seg_at<D1>(a.seg.D, a.seg, wh.bh, seg, a.seg.wide);
+        walk_chunks<T, D1, VEC, Role::Grad, true>(j, lds);
+    } else {
+        j.identity = blk >= 2 * a.nblk;
+        if (!j.identity && seg == a.seg.n - 1) return;
+        j.c0 = (j.identity ? blk - 2 * a.nblk : blk) * kNB;
+        if (j.identity) j.dv = 1 << 20;  // every column there is
+        else j.v = a.v;
+        j.fin = j.identity ? seg_at<D1>(a.seg.M, a.seg, wh.bh, seg, a.seg.wide_k) : seg_at<D1>(a.seg.S, a.seg, wh.bh, seg, a.seg.wide);
+        walk_chunks<T, D1, VEC, Role::State, true>(j, lds);
     }
 }
 
@@ -254,7 +139,7 @@ __device__ __forceinline__ void planes_to(const float (&v)[8], bf16x8 (&p)[N]) {
 
 template <typename T, int D>
 struct GradLds {
-    static constexpr int kN = kSpan<T, D>, kP = kPlanes<T>, kU = kP == 3 ? 3 : 2, kM = kU, kWaves = D / 16;
+    static constexpr int kN = span_of(sizeof(T) == 2, D), kP = kPlanes<T>, kU = kP == 3 ? 3 : 2, kM = kU, kWaves = D / 16;
     static constexpr int kRowsX = kN * kTileRow<D>, kRowsM = kN * kTileRow<kN>;
     struct First {
         bf16 go[kP * kRowsX], u[kU * kRowsX], dr[kU * kRowsX];
@@ -283,7 +168,7 @@ __global__ __launch_bounds__(D * 4) void grad_kernel(BackArgs a) {
     const int cnt = (int)min((int64_t)N, a.L - begin);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
     const int tr_i = m >> 2, tr_c = m & 3;
-    const int steps = a.nblk * 2;  // of 32 columns of dv
+    const int steps = a.nblk * 2, wide = a.nblk * kNB;  // of 32 columns of dv; columns in memory
 
     if (threadIdx.x < N) {
         const int p = threadIdx.x;
@@ -318,8 +203,8 @@ __global__ __launch_bounds__(D * 4) void grad_kernel(BackArgs a) {
             bf16x8 go[kP], up[kU], dp[kU];
             load8<T, VEC>(gop + row * a.grad_o.st[1], c, a.dv, in, go);
             float u[8] = {}, d[8] = {}, dot = 0.0f;
-            if (in && c < a.nblk * kNB) {
-                const float *us = a.U + (base + row) * D + c, *ds = a.dR + (base + row) * D + c;
+            if (in && c < wide) {
+                const float *us = a.U + (base + row) * wide + c, *ds = a.dR + (base + row) * wide + c;
                 *reinterpret_cast<f32x4 *>(&u[0]) = *reinterpret_cast<const f32x4 *>(us);
                 *reinterpret_cast<f32x4 *>(&u[4]) = *reinterpret_cast<const f32x4 *>(us + 4);
                 *reinterpret_cast<f32x4 *>(&d[0]) = *reinterpret_cast<const f32x4 *>(ds);
@@ -370,11 +255,12 @@ __global__ __launch_bounds__(D * 4) void grad_kernel(BackArgs a) {
     // products with S and D: lane m is position 16 it + m, registers are elements 16 wave + 4 q ..
     f32x4 aq[NI] = {}, as[NI] = {}, ad[NI] = {};
     {
-        const int64_t state = (((int64_t)bh * a.spans + span) * D + wave * 16 + m) * D + 8 * q;
+        const int64_t state = (((int64_t)bh * a.spans + span) * a.width + wave * 16 + m) * wide + 8 * q;
         float z = 0.0f;
-        for (int t = 0; t < steps; ++t) {
+        const int steps_s = wave * 16 < a.width ? steps : 0;  // (narrower keys have no rows there)
+        for (int t = 0; t < steps_s; ++t) {
             float sv[8], dv[8];
-            const float *ss = a.S + state + 32 * t, *ds = a.Dn + state + 32 * t;
+            const float *ss = a.S + state + 32 * t, *ds = a.D + state + 32 * t;
             *reinterpret_cast<f32x4 *>(&sv[0]) = *reinterpret_cast<const f32x4 *>(ss);
             *reinterpret_cast<f32x4 *>(&sv[4]) = *reinterpret_cast<const f32x4 *>(ss + 4);
             *reinterpret_cast<f32x4 *>(&dv[0]) = *reinterpret_cast<const f32x4 *>(ds);
@@ -637,7 +523,8 @@ __global__ __launch_bounds__(256) void share_kernel(const float *part_q, const f
 
 namespace {
 
-int back_width(const DeltaArgs &p) {
+// Width that the span kernel is built for: the wider of the two heads'.
+int span_width(const DeltaArgs &p) {
     const int d = std::max(p.dk, p.dv);
     return d <= 64 ? 64 : d <= 128 ? 128 : 256;
 }
@@ -645,36 +532,60 @@ int back_width(const DeltaArgs &p) {
 // Where the parts of the workspace begin.
 struct BackPlan {
     int64_t chunks, spans;
-    size_t rows, states, parts, total;  // bytes of U (and dR), of S (and D), of a shared head's part, of all
-    size_t u, dr, s, d, pq, pk;
+    int span, segs, seg_chunks;
+    size_t u, dr, s, d, pq, pk, seg_s, seg_d, seg_m, total;
+    bool parts;
 };
 BackPlan back_plan(const DeltaArgs &p) {
-    auto round = [](size_t n) { return (n + 255) / 256 * 256; };
     BackPlan w{};
-    const int D = back_width(p);
-    const int64_t span = p.bf16 && D <= 128 ? 64 : 32, pairs = p.B * p.H;
-    w.chunks = (p.L + C - 1) / C;
-    w.spans = (p.L + span - 1) / span;
-    w.rows = (size_t)(pairs * w.spans * span) * D * 4;
-    w.states = (size_t)(pairs * w.spans) * D * D * 4;
-    w.parts = p.H > p.Hk ? round((size_t)(pairs * p.L) * p.dk * 4) : 0;
-    w.u = round((size_t)(pairs * w.chunks) * (p.bf16 ? kRecord<bf16, true> : kRecord<float, true>));
-    w.dr = w.u + w.rows;
-    w.s = w.dr + w.rows;
-    w.d = w.s + w.states;
-    w.pq = w.d + w.states;
-    w.pk = w.pq + w.parts;
-    w.total = w.pk + w.parts;
+    const int64_t pairs = p.B * p.H, D1 = walk_width(p.dk), wide = (p.dv + kNB - 1) / kNB * kNB, wide_k = (D1 + kNB - 1) / kNB * kNB;
+    w.span = span_of(p.bf16, span_width(p));
+    w.chunks = chunks_of(p.L);
+    w.spans = (p.L + w.span - 1) / w.span;
+    w.segs = segments(pairs * 2 * (wide / kNB), w.chunks);
+    w.seg_chunks = (int)((w.chunks + w.segs - 1) / w.segs);
+    w.segs = (int)((w.chunks + w.seg_chunks - 1) / w.seg_chunks);
+    w.parts = p.H > p.Hk;
+    size_t at = 0;
+    auto take = [&](int64_t floats) {
+        const size_t here = at;
+        at += ((size_t)floats * 4 + 255) / 256 * 256;
+        return here;
+    };
+    take(pairs * w.chunks * (p.bf16 ? kRecord<bf16, true> : kRecord<float, true>) / 4);
+    w.u = take(pairs * w.spans * w.span * wide);
+    w.dr = take(pairs * w.spans * w.span * wide);
+    w.s = take(pairs * w.spans * D1 * wide);
+    w.d = take(pairs * w.spans * D1 * wide);
+    w.pq = take(w.parts ? pairs * p.L * p.dk : 0);
+    w.pk = take(w.parts ? pairs * p.L * p.dk : 0);
+    const int64_t slots = w.segs > 1 ? pairs * w.segs * D1 : 0;
+    w.seg_s = take(slots * wide);
+    w.seg_d = take(slots * wide);
+    w.seg_m = take(slots * wide_k);
+    w.total = at;
     return w;
 }
 
-template <typename T, int D, bool VEC>
+template <typename T, int D1, bool VEC>
+hipError_t back_walks(const DeltaArgs &p, const BackPlan &w, BackArgs &a, char *scratch, hipStream_t s) {
+    const int64_t pairs = p.B * p.H, items = pairs * w.chunks, eights = (pairs + 7) / 8 * 8;
+    const PrepArgs prep{p.q, p.k, p.log_decay, p.beta, p.L, items, (int)p.H, a.group, p.dk, (int)w.chunks, p.scale, scratch};
+    prep_kernel<T, D1, VEC, true><<<(unsigned)((items + 3) / 4), 256, 0, s>>>(prep);
+    if (w.segs > 1) {
+        back_segment_kernel<T, D1, VEC><<<(unsigned)(eights * (2 * a.nblk + a.nblk_k) * w.segs), walk::kThreads, 0, s>>>(a);
+        const JoinArgs join{a.seg, p.state, p.grad_out_state, p.dk, p.dv, a.nblk * (kNB / 16)};
+        join_kernel<D1><<<dim3((unsigned)(pairs * join.cols), 2), D1 * 2, 0, s>>>(join);
+    }
+    back_walk_kernel<T, D1, VEC><<<(unsigned)(eights * a.nblk * 2 * w.segs), walk::kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename T, bool VEC>
 hipError_t back_launch(const DeltaArgs &p, char *scratch, hipStream_t s) {
     const BackPlan w = back_plan(p);
-    const int64_t pairs = p.B * p.H, items = pairs * w.chunks;
-    const int group = (int)(p.H / p.Hk);
-    const PrepArgs prep{p.q, p.k, p.log_decay, p.beta, p.L, items, (int)p.H, group, p.dk, (int)w.chunks, p.scale, scratch};
-    prep_kernel<T, D, VEC, true><<<(unsigned)((items + 3) / 4), 256, 0, s>>>(prep);
+    const int64_t pairs = p.B * p.H;
+    auto at = [&](size_t n) { return reinterpret_cast<float *>(scratch + n); };
     BackArgs a{};
     a.q = p.q;
     a.k = p.k;
@@ -685,26 +596,26 @@ hipError_t back_launch(const DeltaArgs &p, char *scratch, hipStream_t s) {
     a.init = p.state;
     a.fin = p.grad_out_state;
     a.grad_init = p.grad_state;
-    a.B = p.B;
     a.L = p.L;
-    a.H = p.H;
-    a.Hk = p.Hk;
-    a.group = group;
+    a.pairs = (int)pairs;
+    a.H = (int)p.H;
+    a.group = (int)(p.H / p.Hk);
     a.dk = p.dk;
     a.dv = p.dv;
     a.chunks = (int)w.chunks;
     a.nblk = (p.dv + kNB - 1) / kNB;
+    a.nblk_k = (walk_width(p.dk) + kNB - 1) / kNB;  // a matrix M is square
     a.spans = (int)w.spans;
+    a.span_chunks = w.span / C;
+    a.width = walk_width(p.dk);
     a.scale = p.scale;
     a.rec = scratch;
-    a.U = reinterpret_cast<float *>(scratch + w.u);
-    a.dR = reinterpret_cast<float *>(scratch + w.dr);
-    a.S = reinterpret_cast<float *>(scratch + w.s);
-    a.Dn = reinterpret_cast<float *>(scratch + w.d);
-    if (w.parts) {
-        a.part_q = reinterpret_cast<float *>(scratch + w.pq);
-        a.part_k = reinterpret_cast<float *>(scratch + w.pk);
-    }
+    a.U = at(w.u);
+    a.dR = at(w.dr);
+    a.S = at(w.s);
+    a.D = at(w.d);
+    a.part_q = w.parts ? at(w.pq) : nullptr;
+    a.part_k = w.parts ? at(w.pk) : nullptr;
     a.grad_q = p.grad_q;
     a.grad_k = p.grad_k;
     a.grad_v = p.grad_v;
@@ -712,29 +623,33 @@ hipError_t back_launch(const DeltaArgs &p, char *scratch, hipStream_t s) {
     a.grad_b = p.grad_beta;
     a.out8 = p.dv % 8 == 0 && aligned16(p.grad_v);
     a.out4 = p.dk % 4 == 0 && aligned_to(p.grad_q, 4 * sizeof(T)) && aligned_to(p.grad_k, 4 * sizeof(T));
-    back_walk_kernel<T, D, VEC><<<(unsigned)((pairs + 7) / 8 * 8 * a.nblk * 2), walk::kThreads, 0, s>>>(a);
-    grad_kernel<T, D, VEC><<<(unsigned)(pairs * w.spans), D * 4, 0, s>>>(a);
+    a.seg = {w.segs, w.seg_chunks, at(w.seg_s), at(w.seg_d), at(w.seg_m), a.nblk * kNB, a.nblk_k * kNB};
+    hipError_t e;
+    switch (a.width) {
+        case 32: e = back_walks<T, 32, VEC>(p, w, a, scratch, s); break;
+        case 64: e = back_walks<T, 64, VEC>(p, w, a, scratch, s); break;
+        case 128: e = back_walks<T, 128, VEC>(p, w, a, scratch, s); break;
+        default: e = back_walks<T, 256, VEC>(p, w, a, scratch, s); break;
+    }
+    if (e != hipSuccess) return e;
+    const unsigned grid = (unsigned)(pairs * w.spans);
+    switch (span_width(p)) {
+        case 64: grad_kernel<T, 64, VEC><<<grid, 64 * 4, 0, s>>>(a); break;
+        case 128: grad_kernel<T, 128, VEC><<<grid, 128 * 4, 0, s>>>(a); break;
+        default: grad_kernel<T, 256, VEC><<<grid, 256 * 4, 0, s>>>(a); break;
+    }
     if (w.parts) {
         const int64_t n = p.B * p.L * p.Hk * p.dk;
-        share_kernel<T><<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, s>>>(a.part_q, a.part_k, a.grad_q, a.grad_k, n, group, p.dk);
+        share_kernel<T><<<dim3((unsigned)((n + 255) / 256), 2), 256, 0, s>>>(a.part_q, a.part_k, a.grad_q, a.grad_k, n, a.group, p.dk);
     }
     return hipGetLastError();
-}
-
-template <typename T, bool VEC>
-hipError_t back_width_launch(const DeltaArgs &p, char *scratch, hipStream_t s) {
-    switch (back_width(p)) {
-        case 64: return back_launch<T, 64, VEC>(p, scratch, s);
-        case 128: return back_launch<T, 128, VEC>(p, scratch, s);
-        default: return back_launch<T, 256, VEC>(p, scratch, s);
-    }
 }
 
 template <typename T>
 hipError_t back_type(const DeltaArgs &p, char *scratch, hipStream_t s) {
     const int es = sizeof(T);
     const bool vec = view_vec(p.q, p.dk, es) && view_vec(p.k, p.dk, es) && view_vec(p.v, p.dv, es) && view_vec(p.grad_o, p.dv, es);
-    return vec ? back_width_launch<T, true>(p, scratch, s) : back_width_launch<T, false>(p, scratch, s);
+    return vec ? back_launch<T, true>(p, scratch, s) : back_launch<T, false>(p, scratch, s);
 }
 
 }  // namespace

@@ -42,49 +42,82 @@ __device__ __forceinline__ int partner(const HeadnormArgs &a, int c) {
 template <typename T, int V>
 __device__ __forceinline__ VecT<T, V> load_row(const T *p) { return *reinterpret_cast<const VecT<T, V> *>(p); }
 
+// Sixteen bytes of floats at a time where a group's elements are consecutive.
+template <int V>
+__device__ __forceinline__ void load_floats(const float *p, float (&f)[V]) {
+    if constexpr (V % 4 == 0) {
+        typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const f32x4_any x = *reinterpret_cast<const f32x4_any *>(p + i);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[i + k] = x[k];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = p[i];
+    }
+}
+
 // A group's share of the rotation: the cosine and the signed sine of each of
-// its elements (y_c = n_c cos + n_partner sin; back: the angle's opposite).
+// its elements (y_c = n_c cos + n_partner sin; back: the angle's opposite), one
+// and zero where there is none.
 template <int V, int NV>
 struct Turn {
     float cos[NV][V], sin[NV][V];
 
-    __device__ __forceinline__ void load(const HeadnormArgs &a, int64_t token, int lane, bool back) {
+    __device__ __forceinline__ void load(const HeadnormArgs &a, int64_t token, int64_t t, int lane, bool back) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                cos[j][i] = 1.0f;
+                sin[j][i] = 0.0f;
+            }
         if (a.R == 0) return;
         int64_t pos;
-        if (a.positions == nullptr) pos = token % a.L;
+        if (a.positions == nullptr) pos = t;
         else pos = a.wide ? static_cast<const int64_t *>(a.positions)[token] : (int64_t) static_cast<const int32_t *>(a.positions)[token];
         const bool in = pos >= 0 && pos < a.P;
         const float *row = a.table + (in ? pos : 0) * a.R;
         const float nan = __builtin_nanf("");
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+            const int c = column<V>(lane, j);
+            if (c >= a.R) continue;
+            if (V > 1 && !a.interleaved) {  // all of them on one side
+                const int k = c >= a.R / 2 ? c - a.R / 2 : c;
+                load_floats<V>(row + k, cos[j]);
+                load_floats<V>(row + a.R / 2 + k, sin[j]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int c = column<V>(lane, j) + i;
-                if (c < a.R) {
-                    const bool second = a.interleaved ? (c & 1) : c >= a.R / 2;
-                    const int k = a.interleaved ? c >> 1 : second ? c - a.R / 2 : c;
-                    cos[j][i] = in ? row[k] : nan;
-                    sin[j][i] = in ? row[a.R / 2 + k] : nan;
-                    if (second == back) sin[j][i] = -sin[j][i];
-                }
+                for (int i = 0; i < V; ++i)
+                    if (c + i < a.R) {
+                        const int k = a.interleaved ? (c + i) >> 1 : c >= a.R / 2 ? c - a.R / 2 : c;
+                        cos[j][i] = row[k];
+                        sin[j][i] = row[a.R / 2 + k];
+                    }
             }
-    }
-    // n turned: p holds the partners of n's elements.
-    __device__ __forceinline__ float operator()(const HeadnormArgs &a, int c, int j, int i, float n, float p) const {
-        return c < a.R ? fmaf(n, cos[j][i], p * sin[j][i]) : n;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (c + i < a.R) {
+                    const bool second = a.interleaved ? (c + i) & 1 : c >= a.R / 2;
+                    if (second == back) sin[j][i] = -sin[j][i];
+                    if (!in) cos[j][i] = sin[j][i] = nan;
+                }
+        }
     }
 };
 
-// Partners of a row's elements in it (interleaved vectors hold their own).
+// Partners of a row's elements in it (interleaved vectors hold their own; past
+// the rotated ones any finite value does: the elements themselves).
 template <typename T, int V>
 __device__ __forceinline__ void load_partner(const HeadnormArgs &a, const T *row, int c, const VecT<T, V> &own, VecT<T, V> &to) {
-    if (c >= a.R) return;
     if (V > 1 && a.interleaved) {
 #pragma unroll
         for (int i = 0; i < V; ++i) to.v[i] = own.v[i ^ 1];
     } else {
-        to = load_row<T, V>(row + partner(a, c));
+        to = load_row<T, V>(row + (c < a.R ? partner(a, c) : c));
     }
 }
 
@@ -108,67 +141,98 @@ __device__ __forceinline__ const T *row_of(const HeadView &v, int64_t b, int64_t
     return static_cast<const T *>(v.p) + b * v.st[0] + t * v.st[1] + head * v.st[2];
 }
 
+// Rows of a group that are on their way at once.
+template <int V, int NV> constexpr int kAhead = V > 1 && NV == 1 ? 2 : 1;
+
 template <typename T, int V, int NV>
 __global__ __launch_bounds__(kThreads) void headnorm_fwd_kernel(Params p) {
+    constexpr int U = kAhead<V, NV>;
     const HeadnormArgs &a = p.a;
     const int lane = threadIdx.x & (kLanes - 1);
     const int64_t items = p.tokens * (p.parts[0] + p.parts[1]);
     const int64_t n = (int64_t)blockIdx.x * kGroups + threadIdx.x / kLanes;
     if (n >= items) return;
     const Item it = item_of(p, n);
-    const int64_t b = it.token / a.L, t = it.token - b * a.L;
+    const int64_t b = (uint32_t)it.token / (uint32_t)a.L, t = it.token - b * a.L;
     const int64_t H = it.which ? a.Hk : a.Hq;
     const float *wp = it.which ? a.w[1] : a.w[0];
     const HeadView x = it.which ? a.x[1] : a.x[0];
-    Turn<V, NV> turn;
-    turn.load(a, it.token, lane, false);
-    float w[NV][V], wp_of[NV][V];
+    const T *first = row_of<T>(x, b, t, it.head);
+    float *r_out = it.which ? a.r[1] : a.r[0];
+    T *y = static_cast<T *>(it.which ? a.y[1] : a.y[0]) + (it.token * H + it.head) * a.d;
+    VecT<T, V> own[U][NV], other[U][NV];
+    auto load = [&](int h0) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+        for (int u = 0; u < U; ++u) {
+            const T *row = first + min(h0 + u, it.heads - 1) * x.st[2];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = column<V>(lane, j) + i;
-            w[j][i] = wp != nullptr && c < a.d ? wp[c] : 1.0f;
-            wp_of[j][i] = wp != nullptr && c < a.R ? wp[partner(a, c)] : 1.0f;
-        }
-    VecT<T, V> own[NV], other[NV];
-    auto load = [&](int head) {
-        const T *row = row_of<T>(x, b, t, head);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = column<V>(lane, j);
-            if (c < a.d) {
-                own[j] = load_row<T, V>(row + c);
-                load_partner<T, V>(a, row, c, own[j], other[j]);
+            for (int j = 0; j < NV; ++j) {
+                const int c = column<V>(lane, j);
+                if (c < a.d) {
+                    own[u][j] = load_row<T, V>(row + c);
+                    load_partner<T, V>(a, row, c, own[u][j], other[u][j]);
+                }
             }
         }
     };
-    load(it.head);
-    for (int h = 0; h < it.heads; ++h) {
-        float f[NV][V], o[NV][V], sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (column<V>(lane, j) < a.d)
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    f[j][i] = (float)own[j].v[i];
-                    o[j][i] = (float)other[j].v[i];
-                    sum = fmaf(f[j][i], f[j][i], sum);
-                }
-        if (h + 1 < it.heads) load(it.head + h + 1);
-        sum = lanes16_sum(sum);
-        const float r = 1.0f / sqrtf((a.l2 ? sum : sum / (float)a.d) + a.eps);
-        const int64_t row = it.token * H + it.head + h;
-        if (lane == 0 && a.r[it.which] != nullptr) a.r[it.which][row] = r;
-        T *y = static_cast<T *>(it.which ? a.y[1] : a.y[0]) + row * a.d;
+    // y = r (x (w cos) + x_partner (w_partner sin))
+    Turn<V, NV> turn;
+    turn.load(a, it.token, t, lane, false);
+    if (wp != nullptr) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = column<V>(lane, j);
-            if (c < a.d) {
-                float v[V];
+            if (c >= a.d) continue;
+            float w[V], wo[V];
+            load_floats<V>(wp + c, w);
+            if (V > 1 && a.interleaved) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = turn(a, c + i, j, i, f[j][i] * r * w[j][i], o[j][i] * r * wp_of[j][i]);
-                store_vec<T, V>(y + c, v);
+                for (int i = 0; i < V; ++i) wo[i] = w[i ^ 1];
+            } else {
+                load_floats<V>(wp + (c < a.R ? partner(a, c) : c), wo);
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                turn.cos[j][i] *= w[i];
+                turn.sin[j][i] *= wo[i];
+            }
+        }
+    }
+    for (int h0 = 0; h0 < it.heads; h0 += U) {
+        load(h0);
+        float f[U][NV][V], o[U][NV][V], sum[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            sum[u] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const bool in = column<V>(lane, j) < a.d;
+                    f[u][j][i] = in ? (float)own[u][j].v[i] : 0.0f;
+                    o[u][j][i] = in ? (float)other[u][j].v[i] : 0.0f;
+                    sum[u] = fmaf(f[u][j][i], f[u][j][i], sum[u]);
+                }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float s = lanes16_sum(sum[u]);
+            const float r = 1.0f / sqrtf((a.l2 ? s : s / (float)a.d) + a.eps);
+            if (h0 + u >= it.heads) continue;
+            if (lane == 0 && r_out != nullptr) r_out[it.token * H + it.head + h0 + u] = r;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = column<V>(lane, j);
+                if (c < a.d) {
+                    float v[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        // an infinity beside a zero sine is no number of this element's
+                        const float n = f[u][j][i] * turn.cos[j][i];
+                        v[i] = r * (c + i < a.R ? fmaf(o[u][j][i], turn.sin[j][i], n) : n);
+                    }
+                    store_vec<T, V>(y + (int64_t)(h0 + u) * a.d + c, v);
+                }
             }
         }
     }
@@ -176,74 +240,94 @@ __global__ __launch_bounds__(kThreads) void headnorm_fwd_kernel(Params p) {
 
 template <typename T, int V, int NV>
 __global__ __launch_bounds__(kThreads) void headnorm_bwd_kernel(Params p) {
+    constexpr int U = kAhead<V, NV>;
     const HeadnormArgs &a = p.a;
     const int lane = threadIdx.x & (kLanes - 1), grp = threadIdx.x / kLanes;
     const int64_t items = p.tokens * (p.parts[0] + p.parts[1]);
     float gw[2][NV][V] = {};
     for (int64_t n = (int64_t)blockIdx.x * kGroups + grp; n < items; n += (int64_t)gridDim.x * kGroups) {
         const Item it = item_of(p, n);
-        const int64_t b = it.token / a.L, t = it.token - b * a.L;
+        const int64_t b = (uint32_t)it.token / (uint32_t)a.L, t = it.token - b * a.L;
         const int64_t H = it.which ? a.Hk : a.Hq;
         const float *wp = it.which ? a.w[1] : a.w[0];
         const HeadView x = it.which ? a.x[1] : a.x[0], g = it.which ? a.g[1] : a.g[0];
+        const T *first = row_of<T>(x, b, t, it.head), *gfirst = row_of<T>(g, b, t, it.head);
+        const float *r_in = (it.which ? a.r[1] : a.r[0]) + it.token * H + it.head;
+        T *out = static_cast<T *>(it.which ? a.y[1] : a.y[0]) + (it.token * H + it.head) * a.d;
+        VecT<T, V> own[U][NV], dy[U][NV], other[U][NV];
+        float r_of[U];
+        auto load = [&](int h0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int h = min(h0 + u, it.heads - 1);
+                const T *row = first + h * x.st[2], *grow = gfirst + h * g.st[2];
+                r_of[u] = r_in[h];
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int c = column<V>(lane, j);
+                    if (c < a.d) {
+                        own[u][j] = load_row<T, V>(row + c);
+                        dy[u][j] = load_row<T, V>(grow + c);
+                        load_partner<T, V>(a, grow, c, dy[u][j], other[u][j]);
+                    }
+                }
+            }
+        };
         Turn<V, NV> turn;
-        turn.load(a, it.token, lane, true);
-        float w[NV][V];
+        turn.load(a, it.token, t, lane, true);
+        float w[NV][V], acc[NV][V] = {};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[j][i] = 1.0f;
+            if (wp != nullptr && column<V>(lane, j) < a.d) load_floats<V>(wp + column<V>(lane, j), w[j]);
+        }
+        for (int h0 = 0; h0 < it.heads; h0 += U) {
+            load(h0);
+            float xh[U][NV][V], v[U][NV][V], sum[U], r[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                r[u] = r_of[u];
+                sum[u] = 0.0f;
+                const bool live = h0 + u < it.heads;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int c = column<V>(lane, j);
+                    if (c < a.d)
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            xh[u][j][i] = (float)own[u][j].v[i] * r[u];
+                            float gn = (float)dy[u][j].v[i] * turn.cos[j][i];
+                            if (c + i < a.R) gn = fmaf((float)other[u][j].v[i], turn.sin[j][i], gn);
+                            if (live) acc[j][i] = fmaf(gn, xh[u][j][i], acc[j][i]);
+                            v[u][j][i] = gn * w[j][i];
+                            sum[u] = fmaf(v[u][j][i], xh[u][j][i], sum[u]);
+                        }
+                }
+            }
+    #pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float s = lanes16_sum(sum[u]);
+                if (!a.l2) s /= (float)a.d;
+                if (h0 + u >= it.heads) continue;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+                    const int c = column<V>(lane, j);
+                    if (c < a.d) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) v[u][j][i] = r[u] * (v[u][j][i] - xh[u][j][i] * s);
+                        store_vec<T, V>(out + (int64_t)(h0 + u) * a.d + c, v[u][j]);
+                    }
+                }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const int c = column<V>(lane, j) + i;
-                w[j][i] = wp != nullptr && c < a.d ? wp[c] : 1.0f;
+                gw[0][j][i] += it.which ? 0.0f : acc[j][i];
+                gw[1][j][i] += it.which ? acc[j][i] : 0.0f;
             }
-        VecT<T, V> own[NV], dy[NV], other[NV];
-        float r_of = 0.0f;
-        auto load = [&](int head) {
-            const T *row = row_of<T>(x, b, t, head), *grow = row_of<T>(g, b, t, head);
-            r_of = (it.which ? a.r[1] : a.r[0])[it.token * H + head];
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = column<V>(lane, j);
-                if (c < a.d) {
-                    own[j] = load_row<T, V>(row + c);
-                    dy[j] = load_row<T, V>(grow + c);
-                    load_partner<T, V>(a, grow, c, dy[j], other[j]);
-                }
-            }
-        };
-        load(it.head);
-        for (int h = 0; h < it.heads; ++h) {
-            const float r = r_of;
-            float xh[NV][V], v[NV][V], sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = column<V>(lane, j);
-                if (c < a.d)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        xh[j][i] = (float)own[j].v[i] * r;
-                        const float gn = turn(a, c + i, j, i, (float)dy[j].v[i], (float)other[j].v[i]);
-                        const float part = gn * xh[j][i];
-                        gw[0][j][i] += it.which ? 0.0f : part;
-                        gw[1][j][i] += it.which ? part : 0.0f;
-                        v[j][i] = gn * w[j][i];
-                        sum = fmaf(v[j][i], xh[j][i], sum);
-                    }
-            }
-            if (h + 1 < it.heads) load(it.head + h + 1);
-            sum = lanes16_sum(sum);
-            if (!a.l2) sum /= (float)a.d;
-            T *out = static_cast<T *>(it.which ? a.y[1] : a.y[0]) + (it.token * H + it.head + h) * a.d;
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = column<V>(lane, j);
-                if (c < a.d) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) v[j][i] = r * (v[j][i] - xh[j][i] * sum);
-                    store_vec<T, V>(out + c, v[j]);
-                }
-            }
-        }
     }
     if (p.part == nullptr) return;
     // the groups' sums, in their order

@@ -156,13 +156,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint3
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00020000);
 }
 // Chunk i of cnt positions; the same in whole words, `skew` bytes before it.
+// (Their sizes are the same in every lane, which the compiler may lose sight of:
+// each access would then be a loop over the lanes' resources.)
+__device__ __forceinline__ uint32_t same_in_lanes(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_of(const Rows &v, int i, int cnt, int C) {
-    return buffer_of(v.at(i, cnt, C), v.bytes(cnt));
+    return buffer_of(v.at(i, cnt, C), same_in_lanes(v.bytes(cnt)));
 }
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_words_of(const Rows &v, int i, int cnt, int C, uint32_t &skew) {
     const char *first = v.at(i, cnt, C);
     skew = Rows::word_skew(first);
-    return buffer_of(first - skew, v.word_bytes(skew, cnt));
+    return buffer_of(first - skew, same_in_lanes(v.word_bytes(skew, cnt)));
 }
 template <typename T>
 __device__ __forceinline__ Rows rows_of(const WalkView &v, int64_t b, int64_t h, int64_t L, int64_t begin, int C, int rev,
