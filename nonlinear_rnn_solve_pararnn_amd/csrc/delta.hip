@@ -38,7 +38,7 @@ __device__ __forceinline__ Job job_of(const ForwardArgs &a, const Where &wh, int
 
 // Workgroups a CU that the registers are shared out for.
 template <typename T, int D1>
-constexpr int kWgs = D1 >= 128 || (sizeof(T) == 4 && D1 >= 64) ? 1 : 2;
+constexpr int kWgs = D1 > 128 || (sizeof(T) == 4 && D1 > 64) ? 1 : 2;
 
 template <typename T, int D1, bool VEC>
 __global__ __launch_bounds__(walk::kThreads, (kWgs<T, D1>)) void walk_kernel(ForwardArgs a) {

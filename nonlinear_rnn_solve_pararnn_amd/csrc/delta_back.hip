@@ -17,9 +17,9 @@
 // The last line adds terms that the gate does take part in; the shorter
 // identity dg_t - dg_(t+1) = do_t.o_t - dv_t.v_t adds up others that cancel.
 //
-// Precision: walks as in the forward pass.  fp32 tensors: three planes of
-// everything.  bf16 tensors: S, D, U, dr, MP and MA to 16 bits (dg and db are fp32
-// results: 2^-17 of a term; dq and dk are differences where a key is written over).
+// Precision: walks as in the forward pass; S, D, U and dr in three planes, as dg
+// and db are fp32 results whatever the tensors are.  MP and MA, which dq and dk
+// alone are made of, have 16 bits with bf16 tensors.
 #include "delta_walk.hpp"
 
 namespace prn {
@@ -48,7 +48,7 @@ struct BackArgs {
 constexpr int span_of(bool bf16, int D) { return bf16 && D <= 128 ? 64 : 32; }
 
 template <typename T, int D1>
-constexpr int kBackWgs = D1 >= 128 || (sizeof(T) == 4 && D1 >= 64) ? 1 : 2;
+constexpr int kBackWgs = D1 > 128 || (sizeof(T) == 4 && D1 > 64) ? 1 : 2;
 
 template <typename T>
 __device__ __forceinline__ Job job_of(const BackArgs &a, const Where &wh) {
@@ -139,10 +139,10 @@ __device__ __forceinline__ void planes_to(const float (&v)[8], bf16x8 (&p)[N]) {
 
 template <typename T, int D>
 struct GradLds {
-    static constexpr int kN = span_of(sizeof(T) == 2, D), kP = kPlanes<T>, kU = kP == 3 ? 3 : 2, kM = kU, kWaves = D / 16;
-    static constexpr int kRowsX = kN * kTileRow<D>, kRowsM = kN * kTileRow<kN>;
+    static constexpr int kN = span_of(sizeof(T) == 2, D), kP = kPlanes<T>, kM = kP == 3 ? 3 : 2, kW = D >= 128 ? 2 : 1, kWaves = D / 16 / kW;
+    static constexpr int kRowsX = kN * kTileRow<D>, kRowsV = kN * kTileRow<kNB>, kRowsM = kN * kTileRow<kN>;
     struct First {
-        bf16 go[kP * kRowsX], u[kU * kRowsX], dr[kU * kRowsX];
+        bf16 go[kP * kRowsV], u[3 * kRowsV], dr[3 * kRowsV];
     };
     struct Second {
         bf16 k[kP * kRowsX], q[kP * kRowsX], mp[kM * kRowsM], ma[kM * kRowsM];
@@ -157,172 +157,218 @@ struct GradLds {
     float row[2][kN / 16][kN], col[2][kN / 16][kN]; // sums of pairs of either kind: of a row in a tile of columns, of a column in one of rows
 };
 
+// A wave has kW tiles of 16 elements of q and k, so that rows read from LDS serve
+// both, and a workgroup leaves room for another one on its CU, whose loads go on
+// while this one multiplies.
+template <int D> constexpr int kGradThreads = D >= 128 ? D * 2 : D * 4;
 template <typename T, int D, bool VEC>
-__global__ __launch_bounds__(D * 4) void grad_kernel(BackArgs a) {
+__global__ __launch_bounds__(kGradThreads<D>, 2) void grad_kernel(BackArgs a) {
     using Lds = GradLds<T, D>;
-    constexpr int N = Lds::kN, kP = Lds::kP, kU = Lds::kU, kM = Lds::kM, kWaves = Lds::kWaves, kThreadsG = D * 4;
-    constexpr int kX = Lds::kRowsX, kMx = Lds::kRowsM, NI = N / 16, NS = N / 32, kTiles = NI * (NI + 1) / 2;
+    constexpr int N = Lds::kN, kP = Lds::kP, kM = Lds::kM, kWaves = Lds::kWaves, kW = Lds::kW, kThreadsG = kGradThreads<D>;
+    constexpr int kX = Lds::kRowsX, kV = Lds::kRowsV, kMx = Lds::kRowsM, NI = N / 16, NS = N / 32, kTiles = NI * (NI + 1) / 2;
     __shared__ Lds l;
-    const uint32_t bh = blockIdx.x / (uint32_t)a.spans, span = blockIdx.x - bh * (uint32_t)a.spans;
-    const int64_t b = bh / (uint32_t)a.H, h = bh - b * a.H, hk = h / a.group, begin = (int64_t)span * N;
+    // (the divisions run on the vector unit; addresses want scalar registers)
+    const uint32_t bh = same_in_lanes(blockIdx.x / (uint32_t)a.spans), span = blockIdx.x - bh * (uint32_t)a.spans;
+    const uint32_t b = same_in_lanes(bh / (uint32_t)a.H), h = bh - b * (uint32_t)a.H, hk = same_in_lanes(h / (uint32_t)a.group);
+    const int64_t begin = (int64_t)span * N;
     const int cnt = (int)min((int64_t)N, a.L - begin);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
     const int tr_i = m >> 2, tr_c = m & 3;
-    const int steps = a.nblk * 2, wide = a.nblk * kNB;  // of 32 columns of dv; columns in memory
+    const int wide = a.nblk * kNB;  // columns in memory
 
-    if (threadIdx.x < N) {
-        const int p = threadIdx.x;
-        auto gate = [&](const HeadView &v) { return static_cast<const float *>(v.p)[b * v.st[0] + (begin + p) * v.st[1] + h * v.st[2]]; };
-        float g = p < cnt ? gate(a.log_decay) : 0.0f;
-        const float beta = p < cnt ? gate(a.beta) : 0.0f;
-        if (g < -1e5f) g = -1e5f;
-        double sum = (double)g * 1.4426950408889634;
-#pragma unroll
-        for (int d = 1; d < N; d *= 2) {
-            const double up = __shfl_up(sum, d, N);
-            if (p >= d) sum += up;
-        }
-        const double whole = __shfl(sum, N - 1, N);
-        l.G[p] = sum;
-        l.f[p] = fast_exp2((float)sum);
-        l.r[p] = fast_exp2((float)(whole - sum));
-        l.b[p] = beta;
-    }
-    __syncthreads();
-
-    // rows of do, U and dr; dv and db on the way
-    {
-        constexpr int kGrp = D / 8, kRowsAt = kThreadsG / kGrp;
-        const int grp = threadIdx.x % kGrp, r0 = threadIdx.x / kGrp;
-        const T *gop = static_cast<const T *>(a.grad_o.p) + b * a.grad_o.st[0] + begin * a.grad_o.st[1] + h * a.grad_o.st[2];
-        const int64_t base = ((int64_t)bh * a.spans + span) * N;
-#pragma unroll
-        for (int n = 0; n < N / kRowsAt; ++n) {
-            const int row = r0 + n * kRowsAt, at = tile_at<D>(row, grp), c = grp * 8;
-            const bool in = row < cnt;
-            bf16x8 go[kP], up[kU], dp[kU];
-            load8<T, VEC>(gop + row * a.grad_o.st[1], c, a.dv, in, go);
-            float u[8] = {}, d[8] = {}, dot = 0.0f;
-            if (in && c < wide) {
-                const float *us = a.U + (base + row) * wide + c, *ds = a.dR + (base + row) * wide + c;
-                *reinterpret_cast<f32x4 *>(&u[0]) = *reinterpret_cast<const f32x4 *>(us);
-                *reinterpret_cast<f32x4 *>(&u[4]) = *reinterpret_cast<const f32x4 *>(us + 4);
-                *reinterpret_cast<f32x4 *>(&d[0]) = *reinterpret_cast<const f32x4 *>(ds);
-                *reinterpret_cast<f32x4 *>(&d[4]) = *reinterpret_cast<const f32x4 *>(ds + 4);
-            }
-            const float beta = l.b[row];
-            const bool tiny = fabsf(beta) < kTinyBeta;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                dot = fmaf(u[i], d[i], dot);
-                d[i] = tiny ? 0.0f : beta * d[i];
-            }
-#pragma unroll
-            for (int s = 1; s < kGrp; s *= 2) dot += __shfl_xor(dot, s, kGrp);
-            if (grp == 0 && in && a.grad_b != nullptr) a.grad_b[((int64_t)b * a.L + begin + row) * a.H + h] = dot / (tiny ? kTinyBeta : beta);
-            if (in) {
-                T *gv = static_cast<T *>(a.grad_v) + (((int64_t)b * a.L + begin + row) * a.H + h) * a.dv + c;
-                if (a.out8) {
-                    if (c < a.dv) {
-                        constexpr int kV = kVec<T>;
-#pragma unroll
-                        for (int o = 0; o < 8; o += kV) {
-                            float w[kV];
-#pragma unroll
-                            for (int i = 0; i < kV; ++i) w[i] = d[o + i];
-                            store_vec<T, kV>(gv + o, w);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (c + i < a.dv) gv[i] = (T)d[i];
-                }
-            }
-            planes_to(u, up);
-            planes_to(d, dp);
-#pragma unroll
-            for (int p = 0; p < kP; ++p) *reinterpret_cast<bf16x8 *>(&l.first.go[p * kX + at]) = go[p];
-#pragma unroll
-            for (int p = 0; p < kU; ++p) {
-                *reinterpret_cast<bf16x8 *>(&l.first.u[p * kX + at]) = up[p];
-                *reinterpret_cast<bf16x8 *>(&l.first.dr[p * kX + at]) = dp[p];
-            }
-        }
-    }
-    __syncthreads();
-
-    // products with S and D: lane m is position 16 it + m, registers are elements 16 wave + 4 q ..
-    f32x4 aq[NI] = {}, as[NI] = {}, ad[NI] = {};
-    {
-        const int64_t state = (((int64_t)bh * a.spans + span) * a.width + wave * 16 + m) * wide + 8 * q;
-        float z = 0.0f;
-        const int steps_s = wave * 16 < a.width ? steps : 0;  // (narrower keys have no rows there)
-        for (int t = 0; t < steps_s; ++t) {
-            float sv[8], dv[8];
-            const float *ss = a.S + state + 32 * t, *ds = a.D + state + 32 * t;
-            *reinterpret_cast<f32x4 *>(&sv[0]) = *reinterpret_cast<const f32x4 *>(ss);
-            *reinterpret_cast<f32x4 *>(&sv[4]) = *reinterpret_cast<const f32x4 *>(ss + 4);
-            *reinterpret_cast<f32x4 *>(&dv[0]) = *reinterpret_cast<const f32x4 *>(ds);
-            *reinterpret_cast<f32x4 *>(&dv[4]) = *reinterpret_cast<const f32x4 *>(ds + 4);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z = fmaf(sv[i], dv[i], z);
-            bf16x8 sp[kU], dp[kU];
-            planes_to(sv, sp);
-            planes_to(dv, dp);
-#pragma unroll
-            for (int it = 0; it < NI; ++it) {
-                const int at = tile_at<D>(16 * it + m, 4 * t + q);
-                bf16x8 go[kP], dr[kU], u[kU];
-#pragma unroll
-                for (int p = 0; p < kP; ++p) go[p] = read_row(&l.first.go[p * kX + at]);
-#pragma unroll
-                for (int p = 0; p < kU; ++p) {
-                    dr[p] = read_row(&l.first.dr[p * kX + at]);
-                    u[p] = read_row(&l.first.u[p * kX + at]);
-                }
-                aq[it] = mfma_planes(sp, go, aq[it]);
-                as[it] = mfma_planes(sp, dr, as[it]);
-                ad[it] = mfma_planes(dp, u, ad[it]);
-            }
-        }
-        z = lanes_sum(z);
-        if (lane == 0) l.z[wave] = z;
-    }
-    // raw do_i.u_j and dr_i.u_j, tiles on and below the diagonal, round the waves: a result's rows are i
+    // Rows of do, U and dr go through LDS 64 columns at a time, dv and db on the
+    // way; products with S and D: lane m is position 16 it + m, registers are
+    // elements 16 (kW wave + w) + 4 q ..; raw do_i.u_j and dr_i.u_j: tiles on and below the
+    // diagonal go round the waves, a result's rows are i.
+    constexpr int kRowsAt = kThreadsG / 8, kMyRows = (N + kRowsAt - 1) / kRowsAt;
     constexpr int kUnits = 2 * kTiles, kMine = (kUnits + kWaves - 1) / kWaves;
-    f32x4 pair[kMine] = {};
+    f32x4 aq[kW][NI] = {}, as[kW][NI] = {}, ad[kW][NI] = {}, pair[kMine] = {};
     auto unit_of = [&](int n) { return min(wave + n * kWaves, kUnits - 1); };
     auto tile_of = [&](int unit, int &it, int &jt) {
         const int tile = unit >= kTiles ? unit - kTiles : unit;
         it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
         jt = tile - it * (it + 1) / 2;
     };
+    {
+        const int grp = threadIdx.x & 7, r0 = threadIdx.x >> 3;
+        const T *gop = static_cast<const T *>(a.grad_o.p) + b * a.grad_o.st[0] + begin * a.grad_o.st[1] + h * a.grad_o.st[2];
+        const int64_t base = ((int64_t)bh * a.spans + span) * N * wide;
+        const float *u_rows = a.U + base, *r_rows = a.dR + base;
+        bf16x8 go[kMyRows][kP];
+        float u[kMyRows][8], d[kMyRows][8], dot[kMyRows] = {}, z = 0.0f;
+        auto load_rows = [&](int blk) {
 #pragma unroll
-    for (int n = 0; n < kMine; ++n) {
-        const int unit = unit_of(n);
-        int it, jt;
-        tile_of(unit, it, jt);
-        const bool erase = unit >= kTiles;
-        for (int t = 0; t < steps; ++t) {
-            const int ai = tile_at<D>(16 * it + m, 4 * t + q), aj = tile_at<D>(16 * jt + m, 4 * t + q);
-            bf16x8 u[kU];
+            for (int n = 0; n < kMyRows; ++n) {
+                const int row = r0 + n * kRowsAt, c = blk * kNB + grp * 8;
+                const bool in = row < cnt;
+                load8<T, VEC>(gop + row * a.grad_o.st[1], c, a.dv, in, go[n]);
 #pragma unroll
-            for (int p = 0; p < kU; ++p) u[p] = read_row(&l.first.u[p * kX + aj]);
-            if (erase) {
-                bf16x8 x[kU];
+                for (int i = 0; i < 8; ++i) u[n][i] = d[n][i] = 0.0f;
+                if (in) {
+                    const uint32_t at = (uint32_t)(row * wide + c);
 #pragma unroll
-                for (int p = 0; p < kU; ++p) x[p] = read_row(&l.first.dr[p * kX + ai]);
-                pair[n] = mfma_planes(x, u, pair[n]);
-            } else {
-                bf16x8 x[kP];
+                    for (int i = 0; i < 8; i += 4) {
+                        *reinterpret_cast<f32x4 *>(&u[n][i]) = *reinterpret_cast<const f32x4 *>(u_rows + at + i);
+                        *reinterpret_cast<f32x4 *>(&d[n][i]) = *reinterpret_cast<const f32x4 *>(r_rows + at + i);
+                    }
+                }
+            }
+        };
+        const bool has_s = wave * kW * 16 < a.width;  // (narrower keys have no rows there)
+        const int64_t state = (((int64_t)bh * a.spans + span) * a.width + (has_s ? wave * kW * 16 : 0)) * wide;
+        const float *s_rows = a.S + state, *d_rows = a.D + state;
+        const uint32_t lane_at = (uint32_t)(m * wide + 8 * q);
+        float sv[kW][8], dv[kW][8];
+        auto load_state = [&](int t) {
 #pragma unroll
-                for (int p = 0; p < kP; ++p) x[p] = read_row(&l.first.go[p * kX + ai]);
-                pair[n] = mfma_planes(x, u, pair[n]);
+            for (int w = 0; w < kW; ++w)
+#pragma unroll
+                for (int i = 0; i < 8; i += 4) {
+                    const uint32_t at = lane_at + (uint32_t)(16 * w * wide + 32 * t + i);
+                    *reinterpret_cast<f32x4 *>(&sv[w][i]) = *reinterpret_cast<const f32x4 *>(s_rows + at);
+                    *reinterpret_cast<f32x4 *>(&dv[w][i]) = *reinterpret_cast<const f32x4 *>(d_rows + at);
+                }
+        };
+        load_rows(0);
+        load_state(0);
+        if (threadIdx.x < N) {
+            const int p = threadIdx.x;
+            auto gate = [&](const HeadView &v) { return static_cast<const float *>(v.p)[b * v.st[0] + (begin + p) * v.st[1] + h * v.st[2]]; };
+            float g = p < cnt ? gate(a.log_decay) : 0.0f;
+            const float beta = p < cnt ? gate(a.beta) : 0.0f;
+            if (g < -1e5f) g = -1e5f;
+            double sum = (double)g * 1.4426950408889634;
+#pragma unroll
+            for (int d = 1; d < N; d *= 2) {
+                const double up = __shfl_up(sum, d, N);
+                if (p >= d) sum += up;
+            }
+            const double whole = __shfl(sum, N - 1, N);
+            l.G[p] = sum;
+            l.f[p] = fast_exp2((float)sum);
+            l.r[p] = fast_exp2((float)(whole - sum));
+            l.b[p] = beta;
+        }
+        __syncthreads();
+        for (int blk = 0; blk < a.nblk; ++blk) {
+#pragma unroll
+            for (int n = 0; n < kMyRows; ++n) {
+                const int row = r0 + n * kRowsAt, at = tile_at<kNB>(row, grp), c = blk * kNB + grp * 8;
+                if (N < kRowsAt && row >= N) continue;  // (whole waves)
+                const float beta = l.b[row];
+                const bool tiny = fabsf(beta) < kTinyBeta;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dot[n] = fmaf(u[n][i], d[n][i], dot[n]);
+                    d[n][i] = tiny ? 0.0f : beta * d[n][i];
+                }
+                if (row < cnt) {
+                    T *gv = static_cast<T *>(a.grad_v) + (((int64_t)b * a.L + begin) * a.H + h) * a.dv + (int64_t)row * a.H * a.dv + c;
+                    if (a.out8) {
+                        constexpr int kVec8 = kVec<T>;
+                        if (c < a.dv) {
+#pragma unroll
+                            for (int o = 0; o < 8; o += kVec8) {
+                                float w[kVec8];
+#pragma unroll
+                                for (int i = 0; i < kVec8; ++i) w[i] = d[n][o + i];
+                                store_vec<T, kVec8>(gv + o, w);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (c + i < a.dv) gv[i] = (T)d[n][i];
+                    }
+                }
+                bf16x8 p3[3];
+                split3(u[n], p3);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8 *>(&l.first.u[p * kV + at]) = p3[p];
+                split3(d[n], p3);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8 *>(&l.first.dr[p * kV + at]) = p3[p];
+#pragma unroll
+                for (int p = 0; p < kP; ++p) *reinterpret_cast<bf16x8 *>(&l.first.go[p * kV + at]) = go[n][p];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (has_s) {
+                    bf16x8 sp[kW][3], x[kP], y[3];
+#pragma unroll
+                    for (int w = 0; w < kW; ++w) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) z = fmaf(sv[w][i], dv[w][i], z);
+                        split3(sv[w], sp[w]);
+                    }
+#pragma unroll
+                    for (int it = 0; it < NI; ++it) {
+                        const int at = tile_at<kNB>(16 * it + m, 4 * t + q);
+#pragma unroll
+                        for (int p = 0; p < kP; ++p) x[p] = read_row(&l.first.go[p * kV + at]);
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.dr[p * kV + at]);
+#pragma unroll
+                        for (int w = 0; w < kW; ++w) {
+                            aq[w][it] = mfma_planes(sp[w], x, aq[w][it]);
+                            as[w][it] = mfma_planes(sp[w], y, as[w][it]);
+                        }
+                        if (it & 1) __builtin_amdgcn_sched_barrier(0);  // or reads are brought forward into registers that are not there
+                    }
+#pragma unroll
+                    for (int w = 0; w < kW; ++w) split3(dv[w], sp[w]);
+                    if (blk * 2 + t + 1 < a.nblk * 2) load_state(blk * 2 + t + 1);
+#pragma unroll
+                    for (int it = 0; it < NI; ++it) {
+                        const int at = tile_at<kNB>(16 * it + m, 4 * t + q);
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.u[p * kV + at]);
+#pragma unroll
+                        for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(sp[w], y, ad[w][it]);
+                        if (it & 1) __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < kMine; ++n) {
+                    const int unit = unit_of(n);
+                    int it, jt;
+                    tile_of(unit, it, jt);
+                    const int ai = tile_at<kNB>(16 * it + m, 4 * t + q), aj = tile_at<kNB>(16 * jt + m, 4 * t + q);
+                    bf16x8 y[3];
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.u[p * kV + aj]);
+                    if (unit >= kTiles) {
+                        bf16x8 x[3];
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) x[p] = read_row(&l.first.dr[p * kV + ai]);
+                        pair[n] = mfma_planes(x, y, pair[n]);
+                    } else {
+                        bf16x8 x[kP];
+#pragma unroll
+                        for (int p = 0; p < kP; ++p) x[p] = read_row(&l.first.go[p * kV + ai]);
+                        pair[n] = mfma_planes(x, y, pair[n]);
+                    }
+                    if (n & 1) __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            __syncthreads();
+            // (not ahead of the products: another workgroup's hide it, and they need the registers)
+            if (blk + 1 < a.nblk) load_rows(blk + 1);
+        }
+        z = lanes_sum(z);
+        if (lane == 0) l.z[wave] = has_s ? z : 0.0f;
+#pragma unroll
+        for (int n = 0; n < kMyRows; ++n) {
+            const int row = r0 + n * kRowsAt;
+#pragma unroll
+            for (int s = 1; s < 8; s *= 2) dot[n] += __shfl_xor(dot[n], s, 8);
+            if (grp == 0 && row < cnt && a.grad_b != nullptr) {
+                const float beta = l.b[row];
+                a.grad_b[((int64_t)b * a.L + begin + row) * a.H + h] = dot[n] / (fabsf(beta) < kTinyBeta ? kTinyBeta : beta);
             }
         }
     }
-    __syncthreads();
 
     // rows of q and k in their place
     {
@@ -342,10 +388,11 @@ __global__ __launch_bounds__(D * 4) void grad_kernel(BackArgs a) {
                 *reinterpret_cast<bf16x8 *>(&l.second.q[p * kX + at]) = y[p];
             }
         }
-        // MP right of the diagonal
-        for (int i = threadIdx.x; i < kM * kMx / 8; i += kThreadsG) {
+        // the tiles above those on the diagonal that are read with them
+        for (int i = threadIdx.x; i < 2 * kM * NS * 16 * 2; i += kThreadsG) {
+            const int half = i & 1, r = i >> 1 & 15, s = (i >> 5) % NS, k = (i >> 5) / NS;
             const bf16x8 zero = {};
-            *reinterpret_cast<bf16x8 *>(&l.second.mp[i * 8]) = zero;
+            *reinterpret_cast<bf16x8 *>(&(k < kM ? l.second.mp : l.second.ma)[(k < kM ? k : k - kM) * kMx + tile_at<N>(32 * s + 16 + r, 4 * s + half)]) = zero;
         }
     }
     __syncthreads();
@@ -368,7 +415,7 @@ __global__ __launch_bounds__(D * 4) void grad_kernel(BackArgs a) {
             }
             dots = mfma_planes(x, y, dots);
         }
-        float cols = 0.0f;
+        float cols = 0.0f, mine[8] = {};
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int i = 16 * it + 4 * q + r, j = 16 * jt + m;
@@ -378,15 +425,14 @@ __global__ __launch_bounds__(D * 4) void grad_kernel(BackArgs a) {
             cols += both;
             const float rows = lanes16_sum(both);
             if (m == 0) l.row[erase][jt][i] = rows;
-            float v[8] = {w};
-            bf16x8 p[kM];
-            planes_to(v, p);
-#pragma unroll
-            for (int k = 0; k < kM; ++k) {
-                if (j <= i) (erase ? l.second.ma : l.second.mp)[k * kMx + tile_at<N>(i, j >> 3) + (j & 7)] = p[k][0];
-                if (erase && j < i) l.second.ma[k * kMx + tile_at<N>(j, i >> 3) + (i & 7)] = p[k][0];
-            }
+            mine[r] = w;
         }
+        // MP and MA are kept by columns: a lane's four results are neighbours there
+        bf16x8 p[kM];
+        walk::to_planes(mine, p);
+        bf16 *to = &(erase ? l.second.ma : l.second.mp)[tile_at<N>(16 * jt + m, 2 * it + (q >> 1)) + 4 * (q & 1)];
+#pragma unroll
+        for (int k = 0; k < kM; ++k) *reinterpret_cast<u32x2 *>(to + k * kMx) = *reinterpret_cast<const u32x2 *>(&p[k]);
         cols += __shfl_xor(cols, 16);
         cols += __shfl_xor(cols, 32);
         if (q == 0) l.col[erase][it][16 * jt + m] = cols;
@@ -396,23 +442,27 @@ __global__ __launch_bounds__(D * 4) void grad_kernel(BackArgs a) {
     // the products with S and D weighted; a row's products with them are the gates' share
 #pragma unroll
     for (int it = 0; it < NI; ++it) {
-        const int pos = 16 * it + m, at = tile_at<D>(pos, 2 * wave + (q >> 1)) + 4 * (q & 1);
+        const int pos = 16 * it + m;
         const float f = l.f[pos], r = l.r[pos];
         float x = 0.0f, y = 0.0f;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            float qv = 0.0f, kv = 0.0f;
+        for (int w = 0; w < kW; ++w) {
+            const int at = tile_at<D>(pos, 2 * (wave * kW + w) + (q >> 1)) + 4 * (q & 1);
 #pragma unroll
-            for (int p = 0; p < kP; ++p) {
-                qv += (float)l.second.q[p * kX + at + n];
-                kv += (float)l.second.k[p * kX + at + n];
+            for (int n = 0; n < 4; ++n) {
+                float qv = 0.0f, kv = 0.0f;
+#pragma unroll
+                for (int p = 0; p < kP; ++p) {
+                    qv += (float)l.second.q[p * kX + at + n];
+                    kv += (float)l.second.k[p * kX + at + n];
+                }
+                aq[w][it][n] *= f * a.scale;
+                as[w][it][n] *= f;
+                ad[w][it][n] *= r;
+                y = fmaf(qv, aq[w][it][n], fmaf(-kv, as[w][it][n], y));
+                x = fmaf(kv, ad[w][it][n], x);
+                ad[w][it][n] -= as[w][it][n];
             }
-            aq[it][n] *= f * a.scale;
-            as[it][n] *= f;
-            ad[it][n] *= r;
-            y = fmaf(qv, aq[it][n], fmaf(-kv, as[it][n], y));
-            x = fmaf(kv, ad[it][n], x);
-            ad[it][n] -= as[it][n];
         }
         x += __shfl_xor(x, 16);
         y += __shfl_xor(y, 16);
@@ -426,57 +476,75 @@ __global__ __launch_bounds__(D * 4) void grad_kernel(BackArgs a) {
     // the pairs: dq += MP K, dk += MP^T Q + (MA + MA^T) K
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-        bf16x8 kt[kP], qt[kP];
-        const int row = 32 * s + 8 * q + tr_i, grp = 2 * wave + (tr_c >> 1), in = 4 * (tr_c & 1);
+        const int row = 32 * s + 8 * q + tr_i, in = 4 * (tr_c & 1);
+        bf16x8 kt[kW][kP], qt[kW][kP];
 #pragma unroll
-        for (int p = 0; p < kP; ++p) {
-            kt[p] = walk::join(read_tr(&l.second.k[p * kX + tile_at<D>(row, grp) + in]), read_tr(&l.second.k[p * kX + tile_at<D>(row + 4, grp) + in]));
-            qt[p] = walk::join(read_tr(&l.second.q[p * kX + tile_at<D>(row, grp) + in]), read_tr(&l.second.q[p * kX + tile_at<D>(row + 4, grp) + in]));
+        for (int w = 0; w < kW; ++w) {
+            const int grp = 2 * (wave * kW + w) + (tr_c >> 1);
+#pragma unroll
+            for (int p = 0; p < kP; ++p) {
+                kt[w][p] = walk::join(read_tr(&l.second.k[p * kX + tile_at<D>(row, grp) + in]), read_tr(&l.second.k[p * kX + tile_at<D>(row + 4, grp) + in]));
+                qt[w][p] = walk::join(read_tr(&l.second.q[p * kX + tile_at<D>(row, grp) + in]), read_tr(&l.second.q[p * kX + tile_at<D>(row + 4, grp) + in]));
+            }
         }
 #pragma unroll
         for (int it = 0; it < NI; ++it) {
-            bf16x8 w[kM];
-            if (s <= it / 2) {
-#pragma unroll
-                for (int p = 0; p < kM; ++p) w[p] = read_row(&l.second.mp[p * kMx + tile_at<N>(16 * it + m, 4 * s + q)]);
-                aq[it] = mfma_planes(kt, w, aq[it]);
-            }
-            if (s >= it / 2) {
+            bf16x8 x[kM];
+            auto down = [&](const bf16 *M) {  // lane m: row 16 it + m of M, elements j
                 const int g2 = 2 * it + (tr_c >> 1);
 #pragma unroll
                 for (int p = 0; p < kM; ++p)
-                    w[p] = walk::join(read_tr(&l.second.mp[p * kMx + tile_at<N>(row, g2) + in]), read_tr(&l.second.mp[p * kMx + tile_at<N>(row + 4, g2) + in]));
-                ad[it] = mfma_planes(qt, w, ad[it]);
-            }
+                    x[p] = walk::join(read_tr(&M[p * kMx + tile_at<N>(row, g2) + in]), read_tr(&M[p * kMx + tile_at<N>(row + 4, g2) + in]));
+            };
+            auto along = [&](const bf16 *M) {  // lane m: column 16 it + m, elements i
 #pragma unroll
-            for (int p = 0; p < kM; ++p) w[p] = read_row(&l.second.ma[p * kMx + tile_at<N>(16 * it + m, 4 * s + q)]);
-            ad[it] = mfma_planes(kt, w, ad[it]);
+                for (int p = 0; p < kM; ++p) x[p] = read_row(&M[p * kMx + tile_at<N>(16 * it + m, 4 * s + q)]);
+            };
+            if (s <= it / 2) {
+                down(l.second.mp);
+#pragma unroll
+                for (int w = 0; w < kW; ++w) aq[w][it] = mfma_planes(kt[w], x, aq[w][it]);
+                down(l.second.ma);
+#pragma unroll
+                for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(kt[w], x, ad[w][it]);
+            }
+            if (s >= it / 2) {
+                along(l.second.mp);
+#pragma unroll
+                for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(qt[w], x, ad[w][it]);
+                along(l.second.ma);
+#pragma unroll
+                for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(kt[w], x, ad[w][it]);
+            }
         }
     }
-    const int c = 16 * wave + 4 * q;
 #pragma unroll
     for (int it = 0; it < NI; ++it) {
         const int pos = 16 * it + m;
         if (pos >= cnt) continue;
         const int64_t row = b * a.L + begin + pos;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float v[4];
+        for (int w = 0; w < kW; ++w) {
+            const int c = 16 * (wave * kW + w) + 4 * q;
 #pragma unroll
-            for (int n = 0; n < 4; ++n) v[n] = k ? ad[it][n] : aq[it][n];
-            if (a.part_q != nullptr) {
-                float *to = (k ? a.part_k : a.part_q) + (row * a.H + h) * a.dk + c;
+            for (int k = 0; k < 2; ++k) {
+                float v[4];
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-                    if (c + n < a.dk) to[n] = v[n];
-            } else {
-                T *to = static_cast<T *>(k ? a.grad_k : a.grad_q) + (row * a.H + h) * a.dk + c;
-                if (a.out4) {
-                    if (c < a.dk) store_vec<T, 4>(to, v);
-                } else {
+                for (int n = 0; n < 4; ++n) v[n] = k ? ad[w][it][n] : aq[w][it][n];
+                if (a.part_q != nullptr) {
+                    float *to = (k ? a.part_k : a.part_q) + (row * a.H + h) * a.dk + c;
 #pragma unroll
                     for (int n = 0; n < 4; ++n)
-                        if (c + n < a.dk) to[n] = (T)v[n];
+                        if (c + n < a.dk) to[n] = v[n];
+                } else {
+                    T *to = static_cast<T *>(k ? a.grad_k : a.grad_q) + (row * a.H + h) * a.dk + c;
+                    if (a.out4) {
+                        if (c < a.dk) store_vec<T, 4>(to, v);
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+                            if (c + n < a.dk) to[n] = (T)v[n];
+                    }
                 }
             }
         }
@@ -634,9 +702,9 @@ hipError_t back_launch(const DeltaArgs &p, char *scratch, hipStream_t s) {
     if (e != hipSuccess) return e;
     const unsigned grid = (unsigned)(pairs * w.spans);
     switch (span_width(p)) {
-        case 64: grad_kernel<T, 64, VEC><<<grid, 64 * 4, 0, s>>>(a); break;
-        case 128: grad_kernel<T, 128, VEC><<<grid, 128 * 4, 0, s>>>(a); break;
-        default: grad_kernel<T, 256, VEC><<<grid, 256 * 4, 0, s>>>(a); break;
+        case 64: grad_kernel<T, 64, VEC><<<grid, kGradThreads<64>, 0, s>>>(a); break;
+        case 128: grad_kernel<T, 128, VEC><<<grid, kGradThreads<128>, 0, s>>>(a); break;
+        default: grad_kernel<T, 256, VEC><<<grid, kGradThreads<256>, 0, s>>>(a); break;
     }
     if (w.parts) {
         const int64_t n = p.B * p.L * p.Hk * p.dk;

@@ -13,8 +13,7 @@
 // A wave is alone on its SIMD in most launches (a (batch row, head) pair has
 // only dv / 16 of them), so the chunk's chain of dependent steps is what bounds
 // it.  LDS reads are issued a step ahead of the matrix instructions that use
-// them, results side by side take turns in the matrix unit, T and P of the next
-// chunk are loaded as soon as those of this one are used, and results are
+// them, results side by side take turns in the matrix unit, and results are
 // stored after the next chunk's operands have arrived (loads and stores are
 // waited for in their order).  B=8, L=2048, H=16, 128x128, bf16: 199 us with
 // reads left to the compiler and one result after the other, 210 with
@@ -77,6 +76,7 @@ struct Job {
 template <typename T, int D1>
 struct alignas(16) WalkLds {
     bf16 K[kPlanes<T> * C * kTileRow<D1>], Q[kPlanes<T> * C * kTileRow<D1>], V[kPlanes<T> * C * kTileRow<kNB>];
+    bf16x8 mats[12][64];  // planes of T's two tiles, then of P's
     Gates gates;
 };
 
@@ -137,7 +137,8 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
     ak.init(rk);
     av.init(rv);
     float gate_ahead = 0.0f;
-    bf16x8 Tm[2][3], Pm[2][kMat];
+    constexpr int kMats = 6 + (kUseQ ? 2 * kMat : 0), kMyMats = (kMats + 3) / 4;
+    bf16x8 mat_ahead[kMyMats];  // this wave's share of T and P
     const int n_chunks = j.to - j.from;
     auto chunk_at = [&](int i) { return kGrad ? j.to - 1 - i : j.from + i; };
     auto positions = [&](int c) { return c < j.all - 1 ? C : last; };
@@ -147,20 +148,15 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
         ak.load(rk, c, cnt);
         if (kUseQ) aq.load(rq, c, cnt);
         av.load(rv, c, has_v ? cnt : 0);
-        if (threadIdx.x < sizeof(Gates) / 4) gate_ahead = reinterpret_cast<const float *>(record(i))[threadIdx.x];
-    };
-    // T and P are loaded anew as soon as they have been used
-    auto load_T = [&](int i) {
-        const char *r = record(i) + (kGrad ? kAtTt : kAtT) + lane * 16;
+        const char *r = record(i);
+        if (threadIdx.x < sizeof(Gates) / 4) gate_ahead = reinterpret_cast<const float *>(r)[threadIdx.x];
 #pragma unroll
-        for (int n = 0; n < 6; ++n) Tm[n / 3][n % 3] = *reinterpret_cast<const bf16x8 *>(r + n * kTile);
+        for (int n = 0; n < kMyMats; ++n) {
+            const int tile = wave * kMyMats + n;
+            const int at = tile < 6 ? (kGrad ? kAtTt : kAtT) + tile * kTile : (kGrad ? kAtPt : kAtP) + (tile - 6) * kTile;
+            if (kMats % 4 == 0 || tile < kMats) mat_ahead[n] = *reinterpret_cast<const bf16x8 *>(r + at + lane * 16);
+        }
     };
-    auto load_P = [&](int i) {
-        const char *r = record(i) + (kGrad ? kAtPt : kAtP) + lane * 16;
-#pragma unroll
-        for (int n = 0; n < 2 * kMat; ++n) Pm[n / kMat][n % kMat] = *reinterpret_cast<const bf16x8 *>(r + n * kTile);
-    };
-
     // a chunk's results on their way out
     using Bits = std::conditional_t<sizeof(T) == 2, u32x2, u32x4>;
     using Bit = std::conditional_t<sizeof(T) == 2, uint16_t, uint32_t>;
@@ -194,8 +190,6 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
     };
 
     load(0);
-    load_T(0);
-    if (kUseQ) load_P(0);
     for (int i = 0; i < n_chunks; ++i) {
         const int c = chunk_at(i), cnt = positions(c);
         lds_barrier();  // the last chunk's reads are done
@@ -203,6 +197,9 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
         if (kUseQ) aq.store(rq, l.Q);
         av.store(rv, l.V);
         if (threadIdx.x < sizeof(Gates) / 4) reinterpret_cast<float *>(&l.gates)[threadIdx.x] = gate_ahead;
+#pragma unroll
+        for (int n = 0; n < kMyMats; ++n)
+            if (kMats % 4 == 0 || wave * kMyMats + n < kMats) l.mats[wave * kMyMats + n][lane] = mat_ahead[n];
         if (i > 0) write(i - 1);
         if (BACK && j.states != nullptr) {
             const int span = (int)j.span_chunks, s = c / span;
@@ -271,6 +268,9 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
         float gb[8];
 #pragma unroll
         for (int n = 0; n < 8; ++n) gb[n] = l.gates.b[8 * q + n];
+        bf16x8 Tm[2][3];
+#pragma unroll
+        for (int n = 0; n < 6; ++n) Tm[n / 3][n % 3] = l.mats[n][lane];
         // the tiles of K^T (and Q^T) for the state's update, a step ahead of their use
         struct Across {
             bf16x8 k[2][kP], q[2][kP];
@@ -301,8 +301,10 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
             bf16x8 zz[kP];
 #pragma unroll
             for (int p = 0; p < kP; ++p) zz[p] = z[p];
+            bf16x8 Pm[2][kMat];
+#pragma unroll
+            for (int n = 0; n < 2 * kMat; ++n) Pm[n / kMat][n % kMat] = l.mats[6 + n][lane];
             mfma_each(Pm, zz, y);
-            load_P(i + 1);
 #pragma unroll
             for (int n = 0; n < 8; ++n) x[n] = y[n >> 2][n & 3];
         } else {
@@ -313,7 +315,6 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
         split3(x, xp);
         f32x4 ua[2] = {};
         mfma_each(Tm, xp, ua);
-        load_T(i + 1);
         const float carry = __uint_as_float(same_in_lanes(__float_as_uint(l.gates.carry)));
         const bool fast = same_in_lanes(__float_as_uint(l.gates.fast)) != 0;
         if constexpr (kGrad) {  // f do' while T^T is at work
@@ -338,8 +339,10 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
             for (int p = 0; p < kO; ++p) up[p] = xp[p];
 #pragma unroll
             for (int it = 0; it < 2; ++it) o[it] *= l.gates.f[16 * it + m] * j.scale;
+            bf16x8 Pm[2][kMat];
+#pragma unroll
+            for (int n = 0; n < 2 * kMat; ++n) Pm[n / kMat][n % kMat] = l.mats[6 + n][lane];
             mfma_each_right(up, Pm, o);
-            load_P(i + 1);
         }
         // the state after the chunk: K^T (r U), or Q^T (f do') - K^T (f b dR)
 #pragma unroll
