@@ -137,9 +137,10 @@ __global__ __launch_bounds__(walk::kThreads, (kBackWgs<T, D1>)) void back_segmen
 template <int N>
 __device__ __forceinline__ void planes_to(const float (&v)[8], bf16x8 (&p)[N]) { walk::to_planes(v, p); }
 
+constexpr int grad_tiles(bool bf16, int D) { return D >= 128 && span_of(bf16, D) == 32 ? 2 : 1; }
 template <typename T, int D>
 struct GradLds {
-    static constexpr int kN = span_of(sizeof(T) == 2, D), kP = kPlanes<T>, kM = kP == 3 ? 3 : 2, kW = D >= 128 ? 2 : 1, kWaves = D / 16 / kW;
+    static constexpr int kN = span_of(sizeof(T) == 2, D), kP = kPlanes<T>, kM = kP == 3 ? 3 : 2, kW = grad_tiles(sizeof(T) == 2, D), kWaves = D / 16 / kW;
     static constexpr int kRowsX = kN * kTileRow<D>, kRowsV = kN * kTileRow<kNB>, kRowsM = kN * kTileRow<kN>;
     struct First {
         bf16 go[kP * kRowsV], u[3 * kRowsV], dr[3 * kRowsV];
@@ -160,11 +161,11 @@ struct GradLds {
 // A wave has kW tiles of 16 elements of q and k, so that rows read from LDS serve
 // both, and a workgroup leaves room for another one on its CU, whose loads go on
 // while this one multiplies.
-template <int D> constexpr int kGradThreads = D >= 128 ? D * 2 : D * 4;
+template <typename T, int D> constexpr int kGradThreads = D * 4 / grad_tiles(sizeof(T) == 2, D);
 template <typename T, int D, bool VEC>
-__global__ __launch_bounds__(kGradThreads<D>, 2) void grad_kernel(BackArgs a) {
+__global__ __launch_bounds__((kGradThreads<T, D>), 2) void grad_kernel(BackArgs a) {
     using Lds = GradLds<T, D>;
-    constexpr int N = Lds::kN, kP = Lds::kP, kM = Lds::kM, kWaves = Lds::kWaves, kW = Lds::kW, kThreadsG = kGradThreads<D>;
+    constexpr int N = Lds::kN, kP = Lds::kP, kM = Lds::kM, kWaves = Lds::kWaves, kW = Lds::kW, kThreadsG = kGradThreads<T, D>;
     constexpr int kX = Lds::kRowsX, kV = Lds::kRowsV, kMx = Lds::kRowsM, NI = N / 16, NS = N / 32, kTiles = NI * (NI + 1) / 2;
     __shared__ Lds l;
     // (the divisions run on the vector unit; addresses want scalar registers)
@@ -180,6 +181,19 @@ __global__ __launch_bounds__(kGradThreads<D>, 2) void grad_kernel(BackArgs a) {
     // way; products with S and D: lane m is position 16 it + m, registers are
     // elements 16 (kW wave + w) + 4 q ..; raw do_i.u_j and dr_i.u_j: tiles on and below the
     // diagonal go round the waves, a result's rows are i.
+    constexpr int kKeysAt = kThreadsG / (D / 8), kMyKeys = N / kKeysAt;
+    const int key_grp = threadIdx.x % (D / 8), key_row = threadIdx.x / (D / 8);
+    bf16x8 key[kMyKeys][kP], query[kMyKeys][kP];
+    auto load_keys = [&]() {
+        const T *kp = static_cast<const T *>(a.k.p) + b * a.k.st[0] + begin * a.k.st[1] + hk * a.k.st[2];
+        const T *qp = static_cast<const T *>(a.q.p) + b * a.q.st[0] + begin * a.q.st[1] + hk * a.q.st[2];
+#pragma unroll
+        for (int n = 0; n < kMyKeys; ++n) {
+            const int row = key_row + n * kKeysAt;
+            load8<T, VEC>(kp + row * a.k.st[1], key_grp * 8, a.dk, row < cnt, key[n]);
+            load8<T, VEC>(qp + row * a.q.st[1], key_grp * 8, a.dk, row < cnt, query[n]);
+        }
+    };
     constexpr int kRowsAt = kThreadsG / 8, kMyRows = (N + kRowsAt - 1) / kRowsAt;
     constexpr int kUnits = 2 * kTiles, kMine = (kUnits + kWaves - 1) / kWaves;
     f32x4 aq[kW][NI] = {}, as[kW][NI] = {}, ad[kW][NI] = {}, pair[kMine] = {};
@@ -200,7 +214,7 @@ __global__ __launch_bounds__(kGradThreads<D>, 2) void grad_kernel(BackArgs a) {
 #pragma unroll
             for (int n = 0; n < kMyRows; ++n) {
                 const int row = r0 + n * kRowsAt, c = blk * kNB + grp * 8;
-                const bool in = row < cnt;
+                const bool in = row < cnt && c < wide;
                 load8<T, VEC>(gop + row * a.grad_o.st[1], c, a.dv, in, go[n]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) u[n][i] = d[n][i] = 0.0f;
@@ -214,7 +228,7 @@ __global__ __launch_bounds__(kGradThreads<D>, 2) void grad_kernel(BackArgs a) {
                 }
             }
         };
-        const bool has_s = wave * kW * 16 < a.width;  // (narrower keys have no rows there)
+        const bool has_s = wave * kW * 16 < a.width;  // narrower keys have no rows there: the first ones stand in, for elements that nothing reads
         const int64_t state = (((int64_t)bh * a.spans + span) * a.width + (has_s ? wave * kW * 16 : 0)) * wide;
         const float *s_rows = a.S + state, *d_rows = a.D + state;
         const uint32_t lane_at = (uint32_t)(m * wide + 8 * q);
@@ -224,7 +238,7 @@ __global__ __launch_bounds__(kGradThreads<D>, 2) void grad_kernel(BackArgs a) {
             for (int w = 0; w < kW; ++w)
 #pragma unroll
                 for (int i = 0; i < 8; i += 4) {
-                    const uint32_t at = lane_at + (uint32_t)(16 * w * wide + 32 * t + i);
+                    const uint32_t at = lane_at + (uint32_t)(16 * w * wide + min(32 * t, wide - 32) + i);
                     *reinterpret_cast<f32x4 *>(&sv[w][i]) = *reinterpret_cast<const f32x4 *>(s_rows + at);
                     *reinterpret_cast<f32x4 *>(&dv[w][i]) = *reinterpret_cast<const f32x4 *>(d_rows + at);
                 }
@@ -250,7 +264,9 @@ __global__ __launch_bounds__(kGradThreads<D>, 2) void grad_kernel(BackArgs a) {
             l.b[p] = beta;
         }
         __syncthreads();
-        for (int blk = 0; blk < a.nblk; ++blk) {
+        // (blocks that dv does not reach are zeros: a loop of any other number moves all sums between registers)
+#pragma unroll
+        for (int blk = 0; blk < D / kNB; ++blk) {
 #pragma unroll
             for (int n = 0; n < kMyRows; ++n) {
                 const int row = r0 + n * kRowsAt, at = tile_at<kNB>(row, grp), c = blk * kNB + grp * 8;
@@ -291,43 +307,47 @@ __global__ __launch_bounds__(kGradThreads<D>, 2) void grad_kernel(BackArgs a) {
 #pragma unroll
                 for (int p = 0; p < kP; ++p) *reinterpret_cast<bf16x8 *>(&l.first.go[p * kV + at]) = go[n][p];
             }
+            // the next rows, ahead of the products
+            auto load_next = [&]() {
+                if (blk + 1 < D / kNB) load_rows(blk + 1);
+                else load_keys();
+            };
+            load_next();
             __syncthreads();
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                if (has_s) {
-                    bf16x8 sp[kW][3], x[kP], y[3];
+                bf16x8 sp[kW][3], x[kP], y[3];
+#pragma unroll
+                for (int w = 0; w < kW; ++w) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) z = fmaf(sv[w][i], blk * 2 + t < a.nblk * 2 ? dv[w][i] : 0.0f, z);
+                    split3(sv[w], sp[w]);
+                }
+#pragma unroll
+                for (int it = 0; it < NI; ++it) {
+                    const int at = tile_at<kNB>(16 * it + m, 4 * t + q);
+#pragma unroll
+                    for (int p = 0; p < kP; ++p) x[p] = read_row(&l.first.go[p * kV + at]);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.dr[p * kV + at]);
 #pragma unroll
                     for (int w = 0; w < kW; ++w) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) z = fmaf(sv[w][i], dv[w][i], z);
-                        split3(sv[w], sp[w]);
+                        aq[w][it] = mfma_planes(sp[w], x, aq[w][it]);
+                        as[w][it] = mfma_planes(sp[w], y, as[w][it]);
                     }
+                    __builtin_amdgcn_sched_barrier(0);  // or reads are brought forward into registers that are not there
+                }
 #pragma unroll
-                    for (int it = 0; it < NI; ++it) {
-                        const int at = tile_at<kNB>(16 * it + m, 4 * t + q);
+                for (int w = 0; w < kW; ++w) split3(dv[w], sp[w]);
+                if (blk * 2 + t + 1 < D / 32) load_state(blk * 2 + t + 1);
 #pragma unroll
-                        for (int p = 0; p < kP; ++p) x[p] = read_row(&l.first.go[p * kV + at]);
+                for (int it = 0; it < NI; ++it) {
+                    const int at = tile_at<kNB>(16 * it + m, 4 * t + q);
 #pragma unroll
-                        for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.dr[p * kV + at]);
+                    for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.u[p * kV + at]);
 #pragma unroll
-                        for (int w = 0; w < kW; ++w) {
-                            aq[w][it] = mfma_planes(sp[w], x, aq[w][it]);
-                            as[w][it] = mfma_planes(sp[w], y, as[w][it]);
-                        }
-                        if (it & 1) __builtin_amdgcn_sched_barrier(0);  // or reads are brought forward into registers that are not there
-                    }
-#pragma unroll
-                    for (int w = 0; w < kW; ++w) split3(dv[w], sp[w]);
-                    if (blk * 2 + t + 1 < a.nblk * 2) load_state(blk * 2 + t + 1);
-#pragma unroll
-                    for (int it = 0; it < NI; ++it) {
-                        const int at = tile_at<kNB>(16 * it + m, 4 * t + q);
-#pragma unroll
-                        for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.u[p * kV + at]);
-#pragma unroll
-                        for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(sp[w], y, ad[w][it]);
-                        if (it & 1) __builtin_amdgcn_sched_barrier(0);
-                    }
+                    for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(sp[w], y, ad[w][it]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
                 for (int n = 0; n < kMine; ++n) {
@@ -338,7 +358,9 @@ __global__ __launch_bounds__(kGradThreads<D>, 2) void grad_kernel(BackArgs a) {
                     bf16x8 y[3];
 #pragma unroll
                     for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.u[p * kV + aj]);
-                    if (unit >= kTiles) {
+                    // (what a unit is is known beforehand but for those in the middle)
+                    const bool erase = n * kWaves >= kTiles || ((n + 1) * kWaves > kTiles && unit >= kTiles);
+                    if (erase) {
                         bf16x8 x[3];
 #pragma unroll
                         for (int p = 0; p < 3; ++p) x[p] = read_row(&l.first.dr[p * kV + ai]);
@@ -349,12 +371,10 @@ __global__ __launch_bounds__(kGradThreads<D>, 2) void grad_kernel(BackArgs a) {
                         for (int p = 0; p < kP; ++p) x[p] = read_row(&l.first.go[p * kV + ai]);
                         pair[n] = mfma_planes(x, y, pair[n]);
                     }
-                    if (n & 1) __builtin_amdgcn_sched_barrier(0);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
             __syncthreads();
-            // (not ahead of the products: another workgroup's hide it, and they need the registers)
-            if (blk + 1 < a.nblk) load_rows(blk + 1);
         }
         z = lanes_sum(z);
         if (lane == 0) l.z[wave] = has_s ? z : 0.0f;
@@ -372,20 +392,13 @@ __global__ __launch_bounds__(kGradThreads<D>, 2) void grad_kernel(BackArgs a) {
 
     // rows of q and k in their place
     {
-        constexpr int kGrp = D / 8, kRowsAt = kThreadsG / kGrp;
-        const int grp = threadIdx.x % kGrp, r0 = threadIdx.x / kGrp;
-        const T *kp = static_cast<const T *>(a.k.p) + b * a.k.st[0] + begin * a.k.st[1] + hk * a.k.st[2];
-        const T *qp = static_cast<const T *>(a.q.p) + b * a.q.st[0] + begin * a.q.st[1] + hk * a.q.st[2];
 #pragma unroll
-        for (int n = 0; n < N / kRowsAt; ++n) {
-            const int row = r0 + n * kRowsAt, at = tile_at<D>(row, grp);
-            bf16x8 x[kP], y[kP];
-            load8<T, VEC>(kp + row * a.k.st[1], grp * 8, a.dk, row < cnt, x);
-            load8<T, VEC>(qp + row * a.q.st[1], grp * 8, a.dk, row < cnt, y);
+        for (int n = 0; n < kMyKeys; ++n) {
+            const int at = tile_at<D>(key_row + n * kKeysAt, key_grp);
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
-                *reinterpret_cast<bf16x8 *>(&l.second.k[p * kX + at]) = x[p];
-                *reinterpret_cast<bf16x8 *>(&l.second.q[p * kX + at]) = y[p];
+                *reinterpret_cast<bf16x8 *>(&l.second.k[p * kX + at]) = key[n][p];
+                *reinterpret_cast<bf16x8 *>(&l.second.q[p * kX + at]) = query[n][p];
             }
         }
         // the tiles above those on the diagonal that are read with them
@@ -702,9 +715,9 @@ hipError_t back_launch(const DeltaArgs &p, char *scratch, hipStream_t s) {
     if (e != hipSuccess) return e;
     const unsigned grid = (unsigned)(pairs * w.spans);
     switch (span_width(p)) {
-        case 64: grad_kernel<T, 64, VEC><<<grid, kGradThreads<64>, 0, s>>>(a); break;
-        case 128: grad_kernel<T, 128, VEC><<<grid, kGradThreads<128>, 0, s>>>(a); break;
-        default: grad_kernel<T, 256, VEC><<<grid, kGradThreads<256>, 0, s>>>(a); break;
+        case 64: grad_kernel<T, 64, VEC><<<grid, kGradThreads<T, 64>, 0, s>>>(a); break;
+        case 128: grad_kernel<T, 128, VEC><<<grid, kGradThreads<T, 128>, 0, s>>>(a); break;
+        default: grad_kernel<T, 256, VEC><<<grid, kGradThreads<T, 256>, 0, s>>>(a); break;
     }
     if (w.parts) {
         const int64_t n = p.B * p.L * p.Hk * p.dk;
