@@ -36,13 +36,9 @@ __device__ __forceinline__ Job job_of(const ForwardArgs &a, const Where &wh, int
     return j;
 }
 
-// Workgroups a CU that the registers are shared out for.
-template <typename T, int D1>
-constexpr int kWgs = D1 > 128 || (sizeof(T) == 4 && D1 > 64) ? 1 : 2;
-
 template <typename T, int D1, bool VEC>
 __global__ __launch_bounds__(walk::kThreads, (kWgs<T, D1>)) void walk_kernel(ForwardArgs a) {
-    __shared__ WalkLds<T, D1> lds;
+    __shared__ WalkLds<T, D1> lds[kStages<T, D1>];
     const Where wh = where(a.nblk * a.seg.n, a.pairs, a.H);
     if (!wh.any) return;
     const int seg = (int)__builtin_amdgcn_readfirstlane(wh.sub / a.nblk), blk = wh.sub - seg * a.nblk;
@@ -62,7 +58,7 @@ __global__ __launch_bounds__(walk::kThreads, (kWgs<T, D1>)) void walk_kernel(For
 // The segments' own parts: blocks of V's columns from zero, then of the identity's.
 template <typename T, int D1, bool VEC>
 __global__ __launch_bounds__(walk::kThreads, (kWgs<T, D1>)) void segment_kernel(ForwardArgs a) {
-    __shared__ WalkLds<T, D1> lds;
+    __shared__ WalkLds<T, D1> lds[kStages<T, D1>];
     const int per = a.nblk + a.nblk_k;
     const Where wh = where(per * (a.seg.n - 1), a.pairs, a.H);
     if (!wh.any) return;

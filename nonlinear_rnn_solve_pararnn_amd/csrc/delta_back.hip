@@ -47,9 +47,6 @@ struct BackArgs {
 // Positions a span of grad_kernel: as many as its operands in LDS allow.
 constexpr int span_of(bool bf16, int D) { return bf16 && D <= 128 ? 64 : 32; }
 
-template <typename T, int D1>
-constexpr int kBackWgs = D1 > 128 || (sizeof(T) == 4 && D1 > 64) ? 1 : 2;
-
 template <typename T>
 __device__ __forceinline__ Job job_of(const BackArgs &a, const Where &wh) {
     Job j{};
@@ -70,8 +67,8 @@ __device__ __forceinline__ Job job_of(const BackArgs &a, const Where &wh) {
 // The two walks: workgroups that take S from the first chunk on, and those
 // that take D from the last one back.
 template <typename T, int D1, bool VEC>
-__global__ __launch_bounds__(walk::kThreads, (kBackWgs<T, D1>)) void back_walk_kernel(BackArgs a) {
-    __shared__ WalkLds<T, D1> lds;
+__global__ __launch_bounds__(walk::kThreads, (kWgs<T, D1>)) void back_walk_kernel(BackArgs a) {
+    __shared__ WalkLds<T, D1> lds[kStages<T, D1>];
     const Where wh = where(a.nblk * 2 * a.seg.n, a.pairs, a.H);
     if (!wh.any) return;
     const int part = (int)__builtin_amdgcn_readfirstlane(wh.sub / a.nblk), blk = wh.sub - part * a.nblk, seg = part >> 1;
@@ -103,8 +100,8 @@ __global__ __launch_bounds__(walk::kThreads, (kBackWgs<T, D1>)) void back_walk_k
 
 // The segments' own parts: of S, of D, and M.
 template <typename T, int D1, bool VEC>
-__global__ __launch_bounds__(walk::kThreads, (kBackWgs<T, D1>)) void back_segment_kernel(BackArgs a) {
-    __shared__ WalkLds<T, D1> lds;
+__global__ __launch_bounds__(walk::kThreads, (kWgs<T, D1>)) void back_segment_kernel(BackArgs a) {
+    __shared__ WalkLds<T, D1> lds[kStages<T, D1>];
     const int per = 2 * a.nblk + a.nblk_k;
     const Where wh = where(per * a.seg.n, a.pairs, a.H);
     if (!wh.any) return;

@@ -80,6 +80,12 @@ struct alignas(16) WalkLds {
     Gates gates;
 };
 
+// Workgroups a CU that a walk's registers are shared out for, and chunks in LDS:
+// two where they fit, so that a chunk's operands arrive while the one before is
+// at work and it has one barrier.
+template <typename T, int D1> constexpr int kWgs = D1 > 128 || (sizeof(T) == 4 && D1 > 64) ? 1 : 2;
+template <typename T, int D1> constexpr int kStages = 2 * kWgs<T, D1> * sizeof(WalkLds<T, D1>) <= 160 * 1024 ? 2 : 1;
+
 // Eight numbers of a lane (a column of its wave's, positions 8 q ..) with the
 // first ones that are not finite, and all after them, taken out.  Returns the
 // first such position of the lane's column, C for none.
@@ -102,7 +108,7 @@ __device__ __forceinline__ int take_odd(float (&v)[8], int q) {
 
 // BACK: records as the backward pass has them; nothing is made of values that are not finite.
 template <typename T, int D1, bool VEC, Role ROLE, bool BACK>
-__device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
+__device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> (&lds)[kStages<T, D1>]) {
     constexpr bool kOut = ROLE == Role::Out, kGrad = ROLE == Role::Grad, kUseQ = kOut || kGrad;
     constexpr int kP = kPlanes<T>, kO = kP == 3 ? 3 : 2;  // planes of operands; of S and U where an output is formed
     constexpr int kMat = kGrad ? 3 : kPP<T>;              // planes of P
@@ -189,10 +195,9 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
         }
     };
 
-    load(0);
-    for (int i = 0; i < n_chunks; ++i) {
-        const int c = chunk_at(i), cnt = positions(c);
-        lds_barrier();  // the last chunk's reads are done
+    // chunk i's operands into LDS, from registers
+    auto put = [&](int i, WalkLds<T, D1> &l) {
+        const int cnt = positions(chunk_at(i));
         ak.store(rk, l.K);
         if (kUseQ) aq.store(rq, l.Q);
         av.store(rv, l.V);
@@ -200,6 +205,17 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
 #pragma unroll
         for (int n = 0; n < kMyMats; ++n)
             if (kMats % 4 == 0 || wave * kMyMats + n < kMats) l.mats[wave * kMyMats + n][lane] = mat_ahead[n];
+        if constexpr (!VEC) {
+            if (cnt < C) {
+                walk::clear_past<kP, D1, C>(l.K, threadIdx.x, cnt);
+                if (kUseQ) walk::clear_past<kP, D1, C>(l.Q, threadIdx.x, cnt);
+                walk::clear_past<kP, kNB, C>(l.V, threadIdx.x, cnt);
+            }
+        }
+    };
+    // what leaves a chunk late, and a span's state before it
+    auto leave = [&](int i) {
+        const int c = chunk_at(i);
         if (i > 0) write(i - 1);
         if (BACK && j.states != nullptr) {
             const int span = (int)j.span_chunks, s = c / span;
@@ -211,16 +227,8 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
                     for (int r = 0; r < 4; ++r) to[state_row(t, q, r) * j.row] = S[t][r];
             }
         }
-        load(i + 1);
-        if constexpr (!VEC) {
-            if (cnt < C) {
-                walk::clear_past<kP, D1, C>(l.K, threadIdx.x, cnt);
-                if (kUseQ) walk::clear_past<kP, D1, C>(l.Q, threadIdx.x, cnt);
-                walk::clear_past<kP, kNB, C>(l.V, threadIdx.x, cnt);
-            }
-        }
-        lds_barrier();
-
+    };
+    auto compute = [&](WalkLds<T, D1> &l) {
         // K S in rows of positions, Q S in rows of columns; operands are read, and
         // S split, a step ahead of the matrix instructions that use them
         struct Step {
@@ -388,6 +396,32 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> &l) {
             for (int it = 0; it < 2; ++it)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) done[it].v[r] = __builtin_bit_cast(Bit, (T)o[it][r]);
+        }
+    };
+    load(0);
+    if constexpr (kStages<T, D1> == 2) {
+        put(0, lds[0]);
+        load(1);
+        lds_barrier();
+        auto step = [&](int i, WalkLds<T, D1> &now, WalkLds<T, D1> &next) {
+            if (i + 1 < n_chunks) put(i + 1, next);
+            leave(i);
+            load(i + 2);
+            compute(now);
+            lds_barrier();
+        };
+        for (int i = 0; i < n_chunks; i += 2) {
+            step(i, lds[0], lds[kStages<T, D1> - 1]);
+            if (i + 1 < n_chunks) step(i + 1, lds[kStages<T, D1> - 1], lds[0]);
+        }
+    } else {
+        for (int i = 0; i < n_chunks; ++i) {
+            lds_barrier();  // the last chunk's reads are done
+            put(i, lds[0]);
+            leave(i);
+            load(i + 1);
+            lds_barrier();
+            compute(lds[0]);
         }
     }
     write(n_chunks - 1);
