@@ -33,9 +33,19 @@ struct Params {
 template <int V>
 __device__ __forceinline__ int column(int lane, int j) { return (lane + kLanes * j) * V; }
 
+// How a launch rotates: not at all, (i, i + R/2), (2i, 2i + 1), or whichever the
+// arguments say (single elements).  Kernels of their own need a third of the
+// registers less.
+enum Turned { kNone, kHalves, kPairs, kAny };
+template <int M>
+__device__ __forceinline__ bool pairs(const HeadnormArgs &a) { return M == kAny ? a.interleaved != 0 : M == kPairs; }
+template <int M>
+__device__ __forceinline__ bool turned(const HeadnormArgs &a, int c) { return M != kNone && c < a.R; }
+
 // Where the rotation's partner of the V elements from c on begins.
+template <int M>
 __device__ __forceinline__ int partner(const HeadnormArgs &a, int c) {
-    if (a.interleaved) return c ^ 1;
+    if (pairs<M>(a)) return c ^ 1;
     return c < a.R / 2 ? c + a.R / 2 : c - a.R / 2;
 }
 
@@ -62,7 +72,7 @@ __device__ __forceinline__ void load_floats(const float *p, float (&f)[V]) {
 // A group's share of the rotation: the cosine and the signed sine of each of
 // its elements (y_c = n_c cos + n_partner sin; back: the angle's opposite), one
 // and zero where there is none.
-template <int V, int NV>
+template <int V, int NV, int M>
 struct Turn {
     float cos[NV][V], sin[NV][V];
 
@@ -74,7 +84,7 @@ struct Turn {
                 cos[j][i] = 1.0f;
                 sin[j][i] = 0.0f;
             }
-        if (a.R == 0) return;
+        if (M == kNone || a.R == 0) return;
         int64_t pos;
         if (a.positions == nullptr) pos = t;
         else pos = a.wide ? static_cast<const int64_t *>(a.positions)[token] : (int64_t) static_cast<const int32_t *>(a.positions)[token];
@@ -85,7 +95,7 @@ struct Turn {
         for (int j = 0; j < NV; ++j) {
             const int c = column<V>(lane, j);
             if (c >= a.R) continue;
-            if (V > 1 && !a.interleaved) {  // all of them on one side
+            if (V > 1 && !pairs<M>(a)) {  // all of them on one side
                 const int k = c >= a.R / 2 ? c - a.R / 2 : c;
                 load_floats<V>(row + k, cos[j]);
                 load_floats<V>(row + a.R / 2 + k, sin[j]);
@@ -93,7 +103,7 @@ struct Turn {
 #pragma unroll
                 for (int i = 0; i < V; ++i)
                     if (c + i < a.R) {
-                        const int k = a.interleaved ? (c + i) >> 1 : c >= a.R / 2 ? c - a.R / 2 : c;
+                        const int k = pairs<M>(a) ? (c + i) >> 1 : c >= a.R / 2 ? c - a.R / 2 : c;
                         cos[j][i] = row[k];
                         sin[j][i] = row[a.R / 2 + k];
                     }
@@ -101,7 +111,7 @@ struct Turn {
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (c + i < a.R) {
-                    const bool second = a.interleaved ? (c + i) & 1 : c >= a.R / 2;
+                    const bool second = pairs<M>(a) ? (c + i) & 1 : c >= a.R / 2;
                     if (second == back) sin[j][i] = -sin[j][i];
                     if (!in) cos[j][i] = sin[j][i] = nan;
                 }
@@ -111,13 +121,14 @@ struct Turn {
 
 // Partners of a row's elements in it (interleaved vectors hold their own; past
 // the rotated ones any finite value does: the elements themselves).
-template <typename T, int V>
+template <typename T, int V, int M>
 __device__ __forceinline__ void load_partner(const HeadnormArgs &a, const T *row, int c, const VecT<T, V> &own, VecT<T, V> &to) {
-    if (V > 1 && a.interleaved) {
+    if (M == kNone) return;
+    if (V > 1 && pairs<M>(a)) {
 #pragma unroll
         for (int i = 0; i < V; ++i) to.v[i] = own.v[i ^ 1];
     } else {
-        to = load_row<T, V>(row + (c < a.R ? partner(a, c) : c));
+        to = load_row<T, V>(row + (c < a.R ? partner<M>(a, c) : c));
     }
 }
 
@@ -144,7 +155,7 @@ __device__ __forceinline__ const T *row_of(const HeadView &v, int64_t b, int64_t
 // Rows of a group that are on their way at once.
 template <int V, int NV> constexpr int kAhead = V > 1 && NV == 1 ? 2 : 1;
 
-template <typename T, int V, int NV>
+template <typename T, int V, int NV, int M>
 __global__ __launch_bounds__(kThreads) void headnorm_fwd_kernel(Params p) {
     constexpr int U = kAhead<V, NV>;
     const HeadnormArgs &a = p.a;
@@ -170,13 +181,13 @@ __global__ __launch_bounds__(kThreads) void headnorm_fwd_kernel(Params p) {
                 const int c = column<V>(lane, j);
                 if (c < a.d) {
                     own[u][j] = load_row<T, V>(row + c);
-                    load_partner<T, V>(a, row, c, own[u][j], other[u][j]);
+                    load_partner<T, V, M>(a, row, c, own[u][j], other[u][j]);
                 }
             }
         }
     };
     // y = r (x (w cos) + x_partner (w_partner sin))
-    Turn<V, NV> turn;
+    Turn<V, NV, M> turn;
     turn.load(a, it.token, t, lane, false);
     if (wp != nullptr) {
 #pragma unroll
@@ -185,11 +196,11 @@ __global__ __launch_bounds__(kThreads) void headnorm_fwd_kernel(Params p) {
             if (c >= a.d) continue;
             float w[V], wo[V];
             load_floats<V>(wp + c, w);
-            if (V > 1 && a.interleaved) {
+            if (V > 1 && pairs<M>(a)) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) wo[i] = w[i ^ 1];
             } else {
-                load_floats<V>(wp + (c < a.R ? partner(a, c) : c), wo);
+                load_floats<V>(wp + (turned<M>(a, c) ? partner<M>(a, c) : c), wo);
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -210,7 +221,7 @@ __global__ __launch_bounds__(kThreads) void headnorm_fwd_kernel(Params p) {
                 for (int i = 0; i < V; ++i) {
                     const bool in = column<V>(lane, j) < a.d;
                     f[u][j][i] = in ? (float)own[u][j].v[i] : 0.0f;
-                    o[u][j][i] = in ? (float)other[u][j].v[i] : 0.0f;
+                    o[u][j][i] = in && M != kNone ? (float)other[u][j].v[i] : 0.0f;
                     sum[u] = fmaf(f[u][j][i], f[u][j][i], sum[u]);
                 }
         }
@@ -229,7 +240,7 @@ __global__ __launch_bounds__(kThreads) void headnorm_fwd_kernel(Params p) {
                     for (int i = 0; i < V; ++i) {
                         // an infinity beside a zero sine is no number of this element's
                         const float n = f[u][j][i] * turn.cos[j][i];
-                        v[i] = r * (c + i < a.R ? fmaf(o[u][j][i], turn.sin[j][i], n) : n);
+                        v[i] = r * (turned<M>(a, c + i) ? fmaf(o[u][j][i], turn.sin[j][i], n) : n);
                     }
                     store_vec<T, V>(y + (int64_t)(h0 + u) * a.d + c, v);
                 }
@@ -238,117 +249,106 @@ __global__ __launch_bounds__(kThreads) void headnorm_fwd_kernel(Params p) {
     }
 }
 
-template <typename T, int V, int NV>
-__global__ __launch_bounds__(kThreads) void headnorm_bwd_kernel(Params p) {
-    constexpr int U = kAhead<V, NV>;
+// A launch's groups are a multiple of a token's parts, so that a group has the
+// same heads of every token it comes to: one weight and one sum of gradients.
+template <typename T, int V, int NV, int M>
+__global__ __launch_bounds__(kThreads, NV * V <= 8 ? 4 : 2) void headnorm_bwd_kernel(Params p) {
+    constexpr int U = 1;
     const HeadnormArgs &a = p.a;
     const int lane = threadIdx.x & (kLanes - 1), grp = threadIdx.x / kLanes;
-    const int64_t items = p.tokens * (p.parts[0] + p.parts[1]);
-    float gw[2][NV][V] = {};
-    for (int64_t n = (int64_t)blockIdx.x * kGroups + grp; n < items; n += (int64_t)gridDim.x * kGroups) {
+    const int64_t items = p.tokens * (p.parts[0] + p.parts[1]), first_item = (int64_t)blockIdx.x * kGroups + grp;
+    const Item mine = item_of(p, first_item);
+    const int which = mine.which;
+    const int64_t H = which ? a.Hk : a.Hq;
+    const float *wp = which ? a.w[1] : a.w[0];
+    const HeadView x = which ? a.x[1] : a.x[0], g = which ? a.g[1] : a.g[0];
+    float w[NV][V], acc[NV][V] = {};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[j][i] = 1.0f;
+        if (wp != nullptr && column<V>(lane, j) < a.d) load_floats<V>(wp + column<V>(lane, j), w[j]);
+    }
+    for (int64_t n = first_item; n < items; n += (int64_t)gridDim.x * kGroups) {
         const Item it = item_of(p, n);
         const int64_t b = (uint32_t)it.token / (uint32_t)a.L, t = it.token - b * a.L;
-        const int64_t H = it.which ? a.Hk : a.Hq;
-        const float *wp = it.which ? a.w[1] : a.w[0];
-        const HeadView x = it.which ? a.x[1] : a.x[0], g = it.which ? a.g[1] : a.g[0];
-        const T *first = row_of<T>(x, b, t, it.head), *gfirst = row_of<T>(g, b, t, it.head);
-        const float *r_in = (it.which ? a.r[1] : a.r[0]) + it.token * H + it.head;
-        T *out = static_cast<T *>(it.which ? a.y[1] : a.y[0]) + (it.token * H + it.head) * a.d;
-        VecT<T, V> own[U][NV], dy[U][NV], other[U][NV];
-        float r_of[U];
-        auto load = [&](int h0) {
+        const T *first = row_of<T>(x, b, t, mine.head), *gfirst = row_of<T>(g, b, t, mine.head);
+        const float *r_in = (which ? a.r[1] : a.r[0]) + it.token * H + mine.head;
+        T *out = static_cast<T *>(which ? a.y[1] : a.y[0]) + (it.token * H + mine.head) * a.d;
+        Turn<V, NV, M> turn;
+        turn.load(a, it.token, t, lane, true);
+#pragma unroll 1
+        for (int h0 = 0; h0 < mine.heads; h0 += U) {
+            VecT<T, V> own[U][NV], dy[U][NV], other[U][NV];
+            float r[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int h = min(h0 + u, it.heads - 1);
+                const int h = min(h0 + u, mine.heads - 1);
                 const T *row = first + h * x.st[2], *grow = gfirst + h * g.st[2];
-                r_of[u] = r_in[h];
+                r[u] = r_in[h];
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
                     const int c = column<V>(lane, j);
                     if (c < a.d) {
                         own[u][j] = load_row<T, V>(row + c);
                         dy[u][j] = load_row<T, V>(grow + c);
-                        load_partner<T, V>(a, grow, c, dy[u][j], other[u][j]);
+                        load_partner<T, V, M>(a, grow, c, dy[u][j], other[u][j]);
                     }
                 }
             }
-        };
-        Turn<V, NV> turn;
-        turn.load(a, it.token, t, lane, true);
-        float w[NV][V], acc[NV][V] = {};
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) w[j][i] = 1.0f;
-            if (wp != nullptr && column<V>(lane, j) < a.d) load_floats<V>(wp + column<V>(lane, j), w[j]);
-        }
-        for (int h0 = 0; h0 < it.heads; h0 += U) {
-            load(h0);
-            float xh[U][NV][V], v[U][NV][V], sum[U], r[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                r[u] = r_of[u];
-                sum[u] = 0.0f;
-                const bool live = h0 + u < it.heads;
+                if (h0 + u >= mine.heads) continue;
+                float xh[NV][V], v[NV][V], sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
                     const int c = column<V>(lane, j);
                     if (c < a.d)
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
-                            xh[u][j][i] = (float)own[u][j].v[i] * r[u];
+                            xh[j][i] = (float)own[u][j].v[i] * r[u];
                             float gn = (float)dy[u][j].v[i] * turn.cos[j][i];
-                            if (c + i < a.R) gn = fmaf((float)other[u][j].v[i], turn.sin[j][i], gn);
-                            if (live) acc[j][i] = fmaf(gn, xh[u][j][i], acc[j][i]);
-                            v[u][j][i] = gn * w[j][i];
-                            sum[u] = fmaf(v[u][j][i], xh[u][j][i], sum[u]);
+                            if (turned<M>(a, c + i)) gn = fmaf((float)other[u][j].v[i], turn.sin[j][i], gn);
+                            acc[j][i] = fmaf(gn, xh[j][i], acc[j][i]);
+                            v[j][i] = gn * w[j][i];
+                            sum = fmaf(v[j][i], xh[j][i], sum);
                         }
                 }
-            }
-    #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float s = lanes16_sum(sum[u]);
-                if (!a.l2) s /= (float)a.d;
-                if (h0 + u >= it.heads) continue;
+                sum = lanes16_sum(sum);
+                if (!a.l2) sum /= (float)a.d;
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
                     const int c = column<V>(lane, j);
                     if (c < a.d) {
 #pragma unroll
-                        for (int i = 0; i < V; ++i) v[u][j][i] = r[u] * (v[u][j][i] - xh[u][j][i] * s);
-                        store_vec<T, V>(out + (int64_t)(h0 + u) * a.d + c, v[u][j]);
+                        for (int i = 0; i < V; ++i) v[j][i] = r[u] * (v[j][i] - xh[j][i] * sum);
+                        store_vec<T, V>(out + (int64_t)(h0 + u) * a.d + c, v[j]);
                     }
                 }
             }
         }
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                gw[0][j][i] += it.which ? 0.0f : acc[j][i];
-                gw[1][j][i] += it.which ? acc[j][i] : 0.0f;
-            }
     }
     if (p.part == nullptr) return;
-    // the groups' sums, in their order
+    // the sums of the groups of either tensor, in their order
     __shared__ float buf[kGroups][kLanes * V];
+    __shared__ int whose[kGroups];
+    if (lane == 0) whose[grp] = which;
     float *part = p.part + (int64_t)blockIdx.x * 2 * a.d;
 #pragma unroll
-    for (int which = 0; which < 2; ++which)
+    for (int j = 0; j < NV; ++j) {
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            __syncthreads();
+        for (int i = 0; i < V; ++i) buf[grp][lane * V + i] = acc[j][i];
+        __syncthreads();
+        for (int k = threadIdx.x; k < 2 * kLanes * V; k += kThreads) {
+            const int of = k >= kLanes * V, at = k - of * kLanes * V, c = kLanes * V * j + at;
+            float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < V; ++i) buf[grp][lane * V + i] = gw[which][j][i];
-            __syncthreads();
-            for (int k = threadIdx.x; k < kLanes * V; k += kThreads) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int m = 0; m < kGroups; ++m) sum += buf[m][k];
-                const int c = kLanes * V * j + k;
-                if (c < a.d) part[which * a.d + c] = sum;
-            }
+            for (int m = 0; m < kGroups; ++m)
+                if (whose[m] == of) sum += buf[m][at];
+            if (c < a.d) part[of * a.d + c] = sum;
         }
+    }
 }
 
 // dw = sum of the G partials, always in the same order: 64 columns a workgroup, 16 threads a column.
@@ -400,14 +400,27 @@ Params params(const HeadnormArgs &a) {
 
 int64_t groups(const Params &p) { return (p.tokens * (p.parts[0] + p.parts[1]) + kGroups - 1) / kGroups; }
 
-// Workgroups of the backward pass, which keep the weights' gradients in registers over all their rows.
-int bwd_grid(const Params &p) { return (int)std::min<int64_t>(groups(p), (int64_t)device_cu_count() * 4); }
+// Workgroups of the backward pass, which keep the weights' gradients in
+// registers over all their rows: a multiple of a token's parts where there are
+// more items than groups.
+int bwd_grid(const Params &p) {
+    const int64_t parts = p.parts[0] + p.parts[1], cap = std::max<int64_t>((int64_t)device_cu_count() * 4, parts);
+    const int64_t n = groups(p);
+    return (int)(n <= cap ? n : cap / parts * parts);
+}
 
-template <typename T, int V, int NV>
+template <typename T, int V, int NV, int M>
 hipError_t launch(const Params &p, bool back, hipStream_t s) {
-    if (back) headnorm_bwd_kernel<T, V, NV><<<bwd_grid(p), kThreads, 0, s>>>(p);
-    else headnorm_fwd_kernel<T, V, NV><<<(unsigned)groups(p), kThreads, 0, s>>>(p);
+    if (back) headnorm_bwd_kernel<T, V, NV, M><<<bwd_grid(p), kThreads, 0, s>>>(p);
+    else headnorm_fwd_kernel<T, V, NV, M><<<(unsigned)groups(p), kThreads, 0, s>>>(p);
     return hipGetLastError();
+}
+
+template <typename T, int NV>
+hipError_t launch_vec(const Params &p, bool back, hipStream_t s) {
+    constexpr int V = kVec<T>;
+    if (p.a.R == 0) return launch<T, V, NV, kNone>(p, back, s);
+    return p.a.interleaved ? launch<T, V, NV, kPairs>(p, back, s) : launch<T, V, NV, kHalves>(p, back, s);
 }
 
 template <typename T>
@@ -415,13 +428,13 @@ hipError_t run(const Params &p, bool back, hipStream_t s) {
     const int d = p.a.d;
     if (rows_vec(p.a, sizeof(T), back)) {
         constexpr int V = kVec<T>;
-        if (d <= kLanes * V) return launch<T, V, 1>(p, back, s);
-        if (d <= kLanes * V * 2) return launch<T, V, 2>(p, back, s);
-        if constexpr (V == 4) return launch<T, V, 4>(p, back, s);
+        if (d <= kLanes * V) return launch_vec<T, 1>(p, back, s);
+        if (d <= kLanes * V * 2) return launch_vec<T, 2>(p, back, s);
+        if constexpr (V == 4) return launch_vec<T, 4>(p, back, s);
     }
-    if (d <= kLanes * 4) return launch<T, 1, 4>(p, back, s);
-    if (d <= kLanes * 8) return launch<T, 1, 8>(p, back, s);
-    return launch<T, 1, 16>(p, back, s);
+    if (d <= kLanes * 4) return launch<T, 1, 4, kAny>(p, back, s);
+    if (d <= kLanes * 8) return launch<T, 1, 8, kAny>(p, back, s);
+    return launch<T, 1, 16, kAny>(p, back, s);
 }
 
 }  // namespace
