@@ -1,8 +1,9 @@
 """A small recurrent language model on the framework's kernels: embedding, then
-blocks of [layer norm, ParaGRU, residual] and [layer norm, linear attention,
-residual], a last norm and tied output weights.
+blocks of [layer norm, ParaGRU, residual] and [layer norm, a mixer with a matrix
+state, residual], a last norm and tied output weights.  The mixer is linear
+attention or the gated delta rule.
 
-    python examples/recurrent_lm.py
+    python examples/recurrent_lm.py [--mixer delta]
 
 trains it for some steps on synthetic text (a fixed random walk over tokens,
 which the model can learn) and decodes a continuation: the prompt in one
@@ -23,11 +24,12 @@ from nonlinear_rnn_solve_pararnn_amd import api, layers, sequence  # noqa: E402
 
 
 class Block(torch.nn.Module):
-    def __init__(self, dim, heads, device):
+    def __init__(self, dim, heads, device, mixer="linear"):
         super().__init__()
         self.norm1, self.norm2 = (sequence.LayerNorm(dim, device=device) for _ in range(2))
         self.gru = layers.ParaGRU(dim, dim, device=device)
-        self.attention = sequence.LinearAttention(dim, heads, dim // heads, device=device)
+        kind = {"linear": sequence.LinearAttention, "delta": sequence.GatedDelta}[mixer]
+        self.attention = kind(dim, heads, dim // heads, device=device)
 
     def forward(self, x, residual, state=None):
         """x is what the sublayer before computed, residual the stream it joins; returns the same pair and the states."""
@@ -52,10 +54,10 @@ class Block(torch.nn.Module):
 
 
 class RecurrentLM(torch.nn.Module):
-    def __init__(self, vocab, dim=256, depth=2, heads=4, device="cuda"):
+    def __init__(self, vocab, dim=256, depth=2, heads=4, device="cuda", mixer="linear"):
         super().__init__()
         self.embedding = sequence.Embedding(vocab, dim, scale=dim ** 0.5, device=device)
-        self.blocks = torch.nn.ModuleList(Block(dim, heads, device) for _ in range(depth))
+        self.blocks = torch.nn.ModuleList(Block(dim, heads, device, mixer) for _ in range(depth))
         self.norm = sequence.LayerNorm(dim, device=device)
 
     def forward(self, ids, states=None):
@@ -126,9 +128,10 @@ def main():
     ap.add_argument("--steps", type=int, default=60)
     ap.add_argument("--batch", type=int, default=16)
     ap.add_argument("--length", type=int, default=512)
+    ap.add_argument("--mixer", choices=("linear", "delta"), default="linear")
     a = ap.parse_args()
     torch.manual_seed(0)
-    model = RecurrentLM(a.vocab, a.dim)
+    model = RecurrentLM(a.vocab, a.dim, mixer=a.mixer)
     train(model, a.vocab, a.steps, a.batch, a.length,
           report=lambda i, x: print("step %d loss %.3f" % (i, float(x)), flush=True) if i % 10 == 0 or i == a.steps - 1 else None)
     prompt = text(2, 64, a.vocab, torch.Generator(device="cuda").manual_seed(9), "cuda")

@@ -1016,45 +1016,53 @@ def delta_step(q, k, v, log_decay, beta, state, *, scale=None, out=None, out_sta
 NORM_KINDS = {"rms": 0, "l2": 1}   # PARARNN_NORM_RMS, PARARNN_NORM_L2
 
 
-def _headnorm_check(q, k, weights, table, positions, kind):
+def _headnorm_check(q, k, q_weight, k_weight, table, positions, kind):
     """(type code, leading shape, B, L, Hq, Hk, d, R, P, bytes of a position); k may be None."""
     code = _type_code(q, "q")
-    if q.dim() not in (3, 4) or (k is not None and (not isinstance(k, torch.Tensor) or k.dim() != q.dim())):
+    shape = q.shape
+    if len(shape) not in (3, 4) or (k is not None and (not isinstance(k, torch.Tensor) or k.dim() != len(shape))):
         raise ValueError("q and k must be [B, L, heads, d] or [B, heads, d]")
-    if q.numel() == 0 or (k is not None and k.numel() == 0):
+    if 0 in shape or (k is not None and 0 in k.shape):
         raise PararnnError("q or k is empty")
     if kind not in NORM_KINDS:
         raise ValueError("kind must be 'rms' or 'l2', got %r" % (kind,))
-    lead, d = q.shape[:-2], q.shape[-1]
+    lead, Hq, d = shape[:-2], shape[-2], shape[-1]
     if d > MAX_HEAD_DIM:
         raise PararnnError("headnorm supports head sizes up to %d, got %d" % (MAX_HEAD_DIM, d))
     if d < 2:
         raise PararnnError("a head of one element has no norm")
-    Hq, Hk = q.shape[-2], 0 if k is None else k.shape[-2]
+    Hk = 0 if k is None else k.shape[-2]
     B, L = lead if len(lead) == 2 else (lead[0], 1)
-    for w, name in zip(weights, ("q_weight", "k_weight")):
-        if w is not None:
-            _need_typed(w, (d,), torch.float32, name, q.device)
+    dev = q.device
+    if q_weight is not None:
+        _need_typed(q_weight, (d,), torch.float32, "q_weight", dev)
+    if k_weight is not None:
+        if k is None:
+            raise ValueError("k_weight is given without k")
+        _need_typed(k_weight, (d,), torch.float32, "k_weight", dev)
     P = R = nb = 0
     if table is not None:
-        if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.numel() == 0:
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
             raise ValueError("table must be a [positions, R] tensor")
         P, R = table.shape
-        if R % 2 or R > d:
-            raise ValueError("table must have an even number of columns of at most %d, got %d" % (d, R))
-        _need_typed(table, (P, R), torch.float32, "table", q.device)
-        if positions is None:
-            if len(lead) == 1:
-                raise ValueError("positions must be given where there is no dimension of positions")
-            if L > P:
-                raise ValueError("table has %d positions, the sequence %d" % (P, L))
-        else:
-            nb = _ids(positions, q.device, "positions")[1]
+        if R % 2 or R > d or R == 0 or P == 0:
+            raise ValueError("table must have rows, and an even number of columns of at most %d, got %s" % (d, (P, R)))
+        _need_typed(table, (P, R), torch.float32, "table", dev)
+        if positions is not None:
+            nb = _ids(positions, dev, "positions")[1]
             if positions.shape != lead:
                 raise ValueError("positions has shape %s, expected %s" % (tuple(positions.shape), tuple(lead)))
+        elif len(lead) == 1:
+            raise ValueError("positions must be given where there is no dimension of positions")
+        elif L > P:
+            raise ValueError("table has %d positions, the sequence %d" % (P, L))
     elif positions is not None:
         raise ValueError("positions are given without a table")
     return code, lead, B, L, Hq, Hk, d, R, P, nb
+
+
+def _dense_like(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def headnorm_forward(q, k=None, q_weight=None, k_weight=None, table=None, positions=None, *, kind="rms", eps=1e-6,
@@ -1071,27 +1079,27 @@ def headnorm_forward(q, k=None, q_weight=None, k_weight=None, table=None, positi
     position outside the table turns the rotated elements to NaN.  Returns
     (yq, yk, rq, rk), r fp32 being what headnorm_backward takes."""
     lib = load_library()
-    code, lead, B, L, Hq, Hk, d, R, P, nb = _headnorm_check(q, k, (q_weight, k_weight), table, positions, kind)
+    code, lead, B, L, Hq, Hk, d, R, P, nb = _headnorm_check(q, k, q_weight, k_weight, table, positions, kind)
     dev, T = q.device, q.dtype
-    ops = [(q, "q", q.shape, T)]
-    if k is not None:
-        ops.append((k, "k", (*lead, Hk, d), T))
-    st = _views(ops, len(lead), dev)
-    if st is not None and k is None:
-        st = (ctypes.c_int64 * 6)(*st, 0, 0, 0)
+    if k is None:
+        if out_k is not None:
+            raise ValueError("out_k is given without k")
+        st = _views(((q, "q", q.shape, T),), len(lead), dev)
+        if st is not None:
+            st = (ctypes.c_int64 * 6)(*st, 0, 0, 0)
+        rk = None
+    else:
+        st = _views(((q, "q", q.shape, T), (k, "k", (*lead, Hk, d), T)), len(lead), dev)
+        rk = torch.empty((*lead, Hk), dtype=torch.float32, device=dev)
+        if out_k is None:
+            out_k = _dense_like(k)
+        else:
+            _need_typed(out_k, k.shape, T, "out_k", dev)
+    rq = torch.empty((*lead, Hq), dtype=torch.float32, device=dev)
     if out_q is None:
-        out_q = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out_q = _dense_like(q)
     else:
         _need_typed(out_q, q.shape, T, "out_q", dev)
-    if k is None:
-        if out_k is not None or k_weight is not None:
-            raise ValueError("out_k or k_weight is given without k")
-    elif out_k is None:
-        out_k = torch.empty_like(k, memory_format=torch.contiguous_format)
-    else:
-        _need_typed(out_k, k.shape, T, "out_k", dev)
-    rq = torch.empty((*lead, Hq), dtype=torch.float32, device=dev)
-    rk = None if k is None else torch.empty((*lead, Hk), dtype=torch.float32, device=dev)
     _check(lib.pararnn_headnorm_forward(code, B, L, Hq, Hk, d, _at(q), _at(k), st, _at(q_weight), _at(k_weight),
                                         _at(table), P, R, _at(positions), nb, NORM_KINDS[kind], interleaved, eps,
                                         _at(out_q), _at(out_k), _at(rq), _at(rk), _raw_stream(dev)),
@@ -1105,25 +1113,26 @@ def headnorm_backward(q, k, rq, rk, grad_q, grad_k=None, q_weight=None, k_weight
     are its results.  Returns (dq, dk, dq_weight, dk_weight); the weights' are
     None unless want_w (default: where a weight is given)."""
     lib = load_library()
-    code, lead, B, L, Hq, Hk, d, R, P, nb = _headnorm_check(q, k, (q_weight, k_weight), table, positions, kind)
+    code, lead, B, L, Hq, Hk, d, R, P, nb = _headnorm_check(q, k, q_weight, k_weight, table, positions, kind)
     dev, T = q.device, q.dtype
-    ops = [(q, "q", q.shape, T)]
     _need_typed(rq, (*lead, Hq), torch.float32, "rq", dev)
-    if k is not None:
-        ops += [(k, "k", (*lead, Hk, d), T), (grad_q, "grad_q", q.shape, T), (grad_k, "grad_k", (*lead, Hk, d), T)]
-        _need_typed(rk, (*lead, Hk), torch.float32, "rk", dev)
+    gwk = dk = None
+    if k is None:
+        if grad_k is not None or rk is not None:
+            raise ValueError("grad_k or rk is given without k")
+        st = _views(((q, "q", q.shape, T), (grad_q, "grad_q", q.shape, T)), len(lead), dev)
+        if st is not None:
+            st = (ctypes.c_int64 * 12)(*st[:3], 0, 0, 0, *st[3:], 0, 0, 0)
     else:
-        if grad_k is not None or rk is not None or k_weight is not None:
-            raise ValueError("grad_k, rk or k_weight is given without k")
-        ops.append((grad_q, "grad_q", q.shape, T))
-    st = _views(ops, len(lead), dev)
-    if st is not None and k is None:
-        st = (ctypes.c_int64 * 12)(*st[:3], 0, 0, 0, *st[3:], 0, 0, 0)
-    dq = torch.empty_like(q, memory_format=torch.contiguous_format)
-    dk = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
-    want = [w is not None if want_w is None else want_w for w in (q_weight, k_weight)]
-    gwq, gwk = (torch.empty(d, dtype=torch.float32, device=dev) if w and t is not None else None
-                for w, t in zip(want, (q, k)))
+        kshape = (*lead, Hk, d)
+        st = _views(((q, "q", q.shape, T), (k, "k", kshape, T), (grad_q, "grad_q", q.shape, T), (grad_k, "grad_k", kshape, T)),
+                    len(lead), dev)
+        _need_typed(rk, (*lead, Hk), torch.float32, "rk", dev)
+        dk = _dense_like(k)
+        if k_weight is not None if want_w is None else want_w:
+            gwk = torch.empty(d, dtype=torch.float32, device=dev)
+    dq = _dense_like(q)
+    gwq = torch.empty(d, dtype=torch.float32, device=dev) if (q_weight is not None if want_w is None else want_w) else None
     buf, n = (None, 0)
     if gwq is not None or gwk is not None:
         buf, n = _workspace_of(_headnorm_ws(B, L, Hq, Hk, d), dev, ws, True)
