@@ -150,14 +150,18 @@ struct GradLds {
         Second second;
     };
     double G[kN];
-    float f[kN], r[kN], b[kN];
+    float f[kN], r[kN];
     float y[kWaves][kN], x[kWaves][kN], z[kWaves];  // the waves' shares of a row's products with S and with D, and of <D, S>
     float row[2][kN / 16][kN], col[2][kN / 16][kN]; // sums of pairs of either kind: of a row in a tile of columns, of a column in one of rows
 };
 
-// A wave has kW tiles of 16 elements of q and k, so that rows read from LDS serve
-// both, and a workgroup leaves room for another one on its CU, whose loads go on
-// while this one multiplies.
+// A wave has kW tiles of 16 elements of q and k.  With two, rows read from LDS
+// serve both, and a workgroup leaves room for another one on its CU, whose loads
+// go on while this one multiplies.  With one (bf16, and fp32 up to heads of 64:
+// two would spill) a workgroup goes through several spans and has the next one's
+// first operands on their way while it works on the pairs.  B=8, L=2048, H=16,
+// 128x128, bf16: the whole backward pass 740 us with a workgroup a span, 710 so.
+template <typename T, int D> constexpr bool kAhead = grad_tiles(sizeof(T) == 2, D) == 1;
 template <typename T, int D> constexpr int kGradThreads = D * 4 / grad_tiles(sizeof(T) == 2, D);
 template <typename T, int D, bool VEC>
 __global__ __launch_bounds__((kGradThreads<T, D>), 2) void grad_kernel(BackArgs a) {
@@ -165,426 +169,517 @@ __global__ __launch_bounds__((kGradThreads<T, D>), 2) void grad_kernel(BackArgs 
     constexpr int N = Lds::kN, kP = Lds::kP, kM = Lds::kM, kWaves = Lds::kWaves, kW = Lds::kW, kThreadsG = kGradThreads<T, D>;
     constexpr int kX = Lds::kRowsX, kV = Lds::kRowsV, kMx = Lds::kRowsM, NI = N / 16, NS = N / 32, kTiles = NI * (NI + 1) / 2;
     __shared__ Lds l;
-    // (the divisions run on the vector unit; addresses want scalar registers)
-    const uint32_t bh = same_in_lanes(blockIdx.x / (uint32_t)a.spans), span = blockIdx.x - bh * (uint32_t)a.spans;
-    const uint32_t b = same_in_lanes(bh / (uint32_t)a.H), h = bh - b * (uint32_t)a.H, hk = same_in_lanes(h / (uint32_t)a.group);
-    const int64_t begin = (int64_t)span * N;
-    const int cnt = (int)min((int64_t)N, a.L - begin);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
-    const int tr_i = m >> 2, tr_c = m & 3;
+    struct Item {
+        uint32_t bh, span, b, h, hk;
+        int64_t begin;
+        int cnt;
+    };
+    auto item_of = [&](uint32_t i) {  // (the divisions run on the vector unit; addresses want scalar registers)
+        Item w;
+        w.bh = same_in_lanes(i / (uint32_t)a.spans);
+        w.span = i - w.bh * (uint32_t)a.spans;
+        w.b = same_in_lanes(w.bh / (uint32_t)a.H);
+        w.h = w.bh - w.b * (uint32_t)a.H;
+        w.hk = same_in_lanes(w.h / (uint32_t)a.group);
+        w.begin = (int64_t)w.span * N;
+        w.cnt = (int)min((int64_t)N, a.L - w.begin);
+        return w;
+    };
+    auto after = [&](Item w) {
+        w.begin += N;
+        if (++w.span == (uint32_t)a.spans) {
+            w.span = 0;
+            w.begin = 0;
+            ++w.bh;
+            if (++w.h == (uint32_t)a.H) {
+                w.h = 0;
+                ++w.b;
+            }
+            w.hk = same_in_lanes(w.h / (uint32_t)a.group);
+        }
+        w.cnt = (int)min((int64_t)N, a.L - w.begin);
+        return w;
+    };
     const int wide = a.nblk * kNB;  // columns in memory
+    constexpr int kKeysAt = kThreadsG / (D / 8), kMyKeys = N / kKeysAt;
+    int wave, lane, m, q, tr_i, tr_c, key_grp, key_row, grp, r0, tid;
+    bool has_s;
+    uint32_t lane_at;
+    // Where this thread stands, worked out again for each span: kept over the loop, the
+    // addresses made of it would take the registers that operands are ahead in.
+    auto stand = [&]() {
+        tid = threadIdx.x;
+        if (kAhead<T, D>) asm volatile("" : "+v"(tid));
+        wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        lane = tid & 63;
+        m = lane & 15;
+        q = lane >> 4;
+        tr_i = m >> 2;
+        tr_c = m & 3;
+        key_grp = tid % (D / 8);
+        key_row = tid / (D / 8);
+        grp = tid & 7;
+        r0 = tid >> 3;
+        has_s = wave * kW * 16 < a.width;  // narrower keys have no rows there: the first ones stand in, for elements that nothing reads
+        lane_at = (uint32_t)(m * wide + 8 * q);
+    };
 
     // Rows of do, U and dr go through LDS 64 columns at a time, dv and db on the
     // way; products with S and D: lane m is position 16 it + m, registers are
     // elements 16 (kW wave + w) + 4 q ..; raw do_i.u_j and dr_i.u_j: tiles on and below the
     // diagonal go round the waves, a result's rows are i.
-    constexpr int kKeysAt = kThreadsG / (D / 8), kMyKeys = N / kKeysAt;
-    const int key_grp = threadIdx.x % (D / 8), key_row = threadIdx.x / (D / 8);
     bf16x8 key[kMyKeys][kP], query[kMyKeys][kP];
-    auto load_keys = [&]() {
-        const T *kp = static_cast<const T *>(a.k.p) + b * a.k.st[0] + begin * a.k.st[1] + hk * a.k.st[2];
-        const T *qp = static_cast<const T *>(a.q.p) + b * a.q.st[0] + begin * a.q.st[1] + hk * a.q.st[2];
+    auto load_keys = [&](const Item &of) {
+        const T *kp = static_cast<const T *>(a.k.p) + of.b * a.k.st[0] + of.begin * a.k.st[1] + of.hk * a.k.st[2];
+        const T *qp = static_cast<const T *>(a.q.p) + of.b * a.q.st[0] + of.begin * a.q.st[1] + of.hk * a.q.st[2];
 #pragma unroll
         for (int n = 0; n < kMyKeys; ++n) {
             const int row = key_row + n * kKeysAt;
-            load8<T, VEC>(kp + row * a.k.st[1], key_grp * 8, a.dk, row < cnt, key[n]);
-            load8<T, VEC>(qp + row * a.q.st[1], key_grp * 8, a.dk, row < cnt, query[n]);
+            load8<T, VEC>(kp + row * a.k.st[1], key_grp * 8, a.dk, row < of.cnt, key[n]);
+            load8<T, VEC>(qp + row * a.q.st[1], key_grp * 8, a.dk, row < of.cnt, query[n]);
         }
     };
     constexpr int kRowsAt = kThreadsG / 8, kMyRows = (N + kRowsAt - 1) / kRowsAt;
     constexpr int kUnits = 2 * kTiles, kMine = (kUnits + kWaves - 1) / kWaves;
-    f32x4 aq[kW][NI] = {}, as[kW][NI] = {}, ad[kW][NI] = {}, pair[kMine] = {};
     auto unit_of = [&](int n) { return min(wave + n * kWaves, kUnits - 1); };
     auto tile_of = [&](int unit, int &it, int &jt) {
         const int tile = unit >= kTiles ? unit - kTiles : unit;
         it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
         jt = tile - it * (it + 1) / 2;
     };
-    {
-        const int grp = threadIdx.x & 7, r0 = threadIdx.x >> 3;
-        const T *gop = static_cast<const T *>(a.grad_o.p) + b * a.grad_o.st[0] + begin * a.grad_o.st[1] + h * a.grad_o.st[2];
-        const int64_t base = ((int64_t)bh * a.spans + span) * N * wide;
+    bf16x8 go[kMyRows][kP];
+    float u[kMyRows][8], d[kMyRows][8], beta[kMyRows];
+    auto load_rows = [&](const Item &of, int blk) {
+        const T *gop = static_cast<const T *>(a.grad_o.p) + of.b * a.grad_o.st[0] + of.begin * a.grad_o.st[1] + of.h * a.grad_o.st[2];
+        const float *bp = static_cast<const float *>(a.beta.p) + of.b * a.beta.st[0] + of.begin * a.beta.st[1] + of.h * a.beta.st[2];
+        const int64_t base = ((int64_t)of.bh * a.spans + of.span) * N * wide;
         const float *u_rows = a.U + base, *r_rows = a.dR + base;
-        bf16x8 go[kMyRows][kP];
-        float u[kMyRows][8], d[kMyRows][8], dot[kMyRows] = {}, z = 0.0f;
-        auto load_rows = [&](int blk) {
-#pragma unroll
-            for (int n = 0; n < kMyRows; ++n) {
-                const int row = r0 + n * kRowsAt, c = blk * kNB + grp * 8;
-                const bool in = row < cnt && c < wide;
-                load8<T, VEC>(gop + row * a.grad_o.st[1], c, a.dv, in, go[n]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[n][i] = d[n][i] = 0.0f;
-                if (in) {
-                    const uint32_t at = (uint32_t)(row * wide + c);
-#pragma unroll
-                    for (int i = 0; i < 8; i += 4) {
-                        *reinterpret_cast<f32x4 *>(&u[n][i]) = *reinterpret_cast<const f32x4 *>(u_rows + at + i);
-                        *reinterpret_cast<f32x4 *>(&d[n][i]) = *reinterpret_cast<const f32x4 *>(r_rows + at + i);
-                    }
-                }
-            }
-        };
-        const bool has_s = wave * kW * 16 < a.width;  // narrower keys have no rows there: the first ones stand in, for elements that nothing reads
-        const int64_t state = (((int64_t)bh * a.spans + span) * a.width + (has_s ? wave * kW * 16 : 0)) * wide;
-        const float *s_rows = a.S + state, *d_rows = a.D + state;
-        const uint32_t lane_at = (uint32_t)(m * wide + 8 * q);
-        float sv[kW][8], dv[kW][8];
-        auto load_state = [&](int t) {
-#pragma unroll
-            for (int w = 0; w < kW; ++w)
-#pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    const uint32_t at = lane_at + (uint32_t)(16 * w * wide + min(32 * t, wide - 32) + i);
-                    *reinterpret_cast<f32x4 *>(&sv[w][i]) = *reinterpret_cast<const f32x4 *>(s_rows + at);
-                    *reinterpret_cast<f32x4 *>(&dv[w][i]) = *reinterpret_cast<const f32x4 *>(d_rows + at);
-                }
-        };
-        load_rows(0);
-        load_state(0);
-        if (threadIdx.x < N) {
-            const int p = threadIdx.x;
-            auto gate = [&](const HeadView &v) { return static_cast<const float *>(v.p)[b * v.st[0] + (begin + p) * v.st[1] + h * v.st[2]]; };
-            float g = p < cnt ? gate(a.log_decay) : 0.0f;
-            const float beta = p < cnt ? gate(a.beta) : 0.0f;
-            if (g < -1e5f) g = -1e5f;
-            double sum = (double)g * 1.4426950408889634;
-#pragma unroll
-            for (int d = 1; d < N; d *= 2) {
-                const double up = __shfl_up(sum, d, N);
-                if (p >= d) sum += up;
-            }
-            const double whole = __shfl(sum, N - 1, N);
-            l.G[p] = sum;
-            l.f[p] = fast_exp2((float)sum);
-            l.r[p] = fast_exp2((float)(whole - sum));
-            l.b[p] = beta;
-        }
-        __syncthreads();
-        // (blocks that dv does not reach are zeros: a loop of any other number moves all sums between registers)
-#pragma unroll
-        for (int blk = 0; blk < D / kNB; ++blk) {
-#pragma unroll
-            for (int n = 0; n < kMyRows; ++n) {
-                const int row = r0 + n * kRowsAt, at = tile_at<kNB>(row, grp), c = blk * kNB + grp * 8;
-                if (N < kRowsAt && row >= N) continue;  // (whole waves)
-                const float beta = l.b[row];
-                const bool tiny = fabsf(beta) < kTinyBeta;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dot[n] = fmaf(u[n][i], d[n][i], dot[n]);
-                    d[n][i] = tiny ? 0.0f : beta * d[n][i];
-                }
-                if (row < cnt) {
-                    T *gv = static_cast<T *>(a.grad_v) + (((int64_t)b * a.L + begin) * a.H + h) * a.dv + (int64_t)row * a.H * a.dv + c;
-                    if (a.out8) {
-                        constexpr int kVec8 = kVec<T>;
-                        if (c < a.dv) {
-#pragma unroll
-                            for (int o = 0; o < 8; o += kVec8) {
-                                float w[kVec8];
-#pragma unroll
-                                for (int i = 0; i < kVec8; ++i) w[i] = d[n][o + i];
-                                store_vec<T, kVec8>(gv + o, w);
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (c + i < a.dv) gv[i] = (T)d[n][i];
-                    }
-                }
-                bf16x8 p3[3];
-                split3(u[n], p3);
-#pragma unroll
-                for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8 *>(&l.first.u[p * kV + at]) = p3[p];
-                split3(d[n], p3);
-#pragma unroll
-                for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8 *>(&l.first.dr[p * kV + at]) = p3[p];
-#pragma unroll
-                for (int p = 0; p < kP; ++p) *reinterpret_cast<bf16x8 *>(&l.first.go[p * kV + at]) = go[n][p];
-            }
-            // the next rows, ahead of the products
-            auto load_next = [&]() {
-                if (blk + 1 < D / kNB) load_rows(blk + 1);
-                else load_keys();
-            };
-            load_next();
-            __syncthreads();
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                bf16x8 sp[kW][3], x[kP], y[3];
-#pragma unroll
-                for (int w = 0; w < kW; ++w) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) z = fmaf(sv[w][i], blk * 2 + t < a.nblk * 2 ? dv[w][i] : 0.0f, z);
-                    split3(sv[w], sp[w]);
-                }
-#pragma unroll
-                for (int it = 0; it < NI; ++it) {
-                    const int at = tile_at<kNB>(16 * it + m, 4 * t + q);
-#pragma unroll
-                    for (int p = 0; p < kP; ++p) x[p] = read_row(&l.first.go[p * kV + at]);
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.dr[p * kV + at]);
-#pragma unroll
-                    for (int w = 0; w < kW; ++w) {
-                        aq[w][it] = mfma_planes(sp[w], x, aq[w][it]);
-                        as[w][it] = mfma_planes(sp[w], y, as[w][it]);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);  // or reads are brought forward into registers that are not there
-                }
-#pragma unroll
-                for (int w = 0; w < kW; ++w) split3(dv[w], sp[w]);
-                if (blk * 2 + t + 1 < D / 32) load_state(blk * 2 + t + 1);
-#pragma unroll
-                for (int it = 0; it < NI; ++it) {
-                    const int at = tile_at<kNB>(16 * it + m, 4 * t + q);
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.u[p * kV + at]);
-#pragma unroll
-                    for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(sp[w], y, ad[w][it]);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-#pragma unroll
-                for (int n = 0; n < kMine; ++n) {
-                    const int unit = unit_of(n);
-                    int it, jt;
-                    tile_of(unit, it, jt);
-                    const int ai = tile_at<kNB>(16 * it + m, 4 * t + q), aj = tile_at<kNB>(16 * jt + m, 4 * t + q);
-                    bf16x8 y[3];
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.u[p * kV + aj]);
-                    // (what a unit is is known beforehand but for those in the middle)
-                    const bool erase = n * kWaves >= kTiles || ((n + 1) * kWaves > kTiles && unit >= kTiles);
-                    if (erase) {
-                        bf16x8 x[3];
-#pragma unroll
-                        for (int p = 0; p < 3; ++p) x[p] = read_row(&l.first.dr[p * kV + ai]);
-                        pair[n] = mfma_planes(x, y, pair[n]);
-                    } else {
-                        bf16x8 x[kP];
-#pragma unroll
-                        for (int p = 0; p < kP; ++p) x[p] = read_row(&l.first.go[p * kV + ai]);
-                        pair[n] = mfma_planes(x, y, pair[n]);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            }
-            __syncthreads();
-        }
-        z = lanes_sum(z);
-        if (lane == 0) l.z[wave] = has_s ? z : 0.0f;
 #pragma unroll
         for (int n = 0; n < kMyRows; ++n) {
-            const int row = r0 + n * kRowsAt;
+            const int row = r0 + n * kRowsAt, c = blk * kNB + grp * 8;
+            const bool in = row < of.cnt && c < wide;
+            load8<T, VEC>(gop + row * a.grad_o.st[1], c, a.dv, in, go[n]);
 #pragma unroll
-            for (int s = 1; s < 8; s *= 2) dot[n] += __shfl_xor(dot[n], s, 8);
-            if (grp == 0 && row < cnt && a.grad_b != nullptr) {
-                const float beta = l.b[row];
-                a.grad_b[((int64_t)b * a.L + begin + row) * a.H + h] = dot[n] / (fabsf(beta) < kTinyBeta ? kTinyBeta : beta);
+            for (int i = 0; i < 8; ++i) u[n][i] = d[n][i] = 0.0f;
+            if (blk == 0) beta[n] = row < of.cnt ? bp[row * a.beta.st[1]] : 0.0f;
+            if (in) {
+                const uint32_t at = (uint32_t)(row * wide + c);
+#pragma unroll
+                for (int i = 0; i < 8; i += 4) {
+                    *reinterpret_cast<f32x4 *>(&u[n][i]) = *reinterpret_cast<const f32x4 *>(u_rows + at + i);
+                    *reinterpret_cast<f32x4 *>(&d[n][i]) = *reinterpret_cast<const f32x4 *>(r_rows + at + i);
+                }
             }
         }
-    }
+    };
+    float sv[kW][8], dv[kW][8];
+    auto load_state = [&](const Item &of, int t) {
+        const int64_t state = (((int64_t)of.bh * a.spans + of.span) * a.width + (has_s ? wave * kW * 16 : 0)) * wide;
+        const float *s_rows = a.S + state, *d_rows = a.D + state;
+#pragma unroll
+        for (int w = 0; w < kW; ++w)
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+                const uint32_t at = lane_at + (uint32_t)(16 * w * wide + min(32 * t, wide - 32) + i);
+                *reinterpret_cast<f32x4 *>(&sv[w][i]) = *reinterpret_cast<const f32x4 *>(s_rows + at);
+                *reinterpret_cast<f32x4 *>(&dv[w][i]) = *reinterpret_cast<const f32x4 *>(d_rows + at);
+            }
+    };
+    float gate = 0.0f;  // of this thread's position
+    auto load_gate = [&](const Item &of) {
+        const int p = tid;
+        if (p < N) gate = p < of.cnt ? static_cast<const float *>(a.log_decay.p)[of.b * a.log_decay.st[0] + (of.begin + p) * a.log_decay.st[1] + of.h * a.log_decay.st[2]] : 0.0f;
+    };
 
-    // rows of q and k in their place
-    {
+    // (a workgroup's spans follow each other)
+    uint32_t left = 1, first = blockIdx.x;
+    if (kAhead<T, D>) {
+        const uint32_t items = (uint32_t)a.pairs * (uint32_t)a.spans;
+        const uint32_t each = items / gridDim.x, over = items - each * gridDim.x;
+        left = each + (blockIdx.x < over ? 1 : 0);
+        first = blockIdx.x * each + min(blockIdx.x, over);
+    }
+    stand();
+    Item w = item_of(first);
+    load_rows(w, 0);
+    load_state(w, 0);
+    load_gate(w);
+    for (;;) {
+        if (kAhead<T, D>) stand();
+        const uint32_t b = w.b, h = w.h;
+        const int64_t begin = w.begin;
+        const int cnt = w.cnt;
+        f32x4 aq[kW][NI] = {}, as[kW][NI] = {}, ad[kW][NI] = {}, pair[kMine] = {};
+        {
+            float dot[kMyRows] = {}, z = 0.0f, b_of[kMyRows];
 #pragma unroll
-        for (int n = 0; n < kMyKeys; ++n) {
-            const int at = tile_at<D>(key_row + n * kKeysAt, key_grp);
+            for (int n = 0; n < kMyRows; ++n) b_of[n] = beta[n];
+            // (blocks that dv does not reach are zeros: a loop of any other number moves all sums between registers)
 #pragma unroll
-            for (int p = 0; p < kP; ++p) {
-                *reinterpret_cast<bf16x8 *>(&l.second.k[p * kX + at]) = key[n][p];
-                *reinterpret_cast<bf16x8 *>(&l.second.q[p * kX + at]) = query[n][p];
+            for (int blk = 0; blk < D / kNB; ++blk) {
+#pragma unroll
+                for (int n = 0; n < kMyRows; ++n) {
+                    const int row = r0 + n * kRowsAt, at = tile_at<kNB>(row, grp), c = blk * kNB + grp * 8;
+                    if (N < kRowsAt && row >= N) continue;  // (whole waves)
+                    const bool tiny = fabsf(b_of[n]) < kTinyBeta;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        dot[n] = fmaf(u[n][i], d[n][i], dot[n]);
+                        d[n][i] = tiny ? 0.0f : b_of[n] * d[n][i];
+                    }
+                    if (row < cnt) {
+                        T *gv = static_cast<T *>(a.grad_v) + (((int64_t)b * a.L + begin) * a.H + h) * a.dv + (int64_t)row * a.H * a.dv + c;
+                        if (a.out8) {
+                            constexpr int kVec8 = kVec<T>;
+                            if (c < a.dv) {
+#pragma unroll
+                                for (int o = 0; o < 8; o += kVec8) {
+                                    float w[kVec8];
+#pragma unroll
+                                    for (int i = 0; i < kVec8; ++i) w[i] = d[n][o + i];
+                                    store_vec<T, kVec8>(gv + o, w);
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (c + i < a.dv) gv[i] = (T)d[n][i];
+                        }
+                    }
+                    bf16x8 p3[3];
+                    split3(u[n], p3);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8 *>(&l.first.u[p * kV + at]) = p3[p];
+                    split3(d[n], p3);
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8 *>(&l.first.dr[p * kV + at]) = p3[p];
+#pragma unroll
+                    for (int p = 0; p < kP; ++p) *reinterpret_cast<bf16x8 *>(&l.first.go[p * kV + at]) = go[n][p];
+                }
+                // the next rows, ahead of the products
+                auto load_next = [&]() {
+                    if (blk + 1 < D / kNB) load_rows(w, blk + 1);
+                    else load_keys(w);
+                };
+                load_next();
+                __syncthreads();
+                if (blk == 0 && tid < N) {  // the gates' factors, which the second half reads
+                    const int p = tid;
+                    double sum = (double)(gate < -1e5f ? -1e5f : gate) * 1.4426950408889634;
+#pragma unroll
+                    for (int n = 1; n < N; n *= 2) {
+                        const double up = __shfl_up(sum, n, N);
+                        if (p >= n) sum += up;
+                    }
+                    const double whole = __shfl(sum, N - 1, N);
+                    l.G[p] = sum;
+                    l.f[p] = fast_exp2((float)sum);
+                    l.r[p] = fast_exp2((float)(whole - sum));
+                }
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    bf16x8 sp[kW][3], x[kP], y[3];
+#pragma unroll
+                    for (int w = 0; w < kW; ++w) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) z = fmaf(sv[w][i], blk * 2 + t < a.nblk * 2 ? dv[w][i] : 0.0f, z);
+                        split3(sv[w], sp[w]);
+                    }
+#pragma unroll
+                    for (int it = 0; it < NI; ++it) {
+                        const int at = tile_at<kNB>(16 * it + m, 4 * t + q);
+#pragma unroll
+                        for (int p = 0; p < kP; ++p) x[p] = read_row(&l.first.go[p * kV + at]);
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.dr[p * kV + at]);
+#pragma unroll
+                        for (int w = 0; w < kW; ++w) {
+                            aq[w][it] = mfma_planes(sp[w], x, aq[w][it]);
+                            as[w][it] = mfma_planes(sp[w], y, as[w][it]);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);  // or reads are brought forward into registers that are not there
+                    }
+#pragma unroll
+                    for (int w = 0; w < kW; ++w) split3(dv[w], sp[w]);
+                    if (blk * 2 + t + 1 < D / 32) load_state(w, blk * 2 + t + 1);
+#pragma unroll
+                    for (int it = 0; it < NI; ++it) {
+                        const int at = tile_at<kNB>(16 * it + m, 4 * t + q);
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.u[p * kV + at]);
+#pragma unroll
+                        for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(sp[w], y, ad[w][it]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+#pragma unroll
+                    for (int n = 0; n < kMine; ++n) {
+                        const int unit = unit_of(n);
+                        int it, jt;
+                        tile_of(unit, it, jt);
+                        const int ai = tile_at<kNB>(16 * it + m, 4 * t + q), aj = tile_at<kNB>(16 * jt + m, 4 * t + q);
+                        bf16x8 y[3];
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) y[p] = read_row(&l.first.u[p * kV + aj]);
+                        // (what a unit is is known beforehand but for those in the middle)
+                        const bool erase = n * kWaves >= kTiles || ((n + 1) * kWaves > kTiles && unit >= kTiles);
+                        if (erase) {
+                            bf16x8 x[3];
+#pragma unroll
+                            for (int p = 0; p < 3; ++p) x[p] = read_row(&l.first.dr[p * kV + ai]);
+                            pair[n] = mfma_planes(x, y, pair[n]);
+                        } else {
+                            bf16x8 x[kP];
+#pragma unroll
+                            for (int p = 0; p < kP; ++p) x[p] = read_row(&l.first.go[p * kV + ai]);
+                            pair[n] = mfma_planes(x, y, pair[n]);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+                __syncthreads();
+            }
+            z = lanes_sum(z);
+            if (lane == 0) l.z[wave] = has_s ? z : 0.0f;
+#pragma unroll
+            for (int n = 0; n < kMyRows; ++n) {
+                const int row = r0 + n * kRowsAt;
+#pragma unroll
+                for (int s = 1; s < 8; s *= 2) dot[n] += __shfl_xor(dot[n], s, 8);
+                if (grp == 0 && row < cnt && a.grad_b != nullptr) {
+                    a.grad_b[((int64_t)b * a.L + begin + row) * a.H + h] = dot[n] / (fabsf(b_of[n]) < kTinyBeta ? kTinyBeta : b_of[n]);
+                }
             }
         }
-        // the tiles above those on the diagonal that are read with them
-        for (int i = threadIdx.x; i < 2 * kM * NS * 16 * 2; i += kThreadsG) {
-            const int half = i & 1, r = i >> 1 & 15, s = (i >> 5) % NS, k = (i >> 5) / NS;
-            const bf16x8 zero = {};
-            *reinterpret_cast<bf16x8 *>(&(k < kM ? l.second.mp : l.second.ma)[(k < kM ? k : k - kM) * kMx + tile_at<N>(32 * s + 16 + r, 4 * s + half)]) = zero;
+
+        // rows of q and k in their place
+        {
+#pragma unroll
+            for (int n = 0; n < kMyKeys; ++n) {
+                const int at = tile_at<D>(key_row + n * kKeysAt, key_grp);
+#pragma unroll
+                for (int p = 0; p < kP; ++p) {
+                    *reinterpret_cast<bf16x8 *>(&l.second.k[p * kX + at]) = key[n][p];
+                    *reinterpret_cast<bf16x8 *>(&l.second.q[p * kX + at]) = query[n][p];
+                }
+            }
+            // the tiles above those on the diagonal that are read with them
+            for (int i = tid; i < 2 * kM * NS * 16 * 2; i += kThreadsG) {
+                const int half = i & 1, r = i >> 1 & 15, s = (i >> 5) % NS, k = (i >> 5) / NS;
+                const bf16x8 zero = {};
+                *reinterpret_cast<bf16x8 *>(&(k < kM ? l.second.mp : l.second.ma)[(k < kM ? k : k - kM) * kMx + tile_at<N>(32 * s + 16 + r, 4 * s + half)]) = zero;
+            }
         }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < kMine; ++n) {
-        if (wave + n * kWaves >= kUnits) continue;
-        const int unit = unit_of(n);
-        int it, jt;
-        tile_of(unit, it, jt);
-        const bool erase = unit >= kTiles;
-        const bf16 *left = erase ? l.second.k : l.second.q;
-        f32x4 dots = {};
-#pragma unroll
-        for (int t = 0; t < D / 32; ++t) {
+        // the next span's first operands, on their way while this one's pairs are at work
+        if (kAhead<T, D>) stand();
+        const bool more = kAhead<T, D> && --left > 0;
+        if (more) {
+            w = after(w);
+            load_rows(w, 0);
+            load_state(w, 0);
+            load_gate(w);
+        }
+        __syncthreads();
+        f32x4 dots[kMine] = {};
+        auto add_dots = [&](int n, int t) {
+            const int unit = unit_of(n);
+            int it, jt;
+            tile_of(unit, it, jt);
+            const bf16 *left = unit >= kTiles ? l.second.k : l.second.q;
             bf16x8 x[kP], y[kP];
 #pragma unroll
             for (int p = 0; p < kP; ++p) {
                 x[p] = read_row(&left[p * kX + tile_at<D>(16 * it + m, 4 * t + q)]);
                 y[p] = read_row(&l.second.k[p * kX + tile_at<D>(16 * jt + m, 4 * t + q)]);
             }
-            dots = mfma_planes(x, y, dots);
-        }
-        float cols = 0.0f, mine[8] = {};
+            dots[n] = mfma_planes(x, y, dots[n]);
+        };
+        if (kAhead<T, D>) {  // side by side where there are registers for it
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = 16 * it + 4 * q + r, j = 16 * jt + m;
-            const float e = j <= i ? fast_exp2((float)(l.G[i] - l.G[j])) : 0.0f;
-            const float w = erase ? (j < i ? -e * pair[n][r] : 0.0f) : a.scale * e * pair[n][r];
-            const float both = j < i ? w * dots[r] : 0.0f;
-            cols += both;
-            const float rows = lanes16_sum(both);
-            if (m == 0) l.row[erase][jt][i] = rows;
-            mine[r] = w;
-        }
-        // MP and MA are kept by columns: a lane's four results are neighbours there
-        bf16x8 p[kM];
-        walk::to_planes(mine, p);
-        bf16 *to = &(erase ? l.second.ma : l.second.mp)[tile_at<N>(16 * jt + m, 2 * it + (q >> 1)) + 4 * (q & 1)];
+            for (int t = 0; t < D / 32; ++t)
 #pragma unroll
-        for (int k = 0; k < kM; ++k) *reinterpret_cast<u32x2 *>(to + k * kMx) = *reinterpret_cast<const u32x2 *>(&p[k]);
-        cols += __shfl_xor(cols, 16);
-        cols += __shfl_xor(cols, 32);
-        if (q == 0) l.col[erase][it][16 * jt + m] = cols;
-    }
-    __syncthreads();
+                for (int n = 0; n < kMine; ++n) add_dots(n, t);
+        }
+#pragma unroll
+        for (int n = 0; n < kMine; ++n) {
+            if (wave + n * kWaves >= kUnits) continue;
+            if (!kAhead<T, D>) {
+#pragma unroll
+                for (int t = 0; t < D / 32; ++t) add_dots(n, t);
+            }
+            const int unit = unit_of(n);
+            int it, jt;
+            tile_of(unit, it, jt);
+            const bool erase = unit >= kTiles;
+            float cols = 0.0f, mine[8] = {};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * it + 4 * q + r, j = 16 * jt + m;
+                const float e = j <= i ? fast_exp2((float)(l.G[i] - l.G[j])) : 0.0f;
+                const float w = erase ? (j < i ? -e * pair[n][r] : 0.0f) : a.scale * e * pair[n][r];
+                const float both = j < i ? w * dots[n][r] : 0.0f;
+                cols += both;
+                const float rows = lanes16_sum(both);
+                if (m == 0) l.row[erase][jt][i] = rows;
+                mine[r] = w;
+            }
+            // MP and MA are kept by columns: a lane's four results are neighbours there
+            bf16x8 p[kM];
+            walk::to_planes(mine, p);
+            bf16 *to = &(erase ? l.second.ma : l.second.mp)[tile_at<N>(16 * jt + m, 2 * it + (q >> 1)) + 4 * (q & 1)];
+#pragma unroll
+            for (int k = 0; k < kM; ++k) *reinterpret_cast<u32x2 *>(to + k * kMx) = *reinterpret_cast<const u32x2 *>(&p[k]);
+            cols += __shfl_xor(cols, 16);
+            cols += __shfl_xor(cols, 32);
+            if (q == 0) l.col[erase][it][16 * jt + m] = cols;
+        }
+        __syncthreads();
 
-    // the products with S and D weighted; a row's products with them are the gates' share
+        // the products with S and D weighted; a row's products with them are the gates' share
 #pragma unroll
-    for (int it = 0; it < NI; ++it) {
-        const int pos = 16 * it + m;
-        const float f = l.f[pos], r = l.r[pos];
-        float x = 0.0f, y = 0.0f;
+        for (int it = 0; it < NI; ++it) {
+            const int pos = 16 * it + m;
+            const float f = l.f[pos], r = l.r[pos];
+            float x = 0.0f, y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kW; ++w) {
-            const int at = tile_at<D>(pos, 2 * (wave * kW + w) + (q >> 1)) + 4 * (q & 1);
+            for (int w = 0; w < kW; ++w) {
+                const int at = tile_at<D>(pos, 2 * (wave * kW + w) + (q >> 1)) + 4 * (q & 1);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                float qv = 0.0f, kv = 0.0f;
+                for (int n = 0; n < 4; ++n) {
+                    float qv = 0.0f, kv = 0.0f;
 #pragma unroll
-                for (int p = 0; p < kP; ++p) {
-                    qv += (float)l.second.q[p * kX + at + n];
-                    kv += (float)l.second.k[p * kX + at + n];
+                    for (int p = 0; p < kP; ++p) {
+                        qv += (float)l.second.q[p * kX + at + n];
+                        kv += (float)l.second.k[p * kX + at + n];
+                    }
+                    aq[w][it][n] *= f * a.scale;
+                    as[w][it][n] *= f;
+                    ad[w][it][n] *= r;
+                    y = fmaf(qv, aq[w][it][n], fmaf(-kv, as[w][it][n], y));
+                    x = fmaf(kv, ad[w][it][n], x);
+                    ad[w][it][n] -= as[w][it][n];
                 }
-                aq[w][it][n] *= f * a.scale;
-                as[w][it][n] *= f;
-                ad[w][it][n] *= r;
-                y = fmaf(qv, aq[w][it][n], fmaf(-kv, as[w][it][n], y));
-                x = fmaf(kv, ad[w][it][n], x);
-                ad[w][it][n] -= as[w][it][n];
+            }
+            x += __shfl_xor(x, 16);
+            y += __shfl_xor(y, 16);
+            x += __shfl_xor(x, 32);
+            y += __shfl_xor(y, 32);
+            if (q == 0) {
+                l.x[wave][pos] = x;
+                l.y[wave][pos] = y;
             }
         }
-        x += __shfl_xor(x, 16);
-        y += __shfl_xor(y, 16);
-        x += __shfl_xor(x, 32);
-        y += __shfl_xor(y, 32);
-        if (q == 0) {
-            l.x[wave][pos] = x;
-            l.y[wave][pos] = y;
-        }
-    }
-    // the pairs: dq += MP K, dk += MP^T Q + (MA + MA^T) K
+        // the pairs: dq += MP K, dk += MP^T Q + (MA + MA^T) K
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-        const int row = 32 * s + 8 * q + tr_i, in = 4 * (tr_c & 1);
-        bf16x8 kt[kW][kP], qt[kW][kP];
+        for (int s = 0; s < NS; ++s) {
+            const int row = 32 * s + 8 * q + tr_i, in = 4 * (tr_c & 1);
+            bf16x8 kt[kW][kP], qt[kW][kP];
 #pragma unroll
-        for (int w = 0; w < kW; ++w) {
-            const int grp = 2 * (wave * kW + w) + (tr_c >> 1);
+            for (int w = 0; w < kW; ++w) {
+                const int grp = 2 * (wave * kW + w) + (tr_c >> 1);
 #pragma unroll
-            for (int p = 0; p < kP; ++p) {
-                kt[w][p] = walk::join(read_tr(&l.second.k[p * kX + tile_at<D>(row, grp) + in]), read_tr(&l.second.k[p * kX + tile_at<D>(row + 4, grp) + in]));
-                qt[w][p] = walk::join(read_tr(&l.second.q[p * kX + tile_at<D>(row, grp) + in]), read_tr(&l.second.q[p * kX + tile_at<D>(row + 4, grp) + in]));
+                for (int p = 0; p < kP; ++p) {
+                    kt[w][p] = walk::join(read_tr(&l.second.k[p * kX + tile_at<D>(row, grp) + in]), read_tr(&l.second.k[p * kX + tile_at<D>(row + 4, grp) + in]));
+                    qt[w][p] = walk::join(read_tr(&l.second.q[p * kX + tile_at<D>(row, grp) + in]), read_tr(&l.second.q[p * kX + tile_at<D>(row + 4, grp) + in]));
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < NI; ++it) {
+                bf16x8 x[kM];
+                auto down = [&](const bf16 *M) {  // lane m: row 16 it + m of M, elements j
+                    const int g2 = 2 * it + (tr_c >> 1);
+#pragma unroll
+                    for (int p = 0; p < kM; ++p)
+                        x[p] = walk::join(read_tr(&M[p * kMx + tile_at<N>(row, g2) + in]), read_tr(&M[p * kMx + tile_at<N>(row + 4, g2) + in]));
+                };
+                auto along = [&](const bf16 *M) {  // lane m: column 16 it + m, elements i
+#pragma unroll
+                    for (int p = 0; p < kM; ++p) x[p] = read_row(&M[p * kMx + tile_at<N>(16 * it + m, 4 * s + q)]);
+                };
+                if (s <= it / 2) {
+                    down(l.second.mp);
+#pragma unroll
+                    for (int w = 0; w < kW; ++w) aq[w][it] = mfma_planes(kt[w], x, aq[w][it]);
+                    down(l.second.ma);
+#pragma unroll
+                    for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(kt[w], x, ad[w][it]);
+                }
+                if (s >= it / 2) {
+                    along(l.second.mp);
+#pragma unroll
+                    for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(qt[w], x, ad[w][it]);
+                    along(l.second.ma);
+#pragma unroll
+                    for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(kt[w], x, ad[w][it]);
+                }
             }
         }
 #pragma unroll
         for (int it = 0; it < NI; ++it) {
-            bf16x8 x[kM];
-            auto down = [&](const bf16 *M) {  // lane m: row 16 it + m of M, elements j
-                const int g2 = 2 * it + (tr_c >> 1);
+            const int pos = 16 * it + m;
+            if (pos >= cnt) continue;
+            const int64_t row = b * a.L + begin + pos;
 #pragma unroll
-                for (int p = 0; p < kM; ++p)
-                    x[p] = walk::join(read_tr(&M[p * kMx + tile_at<N>(row, g2) + in]), read_tr(&M[p * kMx + tile_at<N>(row + 4, g2) + in]));
-            };
-            auto along = [&](const bf16 *M) {  // lane m: column 16 it + m, elements i
+            for (int w = 0; w < kW; ++w) {
+                const int c = 16 * (wave * kW + w) + 4 * q;
 #pragma unroll
-                for (int p = 0; p < kM; ++p) x[p] = read_row(&M[p * kMx + tile_at<N>(16 * it + m, 4 * s + q)]);
-            };
-            if (s <= it / 2) {
-                down(l.second.mp);
+                for (int k = 0; k < 2; ++k) {
+                    float v[4];
 #pragma unroll
-                for (int w = 0; w < kW; ++w) aq[w][it] = mfma_planes(kt[w], x, aq[w][it]);
-                down(l.second.ma);
-#pragma unroll
-                for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(kt[w], x, ad[w][it]);
-            }
-            if (s >= it / 2) {
-                along(l.second.mp);
-#pragma unroll
-                for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(qt[w], x, ad[w][it]);
-                along(l.second.ma);
-#pragma unroll
-                for (int w = 0; w < kW; ++w) ad[w][it] = mfma_planes(kt[w], x, ad[w][it]);
-            }
-        }
-    }
-#pragma unroll
-    for (int it = 0; it < NI; ++it) {
-        const int pos = 16 * it + m;
-        if (pos >= cnt) continue;
-        const int64_t row = b * a.L + begin + pos;
-#pragma unroll
-        for (int w = 0; w < kW; ++w) {
-            const int c = 16 * (wave * kW + w) + 4 * q;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float v[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) v[n] = k ? ad[w][it][n] : aq[w][it][n];
-                if (a.part_q != nullptr) {
-                    float *to = (k ? a.part_k : a.part_q) + (row * a.H + h) * a.dk + c;
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        if (c + n < a.dk) to[n] = v[n];
-                } else {
-                    T *to = static_cast<T *>(k ? a.grad_k : a.grad_q) + (row * a.H + h) * a.dk + c;
-                    if (a.out4) {
-                        if (c < a.dk) store_vec<T, 4>(to, v);
-                    } else {
+                    for (int n = 0; n < 4; ++n) v[n] = k ? ad[w][it][n] : aq[w][it][n];
+                    if (a.part_q != nullptr) {
+                        float *to = (k ? a.part_k : a.part_q) + (row * a.H + h) * a.dk + c;
 #pragma unroll
                         for (int n = 0; n < 4; ++n)
-                            if (c + n < a.dk) to[n] = (T)v[n];
+                            if (c + n < a.dk) to[n] = v[n];
+                    } else {
+                        T *to = static_cast<T *>(k ? a.grad_k : a.grad_q) + (row * a.H + h) * a.dk + c;
+                        if (a.out4) {
+                            if (c < a.dk) store_vec<T, 4>(to, v);
+                        } else {
+#pragma unroll
+                            for (int n = 0; n < 4; ++n)
+                                if (c + n < a.dk) to[n] = (T)v[n];
+                        }
                     }
                 }
             }
         }
-    }
-    if (a.grad_g == nullptr) return;
-    __syncthreads();
-    if (wave == 0) {
-        const int p = lane & (N - 1), t = p >> 4;
-        double x = 0.0, y = 0.0, z = 0.0;
-        for (int w = 0; w < kWaves; ++w) {
-            x += l.x[w][p];
-            y += l.y[w][p];
-            z += l.z[w];
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int n = 0; n < NI; ++n) {
-                if (n <= t) y += l.row[k][n][p];
-                if (n >= t) y -= l.col[k][n][p];
+        const float f_last = l.f[N - 1];
+        __syncthreads();
+        if (wave == kWaves - 1 && a.grad_g != nullptr) {  // (the others go on to the next span)
+            const int p = lane & (N - 1), t = p >> 4;
+            double x = 0.0, y = 0.0, z = 0.0;
+            for (int w = 0; w < kWaves; ++w) {
+                x += l.x[w][p];
+                y += l.y[w][p];
+                z += l.z[w];
             }
-        const double own = x;
 #pragma unroll
-        for (int d = 1; d < N; d *= 2) {
-            const double before = __shfl_up(x, d, N), after = __shfl_down(y, d, N);
-            if (p >= d) x += before;
-            if (p + d < N) y += after;
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int n = 0; n < NI; ++n) {
+                    if (n <= t) y += l.row[k][n][p];
+                    if (n >= t) y -= l.col[k][n][p];
+                }
+            const double own = x;
+#pragma unroll
+            for (int d = 1; d < N; d *= 2) {
+                const double before = __shfl_up(x, d, N), after = __shfl_down(y, d, N);
+                if (p >= d) x += before;
+                if (p + d < N) y += after;
+            }
+            if (lane < cnt) a.grad_g[(b * a.L + begin + p) * a.H + h] = (float)((double)f_last * z + y + (x - own));
         }
-        if (lane < cnt) a.grad_g[(b * a.L + begin + p) * a.H + h] = (float)((double)l.f[N - 1] * z + y + (x - own));
+        if (!more) return;
     }
+}
+
+template <typename T, int D, bool VEC>
+void grad_launch(const BackArgs &a, hipStream_t s) {
+    constexpr int kThreadsG = kGradThreads<T, D>;
+    static const int per_cu = blocks_per_cu(reinterpret_cast<const void *>(grad_kernel<T, D, VEC>), kThreadsG);
+    const int64_t items = (int64_t)a.pairs * a.spans, slots = (int64_t)per_cu * device_cu_count();
+    grad_kernel<T, D, VEC><<<(unsigned)(kAhead<T, D> ? std::min(items, slots) : items), kThreadsG, 0, s>>>(a);
 }
 
 // Gradients of shared heads: out [rows, Hk, dk] = sums of part [rows, Hk, group, dk] over the group, in its order.
@@ -710,11 +805,10 @@ hipError_t back_launch(const DeltaArgs &p, char *scratch, hipStream_t s) {
         default: e = back_walks<T, 256, VEC>(p, w, a, scratch, s); break;
     }
     if (e != hipSuccess) return e;
-    const unsigned grid = (unsigned)(pairs * w.spans);
     switch (span_width(p)) {
-        case 64: grad_kernel<T, 64, VEC><<<grid, kGradThreads<T, 64>, 0, s>>>(a); break;
-        case 128: grad_kernel<T, 128, VEC><<<grid, kGradThreads<T, 128>, 0, s>>>(a); break;
-        default: grad_kernel<T, 256, VEC><<<grid, kGradThreads<T, 256>, 0, s>>>(a); break;
+        case 64: grad_launch<T, 64, VEC>(a, s); break;
+        case 128: grad_launch<T, 128, VEC>(a, s); break;
+        default: grad_launch<T, 256, VEC>(a, s); break;
     }
     if (w.parts) {
         const int64_t n = p.B * p.L * p.Hk * p.dk;
