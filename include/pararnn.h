@@ -493,7 +493,11 @@ int pararnn_embedding_backward(int32_t dtype, int64_t N, int64_t V, int64_t D, c
  * formed of three parts of 8 bits, of which the three smallest of nine
  * products are left out: 2^-23 of a product).  With bf16 tensors an output's
  * own products take the state and the positions' weights at 16 bits.
- * A row's result depends neither on B nor on H.
+ * Long sequences of few rows are walked in segments, whose number depends on
+ * L, B H and the heads' widths: the same row may get other last bits in another
+ * batch.  The same call gives the same bits.  (A segment multiplies with the
+ * matrix that it takes any state through: for keys and beta with which the state
+ * grows, that may pass fp32 where the state itself does not.)
  */
 size_t pararnn_delta_workspace_bytes(int32_t backward, int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk,
                                      int64_t dk, int64_t dv);

@@ -81,7 +81,8 @@ __global__ __launch_bounds__(walk::kThreads, (kWgs<T, D1>)) void segment_kernel(
 // Reads and writes the state once and is bound by that: k S and q S are formed
 // in the one pass that brings S into registers, S' leaves from there.  A
 // workgroup takes 64 columns of one (batch row, head); its threads are columns
-// (V of them each) by rows.
+// (V of them each) by rows.  B=128, H=16, 128x128, bf16: 55 us, 4.9 TB/s; B=1: 11
+// us, most of it the host's.
 constexpr int kStepCols = 64, kMaxHead = 256;
 
 struct StepArgs {
@@ -274,13 +275,20 @@ void step_launch(const DeltaArgs &p, const StepArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// Segments of a sequence of `chunks` that `groups` workgroups walk whole: as
-// many as keep two workgroups on every CU, of at least 8 chunks each.
+// Segments of a sequence of `chunks` that `groups` workgroups walk whole, 1 for
+// none.  Segments cost a second pass, with M's columns beside V's, and a join of
+// some microseconds each: 4 of 8 chunks at the least, or 5 where they are all
+// that fits on the CUs (two workgroups each), and more than 8 if they keep 16
+// chunks.  Forward, us, with the number of segments in brackets, H=16, 128x128,
+// bf16: B=1, L=4096: 286 whole, 129 (8), 147 (16); B=2, L=4096: 298 whole, 207 (4),
+// 204 (8); B=4, L=2048: 176 whole, 178 (2), 190 (4); B=1, L=1024: 85 whole, 90 (2),
+// 67 (4); H=8, L=512: 49 whole, 54 (2).  64x64: B=6, L=2048: 143 whole, 141 (2),
+// 120 (5).  fp32, B=1, H=8, L=32768: 64x64: 2682 whole, 320 (32), 328 (64); 64x128:
+// 420 (16), 350 (32).
 int segments(int64_t groups, int64_t chunks) {
-    const int64_t cus = device_cu_count();
-    if (groups * 2 > cus) return 1;
-    const int64_t n = std::min<int64_t>(2 * cus / groups, chunks / 8);
-    return (int)std::max<int64_t>(n, 1);
+    const int64_t most = 2 * (int64_t)device_cu_count() / groups;
+    const int64_t n = std::min({most, chunks / 8, std::max<int64_t>(8, chunks / 16)});
+    return most < 5 || n < 4 ? 1 : (int)n;
 }
 
 }  // namespace delta

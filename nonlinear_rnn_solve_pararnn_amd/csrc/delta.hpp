@@ -154,6 +154,9 @@ __device__ __forceinline__ void store_planes(char *at, float (&v)[8]) {
 
 __device__ __forceinline__ f32x4 mfma32(float a, float b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
+// A wave a chunk.  Bound by memory where there are many: rows of q and k are read
+// once, records written once.  B=8, L=2048, H=16, 128x128, bf16: 58 us for 134 MB
+// read and 86 written, in the backward pass 66 for 134 and 152.
 template <typename T, int D1, bool VEC, bool BACK>
 __global__ __launch_bounds__(256) void prep_kernel(PrepArgs a) {
     constexpr int kP = kPlanes<T>, NT = D1 / 32, W = 36;

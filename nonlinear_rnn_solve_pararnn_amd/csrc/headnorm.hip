@@ -11,7 +11,9 @@
 // first-level cache) and written once.  A head's row is 16 lanes wide, so a
 // wave has four rows on their way and row sums stay on the vector unit; a group
 // of 16 lanes takes several heads of one position in turn, which share the
-// cosines and sines it has loaded.
+// cosines and sines it has loaded.  B=8, L=2048, 16 + 16 heads of 128, bf16, full
+// rotation: 55 us forward (274 MB, 5.0 TB/s, a large copy's rate), 94 backward (408
+// MB, 4.3 TB/s, 5 us of it the weights' sums).
 #include "mixer.hpp"
 #include "rows.hpp"
 
@@ -35,7 +37,7 @@ __device__ __forceinline__ int column(int lane, int j) { return (lane + kLanes *
 
 // How a launch rotates: not at all, (i, i + R/2), (2i, 2i + 1), or whichever the
 // arguments say (single elements).  Kernels of their own need a third of the
-// registers less.
+// registers less: 72 -> 56 us forward and 123 -> 94 backward at the size above.
 enum Turned { kNone, kHalves, kPairs, kAny };
 template <int M>
 __device__ __forceinline__ bool pairs(const HeadnormArgs &a) { return M == kAny ? a.interleaved != 0 : M == kPairs; }
@@ -386,7 +388,8 @@ bool rows_vec(const HeadnormArgs &a, int es, bool back) {
     return true;
 }
 
-// Heads a group takes in turn: as many as leave four waves a SIMD.
+// Heads a group takes in turn: as many as leave four waves a SIMD, 8 at the most.
+// At the size above 56 and 94 us, with one head each 126 and 159.
 Params params(const HeadnormArgs &a) {
     Params p{};
     p.a = a;
