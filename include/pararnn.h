@@ -474,7 +474,9 @@ int pararnn_embedding_backward(int32_t dtype, int64_t N, int64_t V, int64_t D, c
  * q, k: [B, L, Hk, dk]; v, o: [B, L, H, dv], Hk a divisor of H: head h shares
  * q and k of head h / (H / Hk); log_decay, beta: [B, L, H] fp32; state,
  * out_state: [B, H, dk, dv] fp32 (state NULL: zeros; out_state NULL: not
- * wanted; out_state may be state itself, but not overlap it otherwise).
+ * wanted; out_state may be state itself).  No output may otherwise lie between
+ * the first and the last element of another tensor of the call (refused; so
+ * for the gradients and the single token).
  * 1 <= dk, dv <= 256 (above: PARARNN_ERR_UNSUPPORTED).  B H ceil(L / 32) is
  * below 2^26 - 4 (backward 2^22, and where heads share keys B L Hk dk below
  * 2^32) and B H below 2^23 over the blocks of 64 in the wider of dk and dv.
@@ -511,8 +513,7 @@ int pararnn_delta_forward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_
  * dLoss/d(final state) = grad_out_state ([B, H, dk, dv] or NULL for zeros):
  * grad_q, grad_k [B, L, Hk, dk] (summed over the heads that share them),
  * grad_v [B, L, H, dv], grad_log_decay and grad_beta [B, L, H] fp32 (either may
- * be NULL) and grad_state [B, H, dk, dv] or NULL (it must not overlap state or
- * grad_out_state).  strides: as above and those of grad_o after them (18
+ * be NULL) and grad_state [B, H, dk, dv] or NULL.  strides: as above and those of grad_o after them (18
  * values).  Where a value is not finite, the gradients are not defined.
  */
 int pararnn_delta_backward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
@@ -549,6 +550,8 @@ int pararnn_delta_step(int32_t dtype, int64_t B, int64_t H, int64_t Hk, int64_t 
  * yq, yk: dense outputs in dtype; rq [B, L, Hq], rk [B, L, Hk]: r, fp32, or NULL.
  * strides: HOST array of {batch row, position, head} strides of q and k (6
  * values, not negative, last dimension dense) or NULL for dense tensors.
+ * No output (here and of the gradients) may lie between the first and the last
+ * element of another tensor of the call (refused).
  * 2 <= d <= 256 (above: PARARNN_ERR_UNSUPPORTED), eps >= 0, B L (Hq + Hk) < 2^28.
  */
 enum { PARARNN_NORM_RMS = 0, PARARNN_NORM_L2 = 1 };

@@ -9,6 +9,8 @@
 #include "mixer.hpp"
 #include "sequence.hpp"
 
+#include <initializer_list>
+
 using namespace prn;
 
 namespace {
@@ -34,6 +36,27 @@ bool overlaps(const float *p, const float *q, int64_t n) {
     if (p == nullptr || q == nullptr) return false;
     const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q, len = (uintptr_t)n * sizeof(float);
     return a < b + len && b < a + len;
+}
+
+// The bytes from a tensor's first element to its last (none where it is null).
+struct Bytes {
+    uintptr_t begin, end;
+};
+Bytes bytes_of(const void *p, int64_t n) { return {(uintptr_t)p, (uintptr_t)p + (p != nullptr ? (uintptr_t)n : 0)}; }
+Bytes bytes_of(const HeadView &v, int64_t B, int64_t L, int64_t H, int64_t d, int64_t es) {
+    const uint64_t n = (uint64_t)(B - 1) * v.st[0] + (uint64_t)(L - 1) * v.st[1] + (uint64_t)(H - 1) * v.st[2] + (uint64_t)d;
+    return bytes_of(v.p, (int64_t)(n * (uint64_t)es));
+}
+// Whether outputs share bytes with no input and with each other.
+bool apart(std::initializer_list<Bytes> outs, std::initializer_list<Bytes> ins) {
+    auto meet = [](const Bytes &a, const Bytes &b) { return a.begin < b.end && b.begin < a.end; };
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (const Bytes &i : ins)
+            if (meet(*o, i)) return false;
+        for (auto p = outs.begin(); p != o; ++p)
+            if (meet(*o, *p)) return false;
+    }
+    return true;
 }
 
 // Zeros for trace entries [from, to) that no iteration will write.
@@ -240,6 +263,17 @@ bool delta_args(DeltaArgs &a, int32_t dtype, int64_t B, int64_t L, int64_t H, in
            head_view(a.v, in.v, es, at(2), L, H, dv, true) && head_view(a.log_decay, in.log_decay, 4, at(3), L, H, 1, false) &&
            head_view(a.beta, in.beta, 4, at(4), L, H, 1, false) &&
            (in.grad_o == nullptr || head_view(a.grad_o, in.grad_o, es, at(5), L, H, dv, true));
+}
+
+// o and the new state, which may be the old one itself, share bytes with no other tensor of the call.
+bool delta_outputs_ok(const DeltaArgs &a, const float *state, const void *o, const float *out_state) {
+    const int64_t es = a.bf16 ? 2 : 4;
+    const Bytes to = bytes_of(o, a.B * a.L * a.H * a.dv * es), n = bytes_of(state, a.B * a.H * a.dk * a.dv * 4),
+                out = bytes_of(out_state, a.B * a.H * a.dk * a.dv * 4);
+    return apart({to, out}, {bytes_of(a.q, a.B, a.L, a.Hk, a.dk, es), bytes_of(a.k, a.B, a.L, a.Hk, a.dk, es),
+                             bytes_of(a.v, a.B, a.L, a.H, a.dv, es), bytes_of(a.log_decay, a.B, a.L, a.H, 1, 4),
+                             bytes_of(a.beta, a.B, a.L, a.H, 1, 4)}) &&
+           apart({to}, {n}) && (state == out_state || apart({out}, {n}));
 }
 
 bool headnorm_dims_ok(int32_t dtype, int64_t B, int64_t L, int64_t Hq, int64_t Hk, int64_t d) {
@@ -684,7 +718,7 @@ int pararnn_delta_forward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_
     DeltaArgs a;
     if (!delta_args(a, dtype, B, L, H, Hk, dk, dv, DeltaIn{q, k, v, log_decay, beta, nullptr}, strides)) return PARARNN_ERR_INVALID;
     if (!ws || ws_bytes < delta_ws(a, false) || !aligned(ws, 256)) return PARARNN_ERR_INVALID;
-    if (state != out_state && overlaps(state, out_state, B * H * dk * dv)) return PARARNN_ERR_INVALID;
+    if (!delta_outputs_ok(a, state, o, out_state)) return PARARNN_ERR_INVALID;
     a.state = state;
     a.scale = scale;
     a.o = o;
@@ -705,8 +739,13 @@ int pararnn_delta_backward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64
     DeltaArgs a;
     if (!delta_args(a, dtype, B, L, H, Hk, dk, dv, DeltaIn{q, k, v, log_decay, beta, grad_o}, strides)) return PARARNN_ERR_INVALID;
     if (!ws || ws_bytes < delta_ws(a, true) || !aligned(ws, 256)) return PARARNN_ERR_INVALID;
-    const int64_t n = B * H * dk * dv;
-    if (overlaps(state, grad_state, n) || overlaps(grad_out_state, grad_state, n)) return PARARNN_ERR_INVALID;
+    const int64_t es = dtype == PARARNN_BF16 ? 2 : 4, keys = B * L * Hk * dk * es, gates = B * L * H * 4, n = B * H * dk * dv * 4;
+    if (!apart({bytes_of(grad_q, keys), bytes_of(grad_k, keys), bytes_of(grad_v, B * L * H * dv * es), bytes_of(grad_log_decay, gates),
+                bytes_of(grad_beta, gates), bytes_of(grad_state, n)},
+               {bytes_of(a.q, B, L, Hk, dk, es), bytes_of(a.k, B, L, Hk, dk, es), bytes_of(a.v, B, L, H, dv, es),
+                bytes_of(a.log_decay, B, L, H, 1, 4), bytes_of(a.beta, B, L, H, 1, 4), bytes_of(a.grad_o, B, L, H, dv, es),
+                bytes_of(state, n), bytes_of(grad_out_state, n)}))
+        return PARARNN_ERR_INVALID;
     a.state = state;
     a.scale = scale;
     a.grad_out_state = grad_out_state;
@@ -727,7 +766,7 @@ int pararnn_delta_step(int32_t dtype, int64_t B, int64_t H, int64_t Hk, int64_t 
         return PARARNN_ERR_INVALID;
     DeltaArgs a;
     if (!delta_args(a, dtype, B, 1, H, Hk, dk, dv, DeltaIn{q, k, v, log_decay, beta, nullptr}, strides)) return PARARNN_ERR_INVALID;
-    if (state != out_state && overlaps(state, out_state, B * H * dk * dv)) return PARARNN_ERR_INVALID;
+    if (!delta_outputs_ok(a, state, o, out_state)) return PARARNN_ERR_INVALID;
     a.state = state;
     a.scale = scale;
     a.o = o;
@@ -745,6 +784,11 @@ int pararnn_headnorm_forward(int32_t dtype, int64_t B, int64_t L, int64_t Hq, in
     HeadnormArgs a;
     const void *in[2] = {q, k};
     if (!headnorm_args(a, dtype, B, L, Hq, Hk, d, in, 2, strides, Rotation{table, P, R, positions, position_bytes}, kind, interleaved))
+        return PARARNN_ERR_INVALID;
+    const int64_t es = dtype == PARARNN_BF16 ? 2 : 4, qs = B * L * Hq, ks = B * L * Hk;
+    if (!apart({bytes_of(yq, qs * d * es), bytes_of(yk, ks * d * es), bytes_of(rq, qs * 4), bytes_of(rk, ks * 4)},
+               {bytes_of(a.x[0], B, L, Hq, d, es), bytes_of(a.x[1], B, L, Hk, d, es), bytes_of(wq, d * 4), bytes_of(wk, d * 4),
+                bytes_of(table, P * R * 4), bytes_of(positions, B * L * position_bytes)}))
         return PARARNN_ERR_INVALID;
     a.w[0] = wq;
     a.w[1] = wk;
@@ -782,6 +826,12 @@ int pararnn_headnorm_backward(int32_t dtype, int64_t B, int64_t L, int64_t Hq, i
     if (!headnorm_args(a, dtype, B, L, Hq, Hk, d, in, 4, strides, Rotation{table, P, R, positions, position_bytes}, kind, interleaved))
         return PARARNN_ERR_INVALID;
     if ((grad_wq || grad_wk) && (!ws || ws_bytes < headnorm_ws(a) || !aligned(ws, 256))) return PARARNN_ERR_INVALID;
+    const int64_t es = dtype == PARARNN_BF16 ? 2 : 4, qs = B * L * Hq, ks = B * L * Hk;
+    if (!apart({bytes_of(grad_q, qs * d * es), bytes_of(grad_k, ks * d * es), bytes_of(grad_wq, d * 4), bytes_of(grad_wk, d * 4)},
+               {bytes_of(a.x[0], B, L, Hq, d, es), bytes_of(a.x[1], B, L, Hk, d, es), bytes_of(a.g[0], B, L, Hq, d, es),
+                bytes_of(a.g[1], B, L, Hk, d, es), bytes_of(rq, qs * 4), bytes_of(rk, ks * 4), bytes_of(wq, d * 4),
+                bytes_of(wk, d * 4), bytes_of(table, P * R * 4), bytes_of(positions, B * L * position_bytes)}))
+        return PARARNN_ERR_INVALID;
     a.w[0] = wq;
     a.w[1] = wk;
     a.r[0] = const_cast<float *>(rq);
