@@ -491,10 +491,9 @@ int pararnn_embedding_backward(int32_t dtype, int64_t N, int64_t V, int64_t D, c
  * everything, and finite) it makes every output of the head from t on NaN and
  * its final state.  No output before t is affected.  A key whose squares add
  * up past fp32 counts as not finite.
- * Precision: states and what they are computed from are carried in fp32 (products
- * formed of three parts of 8 bits, of which the three smallest of nine
- * products are left out: 2^-23 of a product).  With bf16 tensors an output's
- * own products take the state and the positions' weights at 16 bits.
+ * Precision: fp32 throughout (products formed of three parts of 8 bits, of which
+ * the three smallest of nine products are left out: 2^-23 of a product), and
+ * one rounding of each output to bf16.
  * Long sequences of few rows are walked in segments, whose number depends on
  * L, B H and the heads' widths: the same row may get other last bits in another
  * batch.  The same call gives the same bits.  (A segment multiplies with the

@@ -42,7 +42,7 @@ __global__ __launch_bounds__(walk::kThreads, (kWgs<T, D1>)) void walk_kernel(For
     const Where wh = where(a.nblk * a.seg.n, a.pairs, a.H);
     if (!wh.any) return;
     const int seg = (int)__builtin_amdgcn_readfirstlane(wh.sub / a.nblk), blk = wh.sub - seg * a.nblk;
-    Job j = job_of(a, wh, kRecord<T, false>);
+    Job j = job_of(a, wh, kRecord<false>);
     j.c0 = blk * kNB;
     j.from = seg * a.seg.chunks;
     j.to = min(j.from + a.seg.chunks, a.chunks);
@@ -63,7 +63,7 @@ __global__ __launch_bounds__(walk::kThreads, (kWgs<T, D1>)) void segment_kernel(
     const Where wh = where(per * (a.seg.n - 1), a.pairs, a.H);
     if (!wh.any) return;
     const int seg = (int)__builtin_amdgcn_readfirstlane(wh.sub / per), blk = wh.sub - seg * per;
-    Job j = job_of(a, wh, kRecord<T, false>);
+    Job j = job_of(a, wh, kRecord<false>);
     j.from = seg * a.seg.chunks;
     j.to = j.from + a.seg.chunks;
     j.identity = blk >= a.nblk;
@@ -200,7 +200,7 @@ ForwardPlan forward_plan(const DeltaArgs &p) {
     w.seg_chunks = (int)((w.chunks + w.segs - 1) / w.segs);
     w.segs = (int)((w.chunks + w.seg_chunks - 1) / w.seg_chunks);
     const size_t slots = w.segs > 1 ? (size_t)(pairs * w.segs) * D1 * 4 : 0;
-    w.seg_s = round256((size_t)(pairs * w.chunks) * (p.bf16 ? kRecord<bf16, false> : kRecord<float, false>));
+    w.seg_s = round256((size_t)(pairs * w.chunks) * kRecord<false>);
     w.seg_m = w.seg_s + round256(slots * blocks_of(p.dv) * kNB);
     w.total = w.seg_m + slots * blocks_of(D1) * kNB;
     return w;

@@ -38,9 +38,8 @@ struct Gates {
     float pad[30];
 };
 constexpr int kTile = 1024;  // bytes of one plane of 16 rows
-template <typename T> constexpr int kPP = sizeof(T) == 2 ? 2 : 3;  // planes of P
-template <typename T, bool BACK> constexpr int kMats = BACK ? 2 * 9 : 2 * (3 + kPP<T>);
-template <typename T, bool BACK> constexpr int64_t kRecord = sizeof(Gates) + (int64_t)kMats<T, BACK> * kTile;
+// T and P, or T, its transpose and that of P, of three planes of two tiles each
+template <bool BACK> constexpr int64_t kRecord = sizeof(Gates) + (BACK ? 18 : 12) * kTile;
 constexpr int kAtT = sizeof(Gates), kAtP = kAtT + 6 * kTile;       // forward
 constexpr int kAtTt = kAtT + 6 * kTile, kAtPt = kAtTt + 6 * kTile;  // backward
 
@@ -140,8 +139,7 @@ __device__ __forceinline__ void load8(const T *row, int c, int d, bool in, bf16x
     walk::planes_of(x.v, p);
 }
 
-// Eight numbers as NP planes without an infinity in them (one would look like a launch tag in the workspace).
-template <int NP>
+// Eight numbers as planes without an infinity in them (one would look like a launch tag in the workspace).
 __device__ __forceinline__ void store_planes(char *at, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -149,14 +147,14 @@ __device__ __forceinline__ void store_planes(char *at, float (&v)[8]) {
     bf16x8 p[3];
     walk::split3(v, p);
 #pragma unroll
-    for (int n = 0; n < NP; ++n) *reinterpret_cast<bf16x8 *>(at + n * kTile) = p[n];
+    for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8 *>(at + n * kTile) = p[n];
 }
 
 __device__ __forceinline__ f32x4 mfma32(float a, float b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
 // A wave a chunk.  Bound by memory where there are many: rows of q and k are read
-// once, records written once.  B=8, L=2048, H=16, 128x128, bf16: 58 us for 134 MB
-// read and 86 written, in the backward pass 66 for 134 and 152.
+// once, records written once.  B=8, L=2048, H=16, 128x128, bf16: 59 us for 134 MB
+// read and 105 written, in the backward pass 66 for 134 and 155.
 template <typename T, int D1, bool VEC, bool BACK>
 __global__ __launch_bounds__(256) void prep_kernel(PrepArgs a) {
     constexpr int kP = kPlanes<T>, NT = D1 / 32, W = 36;
@@ -287,7 +285,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepArgs a) {
     __syncthreads();
 
     if (want >= a.items) return;
-    char *rec = a.rec + item * kRecord<T, BACK>;
+    char *rec = a.rec + item * kRecord<BACK>;
     if (lane < C) {
         Gates *to = reinterpret_cast<Gates *>(rec);
         to->b[p] = p < bad ? beta : __builtin_nanf("");  // tells the walk
@@ -313,15 +311,15 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepArgs a) {
             for (int n = 0; n < 8; ++n) v[n] = src[(8 * q + n) * W + j];
         };
         across(Tw, row);
-        store_planes<3>(rec + kAtT + u * 3 * kTile + lane * 16, v);
+        store_planes(rec + kAtT + u * 3 * kTile + lane * 16, v);
         if constexpr (!BACK) {
             across(A, 16 * u + m);
-            store_planes<kPP<T>>(rec + kAtP + u * kPP<T> * kTile + lane * 16, v);
+            store_planes(rec + kAtP + u * 3 * kTile + lane * 16, v);
         } else {
             down(Tw, row);
-            store_planes<3>(rec + kAtTt + u * 3 * kTile + lane * 16, v);
+            store_planes(rec + kAtTt + u * 3 * kTile + lane * 16, v);
             down(A, row);
-            store_planes<3>(rec + kAtPt + u * 3 * kTile + lane * 16, v);
+            store_planes(rec + kAtPt + u * 3 * kTile + lane * 16, v);
         }
     }
 }

@@ -62,7 +62,7 @@ __device__ __forceinline__ Job job_of(const BackArgs &a, const Where &wh) {
     j.dv = a.dv;
     j.all = a.chunks;
     j.scale = a.scale;
-    j.rec = a.rec + (int64_t)wh.bh * a.chunks * kRecord<T, true>;
+    j.rec = a.rec + (int64_t)wh.bh * a.chunks * kRecord<true>;
     return j;
 }
 
@@ -734,7 +734,7 @@ BackPlan back_plan(const DeltaArgs &p) {
         at += ((size_t)floats * 4 + 255) / 256 * 256;
         return here;
     };
-    take(pairs * w.chunks * (p.bf16 ? kRecord<bf16, true> : kRecord<float, true>) / 4);
+    take(pairs * w.chunks * kRecord<true> / 4);
     w.u = take(pairs * w.spans * w.span * wide);
     w.dr = take(pairs * w.spans * w.span * wide);
     w.s = take(pairs * w.spans * D1 * wide);

@@ -15,12 +15,13 @@
 // it.  LDS reads are issued a step ahead of the matrix instructions that use
 // them, results side by side take turns in the matrix unit, and results are
 // stored after the next chunk's operands have arrived (loads and stores are
-// waited for in their order).  B=8, L=2048, H=16, 128x128, bf16: 157 us, some
-// 5100 cycles a chunk, 2000 of them vector and 1350 matrix instructions; before
-// the second stage in LDS 163, with T and P in registers 172, with reads left to the
-// compiler and one result after the other 199, with the stores before the wait
-// as well 210.  Planes split off by two-element dot products (seven instructions
-// for two numbers, not eleven) took 169.
+// waited for in their order).  B=8, L=2048, H=16, 128x128, bf16: 165 us, some
+// 5400 cycles a chunk.  Before, with S, U and P at 16 bits in outputs (which then
+// rounded some values the other way than fp32 does) 155; measured like that and
+// against 157: before the second stage in LDS 163, with T and P in registers 172,
+// with reads left to the compiler and one result after the other 199, with the
+// stores before the wait as well 210; planes split off by two-element dot products
+// (seven instructions for two numbers, not eleven) 169.
 #pragma once
 
 #include <type_traits>
@@ -115,8 +116,7 @@ __device__ __forceinline__ int take_odd(float (&v)[8], int q) {
 template <typename T, int D1, bool VEC, Role ROLE, bool BACK>
 __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> (&lds)[kStages<T, D1>]) {
     constexpr bool kOut = ROLE == Role::Out, kGrad = ROLE == Role::Grad, kUseQ = kOut || kGrad;
-    constexpr int kP = kPlanes<T>, kO = kP == 3 ? 3 : 2;  // planes of operands; of S and U where an output is formed
-    constexpr int kMat = kGrad ? 3 : kPP<T>;              // planes of P
+    constexpr int kP = kPlanes<T>;  // planes of operands (all that is computed has three)
     constexpr int NA = D1 / 16, NT = D1 / 32;
     constexpr int kPX = C * kTileRow<D1>, kPZ = C * kTileRow<kNB>;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, q = lane >> 4;
@@ -148,12 +148,12 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> (&lds)[
     ak.init(rk);
     av.init(rv);
     float gate_ahead = 0.0f;
-    constexpr int kMats = 6 + (kUseQ ? 2 * kMat : 0), kMyMats = (kMats + 3) / 4;
+    constexpr int kMats = kUseQ ? 12 : 6, kMyMats = (kMats + 3) / 4;
     bf16x8 mat_ahead[kMyMats];  // this wave's share of T and P
     const int n_chunks = j.to - j.from;
     auto chunk_at = [&](int i) { return kGrad ? j.to - 1 - i : j.from + i; };
     auto positions = [&](int c) { return c < j.all - 1 ? C : last; };
-    auto record = [&](int i) { return j.rec + (int64_t)chunk_at(min(i, n_chunks - 1)) * kRecord<T, BACK>; };
+    auto record = [&](int i) { return j.rec + (int64_t)chunk_at(min(i, n_chunks - 1)) * kRecord<BACK>; };
     auto load = [&](int i) {
         const int c = chunk_at(i), cnt = i < n_chunks ? positions(c) : 0;
         ak.load(rk, c, cnt);
@@ -270,12 +270,7 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> (&lds)[
             }
             const Step &now = step[t & 1];
             mfma_each(now.k, now.s, ks);
-            if constexpr (kOut) {
-                bf16x8 so[kO];
-#pragma unroll
-                for (int p = 0; p < kO; ++p) so[p] = now.s[p];
-                mfma_each_right(so, now.q, o);
-            }
+            if constexpr (kOut) mfma_each_right(now.s, now.q, o);
             __builtin_amdgcn_sched_barrier(0);
         }
         float gb[8];
@@ -314,9 +309,9 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> (&lds)[
             bf16x8 zz[kP];
 #pragma unroll
             for (int p = 0; p < kP; ++p) zz[p] = z[p];
-            bf16x8 Pm[2][kMat];
+            bf16x8 Pm[2][3];
 #pragma unroll
-            for (int n = 0; n < 2 * kMat; ++n) Pm[n / kMat][n % kMat] = l.mats[6 + n][lane];
+            for (int n = 0; n < 6; ++n) Pm[n / 3][n % 3] = l.mats[6 + n][lane];
             mfma_each(Pm, zz, y);
 #pragma unroll
             for (int n = 0; n < 8; ++n) x[n] = y[n >> 2][n & 3];
@@ -347,15 +342,12 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> (&lds)[
         }
         if constexpr (kOut) {
             split3(x, xp);
-            bf16x8 up[kO];
-#pragma unroll
-            for (int p = 0; p < kO; ++p) up[p] = xp[p];
 #pragma unroll
             for (int it = 0; it < 2; ++it) o[it] *= l.gates.f[16 * it + m] * j.scale;
-            bf16x8 Pm[2][kMat];
+            bf16x8 Pm[2][3];
 #pragma unroll
-            for (int n = 0; n < 2 * kMat; ++n) Pm[n / kMat][n % kMat] = l.mats[6 + n][lane];
-            mfma_each_right(up, Pm, o);
+            for (int n = 0; n < 6; ++n) Pm[n / 3][n % 3] = l.mats[6 + n][lane];
+            mfma_each_right(xp, Pm, o);
         }
         // the state after the chunk: K^T (r U), or Q^T (f do') - K^T (f b dR)
 #pragma unroll
