@@ -514,6 +514,7 @@ int pararnn_delta_forward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_
  * grad_v [B, L, H, dv], grad_log_decay and grad_beta [B, L, H] fp32 (either may
  * be NULL) and grad_state [B, H, dk, dv] or NULL.  strides: as above and those of grad_o after them (18
  * values).  Where a value is not finite, the gradients are not defined.
+ * Precision as above: fp32 throughout, and one rounding of each gradient.
  */
 int pararnn_delta_backward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
                            const void *q, const void *k, const void *v, const float *log_decay, const float *beta,

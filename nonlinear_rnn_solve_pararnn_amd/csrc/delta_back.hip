@@ -17,9 +17,10 @@
 // The last line adds terms that the gate does take part in; the shorter
 // identity dg_t - dg_(t+1) = do_t.o_t - dv_t.v_t adds up others that cancel.
 //
-// Precision: walks as in the forward pass; S, D, U and dr in three planes, as dg
-// and db are fp32 results whatever the tensors are.  MP and MA, which dq and dk
-// alone are made of, have 16 bits with bf16 tensors.
+// Precision: walks as in the forward pass; S, D, U, dr, MP and MA in three planes
+// whatever the tensors are, so that bf16 gradients are fp32's, rounded once.  (MP
+// and MA at 16 bits: grad_kernel 350 us where it takes 358, B=8, L=2048, H=16,
+// 128x128.)
 #include "delta_walk.hpp"
 
 namespace prn {
@@ -141,7 +142,7 @@ __device__ __forceinline__ void planes_to(const float (&v)[8], bf16x8 (&p)[N]) {
 constexpr int grad_tiles(bool bf16, int D) { return D >= 128 && span_of(bf16, D) == 32 ? 2 : 1; }
 template <typename T, int D>
 struct GradLds {
-    static constexpr int kN = span_of(sizeof(T) == 2, D), kP = kPlanes<T>, kM = kP == 3 ? 3 : 2, kW = grad_tiles(sizeof(T) == 2, D), kWaves = D / 16 / kW;
+    static constexpr int kN = span_of(sizeof(T) == 2, D), kP = kPlanes<T>, kM = 3, kW = grad_tiles(sizeof(T) == 2, D), kWaves = D / 16 / kW;
     static constexpr int kRowsX = kN * kTileRow<D>, kRowsV = kN * kTileRow<kNB>, kRowsM = kN * kTileRow<kN>;
     struct First {
         bf16 go[kP * kRowsV], u[3 * kRowsV], dr[3 * kRowsV];
@@ -164,10 +165,11 @@ struct GradLds {
 // go on while this one multiplies.  With one (bf16, and fp32 up to heads of 64:
 // two would spill) a workgroup goes through several spans and has the next one's
 // first operands on their way while it works on the pairs.
-// B=8, L=2048, H=16, 128x128, bf16: 1.0 GB read and 0.2 written in 350 us, 3.4
+// B=8, L=2048, H=16, 128x128, bf16: 1.0 GB read and 0.2 written in 358 us, 3.4
 // TB/s; the rest is a workgroup's phases, which follow each other on its CU (LDS
 // and matrix instructions of the products with S and D take half of them).  The
-// whole backward pass 740 us with a workgroup a span, 700 so; grad_kernel with two
+// whole backward pass 740 us with a workgroup a span, 700 so (with MP and MA at 16
+// bits; 713 as it is); grad_kernel with two
 // tiles and two workgroups a CU 438-510 us where it took 395.  B=3, L=1000, H=10,
 // 48x80, fp32: grad_kernel 62 us with one tile, 54 with two.
 template <typename T, int D> constexpr bool kAhead = grad_tiles(sizeof(T) == 2, D) == 1;

@@ -52,3 +52,19 @@ def test_outputs_take_writes_and_weights_in_32_bits(L, dk, dv):
     for scale in (1.0 + 2.0 ** -8 + 2.0 ** -20, 1.0 + 5 * 2.0 ** -8 + 2.0 ** -20):
         o, _ = api.delta_forward(q, k, sign, g, torch.ones_like(b), scale=scale)
         assert torch.equal(o, (scale * sign.float())[:, ask].to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("L,dk,dv", [(32, 64, 8), (60, 64, 72), (128, 128, 128), (200, 200, 33)])
+def test_gradients_take_pairs_in_32_bits(L, dk, dv):
+    """One output has a gradient, of one element: its query's gradient at key t is what position t wrote there."""
+    gen = torch.Generator().manual_seed(L + 1)
+    b = numbers(L * 2, gen).view(1, L, 2).to(DEV)
+    t = torch.arange(L)
+    q = k = one_hot(t[None, :, None].expand(1, L, 2), dk)
+    v = torch.ones(1, L, 2, dv, dtype=torch.bfloat16, device=DEV)
+    do = torch.zeros(1, L, 2, dv, dtype=torch.bfloat16, device=DEV)
+    do[:, L - 1, :, 3] = 1.0
+    dq = api.delta_backward(q, k, v, torch.zeros(1, L, 2, device=DEV), b, do, scale=1.0)[0]
+    want = torch.zeros_like(dq)
+    want[0, L - 1, :, :L] = b[0].t().to(torch.bfloat16)
+    assert torch.equal(dq, want)
