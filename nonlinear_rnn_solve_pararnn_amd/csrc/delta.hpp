@@ -71,7 +71,9 @@ __device__ __forceinline__ Where where(int per_, int pairs, int heads) {
 __host__ __device__ __forceinline__ WalkView view_of(const HeadView &v) { return {v.p, v.st[0], v.st[1], v.st[2]}; }
 
 // Whether rows move as 16-byte vectors.  Rows that overlap are left to the
-// loads of any alignment, whose rows past the last position are cleared.
+// loads of any alignment, whose rows past the last position are cleared.  Where
+// all positions have one row, the rows past the last one are that row again: T,
+// P, b and f are zero there.
 inline bool view_vec(const HeadView &v, int d, int es) {
     const int64_t n = 16 / es;
     return d % n == 0 && aligned16(v.p) && v.st[0] % n == 0 && v.st[1] % n == 0 && v.st[2] % n == 0 && (v.st[1] >= d || v.st[1] == 0);
@@ -289,7 +291,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepArgs a) {
     if (lane < C) {
         Gates *to = reinterpret_cast<Gates *>(rec);
         to->b[p] = p < bad ? beta : __builtin_nanf("");  // tells the walk
-        to->f[p] = fast_exp2((float)sum);
+        to->f[p] = in ? fast_exp2((float)sum) : 0.0f;
         to->r[p] = fast_exp2((float)(G[C - 1] - sum));
         if (p == C - 1) {
             const float whole = fast_exp2((float)sum), rest = expm1f((float)(sum * 0.6931471805599453));
