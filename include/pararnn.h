@@ -470,7 +470,7 @@ int pararnn_embedding_backward(int32_t dtype, int64_t N, int64_t V, int64_t D, c
  *     o_t = scale q_t S_t,   S_{-1} = state.
  * It is meant for keys of about unit length and b in [0, 1] (or [0, 2]): for
  * b |k|^2 above 2 the state grows along k.  A position with b = 0 and g = 0
- * leaves the state as it is (padding).
+ * leaves the state as it is, whatever finite v it has (padding).
  * q, k: [B, L, Hk, dk]; v, o: [B, L, H, dv], Hk a divisor of H: head h shares
  * q and k of head h / (H / Hk); log_decay, beta: [B, L, H] fp32; state,
  * out_state: [B, H, dk, dv] fp32 (state NULL: zeros; out_state NULL: not

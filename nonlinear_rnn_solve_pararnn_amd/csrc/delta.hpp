@@ -26,7 +26,10 @@ using walk::bf16x8;
 using walk::kPlanes;
 
 constexpr int C = 32;  // positions a chunk
+// Backward pass: what stands in a beta's place that is no larger, as the gradient
+// of beta divides u by it.  Such a position reaches no other one (writes_none).
 constexpr float kTinyBeta = 1e-20f;
+__device__ __forceinline__ bool writes_none(float beta) { return fabsf(beta) <= kTinyBeta; }
 
 // What is kept of a chunk: gates, then matrices as operands of the 32-wide
 // matrix instructions, plane by plane, 16 bytes a lane.  T (and in the backward
@@ -178,8 +181,7 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepArgs a) {
     auto gate = [&](const HeadView &v) { return static_cast<const float *>(v.p)[b * v.st[0] + (begin + p) * v.st[1] + h * v.st[2]]; };
     float g = in ? gate(a.log_decay) : 0.0f;
     float beta = in ? gate(a.beta) : 0.0f;
-    // the gradient of beta divides u by it; so small a beta adds nothing to any sum
-    if (BACK && fabsf(beta) < kTinyBeta) beta = kTinyBeta;
+    if (BACK && writes_none(beta)) beta = kTinyBeta;
     if (g < -1e5f) g = -1e5f;  // e^g is 0 from -104 on
     const bool bad_gate = abs_bits(g) >= kInfBits || abs_bits(beta) >= kInfBits;
     double sum = bad_gate ? 0.0 : (double)g * 1.4426950408889634;

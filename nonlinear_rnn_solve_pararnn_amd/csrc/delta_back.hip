@@ -332,11 +332,12 @@ __global__ __launch_bounds__((kGradThreads<T, D>), 2) void grad_kernel(BackArgs 
                 for (int n = 0; n < kMyRows; ++n) {
                     const int row = r0 + n * kRowsAt, at = tile_at<kNB>(row, grp), c = blk * kNB + grp * 8;
                     if (N < kRowsAt && row >= N) continue;  // (whole waves)
-                    const bool tiny = fabsf(b_of[n]) < kTinyBeta;
+                    const bool none = writes_none(b_of[n]);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         dot[n] = fmaf(u[n][i], d[n][i], dot[n]);
-                        d[n][i] = tiny ? 0.0f : b_of[n] * d[n][i];
+                        d[n][i] = none ? 0.0f : b_of[n] * d[n][i];
+                        u[n][i] = none ? 0.0f : u[n][i];
                     }
                     if (row < cnt) {
                         T *gv = static_cast<T *>(a.grad_v) + (((int64_t)b * a.L + begin) * a.H + h) * a.dv + (int64_t)row * a.H * a.dv + c;
@@ -457,7 +458,7 @@ __global__ __launch_bounds__((kGradThreads<T, D>), 2) void grad_kernel(BackArgs 
 #pragma unroll
                 for (int s = 1; s < 8; s *= 2) dot[n] += __shfl_xor(dot[n], s, 8);
                 if (grp == 0 && row < cnt && a.grad_b != nullptr) {
-                    a.grad_b[((int64_t)b * a.L + begin + row) * a.H + h] = dot[n] / (fabsf(b_of[n]) < kTinyBeta ? kTinyBeta : b_of[n]);
+                    a.grad_b[((int64_t)b * a.L + begin + row) * a.H + h] = dot[n] / (writes_none(b_of[n]) ? kTinyBeta : b_of[n]);
                 }
             }
         }

@@ -320,8 +320,16 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> (&lds)[
             for (int n = 0; n < 8; ++n) x[n] = gb[n] * fmaf(-ge[n], ks[n >> 2][n & 3], walk::plane_sum(z, n));
             if constexpr (!BACK) odd = take_odd(x, q);
         }
-        split3(x, xp);
         f32x4 ua[2] = {};
+        if constexpr (BACK) {  // what is a position's own where beta is 0 (any number, in padding) stays with it
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const bool alone = writes_none(gb[n]);
+                ua[n >> 2][n & 3] = alone ? x[n] : 0.0f;
+                x[n] = alone ? 0.0f : x[n];
+            }
+        }
+        split3(x, xp);
         mfma_each(Tm, xp, ua);
         const float carry = __uint_as_float(same_in_lanes(__float_as_uint(l.gates.carry)));
         const bool fast = same_in_lanes(__float_as_uint(l.gates.fast)) != 0;
@@ -351,7 +359,10 @@ __device__ __forceinline__ void walk_chunks(const Job &j, WalkLds<T, D1> (&lds)[
         }
         // the state after the chunk: K^T (r U), or Q^T (f do') - K^T (f b dR)
 #pragma unroll
-        for (int n = 0; n < 8; ++n) x[n] *= kGrad ? -ge[n] * gb[n] : ge[n];
+        for (int n = 0; n < 8; ++n) {
+            x[n] *= kGrad ? -ge[n] * gb[n] : ge[n];
+            if (BACK && writes_none(gb[n])) x[n] = 0.0f;
+        }
         split3(x, xp);
         if (fast) {
             asm volatile("");  // a branch: the compiler would work out both and select
