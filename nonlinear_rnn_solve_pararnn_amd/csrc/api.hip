@@ -764,8 +764,11 @@ int pararnn_delta_step(int32_t dtype, int64_t B, int64_t H, int64_t Hk, int64_t 
     if (dk > kMaxHeadDim || dv > kMaxHeadDim) return PARARNN_ERR_UNSUPPORTED;
     if (!delta_dims_ok(LinattnPass::Step, dtype, B, 1, H, Hk, dk, dv) || !q || !k || !v || !log_decay || !beta || !state || !o || !out_state)
         return PARARNN_ERR_INVALID;
+    int64_t one[15];  // there is no next position
+    for (int i = 0; strides && i < 15; ++i) one[i] = i % 3 == 1 ? 0 : strides[i];
     DeltaArgs a;
-    if (!delta_args(a, dtype, B, 1, H, Hk, dk, dv, DeltaIn{q, k, v, log_decay, beta, nullptr}, strides)) return PARARNN_ERR_INVALID;
+    if (!delta_args(a, dtype, B, 1, H, Hk, dk, dv, DeltaIn{q, k, v, log_decay, beta, nullptr}, strides ? one : nullptr))
+        return PARARNN_ERR_INVALID;
     if (!delta_outputs_ok(a, state, o, out_state)) return PARARNN_ERR_INVALID;
     a.state = state;
     a.scale = scale;
