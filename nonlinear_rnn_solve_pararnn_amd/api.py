@@ -1061,6 +1061,11 @@ def _headnorm_check(q, k, q_weight, k_weight, table, positions, kind):
     return code, lead, B, L, Hq, Hk, d, R, P, nb
 
 
+def _dense_positions(positions):
+    """Positions of any strides (a row's for all rows, a column of a batch's) as the library takes them."""
+    return positions.contiguous() if isinstance(positions, torch.Tensor) else positions
+
+
 def _dense_like(t: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
 
@@ -1075,10 +1080,12 @@ def headnorm_forward(q, k=None, q_weight=None, k_weight=None, table=None, positi
     q [B, L, Hq, d] or [B, Hq, d], k alike with its own number of heads or None,
     fp32 or bf16, any strides with a dense last dimension; weights [d] fp32 or
     None; table [P, R] fp32 (a position's cosines, then its sines) or None for
-    no rotation; positions [B, L] (or [B]) int32 or int64, None for 0 .. L-1.  A
-    position outside the table turns the rotated elements to NaN.  Returns
-    (yq, yk, rq, rk), r fp32 being what headnorm_backward takes."""
+    no rotation; positions [B, L] (or [B]) int32 or int64 (copied first unless
+    dense), None for 0 .. L-1.  A position outside the table turns the rotated
+    elements to NaN.  Returns (yq, yk, rq, rk), r fp32 being what
+    headnorm_backward takes."""
     lib = load_library()
+    positions = _dense_positions(positions)
     code, lead, B, L, Hq, Hk, d, R, P, nb = _headnorm_check(q, k, q_weight, k_weight, table, positions, kind)
     dev, T = q.device, q.dtype
     if k is None:
@@ -1113,6 +1120,7 @@ def headnorm_backward(q, k, rq, rk, grad_q, grad_k=None, q_weight=None, k_weight
     are its results.  Returns (dq, dk, dq_weight, dk_weight); the weights' are
     None unless want_w (default: where a weight is given)."""
     lib = load_library()
+    positions = _dense_positions(positions)
     code, lead, B, L, Hq, Hk, d, R, P, nb = _headnorm_check(q, k, q_weight, k_weight, table, positions, kind)
     dev, T = q.device, q.dtype
     _need_typed(rq, (*lead, Hq), torch.float32, "rq", dev)
