@@ -204,7 +204,12 @@ def _workspace(op, B, L, H, device, max_iter=1, ws=None):
 
 
 def _raw_stream(device: torch.device) -> int:
-    """The device's current HIP stream as an integer (a stream object costs more than a small kernel's launch)."""
+    """The device's current HIP stream as an integer (a stream object costs more than a small kernel's launch).  Kernels
+    are launched on the current device, whose default stream has the same number as any other device's."""
+    here = torch._C._cuda_getDevice()
+    if device.index != here:
+        raise PararnnError("tensors are on cuda:%d, which is not the current device (cuda:%d): call inside "
+                           "torch.cuda.device(%d)" % (device.index, here, device.index))
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
