@@ -81,8 +81,11 @@ __global__ __launch_bounds__(walk::kThreads, (kWgs<T, D1>)) void segment_kernel(
 // Reads and writes the state once and is bound by that: k S and q S are formed
 // in the one pass that brings S into registers, S' leaves from there.  A
 // workgroup takes 64 columns of one (batch row, head); its threads are columns
-// (V of them each) by rows.  B=128, H=16, 128x128, bf16: 55 us, 4.9 TB/s; B=1: 11
-// us, most of it the host's.
+// (V of them each) by rows.  B=128, H=16, 128x128, bf16: 55 us (the kernel 48), 4.9
+// TB/s; B=1: 11 us, most of it the host's.  Rows that are not 16-byte vectors move
+// an element a thread, 2.8 TB/s: 128x127 95 us.  (A form of 32 rows a thread for
+// dk up to 128 there, as R is 8 and 16 for vectors, spilled 1796 bytes a lane and
+// took 3650.)
 constexpr int kStepCols = 64, kMaxHead = 256;
 
 struct StepArgs {
@@ -268,8 +271,7 @@ void step_launch(const DeltaArgs &p, const StepArgs &a, hipStream_t s) {
         if (p.dk <= 128) step_kernel<T, 4, 8><<<grid, walk::kThreads, 0, s>>>(a);
         else step_kernel<T, 4, 16><<<grid, walk::kThreads, 0, s>>>(a);
     } else {
-        if (p.dk <= 128) step_kernel<T, 1, 32><<<grid, walk::kThreads, 0, s>>>(a);
-        else step_kernel<T, 1, 64><<<grid, walk::kThreads, 0, s>>>(a);
+        step_kernel<T, 1, 64><<<grid, walk::kThreads, 0, s>>>(a);
     }
 }
 
