@@ -495,8 +495,8 @@ int pararnn_embedding_backward(int32_t dtype, int64_t N, int64_t V, int64_t D, c
  * the three smallest of nine products are left out: 2^-23 of a product), and
  * one rounding of each output to bf16.
  * Long sequences of few rows are walked in segments, whose number depends on
- * L, B H and the heads' widths: the same row may get other last bits in another
- * batch.  The same call gives the same bits.  (A segment multiplies with the
+ * L, B H, the type and the heads' widths: the same row may get other last bits in
+ * another batch.  The same call gives the same bits.  (A segment multiplies with the
  * matrix that it takes any state through: for keys and beta with which the state
  * grows, that may pass fp32 where the state itself does not.)
  */

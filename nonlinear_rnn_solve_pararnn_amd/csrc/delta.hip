@@ -199,7 +199,7 @@ ForwardPlan forward_plan(const DeltaArgs &p) {
     const int D1 = walk_width(p.dk);
     const int64_t pairs = p.B * p.H;
     w.chunks = chunks_of(p.L);
-    w.segs = segments(pairs * blocks_of(p.dv), w.chunks);
+    w.segs = segments(pairs, 1, blocks_of(p.dv), w.chunks, p.bf16, D1);
     w.seg_chunks = (int)((w.chunks + w.segs - 1) / w.segs);
     w.segs = (int)((w.chunks + w.seg_chunks - 1) / w.seg_chunks);
     const size_t slots = w.segs > 1 ? (size_t)(pairs * w.segs) * D1 * 4 : 0;
@@ -277,20 +277,39 @@ void step_launch(const DeltaArgs &p, const StepArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// Segments of a sequence of `chunks` that `groups` workgroups walk whole, 1 for
-// none.  Segments cost a second pass, with M's columns beside V's, and a join of
-// some microseconds each: 4 of 8 chunks at the least, or 5 where they are all
-// that fits on the CUs (two workgroups each), and more than 8 if they keep 16
-// chunks.  Forward, us, with the number of segments in brackets, H=16, 128x128,
-// bf16: B=1, L=4096: 286 whole, 129 (8), 147 (16); B=2, L=4096: 298 whole, 207 (4),
-// 204 (8); B=4, L=2048: 176 whole, 178 (2), 190 (4); B=1, L=1024: 85 whole, 90 (2),
-// 67 (4); H=8, L=512: 49 whole, 54 (2).  64x64: B=6, L=2048: 143 whole, 141 (2),
-// 120 (5).  fp32, B=1, H=8, L=32768: 64x64: 2682 whole, 320 (32), 328 (64); 64x128:
-// 420 (16), 350 (32).
-int segments(int64_t groups, int64_t chunks) {
-    const int64_t most = 2 * (int64_t)device_cu_count() / groups;
-    const int64_t n = std::min({most, chunks / 8, std::max<int64_t>(8, chunks / 16)});
-    return most < 5 || n < 4 ? 1 : (int)n;
+// Segments of a sequence of `chunks` that each (batch row, head) pair's `walks`
+// (one forward, S and D backward) go through for `blocks` of 64 columns, 1 for
+// none: as many as the CUs hold with two workgroups each, of 8 chunks at the
+// least, and more than 8 if they keep 16 chunks, where the estimate below says
+// that they take less time than the whole walk.  It counts in chunks of a walk:
+// both passes' workgroups in rounds of what fits on the card (two workgroups on a
+// CU take 1.4 times as long as one), a segment's own part at 0.8 of a walk, 3
+// chunks until a workgroup is under way, and the join of a segment, twice for S
+// and D.  Heads above 128 join slowly, and take no segments where fewer than four
+// workgroups' room is there for each of the whole walk's.
+// Against whole walks, 540 sizes (seven types and widths, both passes, 8 to 104
+// workgroups, L=1024 to 8192): 0.3% slower on average than the better of the two and
+// 11% at most; segments wherever they fit 6% and twice (B=1, L=1024, H=20, 256x256,
+// bf16 140 whole, 286 with 4), none 44%.  Where they pay, us, with their number in brackets: H=16,
+// 128x128, bf16: B=1, L=4096: 286 whole, 129 (8), 147 (16); B=2, L=4096: 298 whole, 207
+// (4), 204 (8); B=1, L=1024: 85 whole, 90 (2), 67 (4).  fp32, B=1, H=8, L=32768: 64x64:
+// 2682 whole, 320 (32), 328 (64); 64x128: 420 (16), 350 (32).  Backward, H=8, L=2048,
+// 128x128: bf16 204 whole, 120 (8), fp32 322 whole, 172 (8).
+int segments(int64_t pairs, int walks, int blocks, int64_t chunks, bool bf16, int width) {
+    const int64_t cus = device_cu_count(), groups = pairs * walks * blocks;
+    const int64_t most = 2 * cus / groups, n = std::min({most, chunks / 8, std::max<int64_t>(8, chunks / 16)});
+    const int wgs = walk_wgs(bf16, width), key_blocks = blocks_of(width);
+    if (most < 5 || n < 4 || (width > 128 && most < 8)) return 1;
+    auto rounds = [&](int64_t workgroups) {
+        const int64_t full = workgroups / (wgs * cus), rest = workgroups - full * wgs * cus;
+        const double whole = wgs == 2 ? 1.4 : 1.0;
+        return (double)full * whole + (rest == 0 ? 0.0 : rest <= cus ? 1.0 : whole);
+    };
+    const double join = walks * (width <= 64 ? 0.5 : width <= 128 ? 1.0 : bf16 ? 5.0 : 2.9);
+    // (a backward pass takes M of the last segment as well)
+    const double own = 0.8 * rounds(groups * (n - 1) + pairs * key_blocks * (walks == 2 ? n : n - 1));
+    const double cut = (own + rounds(groups * n)) * ((double)chunks / (double)n + 3.0) + join * (double)n;
+    return cut < rounds(groups) * ((double)chunks + 3.0) ? (int)n : 1;
 }
 
 }  // namespace delta

@@ -84,9 +84,11 @@ inline bool view_vec(const HeadView &v, int d, int es) {
 
 // Width of the state's rows that a walk is built for.
 inline int walk_width(int dk) { return dk <= 32 ? 32 : dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }
+// Workgroups a CU that a walk's registers are shared out for.
+constexpr int walk_wgs(bool bf16, int width) { return width > 128 || (!bf16 && width > 64) ? 1 : 2; }
 inline int64_t chunks_of(int64_t L) { return (L + C - 1) / C; }
 // delta.hip
-int segments(int64_t groups, int64_t chunks);
+int segments(int64_t pairs, int walks, int blocks, int64_t chunks, bool bf16, int width);
 // delta_back.hip
 size_t back_ws(const DeltaArgs &p);
 hipError_t backward(const DeltaArgs &p, char *scratch, hipStream_t s);

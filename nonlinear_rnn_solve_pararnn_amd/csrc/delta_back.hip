@@ -727,7 +727,7 @@ BackPlan back_plan(const DeltaArgs &p) {
     w.span = span_of(p.bf16, span_width(p));
     w.chunks = chunks_of(p.L);
     w.spans = (p.L + w.span - 1) / w.span;
-    w.segs = segments(pairs * 2 * (wide / kNB), w.chunks);
+    w.segs = segments(pairs, 2, (int)(wide / kNB), w.chunks, p.bf16, (int)D1);
     w.seg_chunks = (int)((w.chunks + w.segs - 1) / w.segs);
     w.segs = (int)((w.chunks + w.seg_chunks - 1) / w.seg_chunks);
     w.parts = p.H > p.Hk;

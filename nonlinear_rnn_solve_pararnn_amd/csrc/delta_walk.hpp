@@ -89,7 +89,7 @@ struct alignas(16) WalkLds {
 // at work and it has one barrier.  B=8, L=2048, H=16, 128x128, bf16: the forward
 // walk and the two of the backward pass 172 and 360 us with one workgroup, 163
 // and 301 with two; the forward walk 163 with one chunk, 157 with two.
-template <typename T, int D1> constexpr int kWgs = D1 > 128 || (sizeof(T) == 4 && D1 > 64) ? 1 : 2;
+template <typename T, int D1> constexpr int kWgs = walk_wgs(sizeof(T) == 2, D1);
 template <typename T, int D1> constexpr int kStages = 2 * kWgs<T, D1> * sizeof(WalkLds<T, D1>) <= 160 * 1024 ? 2 : 1;
 
 // Eight numbers of a lane (a column of its wave's, positions 8 q ..) with the
