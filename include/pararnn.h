@@ -515,6 +515,9 @@ int pararnn_delta_forward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_
  * be NULL) and grad_state [B, H, dk, dv] or NULL.  strides: as above and those of grad_o after them (18
  * values).  Where a value is not finite, the gradients are not defined.
  * Precision as above: fp32 throughout, and one rounding of each gradient.
+ * The workspace grows with B H L (heads of 128x128, bf16: 3.7 KB a position and
+ * head, 0.96 GB for B=8, L=2048, H=16; fp32 5.7; where heads share keys 8 dk bytes
+ * more), the forward pass's is 0.4 KB a position and head.
  */
 int pararnn_delta_backward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
                            const void *q, const void *k, const void *v, const float *log_decay, const float *beta,
@@ -527,7 +530,8 @@ int pararnn_delta_backward(int32_t dtype, int64_t B, int64_t L, int64_t H, int64
  * One token of the recurrence (its form for decoding): q, k [B, Hk, dk], v, o
  * [B, H, dv], log_decay, beta [B, H], state and out_state [B, H, dk, dv], both
  * required; out_state may be state itself.  strides: as above with the
- * positions' ignored, or NULL.  No workspace.
+ * positions' ignored, or NULL.  No workspace.  A value that is not finite goes
+ * where the formula takes it: what is NaN after a sequence may be infinite here.
  */
 int pararnn_delta_step(int32_t dtype, int64_t B, int64_t H, int64_t Hk, int64_t dk, int64_t dv, const void *q,
                        const void *k, const void *v, const float *log_decay, const float *beta, const int64_t *strides,

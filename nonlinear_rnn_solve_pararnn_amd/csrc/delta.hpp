@@ -161,7 +161,7 @@ __device__ __forceinline__ f32x4 mfma32(float a, float b, f32x4 c) { return __bu
 
 // A wave a chunk.  Bound by memory where there are many: rows of q and k are read
 // once, records written once.  B=8, L=2048, H=16, 128x128, bf16: 59 us for 134 MB
-// read and 105 written, in the backward pass 66 for 134 and 155.
+// read and 104 written, in the backward pass 66 for 134 and 154.
 template <typename T, int D1, bool VEC, bool BACK>
 __global__ __launch_bounds__(256) void prep_kernel(PrepArgs a) {
     constexpr int kP = kPlanes<T>, NT = D1 / 32, W = 36;

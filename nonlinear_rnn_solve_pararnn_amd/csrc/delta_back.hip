@@ -19,8 +19,8 @@
 //
 // Precision: walks as in the forward pass; S, D, U, dr, MP and MA in three planes
 // whatever the tensors are, so that bf16 gradients are fp32's, rounded once.  (MP
-// and MA at 16 bits: grad_kernel 350 us where it takes 358, B=8, L=2048, H=16,
-// 128x128.)
+// and MA at 16 bits took 2% off grad_kernel: B=8, L=2048, H=16, 128x128, 350 and
+// 358 us on one card.)
 #include "delta_walk.hpp"
 
 namespace prn {
@@ -131,14 +131,11 @@ __global__ __launch_bounds__(walk::kThreads, (kWgs<T, D1>)) void back_segment_ke
 
 // ---------------------------------------------------------------- the rest, span by span
 // (The walks before it write S, D, U and dR, 0.79 GB, and read 0.57 at the size
-// below, in 292 us: 4.6 TB/s, memory's rate.)
+// below, in 295 us: 4.6 TB/s, memory's rate.)
 // A wave owns 16 rows of S and D (16 elements of k and q) and the gradients of
 // those elements at all positions of the span; S and D go from memory straight
 // into operands, each element once.  LDS holds the rows of do, U and dr, then,
 // in their place, those of q and k and the matrices MP and MA + MA^T.
-template <int N>
-__device__ __forceinline__ void planes_to(const float (&v)[8], bf16x8 (&p)[N]) { walk::to_planes(v, p); }
-
 constexpr int grad_tiles(bool bf16, int D) { return D >= 128 && span_of(bf16, D) == 32 ? 2 : 1; }
 template <typename T, int D>
 struct GradLds {
@@ -162,16 +159,16 @@ struct GradLds {
 
 // A wave has kW tiles of 16 elements of q and k.  With two, rows read from LDS
 // serve both, and a workgroup leaves room for another one on its CU, whose loads
-// go on while this one multiplies.  With one (bf16, and fp32 up to heads of 64:
-// two would spill) a workgroup goes through several spans and has the next one's
-// first operands on their way while it works on the pairs.
-// B=8, L=2048, H=16, 128x128, bf16: 1.0 GB read and 0.2 written in 358 us, 3.4
-// TB/s; the rest is a workgroup's phases, which follow each other on its CU (LDS
-// and matrix instructions of the products with S and D take half of them).  The
-// whole backward pass 740 us with a workgroup a span, 700 so (with MP and MA at 16
-// bits; 713 as it is); grad_kernel with two
-// tiles and two workgroups a CU 438-510 us where it took 395.  B=3, L=1000, H=10,
-// 48x80, fp32: grad_kernel 62 us with one tile, 54 with two.
+// go on while this one multiplies (fp32 heads of 65 to 128 spill 28 to 52 bytes a
+// lane so).  With one (heads of up to 64, and bf16 up to 128) a workgroup goes
+// through several spans and has the next one's first operands on their way while
+// it works on the pairs.
+// B=8, L=2048, H=16, 128x128, bf16: 1.0 GB read and 0.2 written in 351 us, 3.5
+// TB/s, which is not memory's rate: a workgroup's phases follow each other on its
+// CU (LDS and matrix instructions of the products with S and D take half of them).
+// The whole backward pass 740 us with a workgroup a span, 700 so; grad_kernel with
+// two tiles and two workgroups a CU 438-510 us where it took 395.  B=3, L=1000,
+// H=10, 48x80, fp32: grad_kernel 62 us with one tile, 54 with two.
 template <typename T, int D> constexpr bool kAhead = grad_tiles(sizeof(T) == 2, D) == 1;
 template <typename T, int D> constexpr int kGradThreads = D * 4 / grad_tiles(sizeof(T) == 2, D);
 template <typename T, int D, bool VEC>

@@ -8,20 +8,21 @@
 // stand.  The rows of K and of T are read in the order of row_of, so that K S,
 // the right side and U come out as the operands of the next product as well:
 // between the chunk's operands in LDS and its results nothing crosses the
-// waves, and a chunk has two barriers.
+// waves.  A chunk has one barrier where two chunks fit in LDS (kStages), else two.
 //
 // A wave is alone on its SIMD in most launches (a (batch row, head) pair has
 // only dv / 16 of them), so the chunk's chain of dependent steps is what bounds
 // it.  LDS reads are issued a step ahead of the matrix instructions that use
 // them, results side by side take turns in the matrix unit, and results are
 // stored after the next chunk's operands have arrived (loads and stores are
-// waited for in their order).  B=8, L=2048, H=16, 128x128, bf16: 165 us, some
-// 5400 cycles a chunk.  Before, with S, U and P at 16 bits in outputs (which then
-// rounded some values the other way than fp32 does) 155; measured like that and
-// against 157: before the second stage in LDS 163, with T and P in registers 172,
-// with reads left to the compiler and one result after the other 199, with the
-// stores before the wait as well 210; planes split off by two-element dot products
-// (seven instructions for two numbers, not eleven) 169.
+// waited for in their order).  B=8, L=2048, H=16, 128x128, bf16: 153 us, some
+// 5400 cycles a chunk, 2200 of them vector and 1540 matrix instructions.  With S, U
+// and P at 16 bits in outputs (which then rounded some values the other way than
+// fp32 does) 146; measured like that on a slower card, against 157: before the second
+// stage in LDS 163, with T and P in registers 172, with reads left to the compiler
+// and one result after the other 199, with the stores before the wait as well 210;
+// planes split off by two-element dot products (seven instructions for two numbers,
+// not eleven) 169.
 #pragma once
 
 #include <type_traits>
@@ -468,7 +469,9 @@ struct JoinArgs {
     int dk, dv, cols;         // cols: blocks of 16 columns
 };
 // A workgroup joins 16 columns of one (batch row, head); wave w has 32 rows.
-// The products are fp32's in three planes.  Bound by latency: one step a segment.
+// The products are fp32's in three planes.  Bound by latency: one step a segment,
+// 1.3 us for heads of up to 64; those above 128 do not have the registers for M (988
+// bytes a lane in memory) and take some 20, 40 where S and D are joined.
 template <int D1, bool GRAD>
 __device__ __forceinline__ void join_columns(const JoinArgs &a, int bh, int blk, bf16x8 (&lds)[3][D1 / 32][64]) {
     constexpr int NT = D1 / 32;
