@@ -493,7 +493,9 @@ int pararnn_embedding_backward(int32_t dtype, int64_t N, int64_t V, int64_t D, c
  * up past fp32 counts as not finite.
  * Precision: fp32 throughout (products formed of three parts of 8 bits, of which
  * the three smallest of nine products are left out: 2^-23 of a product), and
- * one rounding of each output to bf16.
+ * one rounding of each output to bf16.  What a chunk of 32 positions leaves of a
+ * state that its keys write over (and of the state's gradient) is a difference, off
+ * by 2^-22 or so of what was there.
  * Long sequences of few rows are walked in segments, whose number depends on
  * L, B H, the type and the heads' widths: the same row may get other last bits in
  * another batch.  The same call gives the same bits.  (A segment multiplies with the
